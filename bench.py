@@ -99,7 +99,8 @@ def read_peaks():
 
 # Sources of kernels that the verify step never launches; a change to them
 # leaves the recorded traffic of the verify workloads valid.
-OTHER_OPS = ("accept_walk.cu", "ddtree_build.cu", "tree_attn.cu")
+OTHER_OPS = ("accept_walk.cu", "ddtree_build.cu", "tree_attn.cu", "cache_common.cuh",
+             "cache_attn.cu", "cache_mass.cu", "cache_evict.cu")
 
 
 def kernel_source_hash(op: str = "verify") -> str:

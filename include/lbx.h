@@ -71,7 +71,9 @@ extern "C" {
 #define LBX_DDTREE_MAX_K 8        /* lbx_ddtree_build: top-K, 1 <= K <= 8       */
 #define LBX_DDTREE_MAX_DEPTH 64   /* lbx_ddtree_build: draft positions D <= 64  */
 #define LBX_ATTN_HEAD_DIM 256     /* lbx_tree_attention: head dimension         */
-#define LBX_ATTN_MAX_NODES 64     /* lbx_tree_attention: N <= 64 tree nodes     */
+#define LBX_EVICT_MAX_T (1 << 20) /* lbx_cache_evict: T <= 2^20 positions      */
+#define LBX_ATTN_MAX_NODES 64     /* lbx_tree_attention and the operators of the
+                                     bounded cache: N <= 64 tree nodes         */
 
 /* Modes of lbx_verify_step. */
 #define LBX_MODE_AUTO 0    /* tree if N <= LBX_MAX_TREE_NODES, else chunked     */
@@ -335,6 +337,135 @@ int lbx_tree_attention(int L, int Bq, int N, int Hq, int Hkv, int dh, int T, flo
                        const uint16_t *k_cache, const uint16_t *v_cache, const uint16_t *k_tree,
                        const uint16_t *v_tree, float *o, void *workspace, size_t workspace_bytes,
                        int32_t *d_status, cudaStream_t stream);
+
+/*
+ * ---- The bounded, shared KV cache of the full-attention layers -------------
+ *
+ * Four operators for serving with a cache that does not grow without end and
+ * prompts that requests share.  They take the draft tree of a verify step;
+ * with N = 1 they are the plain decode step of one token.  lbx_window_attention
+ * and lbx_prefix_attention give the attention output and the log-sum-exp of
+ * each query; lbx_attention_mass turns the latter into per-key sums of
+ * attention weights; lbx_cache_evict appends the accepted nodes' keys and
+ * values to the cache and keeps the entries with the largest sums.
+ * Layers are a batch dimension, as in lbx_tree_attention.  Notation: G =
+ * Hq / Hkv query heads read one KV head (hq reads hq / G); depth(n) is node
+ * n's distance from the root, whose query stands at position ctx_len[b]; the
+ * accepted path is the nodes from the root to accepted[b].
+ */
+
+/* Element types of q, the keys, the values and o (16 bits each, passed as
+ * their patterns). */
+#define LBX_BF16 0
+#define LBX_F16 1
+
+typedef struct lbx_attn_cfg {
+  int L, Bq, N;  /* layers, requests, tree nodes (1 <= N <= LBX_ATTN_MAX_NODES) */
+  int Hq, Hkv;   /* query / KV heads, Hq % Hkv == 0                            */
+  int dh;        /* head dimension: 64, 128 or 256                             */
+  int T;         /* capacity of each request's cache (positions; may be 0)     */
+  int P;         /* length of the shared prefix (lbx_prefix_attention only)    */
+  int window;    /* a query sees the `window` positions up to its own (itself
+                    included); 0 = all of them                                 */
+  int n_sink;    /* the first n_sink positions stay visible / are never evicted */
+  int dtype;     /* LBX_BF16 or LBX_F16                                        */
+  float scale;   /* scale of q . k (> 0, finite)                               */
+} lbx_attn_cfg;
+
+/* Bytes of workspace lbx_window_attention (cfg->P == 0) or
+ * lbx_prefix_attention (cfg->P > 0) needs (0 on a bad cfg).  It must be
+ * zero-filled once before its first use; every call that runs to completion
+ * leaves its counters at zero; two calls that run at the same time must not
+ * share it. */
+size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *cfg);
+
+/*
+ * Tree attention with a sliding window and a few first positions that stay
+ * visible.  Cached position j < ctx_len[b] is visible to node n if
+ *     window == 0  or  ctx_len[b] + depth(n) - j < window  or  j < n_sink,
+ * and tree node m on n's root path (itself included) if the same holds for
+ * m's position ctx_len[b] + depth(m).  Over the visible keys of each query
+ *     o = sum_j exp(scale q.k_j - lse) v_j,  lse = log sum_j exp(scale q.k_j).
+ *   q [L][Bq][N][Hq][dh], k_cache, v_cache [L][Bq][T][Hkv][dh] (may be NULL
+ *   when T == 0), k_tree, v_tree [L][Bq][N][Hkv][dh], o [L][Bq][N][Hq][dh]
+ *   out, all of cfg->dtype; lse [L][Bq][N][Hq] fp32 out, may be NULL;
+ *   ctx_len [Bq] int32 in 0..T, parent [Bq][N] int32.
+ * Keys and values of positions that no query of the request sees (at or past
+ * ctx_len, before every window) may hold anything, NaN included.  A key that
+ * one query of a request sees and another does not has to have a finite
+ * value: it enters the other's sum with weight 0.  A query all of whose
+ * scores are -inf gets o = 0 and lse = -inf.
+ * cfg->P must be 0.  Returns LBX_EINVAL for unsupported shapes, NULL or
+ * misaligned pointers (16 bytes for the 16-bit arrays and the workspace, 4 for
+ * the others) or a short workspace, LBX_ECUDA if a launch fails; an invalid
+ * tree or a ctx_len outside 0..T stores LBX_ETREE in *d_status (may be NULL)
+ * and writes nothing.
+ */
+int lbx_window_attention(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const int32_t *parent,
+                         const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                         const uint16_t *k_tree, const uint16_t *v_tree, uint16_t *o, float *lse,
+                         void *workspace, size_t workspace_bytes, int32_t *d_status,
+                         cudaStream_t stream);
+
+/*
+ * Attention of a batch whose requests share a prefix: every query sees the P
+ * prefix positions, its request's ctx_len[b] cached positions and its root
+ * path in the tree.  The prefix is held once for the batch and each layer's
+ * is multiplied with the queries of all requests together.
+ *   k_prefix, v_prefix [L][P][Hkv][dh]; the others as in lbx_window_attention
+ * (o and lse are over all visible keys).  P >= 1; window and n_sink must be 0.
+ */
+int lbx_prefix_attention(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const int32_t *parent,
+                         const uint16_t *q, const uint16_t *k_prefix, const uint16_t *v_prefix,
+                         const uint16_t *k_cache, const uint16_t *v_cache, const uint16_t *k_tree,
+                         const uint16_t *v_tree, uint16_t *o, float *lse, void *workspace,
+                         size_t workspace_bytes, int32_t *d_status, cudaStream_t stream);
+
+/*
+ * Attention weights per key, gathered over the queries of the accepted path:
+ *     score[l][b][g][j]      += sum_{n on the path, hq / G = g} w(n, hq, j),
+ *     score_tree[l][b][g][m]  = the same for tree node m on the path, else 0,
+ * with w = exp(scale q.k - lse) for visible keys (visible as in
+ * lbx_window_attention), else 0.  lse is what the attention call gave; with a
+ * shared prefix it covers the prefix, whose keys are not scored; a query with
+ * lse = -inf adds nothing.
+ *   accepted [Bq] int32 in 0..N-1; q, k_cache, k_tree, lse as above;
+ *   score [L][Bq][Hkv][T] fp32, in/out (entries j >= ctx_len are not touched;
+ *   may be NULL when T == 0); score_tree [L][Bq][Hkv][N] fp32 out.
+ * cfg->P is not read.  Errors as in lbx_window_attention; an accepted index
+ * out of range is reported like an invalid tree.
+ */
+int lbx_attention_mass(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const int32_t *parent,
+                       const int32_t *accepted, const uint16_t *q, const float *lse,
+                       const uint16_t *k_cache, const uint16_t *k_tree, float *score,
+                       float *score_tree, int32_t *d_status, cudaStream_t stream);
+
+/*
+ * Append the accepted path to the cache and keep at most `budget` entries per
+ * (layer, request, KV head).  The candidates are the cached entries 0 ..
+ * ctx_len[b]-1 and then the accepted path's nodes, root first; node n's
+ * absolute position is seen[b] + depth(n).  With n candidates, size =
+ * min(n, budget) stay: first those whose position is below n_sink or among
+ * the last n_recent (>= seen_out[b] - n_recent), then by score, largest first
+ * (NaN below every number, -0 equal to 0); ties go to the lowest index.
+ * Cached entries that stay at an index below size do not move; the others
+ * that stay, in order of their index, fill the free places below size, in
+ * order.  The order of the cache's entries is thus not that of their
+ * positions, which pos keeps; keys carry their position encoding with them.
+ * Places at or past size keep what they held.
+ *   k_cache, v_cache [L][Bq][T][Hkv][dh], score fp32 and pos int32
+ *   [L][Bq][Hkv][T]: in/out; k_tree, v_tree [L][Bq][N][Hkv][dh], score_tree
+ *   [L][Bq][Hkv][N]; ctx_len, seen, accepted [Bq], parent [Bq][N]: in;
+ *   ctx_out [Bq] = size and seen_out [Bq] = seen + nodes of the path: out
+ *   (no overlap with the inputs; they are the next step's ctx_len and seen).
+ * 1 <= budget <= T <= LBX_EVICT_MAX_T, n_sink >= 0, n_recent >= 0.  cfg->P, window and scale are
+ * not read.  Errors as in lbx_attention_mass.
+ */
+int lbx_cache_evict(const lbx_attn_cfg *cfg, int budget, int n_recent, const int32_t *ctx_len,
+                    const int32_t *seen, const int32_t *parent, const int32_t *accepted,
+                    const uint16_t *k_tree, const uint16_t *v_tree, const float *score_tree,
+                    uint16_t *k_cache, uint16_t *v_cache, float *score, int32_t *pos,
+                    int32_t *ctx_out, int32_t *seen_out, int32_t *d_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -28,11 +28,15 @@ LBX_MODE_AUTO, LBX_MODE_TREE, LBX_MODE_CHUNKED, LBX_MODE_TREE_CUDA_CORES = 0, 1,
 EXPORTS = ("lbx_strerror", "lbx_workspace_size", "lbx_tree_conv", "lbx_tree_deltanet",
            "lbx_tree_persist", "lbx_verify_step", "lbx_verify_step_noalloc",
            "lbx_accept_workspace_size", "lbx_accept_walk", "lbx_ddtree_build",
-           "lbx_attn_workspace_size", "lbx_tree_attention")
+           "lbx_attn_workspace_size", "lbx_tree_attention", "lbx_cache_attn_workspace_size",
+           "lbx_window_attention", "lbx_prefix_attention", "lbx_attention_mass",
+           "lbx_cache_evict")
 LBX_ACCEPT_MAX_NODES = 4096
 LBX_DDTREE_MAX_K, LBX_DDTREE_MAX_DEPTH = 8, 64
 LBX_NOALLOC_MAX_GROUPS = 65536
 LBX_ATTN_HEAD_DIM, LBX_ATTN_MAX_NODES = 256, 64
+LBX_BF16, LBX_F16 = 0, 1
+LBX_EVICT_MAX_T = 1 << 20
 
 
 class LbxError(RuntimeError):
@@ -46,6 +50,13 @@ class lbx_cfg(ctypes.Structure):
                 ("Hk", ctypes.c_int), ("Hv", ctypes.c_int), ("d", ctypes.c_int),
                 ("K", ctypes.c_int), ("n_slots", ctypes.c_int), ("l2_eps", ctypes.c_float),
                 ("q_scale", ctypes.c_float), ("mode", ctypes.c_int)]
+
+
+class lbx_attn_cfg(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("Bq", ctypes.c_int), ("N", ctypes.c_int),
+                ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("dh", ctypes.c_int),
+                ("T", ctypes.c_int), ("P", ctypes.c_int), ("window", ctypes.c_int),
+                ("n_sink", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -84,6 +95,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.lbx_tree_attention.restype = i32
         lib.lbx_tree_attention.argtypes = ([i32] * 7 + [ctypes.c_float] + [vp] * 8
                                            + [vp, ctypes.c_size_t, vp, vp])
+        lib.lbx_cache_attn_workspace_size.restype = ctypes.c_size_t
+        lib.lbx_cache_attn_workspace_size.argtypes = [vp]
+        lib.lbx_window_attention.restype = i32
+        lib.lbx_window_attention.argtypes = [vp] * 10 + [vp, ctypes.c_size_t, vp, vp]
+        lib.lbx_prefix_attention.restype = i32
+        lib.lbx_prefix_attention.argtypes = [vp] * 12 + [vp, ctypes.c_size_t, vp, vp]
+        lib.lbx_attention_mass.restype = i32
+        lib.lbx_attention_mass.argtypes = [vp] * 12
+        lib.lbx_cache_evict.restype = i32
+        lib.lbx_cache_evict.argtypes = [vp, i32, i32] + [vp] * 15
         _lib = lib
     return _lib
 
@@ -260,4 +281,109 @@ def lbx_tree_attention(scale, ctx_len, parent, q, k_cache, v_cache, k_tree, v_tr
         _bf(q, "q"), _bf(k_cache, "k_cache") if T > 0 else None,
         _bf(v_cache, "v_cache") if T > 0 else None, _bf(k_tree, "k_tree"), _bf(v_tree, "v_tree"),
         _f32(o, "o"), _ptr(workspace, None, "workspace"), ws_bytes, _i32(d_status, "d_status"),
+        _stream(stream)))
+
+
+def make_attn_cfg(L, Bq, N, Hq, Hkv, dh, T, P=0, window=0, n_sink=0, dtype=LBX_BF16,
+                  scale=None) -> lbx_attn_cfg:
+    """Config of the bounded cache's operators; scale defaults to 1/sqrt(dh)."""
+    return lbx_attn_cfg(L=L, Bq=Bq, N=N, Hq=Hq, Hkv=Hkv, dh=dh, T=T, P=P, window=window,
+                        n_sink=n_sink, dtype=dtype, scale=dh ** -0.5 if scale is None else scale)
+
+
+def _elem(cfg):
+    """A check for the arrays of the config's element type."""
+    return _bf if cfg.dtype == LBX_BF16 else _f16
+
+
+def _f16(t, name):
+    return _ptr(t, (torch.float16,), name)
+
+
+def _sized(t, shape, name):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
+def _attn_shapes(cfg, **arrays):
+    """Check the shapes of the named arrays against the config."""
+    L, Bq, N, Hq, Hkv, dh, T = cfg.L, cfg.Bq, cfg.N, cfg.Hq, cfg.Hkv, cfg.dh, cfg.T
+    shapes = {"q": (L, Bq, N, Hq, dh), "o": (L, Bq, N, Hq, dh), "lse": (L, Bq, N, Hq),
+              "k_cache": (L, Bq, T, Hkv, dh), "v_cache": (L, Bq, T, Hkv, dh),
+              "k_tree": (L, Bq, N, Hkv, dh), "v_tree": (L, Bq, N, Hkv, dh),
+              "k_prefix": (L, cfg.P, Hkv, dh), "v_prefix": (L, cfg.P, Hkv, dh),
+              "score": (L, Bq, Hkv, T), "pos": (L, Bq, Hkv, T), "score_tree": (L, Bq, Hkv, N),
+              "parent": (Bq, N)}
+    for name, t in arrays.items():
+        _sized(t, shapes.get(name, (Bq,)), name)
+
+
+def lbx_cache_attn_workspace_size(cfg: lbx_attn_cfg) -> int:
+    return int(load().lbx_cache_attn_workspace_size(ctypes.byref(cfg)))
+
+
+def new_cache_attn_workspace(cfg: lbx_attn_cfg, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of lbx_cache_attn_workspace_size(cfg) bytes."""
+    n = lbx_cache_attn_workspace_size(cfg)
+    if n == 0:
+        raise LbxError("lbx_cache_attn_workspace_size", LBX_EINVAL)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def lbx_window_attention(cfg, ctx_len, parent, q, k_cache, v_cache, k_tree, v_tree, o, workspace,
+                         lse=None, d_status=None, stream=None):
+    """Tree attention with a sliding window and visible first positions."""
+    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, q=q, k_cache=k_cache, v_cache=v_cache,
+                 k_tree=k_tree, v_tree=v_tree, o=o, lse=lse)
+    el = _elem(cfg)
+    _check("lbx_window_attention", load().lbx_window_attention(
+        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"), el(q, "q"),
+        el(k_cache, "k_cache"), el(v_cache, "v_cache"), el(k_tree, "k_tree"),
+        el(v_tree, "v_tree"), el(o, "o"), _f32(lse, "lse"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _i32(d_status, "d_status"),
+        _stream(stream)))
+
+
+def lbx_prefix_attention(cfg, ctx_len, parent, q, k_prefix, v_prefix, k_cache, v_cache, k_tree,
+                         v_tree, o, workspace, lse=None, d_status=None, stream=None):
+    """Attention of a batch over one shared prefix, its own caches and trees."""
+    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, q=q, k_prefix=k_prefix, v_prefix=v_prefix,
+                 k_cache=k_cache, v_cache=v_cache, k_tree=k_tree, v_tree=v_tree, o=o, lse=lse)
+    el = _elem(cfg)
+    _check("lbx_prefix_attention", load().lbx_prefix_attention(
+        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"), el(q, "q"),
+        el(k_prefix, "k_prefix"), el(v_prefix, "v_prefix"), el(k_cache, "k_cache"),
+        el(v_cache, "v_cache"), el(k_tree, "k_tree"), el(v_tree, "v_tree"), el(o, "o"),
+        _f32(lse, "lse"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _i32(d_status, "d_status"),
+        _stream(stream)))
+
+
+def lbx_attention_mass(cfg, ctx_len, parent, accepted, q, lse, k_cache, k_tree, score, score_tree,
+                       d_status=None, stream=None):
+    """Accumulate the accepted path's attention weights per key."""
+    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, accepted=accepted, q=q, lse=lse,
+                 k_cache=k_cache, k_tree=k_tree, score=score, score_tree=score_tree)
+    el = _elem(cfg)
+    _check("lbx_attention_mass", load().lbx_attention_mass(
+        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"),
+        _i32(accepted, "accepted"), el(q, "q"), _f32(lse, "lse"), el(k_cache, "k_cache"),
+        el(k_tree, "k_tree"), _f32(score, "score"), _f32(score_tree, "score_tree"),
+        _i32(d_status, "d_status"), _stream(stream)))
+
+
+def lbx_cache_evict(cfg, budget, n_recent, ctx_len, seen, parent, accepted, k_tree, v_tree,
+                    score_tree, k_cache, v_cache, score, pos, ctx_out, seen_out, d_status=None,
+                    stream=None):
+    """Append the accepted path to the cache and keep its `budget` best entries."""
+    _attn_shapes(cfg, ctx_len=ctx_len, seen=seen, parent=parent, accepted=accepted, k_tree=k_tree,
+                 v_tree=v_tree, score_tree=score_tree, k_cache=k_cache, v_cache=v_cache,
+                 score=score, pos=pos, ctx_out=ctx_out, seen_out=seen_out)
+    el = _elem(cfg)
+    _check("lbx_cache_evict", load().lbx_cache_evict(
+        ctypes.byref(cfg), int(budget), int(n_recent), _i32(ctx_len, "ctx_len"),
+        _i32(seen, "seen"), _i32(parent, "parent"), _i32(accepted, "accepted"),
+        el(k_tree, "k_tree"), el(v_tree, "v_tree"), _f32(score_tree, "score_tree"),
+        el(k_cache, "k_cache"), el(v_cache, "v_cache"), _f32(score, "score"), _i32(pos, "pos"),
+        _i32(ctx_out, "ctx_out"), _i32(seen_out, "seen_out"), _i32(d_status, "d_status"),
         _stream(stream)))
