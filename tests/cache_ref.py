@@ -77,6 +77,47 @@ def attention(inp, window=0, n_sink=0, scale=None, prefix=False):
     return o, lse, o_tol, lse_tol
 
 
+def attention_dense(inp, window=0, n_sink=0):
+    """attention() for long caches, as dense masked products in fp64 on the GPU;
+    a prefix is taken as the cache's first positions."""
+    q = inp["q"].cuda().double()
+    L, Bq, N, Hq, dh = q.shape
+    Hkv, T = inp["k_tree"].shape[3], inp["k_cache"].shape[2]
+    G, u = Hq // Hkv, U["f16" if inp["q"].dtype == torch.float16 else "bf16"]
+    P = inp["k_prefix"].shape[1] if "k_prefix" in inp else 0
+    seen = torch.zeros(Bq, N, P + T + N, dtype=torch.bool)
+    seen[:, :, :P] = True
+    for b in range(Bq):
+        for n in range(N):
+            js, ms = visible(inp["parent"][b].tolist(), n, int(inp["ctx_len"][b]), window, n_sink)
+            seen[b, n, [P + j for j in js] + [P + T + m for m in ms]] = True
+    seen = seen.cuda().repeat_interleave(G, 1)
+    o, lse = torch.empty_like(q), torch.empty(L, Bq, N, Hq, dtype=torch.float64, device="cuda")
+    o_tol, lse_tol = torch.empty_like(q), torch.empty_like(lse)
+    for l in range(L):
+        for g in range(Hkv):
+            parts = [[inp[c][l, :, :, g] for c in (x + "_cache", x + "_tree")] for x in "kv"]
+            if P:
+                parts = [[inp[x + "_prefix"][l, None, :, g].expand(Bq, -1, -1)] + p
+                         for x, p in zip("kv", parts)]
+            k, v = (torch.cat(p, 1).cuda().double() for p in parts)
+            qg = q[l, :, :, g * G:(g + 1) * G].reshape(Bq, N * G, dh)
+            s = (qg @ k.transpose(1, 2) * dh ** -0.5).masked_fill(~seen, -torch.inf)
+            e = (qg.abs() @ k.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1)
+            e = e * (dh ** -0.5 * (dh + 2) * 2.0 ** -24)
+            z = s.logsumexp(-1)
+            w = (s - z[..., None]).exp()
+            o1 = w @ v
+            t1 = 1.02 * (u * o1.abs() + (u + 2 * e[..., None] + 2.0 ** -20) * (w @ v.abs()))
+            if inp["q"].dtype == torch.float16:
+                t1 += 1.02 * 2.0 ** -25 * (seen.double() @ v.abs() + 1)
+            o[l, :, :, g * G:(g + 1) * G] = o1.view(Bq, N, G, dh)
+            o_tol[l, :, :, g * G:(g + 1) * G] = t1.view(Bq, N, G, dh)
+            lse[l, :, :, g * G:(g + 1) * G] = z.view(Bq, N, G)
+            lse_tol[l, :, :, g * G:(g + 1) * G] = (e + 2.0 ** -20 * (1 + z.abs())).view(Bq, N, G)
+    return o.cpu().numpy(), lse.cpu().numpy(), o_tol.cpu().numpy(), lse_tol.cpu().numpy()
+
+
 def mass(inp, lse, score, window=0, n_sink=0, scale=None):
     """score, score_tree in fp64 and the bounds of their errors."""
     q, kc, kt = (inp[k].double().numpy() for k in ("q", "k_cache", "k_tree"))

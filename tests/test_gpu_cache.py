@@ -109,6 +109,37 @@ def test_prefix_attention(name):
     check_attention(R.make_inputs(**PREFIX[name], seed=200 + len(name)))
 
 
+# Enough keys that every CTA walks many blocks and several streams, whole ones
+# among them, with lengths that differ from request to request.
+BUSY = {
+    "dh256_two_tiles": (dict(L=4, Bq=4, N=22, Hq=12, Hkv=2, dh=256, T=3000, ctx=[3000, 1, 1501, 2111]), 0, 0),
+    "dh256_window": (dict(L=8, Bq=3, N=9, Hq=8, Hkv=4, dh=256, T=2500, ctx=[2500, 700, 2047]), 1100, 70),
+    "dh128_one_row": (dict(L=4, Bq=6, N=1, Hq=8, Hkv=8, dh=128, T=4000,
+                           ctx=[4000, 3999, 0, 2222, 127, 3100]), 0, 0),
+    "dh128_f16": (dict(L=4, Bq=6, N=5, Hq=32, Hkv=8, dh=128, T=2100, dtype="f16",
+                       ctx=[2100, 2000, 1999, 64, 129, 1024]), 0, 0),
+    "dh64_three_tiles": (dict(L=3, Bq=4, N=64, Hq=30, Hkv=5, dh=64, T=2000, ctx=[2000, 77, 1231, 640]), 0, 0),
+    "dh64_f16_window": (dict(L=9, Bq=5, N=3, Hq=16, Hkv=8, dh=64, T=3000, dtype="f16",
+                             ctx=[3000, 2900, 511, 1025, 2001]), 1500, 3),
+    "prefix_dh256": (dict(L=3, Bq=5, N=22, Hq=12, Hkv=2, dh=256, T=700, P=3001, ctx=[700, 3, 501, 258, 640]), 0, 0),
+    "prefix_dh128_f16": (dict(L=3, Bq=9, N=7, Hq=32, Hkv=4, dh=128, T=900, P=4000, dtype="f16"), 0, 0),
+    "prefix_dh64": (dict(L=4, Bq=40, N=2, Hq=16, Hkv=4, dh=64, T=300, P=2049), 0, 0),
+}
+
+
+@pytest.mark.parametrize("name", sorted(BUSY))
+def test_long_ragged_batches(name):
+    sizes, window, n_sink = BUSY[name]
+    inp = R.make_inputs(**sizes, seed=500 + len(name))
+    o, lse, status = run_attention(inp, window=window, n_sink=n_sink)
+    assert status == 0
+    ref_o, ref_lse, o_tol, lse_tol = R.attention_dense(inp, window=window, n_sink=n_sink)
+    over = np.abs(o.double().numpy() - ref_o) / o_tol
+    assert np.isfinite(over).all() and over.max() <= 1, float(over.max())
+    over = np.abs(lse.double().numpy() - ref_lse) / lse_tol
+    assert np.isfinite(over).all() and over.max() <= 1, float(over.max())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("scale", [0.3, 1.0])
 def test_other_scales(dtype, scale):

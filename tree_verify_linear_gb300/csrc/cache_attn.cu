@@ -1,70 +1,78 @@
 // cache_attn.cu -- attention over a bounded or shared KV cache:
-// lbx_window_attention and lbx_prefix_attention.
-#include "cache_common.cuh"
+// lbx_window_attention and lbx_prefix_attention (host side; the kernel is in
+// cache_attn.cuh).
+//
+// The window call is one launch over the requests' key lists.  The prefix call
+// is two: the queries of all requests over the prefix, whose normalised result
+// and base-2 lse go to the workspace in fp32, then the requests' own keys,
+// whose last step joins the two by their lse.
+#include <cudaTypedefs.h>
+
+#include <cstring>
+#include <mutex>
+
+#include "cache_attn.cuh"
 
 namespace lbx {
 namespace cache {
 namespace {
 
-struct Args {
-  lbx_attn_cfg c;
-  const int32_t *ctx_len, *parent;
-  const uint16_t *q, *kp, *vp, *kc, *vc, *kt, *vt;
-  uint16_t *o;
-  float *lse;
-  int32_t *status;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+bool have_encode() {
+  std::call_once(g_encode_once, [] {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode != nullptr;
+}
+
+// (dh, Hkv, len, lists) view of a [lists][len][Hkv][dh] array of 16-bit
+// values; box: 64 columns of one head's `keys` consecutive positions.
+bool encode(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, int lists,
+            int keys) {
+  const cuuint64_t row = (cuuint64_t)c->Hkv * c->dh * 2;
+  const cuuint64_t gdim[4] = {(cuuint64_t)c->dh, (cuuint64_t)c->Hkv, (cuuint64_t)len,
+                              (cuuint64_t)lists};
+  const cuuint64_t gstride[3] = {(cuuint64_t)c->dh * 2, row, row * (cuuint64_t)len};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)keys, 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), gdim, gstride,
+                  box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The workspace: partials and counters of the requests' launch; with a prefix
+// also the prefix launch's, its results and their lse.
+struct Space {
+  Tiling own, pre;
+  size_t count, pre_count, x_o, x_lse, bytes;  // offsets after the partials
 };
-
-constexpr int kWarps = 8;
-
-// One warp per query row: every visible key in turn, a running maximum and sum.
-__global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const Args A) {
-  const lbx_attn_cfg &c = A.c;
-  if (batch_bad(c.Bq, c.N, c.T, A.ctx_len, A.parent, nullptr)) {
-    if (threadIdx.x == 0 && A.status) *A.status = LBX_ETREE;
-    return;
+Space space_of(const lbx_attn_cfg *c) {
+  Space s;
+  const size_t part = up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
+  const long long G = c->Hq / c->Hkv, rows = (long long)c->N * G;
+  const size_t lists = (size_t)c->L * c->Hkv;
+  s.own = tiling(rows);
+  s.pre = tiling(rows * c->Bq);
+  s.count = part;
+  s.pre_count = s.count + up256(lists * c->Bq * s.own.tiles * 4);
+  s.x_o = s.pre_count, s.x_lse = s.x_o, s.bytes = s.x_lse;
+  if (c->P > 0) {
+    const size_t queries = (size_t)c->L * c->Bq * c->N * c->Hq;
+    s.x_o += up256(lists * s.pre.tiles * 4);
+    s.x_lse = s.x_o + up256(queries * c->dh * 4);
+    s.bytes = s.x_lse + up256(queries * 4);
   }
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (long long)c.L * c.Bq * c.N * c.Hq) return;
-  const int lane = threadIdx.x & 31;
-  const int hq = (int)(row % c.Hq);
-  const long long lbn = row / c.Hq;
-  const int n = (int)(lbn % c.N);
-  const long long lb = lbn / c.N;
-  const int l = (int)(lb / c.Bq), b = (int)(lb % c.Bq);
-  const int g = hq / (c.Hq / c.Hkv), per = c.dh / 32;
-  float q[8], acc[8];
-  for (int e = 0; e < per; ++e) {
-    q[e] = to_f32(A.q[row * c.dh + lane * per + e], c.dtype) * c.scale;
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, sum = 0.f;
-  auto key = [&](const uint16_t *k, const uint16_t *v, long long at) {
-    const size_t off = ((size_t)at * c.Hkv + g) * c.dh + lane * per;
-    float s = 0.f;
-    for (int e = 0; e < per; ++e) s = fmaf(q[e], to_f32(k[off + e], c.dtype), s);
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    const float m1 = fmaxf(m, s);
-    if (m1 == -INFINITY) return;
-    const float old = expf(m - m1), p = expf(s - m1);
-    sum = sum * old + p;
-    for (int e = 0; e < per; ++e) acc[e] = acc[e] * old + p * to_f32(v[off + e], c.dtype);
-    m = m1;
-  };
-  const uint64_t anc = path_mask(A.parent + (size_t)b * c.N, n);
-  const int ctx = A.ctx_len[b], at = ctx + __popcll(anc) - 1;
-  for (int j = 0; j < c.P; ++j) key(A.kp, A.vp, (long long)l * c.P + j);
-  for (int j = 0; j < ctx; ++j)
-    if (sees(at, j, c.window, c.n_sink)) key(A.kc, A.vc, lb * c.T + j);
-  int pos = ctx;
-  for (int t = 0; t < c.N; ++t)
-    if (anc >> t & 1) {
-      if (sees(at, pos, c.window, c.n_sink)) key(A.kt, A.vt, lb * c.N + t);
-      ++pos;
-    }
-  for (int e = 0; e < per; ++e)
-    A.o[row * c.dh + lane * per + e] = from_f32(sum > 0.f ? acc[e] / sum : 0.f, c.dtype);
-  if (A.lse && lane == 0) A.lse[row] = sum > 0.f ? m + logf(sum) : -INFINITY;
+  return s;
 }
 
 int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *parent,
@@ -77,11 +85,59 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if (c->T > 0 && (!aligned_to(kc, 16) || !aligned_to(vc, 16))) return LBX_EINVAL;
   if (c->P > 0 && (!aligned_to(kp, 16) || !aligned_to(vp, 16))) return LBX_EINVAL;
   if ((lse && !aligned_to(lse, 4)) || (status && !aligned_to(status, 4))) return LBX_EINVAL;
-  if (ws_bytes < lbx_cache_attn_workspace_size(c)) return LBX_EINVAL;
-  const Args A = {*c, ctx_len, parent, q, kp, vp, kc, vc, kt, vt, o, lse, status};
-  const long long rows = (long long)c->L * c->Bq * c->N * c->Hq;
-  attn_rows_kernel<<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(A);
-  return cudaGetLastError() == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  const Space s = space_of(c);
+  if (ws_bytes < s.bytes) return LBX_EINVAL;
+  if (!have_encode()) return LBX_ECUDA;
+  const int v_keys = c->dh == 256 ? Lay<256>::kVBox : kUnit;
+  static_assert(Lay<128>::kVBox == kUnit && Lay<64>::kVBox == kUnit, "V boxes");
+
+  int dev = 0, nsm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || nsm < 1)
+    return LBX_ECUDA;
+  if (nsm > kMaxCtas) nsm = kMaxCtas;
+
+  unsigned char *base = static_cast<unsigned char *>(ws);
+  AttnArgs A = {};
+  A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = c->Hq / c->Hkv;
+  A.Bq = c->Bq, A.N = c->N, A.T = c->T;
+  A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.ctx_len = ctx_len, A.parent = parent, A.q = q, A.status = status;
+  A.part = reinterpret_cast<float *>(base);
+  const bool f16 = c->dtype == LBX_F16;
+  auto launch = [&](const AttnMaps &maps) {
+    int grid = nsm / A.til.group * A.til.group;
+    if (grid < A.til.group) grid = A.til.group;
+    const cudaError_t e = c->dh == 64    ? launch_attn<64>(f16, maps, A, grid, stream)
+                          : c->dh == 128 ? launch_attn<128>(f16, maps, A, grid, stream)
+                                         : launch_attn<256>(f16, maps, A, grid, stream);
+    return e == cudaSuccess;
+  };
+  AttnMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  if (c->P > 0) {
+    if (!encode(&maps.k, kp, c, c->P, c->L, kUnit) || !encode(&maps.v, vp, c, c->P, c->L, v_keys))
+      return LBX_ECUDA;
+    maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
+    A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
+    A.o32 = reinterpret_cast<float *>(base + s.x_o);
+    A.lse2 = reinterpret_cast<float *>(base + s.x_lse);
+    A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count);
+    if (!launch(maps)) return LBX_ECUDA;
+    A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr, A.fixed = 0;
+  }
+  const int lists = c->L * c->Bq;
+  if (!encode(&maps.kt, kt, c, c->N, lists, kUnit) || !encode(&maps.vt, vt, c, c->N, lists, v_keys))
+    return LBX_ECUDA;
+  maps.k = maps.kt, maps.v = maps.vt;  // without a cache: never read
+  if (c->T > 0 &&
+      (!encode(&maps.k, kc, c, c->T, lists, kUnit) || !encode(&maps.v, vc, c, c->T, lists, v_keys)))
+    return LBX_ECUDA;
+  A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
+  A.window = c->window, A.n_sink = c->n_sink;
+  A.o = o, A.lse = lse;
+  A.counters = reinterpret_cast<unsigned int *>(base + s.count);
+  return launch(maps) ? LBX_OK : LBX_ECUDA;
 }
 
 }  // namespace
@@ -89,7 +145,8 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
 }  // namespace lbx
 
 extern "C" size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *c) {
-  return lbx::cache::cfg_ok(c) ? 256 : 0;
+  using namespace lbx::cache;
+  return cfg_ok(c) ? space_of(c).bytes : 0;
 }
 
 extern "C" int lbx_window_attention(const lbx_attn_cfg *c, const int32_t *ctx_len,

@@ -1,0 +1,13 @@
+// cache_attn_256.cu -- cache_attn_kernel for head dimension 256.
+#include "cache_attn.cuh"
+
+namespace lbx {
+namespace cache {
+template <>
+cudaError_t launch_attn<256>(bool f16, const AttnMaps &maps, const AttnArgs &A, int grid,
+                             cudaStream_t stream) {
+  return f16 ? launch_attn_of<256, true>(maps, A, grid, stream)
+             : launch_attn_of<256, false>(maps, A, grid, stream);
+}
+}  // namespace cache
+}  // namespace lbx
