@@ -40,6 +40,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "cache_common.cuh"
 #include "cache_ptx.cuh"
 
@@ -115,14 +117,20 @@ struct Lay {
   static constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 };
 
+// What joining the pieces of a cut stream costs, in blocks.
+constexpr int kJoinBlocks = 3;
+
 // Walks a CTA's range of the block list.  Used by whole warps, each lane alike.
+// Where whole streams per group come out within kJoinBlocks of equal ranges of
+// blocks, a stream counts as one entry of the list and is not cut.
 struct Walk {
   const AttnArgs &A;
-  long long total, groups, cg, x, x_end, per_b_base;  // per_b_base: first block of request b
+  long long total, groups, cg, x, x_end, per_b_base;  // per_b_base: first entry of request b
+  bool uncut;
   int slot_in_group, b, nblk, ctx;
   // the current segment
   int l, h, set, tile, blk0, blk1;
-  long long first;  // index of the stream's block 0
+  long long first;  // the stream's first entry
   bool live;        // this CTA has a tile of the stream
 
   // units of a request's key list
@@ -145,12 +153,26 @@ struct Walk {
     return (long long)A.L * A.Hkv * A.til.sets;
   }
 
-  __device__ __forceinline__ Walk(const AttnArgs &a, int lane) : A(a) {
+  // Entries of the current request's streams in the list, each.
+  __device__ __forceinline__ int entries() const { return uncut ? 1 : nblk; }
+
+  __device__ __forceinline__ Walk(const AttnArgs &a, int lane) : A(a), uncut(false) {
     long long sum = 0;
-    for (int r = lane; r < A.n_req; r += 32) sum += blocks_of(r);
-    for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    int most = 0;
+    for (int r = lane; r < A.n_req; r += 32) {
+      sum += blocks_of(r);
+      most = nblk > most ? nblk : most;
+    }
+    for (int w = 16; w; w >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      const int y = __shfl_xor_sync(0xffffffffu, most, w);
+      most = y > most ? y : most;
+    }
     total = sum * streams();
     groups = (long long)gridDim.x / A.til.group;
+    const long long all = streams() * A.n_req;
+    uncut = (all + groups - 1) / groups * most <= (total + groups - 1) / groups + kJoinBlocks;
+    if (uncut) total = all;
     if (groups > total) groups = total;
     cg = blockIdx.x / A.til.group;
     slot_in_group = (int)(blockIdx.x - cg * A.til.group);
@@ -160,7 +182,8 @@ struct Walk {
     b = 0, per_b_base = 0;
     if (x < x_end) {
       for (int r0 = 0;; r0 += 32) {
-        const long long mine = r0 + lane < A.n_req ? blocks_of(r0 + lane) * streams() : 0;
+        long long mine = 0;
+        if (r0 + lane < A.n_req) blocks_of(r0 + lane), mine = entries() * streams();
         long long upto = mine;
         for (int w = 1; w < 32; w <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, upto, w);
@@ -182,18 +205,18 @@ struct Walk {
   // Take the next segment; false at the end of the range.
   __device__ __forceinline__ bool next() {
     if (x >= x_end) return false;
-    while (x - per_b_base >= nblk * streams()) {
-      per_b_base += nblk * streams();
+    while (x - per_b_base >= entries() * streams()) {
+      per_b_base += entries() * streams();
       blocks_of(++b);
     }
-    const long long in_b = x - per_b_base, s = in_b / nblk;
-    blk0 = (int)(in_b - s * nblk);
+    const long long in_b = x - per_b_base, s = in_b / entries();
+    blk0 = (int)(in_b - s * entries());
     first = x - blk0;
     set = (int)(s % A.til.sets);
     const int lh = (int)(s / A.til.sets);
     l = lh / A.Hkv, h = lh - l * A.Hkv;
-    blk1 = x_end - first < nblk ? (int)(x_end - first) : nblk;
-    x = first + blk1;
+    blk1 = uncut || x_end - first >= nblk ? nblk : (int)(x_end - first);
+    x = uncut ? x + 1 : first + blk1;
     tile = set * A.til.group + slot_in_group;
     live = tile < A.til.tiles;
     return true;
@@ -450,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (have) load_q();
     while (have) {
       const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
-      const int nb = blk1 - blk0, nblk = W.nblk, ctx = W.ctx;
+      const int nb = blk1 - blk0, ctx = W.ctx;
       const long long first = W.first;
       const int row = tile * kRows + r;
       const bool real = row < A.til.rows;
@@ -620,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       q += nb;
       // the next Q tile goes in while the last product runs: every score
       // product of this segment is done
-      const long long c_first = W.owner(first), c_last = W.owner(first + nblk - 1);
+      const long long c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
       const int set = W.set;
       have = advance();
       if (have) load_q();
@@ -635,53 +658,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = misc[2] == 0;
       float l_sum = red[r] + red[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
-      const size_t out_row =
-          ((((size_t)l * A.n_req + b) * A.nodes + node) * A.Hq + h * A.G + (row - node * A.G));
-      // Write 32 columns of a finished row, joined with the prefix's if there is one.
-      auto emit = [&](int col, const float *acc, float m, float sum) {
+      // Write C columns of a finished row (its place among all queries), joined
+      // with the prefix's if there is one.
+      auto emit = [&](auto width, size_t at, int col, const float *acc, float m, float sum) {
+        constexpr int C = decltype(width)::value;
         const float own = sum > 0.f ? m + log2f(sum) : -INFINITY;
-        float all = own, w = sum > 0.f ? 1.f / sum : 0.f, wx = 0.f;
+        float all = own, w = sum > 0.f ? 1.f / sum : 0.f;
+        float v[C];
         if (A.x_o) {
-          const float x = __ldcg(A.x_lse2 + out_row);
-          const float top = fmaxf(own, x);
+          float4 f[C / 4];
+          const float4 *xo = reinterpret_cast<const float4 *>(A.x_o + at * DH + col);
+#pragma unroll
+          for (int e = 0; e < C / 4; ++e) f[e] = __ldcg(xo + e);
+          const float x = __ldcg(A.x_lse2 + at), top = fmaxf(own, x);
+          float wx = 0.f;
           if (top != -INFINITY) {
             const float eo = exp2f(own - top), ex = exp2f(x - top), inv = 1.f / (eo + ex);
             w *= eo * inv, wx = ex * inv;
             all = top + log2f(eo + ex);
           }
-        }
-        float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = acc[e] * w;
-        if (A.x_o) {
-          const float4 *xo = reinterpret_cast<const float4 *>(A.x_o + out_row * DH + col);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 f = __ldcg(xo + e);
-            v[4 * e] = fmaf(wx, f.x, v[4 * e]);
-            v[4 * e + 1] = fmaf(wx, f.y, v[4 * e + 1]);
-            v[4 * e + 2] = fmaf(wx, f.z, v[4 * e + 2]);
-            v[4 * e + 3] = fmaf(wx, f.w, v[4 * e + 3]);
+          for (int e = 0; e < C / 4; ++e) {
+            v[4 * e] = fmaf(acc[4 * e], w, wx * f[e].x);
+            v[4 * e + 1] = fmaf(acc[4 * e + 1], w, wx * f[e].y);
+            v[4 * e + 2] = fmaf(acc[4 * e + 2], w, wx * f[e].z);
+            v[4 * e + 3] = fmaf(acc[4 * e + 3], w, wx * f[e].w);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < C; ++e) v[e] = acc[e] * w;
         }
         if (A.o32) {
-          float4 *to = reinterpret_cast<float4 *>(A.o32 + out_row * DH + col);
+          float4 *to = reinterpret_cast<float4 *>(A.o32 + at * DH + col);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < C / 4; ++e)
             to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         } else {
-          uint4 *to = reinterpret_cast<uint4 *>(A.o + out_row * DH + col);
+          uint2 *to = reinterpret_cast<uint2 *>(A.o + at * DH + col);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            to[e] = make_uint4(pack2<F16>(v[8 * e], v[8 * e + 1]),
-                               pack2<F16>(v[8 * e + 2], v[8 * e + 3]),
-                               pack2<F16>(v[8 * e + 4], v[8 * e + 5]),
-                               pack2<F16>(v[8 * e + 6], v[8 * e + 7]));
+          for (int e = 0; e < C / 4; ++e)
+            to[e] = make_uint2(pack2<F16>(v[4 * e], v[4 * e + 1]),
+                               pack2<F16>(v[4 * e + 2], v[4 * e + 3]));
         }
         if (col == 0) {
-          if (A.lse2) A.lse2[out_row] = all;
-          if (A.lse) A.lse[out_row] = all * 0.6931471805599453f;
+          if (A.lse2) A.lse2[at] = all;
+          if (A.lse) A.lse[at] = all * 0.6931471805599453f;
         }
+      };
+      // The place among all queries of a row of the stream.
+      auto place = [&](int rw) {
+        const int nd = rw / A.G;
+        return (((size_t)l * A.n_req + b) * A.nodes + nd) * A.Hq + h * A.G + (rw - nd * A.G);
       };
       const bool whole = c_first == c_last;
       // this CTA's partial: its first segment's, or its last's
@@ -696,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_wait_ld();
           if (!real) continue;
           if (whole) {
-            if (valid) emit(col, ov, m2, l_sum);
+            if (valid) emit(std::integral_constant<int, 32>{}, place(row), col, ov, m2, l_sum);
           } else {
             float4 *to = reinterpret_cast<float4 *>(pp + 2 * kRows + (size_t)r * DH + col);
 #pragma unroll
@@ -717,41 +744,79 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (misc[1]) A.counters[counter] = 0u;  // for the next call
         }
         ptx::named_sync(5, kSoftmaxThreads);
-        if (misc[1] && real) {
+        // the last CTA joins the pieces: four columns of a row per thread, the
+        // pieces' m, l and O of up to eight of them in flight at a time
+        // the last CTA joins the pieces: four columns of a row per thread, eight
+        // loads of O in flight (of several rows where there are few pieces)
+        if (misc[1]) {
           __threadfence();
-          auto piece_of = [&](long long g) {
-            const long long cta = g * A.til.group + (tile - set * A.til.group);
-            return A.part + ((size_t)cta * 2 + (W.begin_of(g) >= first ? 0 : 1)) * part_floats(DH);
-          };
-          float top = -INFINITY, sum = 0.f;
-          for (long long g = c_first; g <= c_last; ++g) top = fmaxf(top, __ldcg(piece_of(g) + r));
-          for (long long g = c_first; g <= c_last; ++g) {
-            const float lg = __ldcg(piece_of(g) + kRows + r);
-            if (lg > 0.f) sum += exp2f(__ldcg(piece_of(g) + r) - top) * lg;
-          }
-#pragma unroll 1
-          for (int c = 0; c < kHalf / 32; ++c) {
-            const int col = hf * kHalf + 32 * c;
-            float acc[32];
+          const int rows = A.til.rows - tile * kRows < kRows ? A.til.rows - tile * kRows : kRows;
+          const int lane_of = tile - set * A.til.group, n_piece = (int)(c_last - c_first) + 1;
+          // only a stream's first piece may not be its CTA's first
+          const int slot0 = W.begin_of(c_first) < first ? 1 : 0;
+          auto join = [&](auto per) {
+            constexpr int PP = decltype(per)::value, II = 8 / PP;  // pieces, items at a time
+            for (int idx0 = tid; idx0 < rows * (DH / 4); idx0 += II * kSoftmaxThreads) {
+              float top[II], sum[II], acc[II][4];
+              size_t at[II];  // of the item in a partial's O
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-            for (long long g = c_first; g <= c_last; ++g) {
-              const float *pg = piece_of(g);
-              if (!(__ldcg(pg + kRows + r) > 0.f)) continue;
-              const float w = exp2f(__ldcg(pg + r) - top);
-              const float4 *from =
-                  reinterpret_cast<const float4 *>(pg + 2 * kRows + (size_t)r * DH + col);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 f = __ldcg(from + e);
-                acc[4 * e] = fmaf(w, f.x, acc[4 * e]);
-                acc[4 * e + 1] = fmaf(w, f.y, acc[4 * e + 1]);
-                acc[4 * e + 2] = fmaf(w, f.z, acc[4 * e + 2]);
-                acc[4 * e + 3] = fmaf(w, f.w, acc[4 * e + 3]);
+              for (int i = 0; i < II; ++i) {
+                const int idx = idx0 + i * kSoftmaxThreads;
+                at[i] = (size_t)(idx < rows * (DH / 4) ? idx : idx0);
+                top[i] = -INFINITY, sum[i] = 0.f;
+                acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
               }
+              for (int g0 = 0; g0 < n_piece; g0 += PP) {
+                float mg[II][PP], lg[II][PP];
+                float4 og[II][PP];
+#pragma unroll
+                for (int e = 0; e < PP; ++e) {
+                  const int g = g0 + e < n_piece ? g0 + e : 0;
+                  const float *pg =
+                      A.part + ((size_t)((c_first + g) * A.til.group + lane_of) * 2 +
+                                (g == 0 ? slot0 : 0)) * part_floats(DH);
+#pragma unroll
+                  for (int i = 0; i < II; ++i) {
+                    const int rr = (int)(at[i] / (DH / 4));
+                    mg[i][e] = g0 + e < n_piece ? __ldcg(pg + rr) : -INFINITY;
+                    lg[i][e] = __ldcg(pg + kRows + rr);
+                    og[i][e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) + at[i]);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < II; ++i) {
+                  float t8 = top[i];
+#pragma unroll
+                  for (int e = 0; e < PP; ++e) t8 = fmaxf(t8, mg[i][e]);
+                  if (t8 == -INFINITY) continue;
+                  const float old = ptx::ex2(top[i] - t8);
+                  top[i] = t8, sum[i] *= old;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[i][e] *= old;
+#pragma unroll
+                  for (int e = 0; e < PP; ++e) {
+                    if (mg[i][e] == -INFINITY) continue;  // an empty piece's O is not read
+                    const float w = ptx::ex2(mg[i][e] - t8);
+                    sum[i] = fmaf(w, lg[i][e], sum[i]);
+                    acc[i][0] = fmaf(w, og[i][e].x, acc[i][0]);
+                    acc[i][1] = fmaf(w, og[i][e].y, acc[i][1]);
+                    acc[i][2] = fmaf(w, og[i][e].z, acc[i][2]);
+                    acc[i][3] = fmaf(w, og[i][e].w, acc[i][3]);
+                  }
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < II; ++i)
+                if (idx0 + i * kSoftmaxThreads < rows * (DH / 4))
+                  emit(std::integral_constant<int, 4>{},
+                       place(tile * kRows + (int)(at[i] / (DH / 4))),
+                       (int)(at[i] % (DH / 4)) * 4, acc[i], top[i], sum[i]);
             }
-            emit(col, acc, top, sum);
-          }
+          };
+          if (n_piece <= 2)
+            join(std::integral_constant<int, 2>{});
+          else
+            join(std::integral_constant<int, 8>{});
         }
       }
       ptx::tc_fence_before();
