@@ -61,18 +61,27 @@ Space space_of(const lbx_attn_cfg *c) {
   const size_t part = up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
   const long long G = c->Hq / c->Hkv, rows = (long long)c->N * G;
   const size_t lists = (size_t)c->L * c->Hkv;
-  s.own = tiling(rows);
-  s.pre = tiling(rows * c->Bq);
+  s.own = tiling(rows, c->dh);
+  s.pre = tiling(rows * c->Bq, c->dh);
   s.count = part;
-  s.pre_count = s.count + up256(lists * c->Bq * s.own.tiles * 4);
+  s.pre_count = s.count + up256(lists * c->Bq * s.own.tiles * s.own.ctas * 4);
   s.x_o = s.pre_count, s.x_lse = s.x_o, s.bytes = s.x_lse;
   if (c->P > 0) {
     const size_t queries = (size_t)c->L * c->Bq * c->N * c->Hq;
-    s.x_o += up256(lists * s.pre.tiles * 4);
+    s.x_o += up256(lists * s.pre.tiles * s.pre.ctas * 4);
     s.x_lse = s.x_o + up256(queries * c->dh * 4);
     s.bytes = s.x_lse + up256(queries * 4);
   }
   return s;
+}
+
+// The block list's indexes are 32-bit.
+bool list_ok(const lbx_attn_cfg *c, const Space &s) {
+  auto fits = [&](const Tiling &t, long long lists, long long len) {
+    return lists * t.sets < (1LL << 31) / (len / kUnit + 3);
+  };
+  const long long lists = (long long)c->L * c->Hkv;
+  return fits(s.own, lists * c->Bq, c->T) && fits(s.pre, lists, c->P);
 }
 
 int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *parent,
@@ -86,10 +95,15 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if (c->P > 0 && (!aligned_to(kp, 16) || !aligned_to(vp, 16))) return LBX_EINVAL;
   if ((lse && !aligned_to(lse, 4)) || (status && !aligned_to(status, 4))) return LBX_EINVAL;
   const Space s = space_of(c);
-  if (ws_bytes < s.bytes) return LBX_EINVAL;
+  if (!list_ok(c, s) || ws_bytes < s.bytes) return LBX_EINVAL;
   if (!have_encode()) return LBX_ECUDA;
-  const int v_keys = c->dh == 256 ? Lay<256>::kVBox : kUnit;
-  static_assert(Lay<128>::kVBox == kUnit && Lay<64>::kVBox == kUnit, "V boxes");
+  // rows of a box of V: a piece of it may hold fewer keys than a unit
+  static_assert(Lay<128, false>::kVBox == kUnit && Lay<64, false>::kVBox == kUnit &&
+                    Lay<128, true>::kVBox == kUnit && Lay<256, true>::kVBox == kUnit,
+                "V boxes");
+  auto v_box = [&](const Tiling &t) {
+    return c->dh == 256 && t.ctas == 1 ? Lay<256, false>::kVBox : kUnit;
+  };
 
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -106,8 +120,8 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   A.part = reinterpret_cast<float *>(base);
   const bool f16 = c->dtype == LBX_F16;
   auto launch = [&](const AttnMaps &maps) {
-    int grid = nsm / A.til.group * A.til.group;
-    if (grid < A.til.group) grid = A.til.group;
+    const int by = A.til.group * A.til.ctas;  // at most 16: fewer than SMs
+    const int grid = nsm / by * by;
     const cudaError_t e = c->dh == 64    ? launch_attn<64>(f16, maps, A, grid, stream)
                           : c->dh == 128 ? launch_attn<128>(f16, maps, A, grid, stream)
                                          : launch_attn<256>(f16, maps, A, grid, stream);
@@ -116,7 +130,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   AttnMaps maps;
   std::memset(&maps, 0, sizeof maps);
   if (c->P > 0) {
-    if (!encode(&maps.k, kp, c, c->P, c->L, kUnit) || !encode(&maps.v, vp, c, c->P, c->L, v_keys))
+    if (!encode(&maps.k, kp, c, c->P, c->L, kUnit) || !encode(&maps.v, vp, c, c->P, c->L, v_box(s.pre)))
       return LBX_ECUDA;
     maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
     A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
@@ -127,11 +141,11 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr, A.fixed = 0;
   }
   const int lists = c->L * c->Bq;
-  if (!encode(&maps.kt, kt, c, c->N, lists, kUnit) || !encode(&maps.vt, vt, c, c->N, lists, v_keys))
+  if (!encode(&maps.kt, kt, c, c->N, lists, kUnit) || !encode(&maps.vt, vt, c, c->N, lists, v_box(s.own)))
     return LBX_ECUDA;
   maps.k = maps.kt, maps.v = maps.vt;  // without a cache: never read
   if (c->T > 0 &&
-      (!encode(&maps.k, kc, c, c->T, lists, kUnit) || !encode(&maps.v, vc, c, c->T, lists, v_keys)))
+      (!encode(&maps.k, kc, c, c->T, lists, kUnit) || !encode(&maps.v, vc, c, c->T, lists, v_box(s.own))))
     return LBX_ECUDA;
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
   A.window = c->window, A.n_sink = c->n_sink;
@@ -146,7 +160,9 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
 
 extern "C" size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *c) {
   using namespace lbx::cache;
-  return cfg_ok(c) ? space_of(c).bytes : 0;
+  if (!cfg_ok(c)) return 0;
+  const Space s = space_of(c);
+  return list_ok(c, s) ? s.bytes : 0;
 }
 
 extern "C" int lbx_window_attention(const lbx_attn_cfg *c, const int32_t *ctx_len,

@@ -21,21 +21,29 @@
 //
 // The key list is cut into units of 64 keys from one array: the visible first
 // positions before the window, the window, the tree's own keys.  A block is
-// two units, one for each of the two threads of a row; the last block may
-// have one.  All blocks of all streams form one list (request, layer, KV
-// head, block), cut into equal ranges, one per CTA (or per group of CTAs, one
-// for each row tile of the stream, which then read the same keys at the same
-// time): one CTA per SM, whatever the lengths.  A range's streams that it does
-// not cover whole leave partials (m, l, O) in the workspace, at most two per
-// CTA, and the last CTA of a row tile to finish joins them.
+// two units, one for each of the two threads of a row (one unit, half for
+// each, at head dimension 256 in one CTA, where O leaves room for two score
+// buffers of 64 columns).  All blocks of all streams form one list (request,
+// layer, KV head, block), cut into equal ranges, one per CTA or pair (or per
+// group of them, one for each row tile of the stream, which then read the same
+// keys at the same time): one CTA per SM, whatever the lengths.  Streams that
+// a range does not cover whole leave partials (m, l, O) in the workspace, at
+// most two per CTA, and the last CTA of a row tile to finish joins them.
+//
+// Streams of more than 128 rows (head dimensions 128 and 256) run on pairs of
+// CTAs that share one product of 256 rows: each CTA keeps half of the block's
+// keys and half of the columns of V, so a block takes half the shared memory
+// and half the reads of L2.  Each CTA's copies arrive on its own barriers; the
+// follower passes the news on to the leader, whose one thread issues all MMAs.
 //
 // Per CTA: warps 0-7 softmax, warp 8 issues the MMAs, warp 9 the copies.  K
-// and V arrive by TMA in 16 KB pieces (K: 128 keys x 64 columns; V: whole
-// rows) through one ring, in the order the MMAs take them, so that all of the
-// shared memory next to the Q tile keeps copies in flight.  S of a block and
-// its P share one of two 128-column buffers.  Every wait is bounded; a CTA
-// whose wait gives up reports LBX_ETIMEOUT, still counts itself in with empty
-// partials, drains its copies and frees its tensor memory.
+// and V arrive by TMA in 16 KB pieces through one ring, in the order the MMAs
+// take them, so that all of the shared memory keeps copies in flight.  The Q
+// tile sits in tensor memory (in shared memory for a pair, whose 128-key
+// blocks need the columns).  S of a block and its P share one of two buffers.
+// Every wait is bounded; a CTA whose wait gives up reports LBX_ETIMEOUT, still
+// counts itself in with empty partials, drains its copies and frees its tensor
+// memory.
 #pragma once
 
 #include <cuda.h>
@@ -48,7 +56,7 @@
 namespace lbx {
 namespace cache {
 
-constexpr int kRows = 128;         // query rows per tile
+constexpr int kRows = 128;         // query rows per CTA
 constexpr int kUnit = 64;          // keys per unit
 constexpr int kPiece = 16 * 1024;  // bytes per ring stage
 constexpr int kMaxCtas = 160;      // largest grid (partials in the workspace)
@@ -56,14 +64,16 @@ constexpr int kMaxGroup = 8;       // most row tiles that run side by side
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = kSoftmaxThreads + 64;
 
-// Row tiles of a stream: `sets` sets of up to `group` tiles each.
+// Row tiles of a stream, of 128 rows (256 for pairs of CTAs): `sets` sets of up
+// to `group` tiles each.
 struct Tiling {
-  int rows, tiles, sets, group;
+  int rows, tiles, sets, group, ctas;  // ctas: per tile
 };
-inline Tiling tiling(long long rows) {
+inline Tiling tiling(long long rows, int dh) {
   Tiling t;
   t.rows = (int)rows;
-  t.tiles = (int)((rows + kRows - 1) / kRows);
+  t.ctas = rows > kRows && dh >= 128 ? 2 : 1;
+  t.tiles = (int)((rows + t.ctas * kRows - 1) / (t.ctas * kRows));
   t.sets = (t.tiles + kMaxGroup - 1) / kMaxGroup;
   t.group = (t.tiles + t.sets - 1) / t.sets;
   return t;
@@ -93,45 +103,75 @@ struct AttnArgs {
   float *lse;                  // natural lse or NULL
   const float *x_o, *x_lse2;   // a prefix's results to join, or NULL
   float *part;
-  unsigned int *counters;      // one per (stream, tile)
+  unsigned int *counters;      // one per (stream, tile, CTA of the pair)
   int32_t *status;
 };
 
-template <int DH>
+template <int DH, bool PAIR>
 struct Lay {
-  static constexpr int kAtoms = DH / 64;
-  static constexpr int kQBytes = kRows * DH * 2;
-  static constexpr int kStages = (227 * 1024 - 3072 - kQBytes) / kPiece;
-  static constexpr int kVKeys = kPiece / (DH * 2);             // keys per V piece
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr bool kQTmem = !PAIR;
+  static constexpr int kBlkUnits = DH == 256 && !PAIR ? 1 : 2;  // units per block
+  static constexpr int kBlk = kBlkUnits * kUnit;                 // keys per block
+  static constexpr int kMine = kBlk / 2;                         // keys per softmax thread
+  // what one CTA holds of a block: kKeys keys of K, kCols columns of V
+  static constexpr int kKeys = kBlk / kCtas, kCols = DH / kCtas;
+  static constexpr int kPieces = kKeys * DH * 2 / kPiece < 1 ? 1 : kKeys * DH * 2 / kPiece;
+  static constexpr int kKAtom = kKeys * 128;           // 64 columns of the K block
+  static constexpr int kKAtoms = kPiece / kKAtom;      // such atoms per K piece
+  static constexpr int kVKeys = kPiece / (kCols * 2);  // keys per V piece
   static constexpr int kVBox = kVKeys < kUnit ? kVKeys : kUnit;  // rows of a V box
-  static constexpr int kVAtom = kVKeys * 128;                  // one 64-column atom of a V piece
+  static constexpr int kVAtom = kVKeys * 128;          // 64 columns of a V piece
+  static_assert(kPieces * kVKeys == kBlk && kPieces * kKAtoms * 64 == DH, "pieces");
+
+  static constexpr int kQBytes = kQTmem ? 0 : kRows * DH * 2;
+  static constexpr int kStages = (227 * 1024 - 3072 - kQBytes) / kPiece;
+  static_assert(kStages > 2 * kPieces, "the next scores do not wait for this block's V");
   static constexpr int kSmemQ = 0;
   static constexpr int kSmemRing = kSmemQ + kQBytes;
   static constexpr int kSmemRed = kSmemRing + kStages * kPiece;  // float [2][2][128]
   static constexpr int kSmemAnc = kSmemRed + 4 * kRows * 4;      // uint64 [64]
   static constexpr int kSmemMisc = kSmemAnc + kMaxNodes * 8;     // int [8]
   static constexpr int kSmemBars = kSmemMisc + 32;
-  static constexpr int kNBars = 2 * kStages + 8;  // full, empty, s[2], p[2], o[2], q, end
+  static constexpr int kNBars = 3 * kStages + 8;  // full, empty, peer, s[2], p[2], o[2], q, end
   static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
   static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0, "shared memory");
-  static constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
+
+  // tensor memory: Q (16-bit pairs), two buffers of S / P, O
+  static constexpr uint32_t kColQ = 0, kColS = kQTmem ? 128 : 0;
+  static constexpr uint32_t kColO = kColS + 2 * kBlk, kTmemCols = 512;
+  static_assert(kColO + DH <= kTmemCols && (!kQTmem || DH / 2 <= 128), "tensor memory");
+};
+
+// A position in a ring of N stages and the parity of its round.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) st = 0, ph ^= 1u;
+  }
 };
 
 // What joining the pieces of a cut stream costs, in blocks.
 constexpr int kJoinBlocks = 3;
 
-// Walks a CTA's range of the block list.  Used by whole warps, each lane alike.
+// Walks a CTA's range of the block list (blocks of BU units).  Used by whole
+// warps, each lane alike; the CTAs of a pair walk alike.
 // Where whole streams per group come out within kJoinBlocks of equal ranges of
 // blocks, a stream counts as one entry of the list and is not cut.
+template <int BU>
 struct Walk {
   const AttnArgs &A;
-  long long total, groups, cg, x, x_end, per_b_base;  // per_b_base: first entry of request b
-  bool uncut;
+  // the list's entries and how they are cut: `more` ranges of each + 1 entries,
+  // then ranges of `each`; per_b_base: first entry of request b
+  int total, groups, each, more, cg, x, x_end, per_b_base;
   int slot_in_group, b, nblk, ctx;
+  bool uncut;
   // the current segment
   int l, h, set, tile, blk0, blk1;
-  long long first;  // the stream's first entry
-  bool live;        // this CTA has a tile of the stream
+  int first;  // the stream's first entry
+  bool live;  // this CTA has a tile of the stream
 
   // units of a request's key list
   int w0, s_eff, ns, nw, units;
@@ -143,50 +183,45 @@ struct Walk {
     ns = (s_eff + kUnit - 1) / kUnit;
     nw = (len - w0 + kUnit - 1) / kUnit;
     units = ns + nw + (A.fixed > 0 ? 0 : 1);
-    nblk = (units + 1) / 2;
+    nblk = (units + BU - 1) / BU;
   }
   __device__ __forceinline__ int blocks_of(int req) {
     plan(A.fixed > 0 ? A.fixed : A.ctx_len[req]);
     return nblk;
   }
-  __device__ __forceinline__ long long streams() const {
-    return (long long)A.L * A.Hkv * A.til.sets;
-  }
-
-  // Entries of the current request's streams in the list, each.
+  // Streams per request; entries of each of the current request's in the list.
+  __device__ __forceinline__ int streams() const { return A.L * A.Hkv * A.til.sets; }
   __device__ __forceinline__ int entries() const { return uncut ? 1 : nblk; }
 
   __device__ __forceinline__ Walk(const AttnArgs &a, int lane) : A(a), uncut(false) {
-    long long sum = 0;
-    int most = 0;
+    int sum = 0, most = 0;
     for (int r = lane; r < A.n_req; r += 32) {
       sum += blocks_of(r);
       most = nblk > most ? nblk : most;
     }
-    for (int w = 16; w; w >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      const int y = __shfl_xor_sync(0xffffffffu, most, w);
-      most = y > most ? y : most;
-    }
+    sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
     total = sum * streams();
-    groups = (long long)gridDim.x / A.til.group;
-    const long long all = streams() * A.n_req;
+    groups = (int)(gridDim.x / (unsigned)(A.til.group * A.til.ctas));
+    const long long all = (long long)streams() * A.n_req;
     uncut = (all + groups - 1) / groups * most <= (total + groups - 1) / groups + kJoinBlocks;
-    if (uncut) total = all;
+    if (uncut) total = (int)all;
     if (groups > total) groups = total;
-    cg = blockIdx.x / A.til.group;
-    slot_in_group = (int)(blockIdx.x - cg * A.til.group);
-    x = cg < groups ? total * cg / groups : total;
-    x_end = cg < groups ? total * (cg + 1) / groups : total;
-    // the request of block x: 32 requests at a time
+    each = total / groups, more = total - each * groups;
+    const int at = (int)blockIdx.x / A.til.ctas;
+    cg = at / A.til.group;
+    slot_in_group = at - cg * A.til.group;
+    x = cg < groups ? begin_of(cg) : total;
+    x_end = cg < groups ? begin_of(cg + 1) : total;
+    // the request of entry x: 32 requests at a time
     b = 0, per_b_base = 0;
     if (x < x_end) {
       for (int r0 = 0;; r0 += 32) {
-        long long mine = 0;
+        int mine = 0;
         if (r0 + lane < A.n_req) blocks_of(r0 + lane), mine = entries() * streams();
-        long long upto = mine;
+        int upto = mine;
         for (int w = 1; w < 32; w <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, upto, w);
+          const int y = __shfl_up_sync(0xffffffffu, upto, w);
           if (lane >= w) upto += y;
         }
         const unsigned past = __ballot_sync(0xffffffffu, per_b_base + upto > x);
@@ -209,27 +244,32 @@ struct Walk {
       per_b_base += entries() * streams();
       blocks_of(++b);
     }
-    const long long in_b = x - per_b_base, s = in_b / entries();
-    blk0 = (int)(in_b - s * entries());
+    const int in_b = x - per_b_base, s = in_b / entries();
+    blk0 = in_b - s * entries();
     first = x - blk0;
-    set = (int)(s % A.til.sets);
-    const int lh = (int)(s / A.til.sets);
+    const int lh = A.til.sets > 1 ? s / A.til.sets : s;
+    set = s - lh * A.til.sets;
     l = lh / A.Hkv, h = lh - l * A.Hkv;
-    blk1 = uncut || x_end - first >= nblk ? nblk : (int)(x_end - first);
+    blk1 = uncut || x_end - first >= nblk ? nblk : x_end - first;
     x = uncut ? x + 1 : first + blk1;
     tile = set * A.til.group + slot_in_group;
     live = tile < A.til.tiles;
     return true;
   }
-  __device__ __forceinline__ long long begin_of(long long g) const { return total * g / groups; }
-  __device__ __forceinline__ long long owner(long long at) const {
-    return ((at + 1) * groups - 1) / total;
+  __device__ __forceinline__ int begin_of(int g) const { return g * each + (g < more ? g : more); }
+  __device__ __forceinline__ int owner(int at) const {
+    const int big = more * (each + 1);
+    return at < big ? at / (each + 1) : more + (at - big) / each;
   }
-  __device__ __forceinline__ int units_in(int blk) const { return 2 * blk + 1 < units ? 2 : 1; }
   // Unit u: the position (or tree node) of its first key, whether it is the
-  // tree's, and how many of its keys any query sees.
+  // tree's, and how many of its keys any query sees.  A unit past the last is
+  // empty: a copy of it lies outside its array and fills in zeros.
   __device__ __forceinline__ void unit(int u, int &start, bool &tree, int &cnt) const {
-    tree = u >= ns + nw;
+    tree = u >= ns + nw && A.fixed <= 0;
+    if (u >= units) {
+      start = tree ? A.N : ctx, cnt = 0;
+      return;
+    }
     start = u < ns ? u * kUnit : tree ? 0 : w0 + (u - ns) * kUnit;
     const int end = u < ns ? s_eff : tree ? A.N : ctx;
     cnt = end - start < kUnit ? end - start : kUnit;
@@ -256,10 +296,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-template <int DH, bool F16>
+template <int DH, bool F16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs A) {
-  using Y = Lay<DH>;
+  using Y = Lay<DH, PAIR>;
   extern __shared__ __align__(1024) unsigned char cache_smem[];
   unsigned char *smem = cache_smem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -268,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // [0] tensor memory base, [1] last of its row tile, [2] a wait gave up
   volatile int *misc = reinterpret_cast<volatile int *>(smem + Y::kSmemMisc);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + Y::kSmemBars);
-  uint64_t *empty = full + Y::kStages, *s_bar = empty + Y::kStages, *p_bar = s_bar + 2;
+  uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
+  uint64_t *s_bar = peer + Y::kStages, *p_bar = s_bar + 2;
   uint64_t *o_bar = p_bar + 2, *q_bar = o_bar + 2, *end_bar = q_bar + 1;
 
   if (batch_bad(A.Bq, A.N, A.T, A.ctx_len, A.parent, nullptr)) {
@@ -278,77 +319,91 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < Y::kNBars; ++i)
       ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1 || full + i == q_bar
-                                   ? kSoftmaxThreads / 32
+                                   ? Y::kCtas * kSoftmaxThreads / 32
                                    : 1);
     ptx::fence_mbar_init();
     misc[2] = 0;
   }
   if (warp == 8) {
-    ptx::tmem_alloc(reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc), Y::kTmemCols);
-    ptx::tmem_relinquish();
+    uint32_t *base = reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc);
+    if constexpr (PAIR) {
+      ptx::tmem_alloc_pair(base, Y::kTmemCols);
+    } else {
+      ptx::tmem_alloc(base, Y::kTmemCols);
+      ptx::tmem_relinquish();
+    }
     ptx::tc_fence_before();
   }
   __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // the other CTA's barriers are set up
   ptx::tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
-  Walk W(A, lane);
+  const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
+  Walk<Y::kBlkUnits> W(A, lane);
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
     return !bad;
   };
-  // V pieces of a block with nu units
-  auto v_pieces = [](int nu) { return (nu * kUnit + Y::kVKeys - 1) / Y::kVKeys; };
+  // for barriers that both CTAs of a pair arrive on
+  auto wait_both = [&](uint64_t *bar, uint32_t parity) {
+    if (!bad && !(PAIR ? ptx::mbar_wait_cluster(bar, parity) : ptx::mbar_wait(bar, parity)))
+      bad = true;
+    return !bad;
+  };
 
   if (warp == 9) {
     // ---- copies ----
-    long long piece = 0;  // ring position
+    Ring<Y::kStages> ring;
+    int loads = 0;
     while (W.next()) {
-      if (!W.live) continue;
+      if (!W.live || lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
       const int z = A.fixed > 0 ? W.l : W.l * A.n_req + W.b;
-      auto take = [&](uint32_t bytes) -> unsigned char * {
-        const int st = (int)(piece % Y::kStages);
-        if (piece >= Y::kStages &&
-            !wait(&empty[st], (uint32_t)((piece / Y::kStages - 1) & 1)))
-          return nullptr;
-        ptx::mbar_arrive_expect_tx(&full[st], bytes);
-        return smem + Y::kSmemRing + st * kPiece;
+      auto take = [&]() -> unsigned char * {
+        // the first round finds every stage free
+        if (!wait(&empty[ring.st], ring.ph ^ 1u)) return nullptr;
+        ptx::mbar_arrive_expect_tx(&full[ring.st], (uint32_t)kPiece);
+        ++loads;
+        return smem + Y::kSmemRing + ring.st * kPiece;
       };
-      for (int i = 0; i <= nb && !bad && lane == 0; ++i) {
+      for (int i = 0; i <= nb && !bad; ++i) {
         if (i < nb) {  // K of block i
-          const int blk = W.blk0 + i, nu = W.units_in(blk);
-          for (int a = 0; a < Y::kAtoms && !bad; ++a) {
-            unsigned char *d = take((uint32_t)(nu * kUnit * 128));
+          const int u0 = (W.blk0 + i) * Y::kBlkUnits + rank;
+          for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+            unsigned char *d = take();
             if (!d) break;
-            for (int u = 0; u < nu; ++u) {
+#pragma unroll
+            for (int u = 0; u < Y::kKeys / kUnit; ++u) {
               int start, cnt;
               bool tree;
-              W.unit(2 * blk + u, start, tree, cnt);
-              ptx::tma_load_4d(d + u * kUnit * 128, tree ? &maps.kt : &maps.k, a * 64, W.h, start, z,
-                               &full[piece % Y::kStages]);
+              W.unit(u0 + u, start, tree, cnt);
+#pragma unroll
+              for (int a = 0; a < Y::kKAtoms; ++a)
+                ptx::tma_load_4d(d + a * Y::kKAtom + u * kUnit * 128, tree ? &maps.kt : &maps.k,
+                                 (p * Y::kKAtoms + a) * 64, W.h, start, z,
+                                 &full[ring.st]);
             }
-            ++piece;
           }
         }
         if (i > 0 && !bad) {  // V of block i - 1
-          const int blk = W.blk0 + i - 1, nu = W.units_in(blk);
-          for (int c = 0; c < v_pieces(nu) && !bad; ++c) {
-            const int keys = nu * kUnit - c * Y::kVKeys < Y::kVKeys ? nu * kUnit - c * Y::kVKeys
-                                                                    : Y::kVKeys;
-            unsigned char *d = take((uint32_t)(keys * DH * 2));
+          const int u0 = (W.blk0 + i - 1) * Y::kBlkUnits;
+          for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+            unsigned char *d = take();
             if (!d) break;
-            for (int k0 = 0; k0 < keys; k0 += Y::kVBox) {
-              const int kk = c * Y::kVKeys + k0;
+#pragma unroll
+            for (int k0 = 0; k0 < Y::kVKeys; k0 += Y::kVBox) {
+              const int kk = p * Y::kVKeys + k0;
               int start, cnt;
               bool tree;
-              W.unit(2 * blk + kk / kUnit, start, tree, cnt);
-              for (int a = 0; a < Y::kAtoms; ++a)
-                ptx::tma_load_4d(d + a * Y::kVAtom + k0 * 128, tree ? &maps.vt : &maps.v, a * 64,
-                                 W.h, start + kk % kUnit, z, &full[piece % Y::kStages]);
+              W.unit(u0 + kk / kUnit, start, tree, cnt);
+#pragma unroll
+              for (int a = 0; a < Y::kCols / 64; ++a)
+                ptx::tma_load_4d(d + a * Y::kVAtom + k0 * 128, tree ? &maps.vt : &maps.v,
+                                 rank * Y::kCols + a * 64, W.h, start + kk % kUnit, z,
+                                 &full[ring.st]);
             }
-            ++piece;
           }
         }
       }
@@ -357,79 +412,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) misc[2] = 1;
       // every copy has landed before the CTA may leave (long since, unless a
       // wait gave up)
-      bad = false;
-      for (long long i = piece > Y::kStages ? piece - Y::kStages : 0; i < piece; ++i)
+      for (int i = loads > Y::kStages ? loads - Y::kStages : 0; i < loads; ++i)
         (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
     }
+  } else if (warp == 8 && rank == 1) {
+    // ---- the follower tells the leader of each piece that has landed ----
+    Ring<Y::kStages> ring;
+    while (W.next()) {
+      if (!W.live || lane != 0) continue;
+      for (int n = 2 * Y::kPieces * (W.blk1 - W.blk0); n > 0; --n, ring.step()) {
+        if (!wait(&full[ring.st], ring.ph)) break;
+        ptx::mbar_arrive_at(&peer[ring.st], 0);
+      }
+    }
+    if (bad) misc[2] = 1;
   } else if (warp == 8) {
-    // ---- MMAs ----
-    long long piece = 0, q = 0;
-    int seg = 0;
+    // ---- MMAs: the warp walks and waits as one, one lane issues ----
+    Ring<Y::kStages> ring;
+    uint32_t q = 0, seg = 0;
+    const bool one = ptx::elect_one();
     const uint64_t qdesc = ptx::sdesc_sw128(ptx::smem_u32(smem + Y::kSmemQ));
     const uint64_t kdesc = ptx::sdesc_sw128(ptx::smem_u32(smem + Y::kSmemRing));
     const uint64_t vdesc =
         ptx::sdesc(ptx::smem_u32(smem + Y::kSmemRing), (uint32_t)Y::kVAtom, 1024u, 2u);
-    bool issued = false;
+    auto commit = [&](uint64_t *bar) {
+      if constexpr (PAIR) ptx::mma_commit_pair(bar);
+      else ptx::mma_commit(bar);
+    };
+    // the waits of the whole warp: given up by one lane, given up by all
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, bool both) {
+      const bool ok = both ? wait_both(bar, parity) : wait(bar, parity);
+      bad = !__all_sync(0xffffffffu, ok);
+      return !bad;
+    };
+    // the ring's next piece, here and at the follower
+    auto arrived = [&]() {
+      return wait_all(&full[ring.st], ring.ph, false) &&
+             (!PAIR || wait_all(&peer[ring.st], ring.ph, true));
+    };
     while (W.next()) {
       if (!W.live) continue;
       const int nb = W.blk1 - W.blk0;
       // S of block i into buffer (q + i) & 1
       auto scores = [&](int i) {
-        const long long qi = q + i;
-        const int nu = W.units_in(W.blk0 + i);
-        // the buffer's last P has been multiplied
-        if (qi >= 2 && !wait(&o_bar[qi & 1], (uint32_t)(((qi - 2) >> 1) & 1))) return;
-        const uint32_t idesc = ptx::idesc_16(F16, kRows, nu * kUnit, false);
-        const uint32_t d = tmem + Y::kColS + (uint32_t)(qi & 1) * 128;
-        for (int a = 0; a < Y::kAtoms; ++a, ++piece) {
-          const int st = (int)(piece % Y::kStages);
-          if (!wait(&full[st], (uint32_t)((piece / Y::kStages) & 1))) return;
-          ptx::tc_fence_after();
-          const uint64_t kd = kdesc + (uint64_t)(st * kPiece >> 4);
-          const uint64_t qd = qdesc + (uint64_t)(a * kRows * 128 >> 4);
+        const uint32_t qi = q + i, buf = qi & 1;
+        // the buffer's last P has been multiplied (the first two find it free)
+        if (!wait_all(&o_bar[buf], ((qi >> 1) & 1) ^ 1u, false)) return;
+        constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, Y::kBlk, false);
+        const uint32_t d = tmem + Y::kColS + buf * Y::kBlk;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            ptx::mma_bf16_ss(d, qd + 2 * ks, kd + 2 * ks, idesc, a + ks > 0 ? 1u : 0u);
-          ptx::mma_commit(&empty[st]);
-        }
-        ptx::mma_commit(&s_bar[qi & 1]);
-      };
-      if (lane == 0) {
-        issued = true;
-        if (wait(q_bar, (uint32_t)(seg & 1))) scores(0);
-        for (int i = 0; i < nb && !bad; ++i) {
-          if (i + 1 < nb) scores(i + 1);
-          const long long qi = q + i;
-          if (!wait(&p_bar[qi & 1], (uint32_t)((qi >> 1) & 1))) break;
+        for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+          if (!arrived()) return;
           ptx::tc_fence_after();
-          const int nu = W.units_in(W.blk0 + i);
-          constexpr uint32_t idesc = ptx::idesc_16(F16, kRows, DH, true);
-          const uint32_t pc = tmem + Y::kColS + (uint32_t)(qi & 1) * 128;
-          for (int c = 0; c < v_pieces(nu); ++c, ++piece) {
-            const int st = (int)(piece % Y::kStages);
-            if (!wait(&full[st], (uint32_t)((piece / Y::kStages) & 1))) break;
-            ptx::tc_fence_after();
-            const int keys = nu * kUnit - c * Y::kVKeys < Y::kVKeys ? nu * kUnit - c * Y::kVKeys
-                                                                    : Y::kVKeys;
-            const uint64_t vd = vdesc + (uint64_t)(st * kPiece >> 4);
-            for (int part = 0; part < kParts<F16>; ++part)
-              for (int ks = 0; ks < keys / 16; ++ks)
-                ptx::mma_bf16_ts(tmem + Y::kColO,
-                                 pc + (uint32_t)(part * 64 + c * Y::kVKeys / 2 + ks * 8),
-                                 vd + (uint64_t)(ks * 2048 >> 4), idesc,
-                                 i + c + part + ks > 0 ? 1u : 0u);
-            ptx::mma_commit(&empty[st]);
+          const uint64_t kd = kdesc + (uint64_t)(ring.st * (kPiece >> 4));
+          if (one) {
+#pragma unroll
+            for (int s = 0; s < 4 * Y::kKAtoms; ++s) {
+              const int step = p * 4 * Y::kKAtoms + s;  // 16 columns of Q and K
+              const uint64_t kb = kd + (uint64_t)((s >> 2) * Y::kKAtom >> 4) + 2 * (s & 3);
+              const uint64_t qa =
+                  qdesc + (uint64_t)((step >> 2) * kRows * 128 >> 4) + 2 * (step & 3);
+              const uint32_t acc = step > 0 ? 1u : 0u;
+              if constexpr (PAIR) ptx::mma_16_ss_pair(d, qa, kb, idesc, acc);
+              else ptx::mma_bf16_ts(d, tmem + Y::kColQ + 8u * step, kb, idesc, acc);
+            }
+            commit(&empty[ring.st]);
+            if (p == Y::kPieces - 1) commit(&s_bar[buf]);
           }
-          ptx::mma_commit(&o_bar[qi & 1]);
+          __syncwarp();
+        }
+      };
+      if (wait_all(q_bar, seg & 1, true)) {
+        ptx::tc_fence_after();
+        scores(0);
+      }
+      for (int i = 0; i < nb && !bad; ++i) {
+        if (i + 1 < nb) scores(i + 1);
+        const uint32_t qi = q + i, buf = qi & 1;
+        if (!wait_all(&p_bar[buf], (qi >> 1) & 1, true)) break;
+        ptx::tc_fence_after();
+        constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, DH, true);
+        const uint32_t pc = tmem + Y::kColS + buf * Y::kBlk;
+        const uint32_t later = i > 0 ? 1u : 0u;
+#pragma unroll
+        for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+          if (!arrived()) break;
+          ptx::tc_fence_after();
+          const uint64_t vd = vdesc + (uint64_t)(ring.st * (kPiece >> 4));
+          if (one) {
+#pragma unroll
+            for (int part = 0; part < kParts<F16>; ++part)
+#pragma unroll
+              for (int s = 0; s < Y::kVKeys / 16; ++s) {
+                const uint32_t pa =
+                    pc + (uint32_t)(part * Y::kBlk / 2 + p * Y::kVKeys / 2 + s * 8);
+                const uint64_t vb = vd + (uint64_t)(s * 2048 >> 4);
+                const uint32_t acc = p + part + s > 0 ? 1u : later;
+                if constexpr (PAIR) ptx::mma_16_ts_pair(tmem + Y::kColO, pa, vb, idesc, acc);
+                else ptx::mma_bf16_ts(tmem + Y::kColO, pa, vb, idesc, acc);
+              }
+            commit(&empty[ring.st]);
+            if (p == Y::kPieces - 1) commit(&o_bar[buf]);
+          }
+          __syncwarp();
         }
       }
       q += nb;
       ++seg;
-      if (__shfl_sync(0xffffffffu, (int)bad, 0)) break;
+      if (bad) break;
     }
-    if (lane == 0 && issued) {
+    if (one) {
       if (bad) misc[2] = 1;
-      ptx::mma_commit(end_bar);
+      commit(end_bar);
       (void)ptx::mbar_wait(end_bar, 0);
     }
   } else {
@@ -439,28 +533,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quad * 32 + lane;  // row of the tile
     const float sl2 = A.scale_log2;
     constexpr int kHalf = DH / 2;
-    long long q = 0, piece = 0;
+    uint32_t q = 0, piece = 0;  // blocks and ring pieces so far
     int req = -1;
 
-    // The Q tile of the walk's segment, rows past the stream's zero: a warp
-    // per row, 16 bytes per lane, in the swizzled layout of the MMA's operand.
+    // One arrival of this warp on a barrier of the CTA that issues the MMAs.
+    auto tell = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) ptx::mbar_arrive_at(bar, 0);
+        else ptx::mbar_arrive(bar);
+      }
+    };
+    // Query rows of the walk's tile from this CTA's first on.
+    auto first_row = [&]() { return (W.tile * Y::kCtas + rank) * kRows; };
+    // The walk's place of a row of the stream among all queries.
+    auto query_of = [&](int row) {
+      const int node = row / A.G;
+      return (((size_t)W.l * A.n_req + W.b) * A.nodes + node) * A.Hq + W.h * A.G +
+             (row - node * A.G);
+    };
+    // The Q tile of the walk's segment, rows past the stream's zero.
     auto load_q = [&]() {
       constexpr int kPer = DH / 8;  // 16-byte pieces per row
-      constexpr int kStep = kSoftmaxThreads / kPer;
-      for (int rr = tid / kPer; rr < kRows; rr += kStep) {
-        const int row = W.tile * kRows + rr, c = tid % kPer;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row < A.til.rows) {
-          const int node = row / A.G, hd = row - node * A.G;
-          const size_t at = ((size_t)W.l * A.n_req + W.b) * A.nodes + node;
-          v = reinterpret_cast<const uint4 *>(A.q)[(at * A.Hq + W.h * A.G + hd) * kPer + c];
+      const uint4 *qg = reinterpret_cast<const uint4 *>(A.q);
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (Y::kQTmem) {  // half a row per thread, pairs along dh
+        const int row = first_row() + r;
+        const bool in = row < A.til.rows;
+        const uint4 *from = qg + (in ? query_of(row) * kPer + hf * (kPer / 2) : 0);
+        constexpr int kC = DH / 4 < 32 ? DH / 4 : 32;  // columns per store
+#pragma unroll
+        for (int c = 0; c < DH / 4; c += kC) {
+          uint32_t w[kC];
+#pragma unroll
+          for (int e = 0; e < kC / 4; ++e) {
+            const uint4 v = in ? from[c / 4 + e] : none;
+            w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+          }
+          if constexpr (kC == 32) ptx::tmem_st32(tq + Y::kColQ + hf * (DH / 4) + c, w);
+          else ptx::tmem_st16(tq + Y::kColQ + hf * (DH / 4) + c, w);
         }
-        *reinterpret_cast<uint4 *>(smem + Y::kSmemQ + (c / 8) * kRows * 128 + rr * 128 +
-                                   ((c & 7) ^ (rr & 7)) * 16) = v;
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      } else {  // swizzled in shared memory, 16 bytes per lane
+        constexpr int kStep = kSoftmaxThreads / kPer, kLoads = kRows / kStep;
+        const int c = tid % kPer, r0 = tid / kPer;
+        uint4 v[kLoads];
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int row = first_row() + r0 + e * kStep;
+          v[e] = row < A.til.rows ? qg[query_of(row) * kPer + c] : none;
+        }
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int rr = r0 + e * kStep;
+          *reinterpret_cast<uint4 *>(smem + Y::kSmemQ + (c / 8) * kRows * 128 + rr * 128 +
+                                     ((c & 7) ^ (rr & 7)) * 16) = v[e];
+        }
+        ptx::fence_proxy_async();
       }
-      ptx::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(q_bar);
+      tell(q_bar);
     };
     // The next segment with a tile for this CTA.
     auto advance = [&]() {
@@ -474,9 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (have) {
       const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
       const int nb = blk1 - blk0, ctx = W.ctx;
-      const long long first = W.first;
-      const int row = tile * kRows + r;
+      const int first = W.first;
+      const int row0 = first_row(), row = row0 + r;
       const bool real = row < A.til.rows;
+      const bool busy = row0 + quad * 32 < A.til.rows;  // the warp has rows
       const int node = real ? row / A.G : 0;
       // ancestor masks of the request's tree, by doubling
       if (A.fixed <= 0 && b != req) {
@@ -525,62 +658,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       float m_run = -INFINITY, l_run = 0.f;  // the row's reference (raw); this half's sum
-      long long v_piece = 0;                 // ring position of the block's V
       for (int i = 0; i < nb; ++i) {
-        const long long qi = q + i;
-        const int nu = W.units_in(blk0 + i);
-        v_piece = piece + (long long)Y::kAtoms * (i + 1 < nb ? i + 2 : nb) + i * v_pieces(2);
-        wait(&s_bar[qi & 1], (uint32_t)((qi >> 1) & 1));
+        const uint32_t qi = q + i;
+        wait(&s_bar[qi & 1], (qi >> 1) & 1);
         ptx::tc_fence_after();
-        const bool has = hf < nu;  // this half's unit
-        float sv[64], mh = -INFINITY;
-        const uint32_t sc = tq + Y::kColS + (uint32_t)(qi & 1) * 128;
-        if (has) {
-          ptx::tmem_ld32(sc + hf * 64, *reinterpret_cast<float(*)[32]>(sv));
-          ptx::tmem_ld32(sc + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
-          int start, cnt;
-          bool tree;
-          W.unit(2 * (blk0 + i) + hf, start, tree, cnt);
-          const uint64_t ok = tree ? tree_bits
+        const uint32_t sc = tq + Y::kColS + (qi & 1) * Y::kBlk;
+        float sv[Y::kMine], mh = -INFINITY;
+        if (busy) {
+          ptx::tmem_ld32(sc + hf * Y::kMine, *reinterpret_cast<float(*)[32]>(sv));
+          if constexpr (Y::kMine == 64)
+            ptx::tmem_ld32(sc + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+        }
+        // this thread's unit: its own, or the upper or lower half of the one
+        constexpr bool kOne = Y::kBlkUnits == 1;
+        int start, cnt;
+        bool tree;
+        W.unit((blk0 + i) * Y::kBlkUnits + (kOne ? 0 : hf), start, tree, cnt);
+        // values no query sees must not reach O through a zero weight
+        if (!tree && cnt > 0 && cnt < kUnit) {
+          // the stage's earlier pieces have been multiplied, so that its barrier
+          // is in the phase that ends with this one's arrival
+          if (i > 0) wait(&o_bar[(qi - 1) & 1], ((qi - 1) >> 1) & 1);
+          // V comes after K of the next block
+          const uint32_t v_piece = piece + Y::kPieces * ((i + 1 < nb ? i + 2 : nb) + i);
+          constexpr int kWide = Y::kCols / 8, kBy = kOne ? 256 : 128;
+          for (int idx = tid % kBy; idx < (kUnit - cnt) * kWide; idx += kBy) {
+            const int c = idx % kWide, at = (kOne ? 0 : hf * kUnit) + cnt + idx / kWide;
+            const uint32_t pc = v_piece + at / Y::kVKeys, st = pc % Y::kStages;
+            wait(&full[st], (pc / Y::kStages) & 1);
+            *reinterpret_cast<uint4 *>(smem + Y::kSmemRing + st * kPiece + (c / 8) * Y::kVAtom +
+                                       (at % Y::kVKeys) * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async();
+        }
+        if (!busy) {  // no rows: keep step with the others
+          tell(&p_bar[qi & 1]);
+          continue;
+        }
+        const uint64_t seen = tree ? tree_bits
                                    : low_bits(cnt) & (~low_bits(lo - start) |
                                                       low_bits(A.n_sink - start));
-          // values no query sees must not reach O through a zero weight
-          if (!tree && cnt < kUnit) {
-            // the stage's earlier V has been multiplied, so that its barrier is
-            // in the phase that ends with this one's arrival
-            if (i > 0) wait(&o_bar[(qi - 1) & 1], (uint32_t)(((qi - 1) >> 1) & 1));
-            const int gone = kUnit - cnt;
-            for (int idx = tid & 127; idx < gone * (DH / 8); idx += 128) {
-              const int key = cnt + idx / (DH / 8), c = idx % (DH / 8);
-              const int at = hf * kUnit + key;
-              const long long pc = v_piece + at / Y::kVKeys;
-              const int st = (int)(pc % Y::kStages);
-              wait(&full[st], (uint32_t)((pc / Y::kStages) & 1));
-              *reinterpret_cast<uint4 *>(smem + Y::kSmemRing + st * kPiece + (c / 8) * Y::kVAtom +
-                                         (at % Y::kVKeys) * 128 + (c & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            ptx::fence_proxy_async();
-          }
-          ptx::tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, ok == ~0ull)) {
-            const uint32_t ok0 = (uint32_t)ok, ok1 = (uint32_t)(ok >> 32);
+        const uint64_t ok = (cnt > 0 ? seen : 0ull) >> (kOne ? hf * 32 : 0);
+        constexpr uint64_t kAll = Y::kMine == 64 ? ~0ull : 0xffffffffull;
+        ptx::tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, (ok & kAll) == kAll)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(ok0 >> e & 1)) sv[e] = -INFINITY;
-              if (!(ok1 >> e & 1)) sv[32 + e] = -INFINITY;
-            }
-          }
+          for (int e = 0; e < Y::kMine; ++e)
+            if (!((uint32_t)(ok >> (e & 32)) >> (e & 31) & 1)) sv[e] = -INFINITY;
+        }
+        {
           float mx[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx[e] = sv[e];
 #pragma unroll
-          for (int e = 8; e < 64; ++e) mx[e & 7] = fmaxf(mx[e & 7], sv[e]);
+          for (int e = 8; e < Y::kMine; ++e) mx[e & 7] = fmaxf(mx[e & 7], sv[e]);
           mh = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                      fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         }
         // (two buffers: the other half may not have read the last block's yet)
-        float *max_of = red + (int)(qi & 1) * 2 * kRows;
+        float *max_of = red + (qi & 1) * 2 * kRows;
         max_of[hf * kRows + r] = mh;
         ptx::tc_fence_before();
         ptx::named_sync(1 + quad, 64);  // the row's other half: maxima out, scores read
@@ -595,11 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_run = mb;
         }
         const float ref = m_run == -INFINITY ? 0.f : m_run * sl2;
-        if (has) {
+        {
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[32];
+          uint32_t pk[Y::kMine / 2];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < Y::kMine / 2; ++e) {
             const float p0 = ptx::ex2(fmaf(sv[2 * e], sl2, -ref));
             const float p1 = ptx::ex2(fmaf(sv[2 * e + 1], sl2, -ref));
             sum[e & 3] += p0 + p1;
@@ -610,17 +747,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          ptx::tmem_st32(sc + hf * 32, pk);
+          auto store = [&](uint32_t col) {
+            if constexpr (Y::kMine == 64) ptx::tmem_st32(col, pk);
+            else ptx::tmem_st16(col, pk);
+          };
+          store(sc + hf * (Y::kMine / 2));
           if constexpr (!F16) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) pk[e] = pack2<false>(sv[2 * e], sv[2 * e + 1]);
-            ptx::tmem_st32(sc + 64 + hf * 32, pk);
+            for (int e = 0; e < Y::kMine / 2; ++e) pk[e] = pack2<false>(sv[2 * e], sv[2 * e + 1]);
+            store(sc + Y::kMine + hf * (Y::kMine / 2));
           }
         }
         // rows whose reference moved rescale their half of O's columns, once
         // the previous product is done
         if (__any_sync(0xffffffffu, need)) {
-          wait(&o_bar[(qi - 1) & 1], (uint32_t)(((qi - 1) >> 1) & 1));
+          wait(&o_bar[(qi - 1) & 1], ((qi - 1) >> 1) & 1);
           ptx::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < kHalf / 32; ++c) {
@@ -636,20 +777,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_bar[qi & 1]);
+        tell(&p_bar[qi & 1]);
       }
-      piece = v_piece + v_pieces(W.units_in(blk1 - 1));
+      piece += 2 * Y::kPieces * nb;
       q += nb;
       // the next Q tile goes in while the last product runs: every score
       // product of this segment is done
-      const long long c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
+      const int c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
       const int set = W.set;
       have = advance();
       if (have) load_q();
 
       // ---- this segment's result: whole, or a partial ----
-      wait(&o_bar[(q - 1) & 1], (uint32_t)(((q - 1) >> 1) & 1));
+      wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
       ptx::tc_fence_after();
       ptx::named_sync(1 + quad, 64);  // the last maxima are read
       red[hf * kRows + r] = l_run;
@@ -714,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this CTA's partial: its first segment's, or its last's
       float *pp = A.part + ((size_t)blockIdx.x * 2 + (W.begin_of(W.cg) >= first ? 0 : 1)) *
                                part_floats(DH);
-      if (quad * 32 < A.til.rows - tile * kRows && (whole || valid)) {
+      if (busy && (whole || valid)) {
 #pragma unroll 1
         for (int c = 0; c < kHalf / 32; ++c) {
           const int col = hf * kHalf + 32 * c;
@@ -732,15 +872,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!whole) {
+      if (!whole && row0 < A.til.rows) {
         if (real && hf == 0) pp[r] = m2, pp[kRows + r] = l_sum;
         __threadfence();
         ptx::named_sync(5, kSoftmaxThreads);
         const size_t counter =
-            (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles + tile;
+            ((((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles + tile) * Y::kCtas + rank;
         if (tid == 0) {
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
-          misc[1] = (long long)prev == c_last - c_first ? 1 : 0;
+          misc[1] = (int)prev == c_last - c_first ? 1 : 0;
           if (misc[1]) A.counters[counter] = 0u;  // for the next call
         }
         ptx::named_sync(5, kSoftmaxThreads);
@@ -750,8 +890,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // loads of O in flight (of several rows where there are few pieces)
         if (misc[1]) {
           __threadfence();
-          const int rows = A.til.rows - tile * kRows < kRows ? A.til.rows - tile * kRows : kRows;
-          const int lane_of = tile - set * A.til.group, n_piece = (int)(c_last - c_first) + 1;
+          const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
+          const int lane_of = tile - set * A.til.group, n_piece = c_last - c_first + 1;
           // only a stream's first piece may not be its CTA's first
           const int slot0 = W.begin_of(c_first) < first ? 1 : 0;
           auto join = [&](auto per) {
@@ -773,8 +913,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < PP; ++e) {
                   const int g = g0 + e < n_piece ? g0 + e : 0;
                   const float *pg =
-                      A.part + ((size_t)((c_first + g) * A.til.group + lane_of) * 2 +
-                                (g == 0 ? slot0 : 0)) * part_floats(DH);
+                      A.part + ((size_t)(((c_first + g) * A.til.group + lane_of) * Y::kCtas +
+                                         rank) * 2 + (g == 0 ? slot0 : 0)) * part_floats(DH);
 #pragma unroll
                   for (int i = 0; i < II; ++i) {
                     const int rr = (int)(at[i] / (DH / 4));
@@ -809,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < II; ++i)
                 if (idx0 + i * kSoftmaxThreads < rows * (DH / 4))
                   emit(std::integral_constant<int, 4>{},
-                       place(tile * kRows + (int)(at[i] / (DH / 4))),
+                       place(row0 + (int)(at[i] / (DH / 4))),
                        (int)(at[i] % (DH / 4)) * 4, acc[i], top[i], sum[i]);
             }
           };
@@ -827,10 +967,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // neither leaves while the other may reach it
   if (tid == 0 && misc[2] && A.status) *A.status = LBX_ETIMEOUT;
   if (warp == 8) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, Y::kTmemCols);
+    if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, Y::kTmemCols);
+    else ptx::tmem_dealloc(tmem, Y::kTmemCols);
   }
 }
 
@@ -838,15 +980,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DH>
 cudaError_t launch_attn(bool f16, const AttnMaps &maps, const AttnArgs &A, int grid,
                         cudaStream_t stream);
-template <int DH, bool F16>
+template <int DH, bool F16, bool PAIR>
 cudaError_t launch_attn_of(const AttnMaps &maps, const AttnArgs &A, int grid,
                            cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<DH, F16>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Lay<DH>::kSmemTotal);
+  auto kernel = cache_attn_kernel<DH, F16, PAIR>;
+  constexpr int bytes = Lay<DH, PAIR>::kSmemTotal;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  cache_attn_kernel<DH, F16><<<(unsigned)grid, kThreads, Lay<DH>::kSmemTotal, stream>>>(maps, A);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes, cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = PAIR ? 2 : 1, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, A);
 }
 
 }  // namespace cache

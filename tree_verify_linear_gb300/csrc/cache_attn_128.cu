@@ -6,8 +6,11 @@ namespace cache {
 template <>
 cudaError_t launch_attn<128>(bool f16, const AttnMaps &maps, const AttnArgs &A, int grid,
                              cudaStream_t stream) {
-  return f16 ? launch_attn_of<128, true>(maps, A, grid, stream)
-             : launch_attn_of<128, false>(maps, A, grid, stream);
+  if (A.til.ctas == 2)
+    return f16 ? launch_attn_of<128, true, true>(maps, A, grid, stream)
+               : launch_attn_of<128, false, true>(maps, A, grid, stream);
+  return f16 ? launch_attn_of<128, true, false>(maps, A, grid, stream)
+             : launch_attn_of<128, false, false>(maps, A, grid, stream);
 }
 }  // namespace cache
 }  // namespace lbx
