@@ -48,8 +48,6 @@
 
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "cache_common.cuh"
 #include "cache_ptx.cuh"
 
@@ -153,6 +151,8 @@ struct Ring {
   }
 };
 
+// Most rows whose pieces are joined by columns instead of by rows.
+constexpr int kFewRows = 32;
 // What joining the pieces of a cut stream costs, in blocks.
 constexpr int kJoinBlocks = 3;
 
@@ -346,17 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
     return !bad;
   };
-  // for barriers that both CTAs of a pair arrive on
-  auto wait_both = [&](uint64_t *bar, uint32_t parity) {
-    if (!bad && !(PAIR ? ptx::mbar_wait_cluster(bar, parity) : ptx::mbar_wait(bar, parity)))
-      bad = true;
-    return !bad;
-  };
-
   if (warp == 9) {
     // ---- copies ----
     Ring<Y::kStages> ring;
     int loads = 0;
+    // behind the first Q tile's loads, which would wait for all of these
+    ptx::named_sync(6, kSoftmaxThreads + 32);
     while (W.next()) {
       if (!W.live || lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
@@ -440,15 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       else ptx::mma_commit(bar);
     };
     // the waits of the whole warp: given up by one lane, given up by all
-    auto wait_all = [&](uint64_t *bar, uint32_t parity, bool both) {
-      const bool ok = both ? wait_both(bar, parity) : wait(bar, parity);
-      bad = !__all_sync(0xffffffffu, ok);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+      bad = !__all_sync(0xffffffffu, wait(bar, parity));
       return !bad;
     };
     // the ring's next piece, here and at the follower
     auto arrived = [&]() {
-      return wait_all(&full[ring.st], ring.ph, false) &&
-             (!PAIR || wait_all(&peer[ring.st], ring.ph, true));
+      return wait_all(&full[ring.st], ring.ph) && (!PAIR || wait_all(&peer[ring.st], ring.ph));
     };
     while (W.next()) {
       if (!W.live) continue;
@@ -457,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scores = [&](int i) {
         const uint32_t qi = q + i, buf = qi & 1;
         // the buffer's last P has been multiplied (the first two find it free)
-        if (!wait_all(&o_bar[buf], ((qi >> 1) & 1) ^ 1u, false)) return;
+        if (!wait_all(&o_bar[buf], ((qi >> 1) & 1) ^ 1u)) return;
         constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, Y::kBlk, false);
         const uint32_t d = tmem + Y::kColS + buf * Y::kBlk;
 #pragma unroll
@@ -482,14 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      if (wait_all(q_bar, seg & 1, true)) {
+      if (wait_all(q_bar, seg & 1)) {
         ptx::tc_fence_after();
         scores(0);
       }
       for (int i = 0; i < nb && !bad; ++i) {
         if (i + 1 < nb) scores(i + 1);
         const uint32_t qi = q + i, buf = qi & 1;
-        if (!wait_all(&p_bar[buf], (qi >> 1) & 1, true)) break;
+        if (!wait_all(&p_bar[buf], (qi >> 1) & 1)) break;
         ptx::tc_fence_after();
         constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, DH, true);
         const uint32_t pc = tmem + Y::kColS + buf * Y::kBlk;
@@ -552,7 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       return (((size_t)W.l * A.n_req + W.b) * A.nodes + node) * A.Hq + W.h * A.G +
              (row - node * A.G);
     };
-    // The Q tile of the walk's segment, rows past the stream's zero.
+    // The Q tile of the walk's segment, rows past the stream's zero; its loads
+    // go ahead of the first copies of K and V.
+    bool ahead = true;
+    auto go_ahead = [&]() {
+      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(kSoftmaxThreads + 32) : "memory");
+      ahead = false;
+    };
     auto load_q = [&]() {
       constexpr int kPer = DH / 8;  // 16-byte pieces per row
       const uint4 *qg = reinterpret_cast<const uint4 *>(A.q);
@@ -562,13 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool in = row < A.til.rows;
         const uint4 *from = qg + (in ? query_of(row) * kPer + hf * (kPer / 2) : 0);
         constexpr int kC = DH / 4 < 32 ? DH / 4 : 32;  // columns per store
+        uint4 v[DH / 16];
+#pragma unroll
+        for (int e = 0; e < DH / 16; ++e) v[e] = in ? from[e] : none;
+        go_ahead();
 #pragma unroll
         for (int c = 0; c < DH / 4; c += kC) {
           uint32_t w[kC];
 #pragma unroll
           for (int e = 0; e < kC / 4; ++e) {
-            const uint4 v = in ? from[c / 4 + e] : none;
-            w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+            const uint4 f = v[c / 4 + e];
+            w[4 * e] = f.x, w[4 * e + 1] = f.y, w[4 * e + 2] = f.z, w[4 * e + 3] = f.w;
           }
           if constexpr (kC == 32) ptx::tmem_st32(tq + Y::kColQ + hf * (DH / 4) + c, w);
           else ptx::tmem_st16(tq + Y::kColQ + hf * (DH / 4) + c, w);
@@ -584,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = first_row() + r0 + e * kStep;
           v[e] = row < A.til.rows ? qg[query_of(row) * kPer + c] : none;
         }
+        go_ahead();
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
           const int rr = r0 + e * kStep;
@@ -591,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      ((c & 7) ^ (rr & 7)) * 16) = v[e];
         }
         ptx::fence_proxy_async();
+        if constexpr (PAIR) ptx::fence_cluster();
       }
       tell(q_bar);
     };
@@ -602,7 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     bool have = advance();
+    // this thread's node's parent in the walk's request, ahead of its use
+    auto parent_of = [&]() {
+      return A.fixed <= 0 && tid < A.N ? A.parent[(size_t)W.b * A.N + tid] : -1;
+    };
+    int up_next = have ? parent_of() : -1;
     if (have) load_q();
+    else go_ahead();
     while (have) {
       const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
       const int nb = blk1 - blk0, ctx = W.ctx;
@@ -613,33 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int node = real ? row / A.G : 0;
       // ancestor masks of the request's tree, by doubling
       if (A.fixed <= 0 && b != req) {
-        ptx::named_sync(5, kSoftmaxThreads);  // the last request's masks are read
-        if (tid < 32) {
-          uint64_t m[2];
-          int up[2];
-          for (int e = 0; e < 2; ++e) {
-            const int n = lane + 32 * e;
-            up[e] = n < A.N ? A.parent[(size_t)b * A.N + n] : -1;
-            m[e] = 1ull << n;
-            anc[n] = m[e];
-          }
-          int *ups = reinterpret_cast<int *>(red);  // not in use between segments
-          for (int e = 0; e < 2; ++e) ups[lane + 32 * e] = up[e];
-          __syncwarp();
-          for (int step = 0; step < 6; ++step) {
-            uint64_t add[2];
-            int nu[2];
-            for (int e = 0; e < 2; ++e) {
-              add[e] = up[e] >= 0 ? anc[up[e]] : 0ull;
-              nu[e] = up[e] >= 0 ? ups[up[e]] : -1;
-            }
-            __syncwarp();
-            for (int e = 0; e < 2; ++e) {
-              m[e] |= add[e], up[e] = nu[e];
-              anc[lane + 32 * e] = m[e], ups[lane + 32 * e] = up[e];
-            }
-            __syncwarp();
-          }
+        int *ups = reinterpret_cast<int *>(red);  // not in use between segments
+        int up = up_next;
+        uint64_t m = 1ull << (tid & 63);
+        if (tid < kMaxNodes) anc[tid] = m, ups[tid] = up;
+        for (int step = 0; step < 6; ++step) {
+          ptx::named_sync(5, kSoftmaxThreads);
+          const uint64_t add = tid < kMaxNodes && up >= 0 ? anc[up] : 0ull;
+          const int next_up = tid < kMaxNodes && up >= 0 ? ups[up] : -1;
+          ptx::named_sync(5, kSoftmaxThreads);
+          m |= add, up = next_up;
+          if (tid < kMaxNodes) anc[tid] = m, ups[tid] = up;
         }
         ptx::named_sync(5, kSoftmaxThreads);
         req = b;
@@ -674,25 +669,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         int start, cnt;
         bool tree;
         W.unit((blk0 + i) * Y::kBlkUnits + (kOne ? 0 : hf), start, tree, cnt);
-        // values no query sees must not reach O through a zero weight
-        if (!tree && cnt > 0 && cnt < kUnit) {
-          // the stage's earlier pieces have been multiplied, so that its barrier
-          // is in the phase that ends with this one's arrival
-          if (i > 0) wait(&o_bar[(qi - 1) & 1], ((qi - 1) >> 1) & 1);
-          // V comes after K of the next block
-          const uint32_t v_piece = piece + Y::kPieces * ((i + 1 < nb ? i + 2 : nb) + i);
-          constexpr int kWide = Y::kCols / 8, kBy = kOne ? 256 : 128;
-          for (int idx = tid % kBy; idx < (kUnit - cnt) * kWide; idx += kBy) {
-            const int c = idx % kWide, at = (kOne ? 0 : hf * kUnit) + cnt + idx / kWide;
-            const uint32_t pc = v_piece + at / Y::kVKeys, st = pc % Y::kStages;
-            wait(&full[st], (pc / Y::kStages) & 1);
-            *reinterpret_cast<uint4 *>(smem + Y::kSmemRing + st * kPiece + (c / 8) * Y::kVAtom +
-                                       (at % Y::kVKeys) * 128 + (c & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+        auto clear_unseen = [&]() {
+          // values no query sees must not reach O through a zero weight
+          if (!tree && cnt > 0 && cnt < kUnit) {
+            // the stage's earlier pieces have been multiplied, so that its barrier
+            // is in the phase that ends with this one's arrival
+            if (i > 0) wait(&o_bar[(qi - 1) & 1], ((qi - 1) >> 1) & 1);
+            // V comes after K of the next block
+            const uint32_t v_piece = piece + Y::kPieces * ((i + 1 < nb ? i + 2 : nb) + i);
+            constexpr int kWide = Y::kCols / 8, kBy = kOne ? 256 : 128;
+            for (int idx = tid % kBy; idx < (kUnit - cnt) * kWide; idx += kBy) {
+              const int c = idx % kWide, at = (kOne ? 0 : hf * kUnit) + cnt + idx / kWide;
+              const uint32_t pc = v_piece + at / Y::kVKeys, st = pc % Y::kStages;
+              wait(&full[st], (pc / Y::kStages) & 1);
+              *reinterpret_cast<uint4 *>(smem + Y::kSmemRing + st * kPiece + (c / 8) * Y::kVAtom +
+                                         (at % Y::kVKeys) * 128 + (c & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async();
+            if constexpr (PAIR) ptx::fence_cluster();
           }
-          ptx::fence_proxy_async();
-        }
+        };
         if (!busy) {  // no rows: keep step with the others
+          clear_unseen();
           tell(&p_bar[qi & 1]);
           continue;
         }
@@ -775,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_st32(col, w);
           }
         }
+        clear_unseen();
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         tell(&p_bar[qi & 1]);
@@ -786,7 +786,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
       const int set = W.set;
       have = advance();
-      if (have) load_q();
+      if (have) {
+        up_next = parent_of();
+        load_q();
+      }
 
       // ---- this segment's result: whole, or a partial ----
       wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
@@ -798,165 +801,196 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = misc[2] == 0;
       float l_sum = red[r] + red[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
-      // Write C columns of a finished row (its place among all queries), joined
-      // with the prefix's if there is one.
-      auto emit = [&](auto width, size_t at, int col, const float *acc, float m, float sum) {
-        constexpr int C = decltype(width)::value;
+      // A finished row of the stream: its place among all queries, and in the
+      // prefix's results ([layer, KV head][DH / 4][all rows] of four columns).
+      auto place = [&](int rw) {
+        const int nd = rw / A.G;
+        return (((size_t)l * A.n_req + b) * A.nodes + nd) * A.Hq + h * A.G + (rw - nd * A.G);
+      };
+      const size_t rows_all = (size_t)A.n_req * A.til.rows;
+      auto place_x = [&](int rw) {
+        return (size_t)(l * A.Hkv + h) * rows_all * (DH / 4) + (size_t)b * A.til.rows + rw;
+      };
+      auto place_xl = [&](int rw) {
+        return (size_t)(l * A.Hkv + h) * rows_all + (size_t)b * A.til.rows + rw;
+      };
+      // The factors of this stream's O and of the prefix's o, and the row's lse.
+      auto factors = [&](int rw, float m, float sum, float &w, float &wx) {
         const float own = sum > 0.f ? m + log2f(sum) : -INFINITY;
-        float all = own, w = sum > 0.f ? 1.f / sum : 0.f;
-        float v[C];
+        float all = own;
+        w = sum > 0.f ? 1.f / sum : 0.f, wx = 0.f;
         if (A.x_o) {
-          float4 f[C / 4];
-          const float4 *xo = reinterpret_cast<const float4 *>(A.x_o + at * DH + col);
-#pragma unroll
-          for (int e = 0; e < C / 4; ++e) f[e] = __ldcg(xo + e);
-          const float x = __ldcg(A.x_lse2 + at), top = fmaxf(own, x);
-          float wx = 0.f;
+          const float x = __ldcg(A.x_lse2 + place_xl(rw)), top = fmaxf(own, x);
           if (top != -INFINITY) {
             const float eo = exp2f(own - top), ex = exp2f(x - top), inv = 1.f / (eo + ex);
             w *= eo * inv, wx = ex * inv;
             all = top + log2f(eo + ex);
           }
-#pragma unroll
-          for (int e = 0; e < C / 4; ++e) {
-            v[4 * e] = fmaf(acc[4 * e], w, wx * f[e].x);
-            v[4 * e + 1] = fmaf(acc[4 * e + 1], w, wx * f[e].y);
-            v[4 * e + 2] = fmaf(acc[4 * e + 2], w, wx * f[e].z);
-            v[4 * e + 3] = fmaf(acc[4 * e + 3], w, wx * f[e].w);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < C; ++e) v[e] = acc[e] * w;
         }
-        if (A.o32) {
-          float4 *to = reinterpret_cast<float4 *>(A.o32 + at * DH + col);
-#pragma unroll
-          for (int e = 0; e < C / 4; ++e)
-            to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else {
-          uint2 *to = reinterpret_cast<uint2 *>(A.o + at * DH + col);
-#pragma unroll
-          for (int e = 0; e < C / 4; ++e)
-            to[e] = make_uint2(pack2<F16>(v[4 * e], v[4 * e + 1]),
-                               pack2<F16>(v[4 * e + 2], v[4 * e + 3]));
-        }
-        if (col == 0) {
-          if (A.lse2) A.lse2[at] = all;
-          if (A.lse) A.lse[at] = all * 0.6931471805599453f;
-        }
+        return all;
       };
-      // The place among all queries of a row of the stream.
-      auto place = [&](int rw) {
-        const int nd = rw / A.G;
-        return (((size_t)l * A.n_req + b) * A.nodes + nd) * A.Hq + h * A.G + (rw - nd * A.G);
+      auto put_lse = [&](int rw, float all) {
+        if (A.lse2) A.lse2[place_xl(rw)] = all;
+        if (A.lse) A.lse[place(rw)] = all * 0.6931471805599453f;
       };
       const bool whole = c_first == c_last;
-      // this CTA's partial: its first segment's, or its last's
-      float *pp = A.part + ((size_t)blockIdx.x * 2 + (W.begin_of(W.cg) >= first ? 0 : 1)) *
-                               part_floats(DH);
-      if (busy && (whole || valid)) {
+      const int lane_of = tile - set * A.til.group, n_piece = c_last - c_first + 1;
+      const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
+      // Partial g of the stream: m and l per row, then O as [DH / 4][128] of
+      // four columns.  Each CTA has two: its first segment's, and its last's.
+      auto partial = [&](int g) {
+        const int cta = ((c_first + g) * A.til.group + lane_of) * Y::kCtas + rank;
+        const int slot = g == 0 && W.begin_of(c_first) < first ? 1 : 0;
+        return A.part + (size_t)(2 * cta + slot) * part_floats(DH);
+      };
+      bool join = false;
+      if (!whole && rows > 0) {
+        float4 *to = reinterpret_cast<float4 *>(partial(W.cg - c_first) + 2 * kRows);
+        if (busy && valid) {
 #pragma unroll 1
-        for (int c = 0; c < kHalf / 32; ++c) {
-          const int col = hf * kHalf + 32 * c;
-          float ov[32];
-          ptx::tmem_ld32(tq + Y::kColO + (uint32_t)col, ov);
-          ptx::tmem_wait_ld();
-          if (!real) continue;
-          if (whole) {
-            if (valid) emit(std::integral_constant<int, 32>{}, place(row), col, ov, m2, l_sum);
-          } else {
-            float4 *to = reinterpret_cast<float4 *>(pp + 2 * kRows + (size_t)r * DH + col);
+          for (int c = 0; c < kHalf / 32; ++c) {
+            const int col = hf * kHalf + 32 * c;
+            float ov[32];
+            ptx::tmem_ld32(tq + Y::kColO + (uint32_t)col, ov);
+            ptx::tmem_wait_ld();
+            if (real) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              to[e] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              for (int e = 0; e < 8; ++e)
+                to[(col / 4 + e) * kRows + r] =
+                    make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+            }
           }
         }
-      }
-      if (!whole && row0 < A.til.rows) {
-        if (real && hf == 0) pp[r] = m2, pp[kRows + r] = l_sum;
+        if (real && hf == 0) {
+          float *ml = partial(W.cg - c_first);
+          ml[r] = m2, ml[kRows + r] = l_sum;
+        }
         __threadfence();
         ptx::named_sync(5, kSoftmaxThreads);
         const size_t counter =
             ((((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles + tile) * Y::kCtas + rank;
         if (tid == 0) {
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
-          misc[1] = (int)prev == c_last - c_first ? 1 : 0;
+          misc[1] = (int)prev == n_piece - 1 ? 1 : 0;
           if (misc[1]) A.counters[counter] = 0u;  // for the next call
         }
         ptx::named_sync(5, kSoftmaxThreads);
-        // the last CTA joins the pieces: four columns of a row per thread, the
-        // pieces' m, l and O of up to eight of them in flight at a time
-        // the last CTA joins the pieces: four columns of a row per thread, eight
-        // loads of O in flight (of several rows where there are few pieces)
-        if (misc[1]) {
-          __threadfence();
-          const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
-          const int lane_of = tile - set * A.til.group, n_piece = c_last - c_first + 1;
-          // only a stream's first piece may not be its CTA's first
-          const int slot0 = W.begin_of(c_first) < first ? 1 : 0;
-          auto join = [&](auto per) {
-            constexpr int PP = decltype(per)::value, II = 8 / PP;  // pieces, items at a time
-            for (int idx0 = tid; idx0 < rows * (DH / 4); idx0 += II * kSoftmaxThreads) {
-              float top[II], sum[II], acc[II][4];
-              size_t at[II];  // of the item in a partial's O
+        join = misc[1] != 0;
+        if (join) __threadfence();
+      }
+      if (join && rows <= kFewRows) {
+        // few rows, maybe many pieces: four columns of a row per thread, eight
+        // pieces in flight
+        for (int idx = tid; idx < rows * (DH / 4); idx += kSoftmaxThreads) {
+          const int rr = idx / (DH / 4), c4 = idx % (DH / 4);
+          float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int g0 = 0; g0 < n_piece; g0 += 8) {
+            float mg[8], lg[8];
+            float4 og[8];
 #pragma unroll
-              for (int i = 0; i < II; ++i) {
-                const int idx = idx0 + i * kSoftmaxThreads;
-                at[i] = (size_t)(idx < rows * (DH / 4) ? idx : idx0);
-                top[i] = -INFINITY, sum[i] = 0.f;
-                acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-              }
-              for (int g0 = 0; g0 < n_piece; g0 += PP) {
-                float mg[II][PP], lg[II][PP];
-                float4 og[II][PP];
+            for (int e = 0; e < 8; ++e) {
+              const float *pg = partial(g0 + e < n_piece ? g0 + e : 0);
+              mg[e] = g0 + e < n_piece ? __ldcg(pg + rr) : -INFINITY;
+              lg[e] = __ldcg(pg + kRows + rr);
+              og[e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) + c4 * kRows + rr);
+            }
+            float t8 = top;
 #pragma unroll
-                for (int e = 0; e < PP; ++e) {
-                  const int g = g0 + e < n_piece ? g0 + e : 0;
-                  const float *pg =
-                      A.part + ((size_t)(((c_first + g) * A.til.group + lane_of) * Y::kCtas +
-                                         rank) * 2 + (g == 0 ? slot0 : 0)) * part_floats(DH);
+            for (int e = 0; e < 8; ++e) t8 = fmaxf(t8, mg[e]);
+            if (t8 == -INFINITY) continue;
+            const float old = ptx::ex2(top - t8);
+            top = t8, sum *= old;
 #pragma unroll
-                  for (int i = 0; i < II; ++i) {
-                    const int rr = (int)(at[i] / (DH / 4));
-                    mg[i][e] = g0 + e < n_piece ? __ldcg(pg + rr) : -INFINITY;
-                    lg[i][e] = __ldcg(pg + kRows + rr);
-                    og[i][e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) + at[i]);
-                  }
-                }
+            for (int e = 0; e < 4; ++e) acc[e] *= old;
 #pragma unroll
-                for (int i = 0; i < II; ++i) {
-                  float t8 = top[i];
+            for (int e = 0; e < 8; ++e) {
+              if (mg[e] == -INFINITY) continue;  // an empty piece's O is not read
+              const float w = ptx::ex2(mg[e] - top);
+              sum = fmaf(w, lg[e], sum);
+              acc[0] = fmaf(w, og[e].x, acc[0]), acc[1] = fmaf(w, og[e].y, acc[1]);
+              acc[2] = fmaf(w, og[e].z, acc[2]), acc[3] = fmaf(w, og[e].w, acc[3]);
+            }
+          }
+          const int rw = row0 + rr;
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (A.x_o)
+            f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);
+          float w, wx;
+          const float all = factors(rw, top, sum, w, wx);
+          f.x = fmaf(acc[0], w, wx * f.x), f.y = fmaf(acc[1], w, wx * f.y);
+          f.z = fmaf(acc[2], w, wx * f.z), f.w = fmaf(acc[3], w, wx * f.w);
+          if (A.o32)
+            reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;
+          else
+            reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] =
+                make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
+          if (c4 == 0) put_lse(rw, all);
+        }
+      } else if (busy && valid && (whole || join)) {
+        // a row per two threads; this CTA's piece is still in tensor memory,
+        // the others' (all but one, mostly) are read 32 columns at a time
+        float top = m2, sum = l_sum, w_own = 1.f;
+        if (join) {
+          for (int g = 0; g < n_piece; ++g)
+            if (c_first + g != W.cg) top = fmaxf(top, __ldcg(partial(g) + r));
+          const float ref = top == -INFINITY ? 0.f : top;
+          w_own = ptx::ex2(m2 - ref), sum = l_sum * w_own;
+          for (int g = 0; g < n_piece; ++g)
+            if (c_first + g != W.cg)
+              sum += ptx::ex2(__ldcg(partial(g) + r) - ref) * __ldcg(partial(g) + kRows + r);
+          top = ref;
+        }
+        float w = 0.f, wx = 0.f, all = 0.f;
+        if (real) all = factors(row, top, sum, w, wx);
+        if (real && hf == 0) put_lse(row, all);
+#pragma unroll 1
+        for (int c = 0; c < kHalf / 32; ++c) {
+          const int col = hf * kHalf + 32 * c;
+          float v[32];
+          ptx::tmem_ld32(tq + Y::kColO + (uint32_t)col, v);
+          ptx::tmem_wait_ld();
+          if (!real) continue;
 #pragma unroll
-                  for (int e = 0; e < PP; ++e) t8 = fmaxf(t8, mg[i][e]);
-                  if (t8 == -INFINITY) continue;
-                  const float old = ptx::ex2(top[i] - t8);
-                  top[i] = t8, sum[i] *= old;
+          for (int e = 0; e < 32; ++e) v[e] *= w * w_own;
+          // add f times 32 columns of this row in an array of four-column rows
+          auto add = [&](float f, const float4 *from, size_t stride) {
+            float4 x[8];
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) acc[i][e] *= old;
+            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + e * stride);
 #pragma unroll
-                  for (int e = 0; e < PP; ++e) {
-                    if (mg[i][e] == -INFINITY) continue;  // an empty piece's O is not read
-                    const float w = ptx::ex2(mg[i][e] - t8);
-                    sum[i] = fmaf(w, lg[i][e], sum[i]);
-                    acc[i][0] = fmaf(w, og[i][e].x, acc[i][0]);
-                    acc[i][1] = fmaf(w, og[i][e].y, acc[i][1]);
-                    acc[i][2] = fmaf(w, og[i][e].z, acc[i][2]);
-                    acc[i][3] = fmaf(w, og[i][e].w, acc[i][3]);
-                  }
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < II; ++i)
-                if (idx0 + i * kSoftmaxThreads < rows * (DH / 4))
-                  emit(std::integral_constant<int, 4>{},
-                       place(row0 + (int)(at[i] / (DH / 4))),
-                       (int)(at[i] % (DH / 4)) * 4, acc[i], top[i], sum[i]);
+            for (int e = 0; e < 8; ++e) {
+              v[4 * e] = fmaf(f, x[e].x, v[4 * e]);
+              v[4 * e + 1] = fmaf(f, x[e].y, v[4 * e + 1]);
+              v[4 * e + 2] = fmaf(f, x[e].z, v[4 * e + 2]);
+              v[4 * e + 3] = fmaf(f, x[e].w, v[4 * e + 3]);
             }
           };
-          if (n_piece <= 2)
-            join(std::integral_constant<int, 2>{});
-          else
-            join(std::integral_constant<int, 8>{});
+          if (join) {
+            for (int g = 0; g < n_piece; ++g) {
+              const float *pg = partial(g);
+              const float mg = c_first + g != W.cg ? __ldcg(pg + r) : -INFINITY;
+              if (mg == -INFINITY) continue;  // an empty piece's O is not read
+              add(w * ptx::ex2(mg - top),
+                  reinterpret_cast<const float4 *>(pg + 2 * kRows) + col / 4 * kRows + r, kRows);
+            }
+          }
+          if (A.x_o)
+            add(wx, reinterpret_cast<const float4 *>(A.x_o) + place_x(row) + col / 4 * rows_all,
+                rows_all);
+          if (A.o32) {
+            float4 *to = reinterpret_cast<float4 *>(A.o32) + place_x(row) + col / 4 * rows_all;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              to[e * rows_all] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else {
+            uint4 *to = reinterpret_cast<uint4 *>(A.o + place(row) * DH + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(pack2<F16>(v[8 * e], v[8 * e + 1]),
+                                 pack2<F16>(v[8 * e + 2], v[8 * e + 3]),
+                                 pack2<F16>(v[8 * e + 4], v[8 * e + 5]),
+                                 pack2<F16>(v[8 * e + 6], v[8 * e + 7]));
+          }
         }
       }
       ptx::tc_fence_before();

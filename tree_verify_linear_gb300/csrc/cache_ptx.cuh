@@ -59,37 +59,23 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.wait.acquire;" ::
           : "memory");
 }
-// One arrival on the same mbarrier of CTA `rank` of the cluster.
+// Order this thread's shared-memory writes before its next arrival at another
+// CTA of the cluster.
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+// One arrival on the same mbarrier of CTA `rank` of the cluster.  It does not
+// wait for earlier memory operations as a cluster-wide release would (1000
+// cycles and more while copies are in flight): tensor-memory writes are
+// ordered by tcgen05 fences, shared-memory writes by fence_cluster.
 __device__ __forceinline__ void mbar_arrive_at(uint64_t *bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
-// mbar_wait for barriers that CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > kWaitNs) return false;
-  }
-  return false;
-}
-
 // Tensor memory of both CTAs: one warp of each calls these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
