@@ -101,7 +101,7 @@ def read_peaks():
 # leaves the recorded traffic of the verify workloads valid.
 OTHER_OPS = ("accept_walk.cu", "ddtree_build.cu", "tree_attn.cu", "cache_common.cuh",
              "cache_attn.cu", "cache_attn.cuh", "cache_attn_64.cu", "cache_attn_128.cu",
-             "cache_attn_256.cu", "cache_ptx.cuh", "cache_mass.cu", "cache_evict.cu")
+             "cache_attn_256.cu", "cache_ptx.cuh", "cache_walk.cuh", "cache_mass.cu", "cache_evict.cu")
 
 
 def kernel_source_hash(op: str = "verify") -> str:

@@ -32,10 +32,11 @@ bool have_encode() {
   return g_encode != nullptr;
 }
 
-// (dh, Hkv, len, lists) view of a [lists][len][Hkv][dh] array of 16-bit
-// values; box: 64 columns of one head's `keys` consecutive positions.
-bool encode(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, int lists,
-            int keys) {
+}  // namespace
+
+bool encode_list(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, int lists,
+                 int keys) {
+  if (!have_encode()) return false;
   const cuuint64_t row = (cuuint64_t)c->Hkv * c->dh * 2;
   const cuuint64_t gdim[4] = {(cuuint64_t)c->dh, (cuuint64_t)c->Hkv, (cuuint64_t)len,
                               (cuuint64_t)lists};
@@ -47,6 +48,16 @@ bool encode(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+int grid_limit() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 0;
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -96,7 +107,6 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if ((lse && !aligned_to(lse, 4)) || (status && !aligned_to(status, 4))) return LBX_EINVAL;
   const Space s = space_of(c);
   if (!list_ok(c, s) || ws_bytes < s.bytes) return LBX_EINVAL;
-  if (!have_encode()) return LBX_ECUDA;
   // rows of a box of V: a piece of it may hold fewer keys than a unit
   static_assert(Lay<128, false>::kVBox == kUnit && Lay<64, false>::kVBox == kUnit &&
                     Lay<128, true>::kVBox == kUnit && Lay<256, true>::kVBox == kUnit,
@@ -105,12 +115,8 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     return c->dh == 256 && t.ctas == 1 ? Lay<256, false>::kVBox : kUnit;
   };
 
-  int dev = 0, nsm = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || nsm < 1)
-    return LBX_ECUDA;
-  if (nsm > kMaxCtas) nsm = kMaxCtas;
-
+  const int nsm = grid_limit();
+  if (nsm < 1) return LBX_ECUDA;
   unsigned char *base = static_cast<unsigned char *>(ws);
   AttnArgs A = {};
   A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = c->Hq / c->Hkv;
@@ -130,7 +136,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   AttnMaps maps;
   std::memset(&maps, 0, sizeof maps);
   if (c->P > 0) {
-    if (!encode(&maps.k, kp, c, c->P, c->L, kUnit) || !encode(&maps.v, vp, c, c->P, c->L, v_box(s.pre)))
+    if (!encode_list(&maps.k, kp, c, c->P, c->L, kUnit) || !encode_list(&maps.v, vp, c, c->P, c->L, v_box(s.pre)))
       return LBX_ECUDA;
     maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
     A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
@@ -141,11 +147,11 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr, A.fixed = 0;
   }
   const int lists = c->L * c->Bq;
-  if (!encode(&maps.kt, kt, c, c->N, lists, kUnit) || !encode(&maps.vt, vt, c, c->N, lists, v_box(s.own)))
+  if (!encode_list(&maps.kt, kt, c, c->N, lists, kUnit) || !encode_list(&maps.vt, vt, c, c->N, lists, v_box(s.own)))
     return LBX_ECUDA;
   maps.k = maps.kt, maps.v = maps.vt;  // without a cache: never read
   if (c->T > 0 &&
-      (!encode(&maps.k, kc, c, c->T, lists, kUnit) || !encode(&maps.v, vc, c, c->T, lists, v_box(s.own))))
+      (!encode_list(&maps.k, kc, c, c->T, lists, kUnit) || !encode_list(&maps.v, vc, c, c->T, lists, v_box(s.own))))
     return LBX_ECUDA;
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
   A.window = c->window, A.n_sink = c->n_sink;

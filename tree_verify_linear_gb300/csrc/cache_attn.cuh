@@ -46,44 +46,18 @@
 // memory.
 #pragma once
 
-#include <cuda.h>
-
 #include "cache_common.cuh"
 #include "cache_ptx.cuh"
+#include "cache_walk.cuh"
 
 namespace lbx {
 namespace cache {
 
-constexpr int kRows = 128;         // query rows per CTA
-constexpr int kUnit = 64;          // keys per unit
-constexpr int kPiece = 16 * 1024;  // bytes per ring stage
-constexpr int kMaxCtas = 160;      // largest grid (partials in the workspace)
-constexpr int kMaxGroup = 8;       // most row tiles that run side by side
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = kSoftmaxThreads + 64;
 
-// Row tiles of a stream, of 128 rows (256 for pairs of CTAs): `sets` sets of up
-// to `group` tiles each.
-struct Tiling {
-  int rows, tiles, sets, group, ctas;  // ctas: per tile
-};
-inline Tiling tiling(long long rows, int dh) {
-  Tiling t;
-  t.rows = (int)rows;
-  t.ctas = rows > kRows && dh >= 128 ? 2 : 1;
-  t.tiles = (int)((rows + t.ctas * kRows - 1) / (t.ctas * kRows));
-  t.sets = (t.tiles + kMaxGroup - 1) / kMaxGroup;
-  t.group = (t.tiles + t.sets - 1) / t.sets;
-  return t;
-}
-
 // Floats of one partial: m (base 2) and l per row, then O.
 constexpr size_t part_floats(int dh) { return 2 * (size_t)kRows + (size_t)kRows * dh; }
-
-struct AttnMaps {
-  CUtensorMap k, v;    // (dh, Hkv, positions, layer x request), boxes of 64 columns
-  CUtensorMap kt, vt;  // the tree's
-};
 
 struct AttnArgs {
   int L, Hq, Hkv, G;
@@ -141,145 +115,10 @@ struct Lay {
   static_assert(kColO + DH <= kTmemCols && (!kQTmem || DH / 2 <= 128), "tensor memory");
 };
 
-// A position in a ring of N stages and the parity of its round.
-template <int N>
-struct Ring {
-  int st = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void step() {
-    if (++st == N) st = 0, ph ^= 1u;
-  }
-};
-
 // Most rows whose pieces are joined by columns instead of by rows.
 constexpr int kFewRows = 32;
 // What joining the pieces of a cut stream costs, in blocks.
 constexpr int kJoinBlocks = 3;
-
-// Walks a CTA's range of the block list (blocks of BU units).  Used by whole
-// warps, each lane alike; the CTAs of a pair walk alike.
-// Where whole streams per group come out within kJoinBlocks of equal ranges of
-// blocks, a stream counts as one entry of the list and is not cut.
-template <int BU>
-struct Walk {
-  const AttnArgs &A;
-  // the list's entries and how they are cut: `more` ranges of each + 1 entries,
-  // then ranges of `each`; per_b_base: first entry of request b
-  int total, groups, each, more, cg, x, x_end, per_b_base;
-  int slot_in_group, b, nblk, ctx;
-  bool uncut;
-  // the current segment
-  int l, h, set, tile, blk0, blk1;
-  int first;  // the stream's first entry
-  bool live;  // this CTA has a tile of the stream
-
-  // units of a request's key list
-  int w0, s_eff, ns, nw, units;
-
-  __device__ __forceinline__ void plan(int len) {  // of length `len`
-    ctx = len;
-    w0 = A.window > 0 && len - A.window + 1 > 0 ? len - A.window + 1 : 0;
-    s_eff = A.n_sink < w0 ? A.n_sink : w0;
-    ns = (s_eff + kUnit - 1) / kUnit;
-    nw = (len - w0 + kUnit - 1) / kUnit;
-    units = ns + nw + (A.fixed > 0 ? 0 : 1);
-    nblk = (units + BU - 1) / BU;
-  }
-  __device__ __forceinline__ int blocks_of(int req) {
-    plan(A.fixed > 0 ? A.fixed : A.ctx_len[req]);
-    return nblk;
-  }
-  // Streams per request; entries of each of the current request's in the list.
-  __device__ __forceinline__ int streams() const { return A.L * A.Hkv * A.til.sets; }
-  __device__ __forceinline__ int entries() const { return uncut ? 1 : nblk; }
-
-  __device__ __forceinline__ Walk(const AttnArgs &a, int lane) : A(a), uncut(false) {
-    int sum = 0, most = 0;
-    for (int r = lane; r < A.n_req; r += 32) {
-      sum += blocks_of(r);
-      most = nblk > most ? nblk : most;
-    }
-    sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
-    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
-    total = sum * streams();
-    groups = (int)(gridDim.x / (unsigned)(A.til.group * A.til.ctas));
-    const long long all = (long long)streams() * A.n_req;
-    uncut = (all + groups - 1) / groups * most <= (total + groups - 1) / groups + kJoinBlocks;
-    if (uncut) total = (int)all;
-    if (groups > total) groups = total;
-    each = total / groups, more = total - each * groups;
-    const int at = (int)blockIdx.x / A.til.ctas;
-    cg = at / A.til.group;
-    slot_in_group = at - cg * A.til.group;
-    x = cg < groups ? begin_of(cg) : total;
-    x_end = cg < groups ? begin_of(cg + 1) : total;
-    // the request of entry x: 32 requests at a time
-    b = 0, per_b_base = 0;
-    if (x < x_end) {
-      for (int r0 = 0;; r0 += 32) {
-        int mine = 0;
-        if (r0 + lane < A.n_req) blocks_of(r0 + lane), mine = entries() * streams();
-        int upto = mine;
-        for (int w = 1; w < 32; w <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, w);
-          if (lane >= w) upto += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, per_b_base + upto > x);
-        if (past) {
-          const int f = __ffs(past) - 1;
-          b = r0 + f;
-          per_b_base += __shfl_sync(0xffffffffu, upto - mine, f);
-          break;
-        }
-        per_b_base += __shfl_sync(0xffffffffu, upto, 31);
-      }
-      blocks_of(b);
-    }
-  }
-
-  // Take the next segment; false at the end of the range.
-  __device__ __forceinline__ bool next() {
-    if (x >= x_end) return false;
-    while (x - per_b_base >= entries() * streams()) {
-      per_b_base += entries() * streams();
-      blocks_of(++b);
-    }
-    const int in_b = x - per_b_base, s = in_b / entries();
-    blk0 = in_b - s * entries();
-    first = x - blk0;
-    const int lh = A.til.sets > 1 ? s / A.til.sets : s;
-    set = s - lh * A.til.sets;
-    l = lh / A.Hkv, h = lh - l * A.Hkv;
-    blk1 = uncut || x_end - first >= nblk ? nblk : x_end - first;
-    x = uncut ? x + 1 : first + blk1;
-    tile = set * A.til.group + slot_in_group;
-    live = tile < A.til.tiles;
-    return true;
-  }
-  __device__ __forceinline__ int begin_of(int g) const { return g * each + (g < more ? g : more); }
-  __device__ __forceinline__ int owner(int at) const {
-    const int big = more * (each + 1);
-    return at < big ? at / (each + 1) : more + (at - big) / each;
-  }
-  // Unit u: the position (or tree node) of its first key, whether it is the
-  // tree's, and how many of its keys any query sees.  A unit past the last is
-  // empty: a copy of it lies outside its array and fills in zeros.
-  __device__ __forceinline__ void unit(int u, int &start, bool &tree, int &cnt) const {
-    tree = u >= ns + nw && A.fixed <= 0;
-    if (u >= units) {
-      start = tree ? A.N : ctx, cnt = 0;
-      return;
-    }
-    start = u < ns ? u * kUnit : tree ? 0 : w0 + (u - ns) * kUnit;
-    const int end = u < ns ? s_eff : tree ? A.N : ctx;
-    cnt = end - start < kUnit ? end - start : kUnit;
-  }
-};
-
-// The low k (0..64) bits.
-__device__ __forceinline__ uint64_t low_bits(int k) {
-  return k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
-}
 
 // Parts of P: f16 once, bf16 hi + lo.
 template <bool F16>
@@ -340,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
-  Walk<Y::kBlkUnits> W(A, lane);
+  Walk<Y::kBlkUnits, kJoinBlocks, AttnArgs> W(A, lane);
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
@@ -352,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int loads = 0;
     // behind the first Q tile's loads, which would wait for all of these
     ptx::named_sync(6, kSoftmaxThreads + 32);
+#pragma unroll 1
     while (W.next()) {
       if (!W.live || lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
@@ -363,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++loads;
         return smem + Y::kSmemRing + ring.st * kPiece;
       };
+#pragma unroll 1
       for (int i = 0; i <= nb && !bad; ++i) {
         if (i < nb) {  // K of block i
           const int u0 = (W.blk0 + i) * Y::kBlkUnits + rank;
@@ -407,14 +248,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) misc[2] = 1;
       // every copy has landed before the CTA may leave (long since, unless a
       // wait gave up)
+#pragma unroll 1
       for (int i = loads > Y::kStages ? loads - Y::kStages : 0; i < loads; ++i)
         (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
     }
   } else if (warp == 8 && rank == 1) {
     // ---- the follower tells the leader of each piece that has landed ----
     Ring<Y::kStages> ring;
+#pragma unroll 1
     while (W.next()) {
       if (!W.live || lane != 0) continue;
+#pragma unroll 1
       for (int n = 2 * Y::kPieces * (W.blk1 - W.blk0); n > 0; --n, ring.step()) {
         if (!wait(&full[ring.st], ring.ph)) break;
         ptx::mbar_arrive_at(&peer[ring.st], 0);
@@ -443,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto arrived = [&]() {
       return wait_all(&full[ring.st], ring.ph) && (!PAIR || wait_all(&peer[ring.st], ring.ph));
     };
+#pragma unroll 1
     while (W.next()) {
       if (!W.live) continue;
       const int nb = W.blk1 - W.blk0;
@@ -479,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         scores(0);
       }
+#pragma unroll 1
       for (int i = 0; i < nb && !bad; ++i) {
         if (i + 1 < nb) scores(i + 1);
         const uint32_t qi = q + i, buf = qi & 1;
@@ -601,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The next segment with a tile for this CTA.
     auto advance = [&]() {
+#pragma unroll 1
       while (W.next())
         if (W.live) return true;
       return false;
@@ -614,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int up_next = have ? parent_of() : -1;
     if (have) load_q();
     else go_ahead();
+#pragma unroll 1
     while (have) {
       const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
       const int nb = blk1 - blk0, ctx = W.ctx;
@@ -628,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int up = up_next;
         uint64_t m = 1ull << (tid & 63);
         if (tid < kMaxNodes) anc[tid] = m, ups[tid] = up;
+#pragma unroll 1
         for (int step = 0; step < 6; ++step) {
           ptx::named_sync(5, kSoftmaxThreads);
           const uint64_t add = tid < kMaxNodes && up >= 0 ? anc[up] : 0ull;
@@ -647,12 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (A.window > 0) {
           lo = ctx + __popcll(tree_bits) - A.window;  // ctx + depth - window + 1
           uint64_t m = tree_bits;
+#pragma unroll 1
           for (int pos = ctx; m; ++pos, m &= m - 1)  // nodes of the path, root first
             if (pos < lo && pos >= A.n_sink) tree_bits &= ~(m & (0 - m));
         }
       }
 
       float m_run = -INFINITY, l_run = 0.f;  // the row's reference (raw); this half's sum
+#pragma unroll 1
       for (int i = 0; i < nb; ++i) {
         const uint32_t qi = q + i;
         wait(&s_bar[qi & 1], (qi >> 1) & 1);
@@ -678,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // V comes after K of the next block
             const uint32_t v_piece = piece + Y::kPieces * ((i + 1 < nb ? i + 2 : nb) + i);
             constexpr int kWide = Y::kCols / 8, kBy = kOne ? 256 : 128;
+#pragma unroll 1
             for (int idx = tid % kBy; idx < (kUnit - cnt) * kWide; idx += kBy) {
               const int c = idx % kWide, at = (kOne ? 0 : hf * kUnit) + cnt + idx / kWide;
               const uint32_t pc = v_piece + at / Y::kVKeys, st = pc % Y::kStages;
@@ -881,9 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (join && rows <= kFewRows) {
         // few rows, maybe many pieces: four columns of a row per thread, eight
         // pieces in flight
+#pragma unroll 1
         for (int idx = tid; idx < rows * (DH / 4); idx += kSoftmaxThreads) {
           const int rr = idx / (DH / 4), c4 = idx % (DH / 4);
           float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
           for (int g0 = 0; g0 < n_piece; g0 += 8) {
             float mg[8], lg[8];
             float4 og[8];
@@ -931,10 +785,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the others' (all but one, mostly) are read 32 columns at a time
         float top = m2, sum = l_sum, w_own = 1.f;
         if (join) {
+#pragma unroll 1
           for (int g = 0; g < n_piece; ++g)
             if (c_first + g != W.cg) top = fmaxf(top, __ldcg(partial(g) + r));
           const float ref = top == -INFINITY ? 0.f : top;
           w_own = ptx::ex2(m2 - ref), sum = l_sum * w_own;
+#pragma unroll 1
           for (int g = 0; g < n_piece; ++g)
             if (c_first + g != W.cg)
               sum += ptx::ex2(__ldcg(partial(g) + r) - ref) * __ldcg(partial(g) + kRows + r);
@@ -966,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           if (join) {
+#pragma unroll 1
             for (int g = 0; g < n_piece; ++g) {
               const float *pg = partial(g);
               const float mg = c_first + g != W.cg ? __ldcg(pg + r) : -INFINITY;

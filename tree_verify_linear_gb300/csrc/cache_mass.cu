@@ -1,71 +1,319 @@
 // cache_mass.cu -- attention weights per key, gathered over the queries of the
-// accepted path: lbx_attention_mass.
-#include "cache_common.cuh"
+// accepted path, on the tensor cores: lbx_attention_mass.
+//
+//   score[j] += sum over rows r (path node, head of the group) of
+//               exp(scale q_r . k_j - lse_r)
+//
+// The product is taken as S^T = K Q^T: keys are the 128 lanes of tensor memory
+// and the path's queries its columns, so that a thread has all weights of its
+// key and sums them by itself, in row order: no exchange between threads, no
+// maximum (the lse is known), no atomics.  K is read once and the work on it
+// is 2 dh operations per row and key, far below what the tensor cores do in
+// the time a key takes to arrive: the kernel is bound by reading K.
+//
+// The path's nodes are taken root first, so row d G + h belongs to the node of
+// depth d, and the rows that see a key are one range of rows.  Up to 128 rows
+// (256 for head dimensions below 256) are multiplied at a time; longer paths
+// take further passes over the CTA's keys, each added to the same scores by
+// the same threads.  Keys come as blocks of two units (cache_walk.cuh), cut into
+// equal ranges, one per CTA; nothing has to be joined.  Warps 0-3 and 4-7 take
+// the blocks in turn, each with a score buffer of its own; warp 8 issues the
+// MMAs, warp 9 the copies, through a ring of 16 KB pieces (128 keys x 64
+// columns).  Waits are bounded as in the attention kernel.
+#include "cache_ptx.cuh"
+#include "cache_walk.cuh"
 
 namespace lbx {
 namespace cache {
 namespace {
 
-struct Args {
-  lbx_attn_cfg c;
+struct MassArgs {
+  int L, Hq, Hkv, G, n_req, fixed, Bq, N, T, window, n_sink;
+  int cap, stages;  // rows per pass, ring stages
+  float scale_log2;
+  Tiling til;
   const int32_t *ctx_len, *parent, *accepted;
-  const uint16_t *q, *kc, *kt;
+  const uint16_t *q;
   const float *lse;
   float *score, *score_tree;
   int32_t *status;
 };
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 320;
+constexpr int kMaxRows = 256;    // rows per pass
+constexpr int kMaxStages = 13;
+// shared memory after the Q rows and the ring
+constexpr int kTailLse = 0;                              // float [256]
+constexpr int kTailNodes = kTailLse + kMaxRows * 4;      // int [64]
+constexpr int kTailMisc = kTailNodes + kMaxNodes * 4;    // int [4]
+constexpr int kTailBars = kTailMisc + 16;                // full, empty, s[2], free[2], q, end
+constexpr int kTail = kTailBars + (2 * kMaxStages + 6) * 8;
+static_assert(kTail <= 3072, "shared memory");
 
-// One warp per key of a (layer, request, KV head): every query row of the
-// accepted path in turn.
-__global__ void __launch_bounds__(kWarps * 32) mass_keys_kernel(const Args A) {
-  const lbx_attn_cfg &c = A.c;
-  if (batch_bad(c.Bq, c.N, c.T, A.ctx_len, A.parent, A.accepted)) {
-    if (threadIdx.x == 0 && A.status) *A.status = LBX_ETREE;
+// The path from the root to `node` as a bit mask: the warp holds two parents
+// per lane.
+__device__ __forceinline__ uint64_t warp_path(const int32_t *parent, int N, int node, int lane) {
+  const int p0 = lane < N ? parent[lane] : -1, p1 = lane + 32 < N ? parent[lane + 32] : -1;
+  uint64_t m = 0;
+#pragma unroll 1
+  for (int s = 0; s < kMaxNodes && node >= 0; ++s) {
+    m |= 1ull << node;
+    const int a = __shfl_sync(0xffffffffu, p0, node & 31), b = __shfl_sync(0xffffffffu, p1, node & 31);
+    node = node < 32 ? a : b;
+  }
+  return m;
+}
+
+template <int DH, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    mass_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ MassArgs A) {
+  constexpr int kPieces = DH / 64;  // per block of 128 keys
+  extern __shared__ __align__(1024) unsigned char cache_smem[];
+  unsigned char *ring_mem = cache_smem + A.cap * DH * 2, *tail = ring_mem + A.stages * kPiece;
+  float *lse2 = reinterpret_cast<float *>(tail + kTailLse);
+  int *nodes = reinterpret_cast<int *>(tail + kTailNodes);
+  volatile int *misc = reinterpret_cast<volatile int *>(tail + kTailMisc);  // TMEM base, gave up
+  uint64_t *full = reinterpret_cast<uint64_t *>(tail + kTailBars);
+  uint64_t *empty = full + kMaxStages, *s_bar = empty + kMaxStages, *free_bar = s_bar + 2;
+  uint64_t *q_bar = free_bar + 2, *end_bar = q_bar + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (batch_bad(A.Bq, A.N, A.T, A.ctx_len, A.parent, A.accepted)) {
+    if (tid == 0 && A.status) *A.status = LBX_ETREE;
     return;
   }
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, keys = c.T + c.N;
-  const long long lbg = item / keys;
-  if (lbg >= (long long)c.L * c.Bq * c.Hkv) return;
-  const int j = (int)(item % keys), g = (int)(lbg % c.Hkv), G = c.Hq / c.Hkv, per = c.dh / 32;
-  const long long lb = lbg / c.Hkv;
-  const int b = (int)(lb % c.Bq), ctx = A.ctx_len[b];
-  const int32_t *parent = A.parent + (size_t)b * c.N;
-  const uint64_t path = path_mask(parent, A.accepted[b]);
-  const int node = j - c.T;
-  if (node < 0 && j >= ctx) return;
-  if (node >= 0 && !(path >> node & 1)) {
-    if (lane == 0) A.score_tree[lbg * c.N + node] = 0.f;
-    return;
+  if (tid == 0) {
+#pragma unroll 1
+    for (int i = 0; i < 2 * kMaxStages + 6; ++i)
+      ptx::mbar_init(full + i, full + i == q_bar                             ? 8
+                               : full + i == free_bar || full + i == free_bar + 1 ? 4
+                                                                                  : 1);
+    ptx::fence_mbar_init();
+    misc[1] = 0;
   }
-  const int at_k = node < 0 ? j : ctx + __popcll(path & ((2ull << node) - 1)) - 1;
-  const uint16_t *k = node < 0 ? A.kc + (((size_t)lb * c.T + j) * c.Hkv + g) * c.dh
-                               : A.kt + (((size_t)lb * c.N + node) * c.Hkv + g) * c.dh;
-  float kf[8], sum = 0.f;
-  for (int e = 0; e < per; ++e) kf[e] = to_f32(k[lane * per + e], c.dtype);
-  int at = ctx - 1;
-  for (int n = 0; n < c.N; ++n) {
-    if (!(path >> n & 1)) continue;
-    ++at;
-    if (at < at_k || !sees(at, at_k, c.window, c.n_sink)) continue;
-    for (int h = 0; h < G; ++h) {
-      const size_t row = ((size_t)lb * c.N + n) * c.Hq + g * G + h;
-      float s = 0.f;
-      for (int e = 0; e < per; ++e)
-        s = fmaf(to_f32(A.q[row * c.dh + lane * per + e], c.dtype), kf[e], s);
-      for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-      // a query with no finite score (lse = -inf) has no weights to give
-      if (A.lse[row] != -INFINITY) sum += expf(s * c.scale - A.lse[row]);
+  if (warp == 8) {
+    ptx::tmem_alloc(reinterpret_cast<uint32_t *>(tail + kTailMisc), 512);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  Walk<2, 0, MassArgs> W(A, lane);
+  bool bad = false;  // a wait of this thread gave up: it waits no more
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
+    return !bad;
+  };
+  int req = -1;
+  uint64_t path = 0;
+  auto rows_of = [&]() {  // query rows of the walk's request
+    if (W.b != req) {
+      req = W.b;
+      path = warp_path(A.parent + (size_t)req * A.N, A.N, A.accepted[req], lane);
     }
+    return __popcll(path) * A.G;
+  };
+
+  if (warp == 9) {
+    // ---- copies ----
+    int st = 0, loads = 0;
+    uint32_t ph = 0;
+#pragma unroll 1
+    while (W.next()) {
+      const int rows = rows_of(), z = W.l * A.n_req + W.b;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows && lane == 0; r0 += A.cap)
+#pragma unroll 1
+        for (int blk = W.blk0; blk < W.blk1 && !bad; ++blk) {
+          int start[2], cnt;
+          bool tree[2];
+          W.unit(2 * blk, start[0], tree[0], cnt);
+          W.unit(2 * blk + 1, start[1], tree[1], cnt);
+#pragma unroll 1
+          for (int a = 0; a < kPieces; ++a) {
+            if (!wait(&empty[st], ph ^ 1u)) break;
+            ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)kPiece);
+            unsigned char *d = ring_mem + st * kPiece;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              ptx::tma_load_4d(d + u * kUnit * 128, tree[u] ? &maps.kt : &maps.k, a * 64, W.h,
+                               start[u], z, &full[st]);
+            ++loads;
+            if (++st == A.stages) st = 0, ph ^= 1u;
+          }
+        }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      if (bad) misc[1] = 1;
+      // every copy has landed before the CTA may leave
+#pragma unroll 1
+      for (int i = loads > A.stages ? loads - A.stages : 0; i < loads; ++i)
+        (void)ptx::mbar_wait(&full[i % A.stages], (uint32_t)((i / A.stages) & 1));
+    }
+  } else if (warp == 8) {
+    // ---- MMAs: the warp walks and waits as one, one lane issues ----
+    int st = 0;
+    uint32_t ph = 0, seg = 0, used[2] = {0, 0};
+    const bool one = ptx::elect_one();
+    const uint64_t kdesc = ptx::sdesc_sw128(ptx::smem_u32(ring_mem));
+    const uint64_t qdesc = ptx::sdesc_sw128(ptx::smem_u32(cache_smem));
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+      bad = !__all_sync(0xffffffffu, wait(bar, parity));
+      return !bad;
+    };
+#pragma unroll 1
+    while (!bad && W.next()) {
+      const int rows = rows_of();
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows && !bad; r0 += A.cap, ++seg) {
+        const int nr = (rows - r0 < A.cap ? rows - r0 + 31 : A.cap) & ~31;
+        const uint32_t idesc = ptx::idesc_16(F16, 128, nr, false);
+        if (!wait_all(q_bar, seg & 1)) break;
+#pragma unroll 1
+        for (int i = 0; i < W.blk1 - W.blk0 && !bad; ++i) {
+          const int buf = i & 1;
+          if (!wait_all(&free_bar[buf], (used[buf] & 1) ^ 1u)) break;
+#pragma unroll 1
+          for (int a = 0; a < kPieces; ++a) {
+            if (!wait_all(&full[st], ph)) break;
+            ptx::tc_fence_after();
+            const uint64_t kd = kdesc + (uint64_t)(st * (kPiece >> 4));
+            const uint64_t qd = qdesc + (uint64_t)(a * A.cap * (128 >> 4));
+            if (one) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                ptx::mma_bf16_ss(tmem + buf * 256, kd + 2 * s, qd + 2 * s, idesc,
+                                 a + s > 0 ? 1u : 0u);
+              ptx::mma_commit(&empty[st]);
+              if (a == kPieces - 1) ptx::mma_commit(&s_bar[buf]);
+            }
+            __syncwarp();
+            if (++st == A.stages) st = 0, ph ^= 1u;
+          }
+          ++used[buf];
+        }
+      }
+    }
+    if (one) {
+      if (bad) misc[1] = 1;
+      ptx::mma_commit(end_bar);
+      (void)ptx::mbar_wait(end_bar, 0);
+    }
+  } else {
+    // ---- Q rows in, weights out ----
+    const int wg = warp >> 2;
+    const int key = (warp & 3) * 32 + lane;  // of a block: its lane of tensor memory
+    const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * 256;
+    uint32_t used = 0;
+#pragma unroll 1
+    while (W.next()) {
+      const int rows = rows_of(), len = rows / A.G;
+      const size_t lb = (size_t)W.l * A.n_req + W.b, lbg = lb * A.Hkv + W.h;
+      if (tid < kMaxNodes && (path >> tid & 1))
+        nodes[__popcll(path & ((1ull << tid) - 1))] = tid;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += A.cap) {
+        const int in = rows - r0 < A.cap ? rows - r0 : A.cap, nr = (in + 31) & ~31;
+        ptx::named_sync(5, 256);  // nodes are listed; the last pass is done everywhere
+        constexpr int kPer = DH / 8;  // 16-byte pieces per row
+        auto query = [&](int r) {  // row r of the pass among all queries
+          const int d = (r0 + r) / A.G;
+          return (lb * A.N + nodes[d]) * A.Hq + W.h * A.G + (r0 + r - d * A.G);
+        };
+#pragma unroll 4
+        for (int i = tid; i < nr * kPer; i += 256) {
+          const int r = i / kPer, c = i % kPer;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (r < in) v = reinterpret_cast<const uint4 *>(A.q)[query(r) * kPer + c];
+          *reinterpret_cast<uint4 *>(cache_smem + (c / 8) * A.cap * 128 + r * 128 +
+                                     ((c & 7) ^ (r & 7)) * 16) = v;
+        }
+        if (tid < nr) {
+          // rows past the last, and those without a finite score, weigh nothing
+          const float z = tid < in ? A.lse[query(tid)] : -INFINITY;
+          lse2[tid] = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;
+        }
+        ptx::fence_proxy_async();
+        ptx::named_sync(5, 256);
+        if (lane == 0) ptx::mbar_arrive(q_bar);
+
+#pragma unroll 1
+        for (int i = wg; i < W.blk1 - W.blk0; i += 2) {
+          int start, cnt;
+          bool tree;
+          W.unit(2 * (W.blk0 + i) + (key >> 6), start, tree, cnt);
+          const int off = key & 63;
+          // the range of rows that see the key, and where its sum goes
+          int lo = 0, hi = rows;
+          float *to = nullptr;
+          if (off < cnt && !tree) {
+            const int j = start + off;
+            if (A.window > 0 && j >= A.n_sink) {
+              const int d = A.window - W.ctx + j;  // depths below see it
+              hi = d >= len ? rows : d > 0 ? d * A.G : 0;
+            }
+            to = A.score + lbg * A.T + j;
+          } else if (off < cnt) {
+            const int d = __popcll(path & ((2ull << off) - 1)) - 1;
+            lo = d * A.G;
+            if (A.window > 0 && W.ctx + d >= A.n_sink && d + A.window < len)
+              hi = (d + A.window) * A.G;
+            if (!(path >> off & 1)) hi = 0;
+            to = A.score_tree + lbg * A.N + off;
+          }
+          const bool add = to && (!tree || r0 > 0);
+          const float before = add ? *to : 0.f;
+          lo -= r0, hi -= r0;
+          wait(&s_bar[wg], used & 1);
+          ++used;
+          ptx::tc_fence_after();
+          const bool all = __all_sync(0xffffffffu, !to || (lo <= 0 && hi >= in));
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int c = 0; c < nr; c += 32) {
+            float s[32];
+            ptx::tmem_ld32(tq + c, s);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = ptx::ex2(fmaf(s[e], A.scale_log2, -lse2[c + e]));
+            if (!all) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e < lo || c + e >= hi) s[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sum[e & 3] += s[e];
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&free_bar[wg]);
+          if (to && !bad) *to = before + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        }
+      }
+      ptx::named_sync(5, 256);  // nodes and lse are read
+    }
+    if (bad) misc[1] = 1;
   }
-  if (lane == 0) {
-    if (node < 0)
-      A.score[lbg * c.T + j] += sum;
-    else
-      A.score_tree[lbg * c.N + node] = sum;
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && misc[1] && A.status) *A.status = LBX_ETIMEOUT;
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
   }
+}
+
+template <int DH>
+cudaError_t launch_mass(bool f16, const AttnMaps &maps, const MassArgs &A, int grid, int bytes,
+                        cudaStream_t stream) {
+  auto kernel = f16 ? mass_kernel<DH, true> : mass_kernel<DH, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)grid, kThreads, (size_t)bytes, stream>>>(maps, A);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -84,11 +332,32 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
       !aligned_to(score_tree, 4) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
   if (c->T > 0 && (!aligned_to(k_cache, 16) || !aligned_to(score, 4))) return LBX_EINVAL;
-  const Args A = {*c,      ctx_len, parent, accepted,   q,       k_cache,
-                  k_tree,  lse,     score,  score_tree, d_status};
-  const long long items = (long long)c->L * c->Bq * c->Hkv * (c->T + c->N);
-  const long long blocks = (items + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffLL) return LBX_EINVAL;
-  mass_keys_kernel<<<(unsigned)blocks, kWarps * 32, 0, stream>>>(A);
-  return cudaGetLastError() == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  const int lists = c->L * c->Bq, G = c->Hq / c->Hkv;
+  // the block list's indexes are 32-bit
+  if ((long long)lists * c->Hkv >= (1LL << 31) / (c->T / kUnit + 3)) return LBX_EINVAL;
+  const int grid = grid_limit();
+  if (grid < 1) return LBX_ECUDA;
+  AttnMaps maps = {};
+  if (!encode_list(&maps.kt, k_tree, c, c->N, lists, kUnit)) return LBX_ECUDA;
+  maps.k = maps.kt;  // without a cache: never read
+  if (c->T > 0 && !encode_list(&maps.k, k_cache, c, c->T, lists, kUnit)) return LBX_ECUDA;
+  MassArgs A = {};
+  A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = G, A.n_req = c->Bq;
+  A.Bq = c->Bq, A.N = c->N, A.T = c->T, A.window = c->window, A.n_sink = c->n_sink;
+  A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.til = {c->N * G, 1, 1, 1, 1};
+  A.ctx_len = ctx_len, A.parent = parent, A.accepted = accepted, A.q = q, A.lse = lse;
+  A.score = score, A.score_tree = score_tree, A.status = d_status;
+  // 64 KB of Q rows at most; the ring takes what they leave
+  const int most = c->dh == 256 ? 128 : kMaxRows;
+  A.cap = c->N * G < most ? (c->N * G + 31) & ~31 : most;
+  const int q_bytes = A.cap * c->dh * 2;
+  A.stages = (227 * 1024 - kTail - q_bytes) / kPiece;
+  if (A.stages > kMaxStages) A.stages = kMaxStages;
+  const int bytes = q_bytes + A.stages * kPiece + kTail;
+  const bool f16 = c->dtype == LBX_F16;
+  const cudaError_t e = c->dh == 64    ? launch_mass<64>(f16, maps, A, grid, bytes, stream)
+                        : c->dh == 128 ? launch_mass<128>(f16, maps, A, grid, bytes, stream)
+                                       : launch_mass<256>(f16, maps, A, grid, bytes, stream);
+  return e == cudaSuccess ? LBX_OK : LBX_ECUDA;
 }
