@@ -193,7 +193,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::named_sync(6, kSoftmaxThreads + 32);
 #pragma unroll 1
     while (W.next()) {
-      if (!W.live || lane != 0) continue;
+      if (!W.live) continue;
+      // the segment's queries into L2, ahead of its keys: loads of them would
+      // wait for all the copies in flight
+#pragma unroll 1
+      for (int rr = lane; rr < kRows; rr += 32) {
+        const int row = (W.tile * Y::kCtas + rank) * kRows + rr, node = row / A.G;
+        if (row >= A.til.rows) break;
+        const size_t at = (((size_t)W.l * A.n_req + W.b) * A.nodes + node) * A.Hq + W.h * A.G +
+                          (row - node * A.G);
+#pragma unroll
+        for (int i = 0; i < DH * 2; i += 128)
+          ptx::prefetch_line(reinterpret_cast<const char *>(A.q + at * DH) + i);
+      }
+      if (lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
       const int z = A.fixed > 0 ? W.l : W.l * A.n_req + W.b;
       auto take = [&]() -> unsigned char * {

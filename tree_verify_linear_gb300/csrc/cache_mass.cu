@@ -122,6 +122,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     while (W.next()) {
       const int rows = rows_of(), z = W.l * A.n_req + W.b;
+      // the segment's queries into L2, ahead of its keys: loads of them would
+      // wait for all the copies in flight
+#pragma unroll 1
+      for (uint64_t m = path; m; m &= m - 1) {
+        const size_t at = ((size_t)z * A.N + (__ffsll((long long)m) - 1)) * A.Hq + W.h * A.G;
+        const char *line = reinterpret_cast<const char *>(A.q + at * DH);
+#pragma unroll 1
+        for (int i = lane * 128; i < A.G * DH * 2; i += 32 * 128) ptx::prefetch_line(line + i);
+        if (lane == 0) ptx::prefetch_line(A.lse + at);
+      }
 #pragma unroll 1
       for (int r0 = 0; r0 < rows && lane == 0; r0 += A.cap)
 #pragma unroll 1
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int d = (r0 + r) / A.G;
           return (lb * A.N + nodes[d]) * A.Hq + W.h * A.G + (r0 + r - d * A.G);
         };
-#pragma unroll 4
+#pragma unroll 8
         for (int i = tid; i < nr * kPer; i += 256) {
           const int r = i / kPer, c = i % kPer;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -271,20 +281,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           const bool all = __all_sync(0xffffffffu, !to || (lo <= 0 && hi >= in));
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int c = 0; c < nr; c += 32) {
-            float s[32];
-            ptx::tmem_ld32(tq + c, s);
-            ptx::tmem_wait_ld();
+          // 32 columns at a time, the next ones on their way meanwhile
+          auto weigh = [&](const float(&s)[32], int c) {
+            float p[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = ptx::ex2(fmaf(s[e], A.scale_log2, -lse2[c + e]));
+            for (int e = 0; e < 32; e += 4) {
+              const float4 z = *reinterpret_cast<const float4 *>(lse2 + c + e);
+              p[e] = ptx::ex2(fmaf(s[e], A.scale_log2, -z.x));
+              p[e + 1] = ptx::ex2(fmaf(s[e + 1], A.scale_log2, -z.y));
+              p[e + 2] = ptx::ex2(fmaf(s[e + 2], A.scale_log2, -z.z));
+              p[e + 3] = ptx::ex2(fmaf(s[e + 3], A.scale_log2, -z.w));
+            }
             if (!all) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (c + e < lo || c + e >= hi) s[e] = 0.f;
+                if (c + e < lo || c + e >= hi) p[e] = 0.f;
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sum[e & 3] += s[e];
+            for (int e = 0; e < 32; ++e) sum[e & 3] += p[e];
+          };
+          float s0[32], s1[32];
+          ptx::tmem_ld32(tq, s0);
+#pragma unroll 1
+          for (int c = 0; c < nr; c += 64) {
+            ptx::tmem_wait_ld();
+            if (c + 32 < nr) ptx::tmem_ld32(tq + c + 32, s1);
+            weigh(s0, c);
+            if (c + 32 < nr) {
+              ptx::tmem_wait_ld();
+              if (c + 64 < nr) ptx::tmem_ld32(tq + c + 64, s0);
+              weigh(s1, c + 32);
+            }
           }
           ptx::tc_fence_before();
           __syncwarp();
