@@ -91,7 +91,8 @@ bool list_ok(const lbx_attn_cfg *c, const Space &s) {
   auto fits = [&](const Tiling &t, long long lists, long long len) {
     return lists * t.sets < (1LL << 31) / (len / kUnit + 3);
   };
-  const long long lists = (long long)c->L * c->Hkv;
+  const long long lists = (long long)c->L * c->Hkv, G = c->Hq / c->Hkv;
+  if ((long long)c->Bq * c->N * G >= (1LL << 32) / G) return false;  // see PerGroup
   return fits(s.own, lists * c->Bq, c->T) && fits(s.pre, lists, c->P);
 }
 
@@ -122,6 +123,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = c->Hq / c->Hkv;
   A.Bq = c->Bq, A.N = c->N, A.T = c->T;
   A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.per = per_group(A.G);
   A.ctx_len = ctx_len, A.parent = parent, A.q = q, A.status = status;
   A.part = reinterpret_cast<float *>(base);
   const bool f16 = c->dtype == LBX_F16;

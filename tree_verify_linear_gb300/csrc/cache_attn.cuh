@@ -54,7 +54,6 @@ namespace lbx {
 namespace cache {
 
 constexpr int kSoftmaxThreads = 256;
-constexpr int kThreads = kSoftmaxThreads + 64;
 
 // Floats of one partial: m (base 2) and l per row, then O.
 constexpr size_t part_floats(int dh) { return 2 * (size_t)kRows + (size_t)kRows * dh; }
@@ -67,6 +66,7 @@ struct AttnArgs {
   int Bq, N, T;   // of the batch (its check, the trees)
   int window, n_sink;
   float scale_log2;
+  PerGroup per;
   Tiling til;
   const int32_t *ctx_len, *parent;
   const uint16_t *q;
@@ -84,6 +84,8 @@ struct Lay {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr bool kQTmem = !PAIR;
   static constexpr int kBlkUnits = DH == 256 && !PAIR ? 1 : 2;  // units per block
+  static constexpr int kLoaders = PAIR ? 64 : kSoftmaxThreads;   // threads that bring Q
+  static constexpr int kThreads = kSoftmaxThreads + (PAIR ? 128 : 64);
   static constexpr int kBlk = kBlkUnits * kUnit;                 // keys per block
   static constexpr int kMine = kBlk / 2;                         // keys per softmax thread
   // what one CTA holds of a block: kKeys keys of K, kCols columns of V
@@ -105,7 +107,8 @@ struct Lay {
   static constexpr int kSmemAnc = kSmemRed + 4 * kRows * 4;      // uint64 [64]
   static constexpr int kSmemMisc = kSmemAnc + kMaxNodes * 8;     // int [8]
   static constexpr int kSmemBars = kSmemMisc + 32;
-  static constexpr int kNBars = 3 * kStages + 8;  // full, empty, peer, s[2], p[2], o[2], q, end
+  // full, empty, peer (of a pair), s[2], p[2], o[2], lo[2], q, q free, end
+  static constexpr int kNBars = (PAIR ? 3 : 2) * kStages + 11;
   static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
   static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0, "shared memory");
 
@@ -136,7 +139,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 template <int DH, bool F16, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     cache_attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnArgs A) {
   using Y = Lay<DH, PAIR>;
   extern __shared__ __align__(1024) unsigned char cache_smem[];
@@ -148,8 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *misc = reinterpret_cast<volatile int *>(smem + Y::kSmemMisc);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + Y::kSmemBars);
   uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
-  uint64_t *s_bar = peer + Y::kStages, *p_bar = s_bar + 2;
-  uint64_t *o_bar = p_bar + 2, *q_bar = o_bar + 2, *end_bar = q_bar + 1;
+  uint64_t *s_bar = peer + (PAIR ? Y::kStages : 0), *p_bar = s_bar + 2;
+  uint64_t *o_bar = p_bar + 2, *lo_bar = o_bar + 2, *q_bar = lo_bar + 2, *qf_bar = q_bar + 1;
+  uint64_t *end_bar = qf_bar + 1;
 
   if (batch_bad(A.Bq, A.N, A.T, A.ctx_len, A.parent, nullptr)) {
     if (tid == 0 && A.status) *A.status = LBX_ETREE;
@@ -157,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < Y::kNBars; ++i)
-      ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1 || full + i == q_bar
+      ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1
                                    ? Y::kCtas * kSoftmaxThreads / 32
-                                   : 1);
+                               : full + i == q_bar ? Y::kCtas * Y::kLoaders / 32
+                                                   : 1);
     ptx::fence_mbar_init();
     misc[2] = 0;
   }
@@ -185,27 +190,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
     return !bad;
   };
+  // One arrival of this warp on a barrier of the CTA that issues the MMAs.
+  auto tell = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (PAIR) ptx::mbar_arrive_at(bar, 0);
+      else ptx::mbar_arrive(bar);
+    }
+  };
+  // Query rows of the walk's tile from this CTA's first on.
+  auto first_row = [&]() { return (W.tile * Y::kCtas + rank) * kRows; };
+  // The place of a row of the stream among all queries: of its first one, and
+  // of the row from there.
+  auto queries = [&](int l, int b, int h) {
+    return (size_t)(l * A.n_req + b) * A.nodes * A.Hq + h * A.G;
+  };
+  auto query_of = [&](int row) { return row + A.per.node(row) * (A.Hq - A.G); };
+  // The segment's queries into L2, ahead of its keys: loads of them would wait
+  // for all the copies in flight.
+  // A prefix's results that the segment will be joined with, too.
+  // A prefix's results that the segment will be joined with, too.  One warp.
+  auto prefetch_q = [&]() {
+    const int row = first_row(), rows = A.til.rows - row < kRows ? A.til.rows - row : kRows;
+    if (rows <= 0) return;
+    const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
+#pragma unroll 1
+    for (int n = A.per.node(row) + lane; n <= A.per.node(row + rows - 1); n += 32)
+      ptx::prefetch_bytes(q0 + (size_t)n * A.Hq * DH, (uint32_t)(A.G * DH * 2));
+    if (A.x_o) {
+      const size_t rows_all = (size_t)A.n_req * A.til.rows;
+      const float4 *x0 = reinterpret_cast<const float4 *>(A.x_o) +
+                         (size_t)(W.l * A.Hkv + W.h) * rows_all * (DH / 4) +
+                         (size_t)W.b * A.til.rows + row;
+#pragma unroll 1
+      for (int c = lane; c < DH / 4; c += 32)
+        ptx::prefetch_bytes(x0 + c * rows_all, (uint32_t)(rows * 16));
+    }
+  };
+  // The next segment with a tile for this CTA.
+  auto advance = [&]() {
+#pragma unroll 1
+    while (W.next())
+      if (W.live) return true;
+    return false;
+  };
+
   if (warp == 9) {
     // ---- copies ----
     Ring<Y::kStages> ring;
     int loads = 0;
-    // behind the first Q tile's loads, which would wait for all of these
-    ptx::named_sync(6, kSoftmaxThreads + 32);
+    // behind the first Q tile's loads or prefetches
+    ptx::named_sync(6, Y::kLoaders + 32);
 #pragma unroll 1
-    while (W.next()) {
-      if (!W.live) continue;
-      // the segment's queries into L2, ahead of its keys: loads of them would
-      // wait for all the copies in flight
-#pragma unroll 1
-      for (int rr = lane; rr < kRows; rr += 32) {
-        const int row = (W.tile * Y::kCtas + rank) * kRows + rr, node = row / A.G;
-        if (row >= A.til.rows) break;
-        const size_t at = (((size_t)W.l * A.n_req + W.b) * A.nodes + node) * A.Hq + W.h * A.G +
-                          (row - node * A.G);
-#pragma unroll
-        for (int i = 0; i < DH * 2; i += 128)
-          ptx::prefetch_line(reinterpret_cast<const char *>(A.q + at * DH) + i);
-      }
+    while (advance()) {
+      if (!PAIR) prefetch_q();
       if (lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
       const int z = A.fixed > 0 ? W.l : W.l * A.n_req + W.b;
@@ -265,6 +303,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = loads > Y::kStages ? loads - Y::kStages : 0; i < loads; ++i)
         (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
     }
+  } else if (PAIR && warp >= 10) {
+    // ---- Q rows of a pair, swizzled into shared memory, 16 bytes per lane ----
+    constexpr int kPer = DH / 8, kStep = 64 / kPer, kBatch = 8;  // rows per load, loads in flight
+    const int c = (tid & 63) % kPer, r0 = (tid & 63) / kPer;
+    bool ahead = true;
+    uint32_t seg = 0;
+#pragma unroll 1
+    for (bool have = advance(); have || ahead; have = advance(), ++seg) {
+      if (have && warp == 10) prefetch_q();
+      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
+      ahead = false;
+      if (!have) break;
+      const uint4 *q0 = reinterpret_cast<const uint4 *>(A.q) + queries(W.l, W.b, W.h) * kPer;
+      // the last segment's score products are done
+      if (seg > 0 && !wait(qf_bar, (seg - 1) & 1)) break;
+#pragma unroll 1
+      for (int b0 = r0; b0 < kRows; b0 += kBatch * kStep) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int row = first_row() + b0 + e * kStep;
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (row < A.til.rows) v[e] = q0[(size_t)query_of(row) * kPer + c];
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int rr = b0 + e * kStep;
+          *reinterpret_cast<uint4 *>(smem + Y::kSmemQ + (c / 8) * kRows * 128 + rr * 128 +
+                                     ((c & 7) ^ (rr & 7)) * 16) = v[e];
+        }
+      }
+      ptx::fence_proxy_async();
+      ptx::fence_cluster();
+      tell(q_bar);
+    }
+    if (bad) misc[2] = 1;
   } else if (warp == 8 && rank == 1) {
     // ---- the follower tells the leader of each piece that has landed ----
     Ring<Y::kStages> ring;
@@ -304,33 +378,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (W.next()) {
       if (!W.live) continue;
       const int nb = W.blk1 - W.blk0;
-      // S of block i into buffer (q + i) & 1
+      // S of block i into buffer (q + i) & 1, once the buffer's last P has been
+      // multiplied (the first two blocks find it free).  A pair takes the keys in
+      // two halves, the upper half of each CTA's first: its columns held the lo
+      // part of P, which is multiplied first (or nothing, in f16), so that they
+      // are free while the hi part keeps the tensor cores busy.
+      constexpr int kHalves = PAIR ? 2 : 1;
       auto scores = [&](int i) {
-        const uint32_t qi = q + i, buf = qi & 1;
-        // the buffer's last P has been multiplied (the first two find it free)
-        if (!wait_all(&o_bar[buf], ((qi >> 1) & 1) ^ 1u)) return;
-        constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, Y::kBlk, false);
-        const uint32_t d = tmem + Y::kColS + buf * Y::kBlk;
+        const uint32_t qi = q + i, buf = qi & 1, last = ((qi >> 1) & 1) ^ 1u;
+        constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, Y::kBlk / kHalves, false);
+        const Ring<Y::kStages> ring0 = ring;
 #pragma unroll
-        for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
-          if (!arrived()) return;
-          ptx::tc_fence_after();
-          const uint64_t kd = kdesc + (uint64_t)(ring.st * (kPiece >> 4));
-          if (one) {
+        for (int half = kHalves - 1; half >= 0; --half) {
+          if (half == 1 ? !F16 && !wait_all(&lo_bar[buf], last) : !wait_all(&o_bar[buf], last))
+            return;
+          const uint32_t d = tmem + Y::kColS + buf * Y::kBlk + half * 64;
+          ring = ring0;
 #pragma unroll
-            for (int s = 0; s < 4 * Y::kKAtoms; ++s) {
-              const int step = p * 4 * Y::kKAtoms + s;  // 16 columns of Q and K
-              const uint64_t kb = kd + (uint64_t)((s >> 2) * Y::kKAtom >> 4) + 2 * (s & 3);
-              const uint64_t qa =
-                  qdesc + (uint64_t)((step >> 2) * kRows * 128 >> 4) + 2 * (step & 3);
-              const uint32_t acc = step > 0 ? 1u : 0u;
-              if constexpr (PAIR) ptx::mma_16_ss_pair(d, qa, kb, idesc, acc);
-              else ptx::mma_bf16_ts(d, tmem + Y::kColQ + 8u * step, kb, idesc, acc);
+          for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+            if (half == kHalves - 1 && !arrived()) return;
+            ptx::tc_fence_after();
+            const uint64_t kd =
+                kdesc + (uint64_t)(ring.st * (kPiece >> 4)) + half * (32 * 128 >> 4);
+            if (one) {
+#pragma unroll
+              for (int s = 0; s < 4 * Y::kKAtoms; ++s) {
+                const int step = p * 4 * Y::kKAtoms + s;  // 16 columns of Q and K
+                const uint64_t kb = kd + (uint64_t)((s >> 2) * Y::kKAtom >> 4) + 2 * (s & 3);
+                const uint64_t qa =
+                    qdesc + (uint64_t)((step >> 2) * kRows * 128 >> 4) + 2 * (step & 3);
+                const uint32_t acc = step > 0 ? 1u : 0u;
+                if constexpr (PAIR) ptx::mma_16_ss_pair(d, qa, kb, idesc, acc);
+                else ptx::mma_bf16_ts(d, tmem + Y::kColQ + 8u * step, kb, idesc, acc);
+              }
+              if (half == 0) {
+                commit(&empty[ring.st]);
+                if (p == Y::kPieces - 1) {
+                  commit(&s_bar[buf]);
+                  if (PAIR && i == nb - 1) commit(qf_bar);
+                }
+              }
             }
-            commit(&empty[ring.st]);
-            if (p == Y::kPieces - 1) commit(&s_bar[buf]);
+            __syncwarp();
           }
-          __syncwarp();
         }
       };
       if (wait_all(q_bar, seg & 1)) {
@@ -346,27 +436,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc = ptx::idesc_16(F16, kRows * Y::kCtas, DH, true);
         const uint32_t pc = tmem + Y::kColS + buf * Y::kBlk;
         const uint32_t later = i > 0 ? 1u : 0u;
+        const Ring<Y::kStages> ring0 = ring;
 #pragma unroll
-        for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
-          if (!arrived()) break;
-          ptx::tc_fence_after();
-          const uint64_t vd = vdesc + (uint64_t)(ring.st * (kPiece >> 4));
-          if (one) {
+        for (int part = kParts<F16> - 1; part >= 0; --part) {
+          ring = ring0;
 #pragma unroll
-            for (int part = 0; part < kParts<F16>; ++part)
+          for (int p = 0; p < Y::kPieces; ++p, ring.step()) {
+            if (part == kParts<F16> - 1 && !arrived()) break;
+            ptx::tc_fence_after();
+            const uint64_t vd = vdesc + (uint64_t)(ring.st * (kPiece >> 4));
+            if (one) {
 #pragma unroll
               for (int s = 0; s < Y::kVKeys / 16; ++s) {
                 const uint32_t pa =
                     pc + (uint32_t)(part * Y::kBlk / 2 + p * Y::kVKeys / 2 + s * 8);
                 const uint64_t vb = vd + (uint64_t)(s * 2048 >> 4);
-                const uint32_t acc = p + part + s > 0 ? 1u : later;
+                const uint32_t acc = part < kParts<F16> - 1 || p + s > 0 ? 1u : later;
                 if constexpr (PAIR) ptx::mma_16_ts_pair(tmem + Y::kColO, pa, vb, idesc, acc);
                 else ptx::mma_bf16_ts(tmem + Y::kColO, pa, vb, idesc, acc);
               }
-            commit(&empty[ring.st]);
-            if (p == Y::kPieces - 1) commit(&o_bar[buf]);
+              if (part == 0) commit(&empty[ring.st]);
+              if (p == Y::kPieces - 1) {
+                if (part == 0) commit(&o_bar[buf]);
+                else if (PAIR) commit(&lo_bar[buf]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (bad) break;
         }
       }
       q += nb;
@@ -388,132 +485,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t q = 0, piece = 0;  // blocks and ring pieces so far
     int req = -1;
 
-    // One arrival of this warp on a barrier of the CTA that issues the MMAs.
-    auto tell = [&](uint64_t *bar) {
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) ptx::mbar_arrive_at(bar, 0);
-        else ptx::mbar_arrive(bar);
-      }
-    };
-    // Query rows of the walk's tile from this CTA's first on.
-    auto first_row = [&]() { return (W.tile * Y::kCtas + rank) * kRows; };
-    // The walk's place of a row of the stream among all queries.
-    auto query_of = [&](int row) {
-      const int node = row / A.G;
-      return (((size_t)W.l * A.n_req + W.b) * A.nodes + node) * A.Hq + W.h * A.G +
-             (row - node * A.G);
-    };
-    // The Q tile of the walk's segment, rows past the stream's zero; its loads
-    // go ahead of the first copies of K and V.
-    bool ahead = true;
+    // Without a pair: the Q tile of the walk's segment into tensor memory, half a
+    // row per thread, pairs along dh, rows past the stream's zero.  The first
+    // tile's loads go ahead of the first copies of K and V.
+    bool ahead = !PAIR;
     auto go_ahead = [&]() {
-      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(kSoftmaxThreads + 32) : "memory");
+      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
       ahead = false;
     };
     auto load_q = [&]() {
       constexpr int kPer = DH / 8;  // 16-byte pieces per row
-      const uint4 *qg = reinterpret_cast<const uint4 *>(A.q);
-      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (Y::kQTmem) {  // half a row per thread, pairs along dh
-        const int row = first_row() + r;
-        const bool in = row < A.til.rows;
-        const uint4 *from = qg + (in ? query_of(row) * kPer + hf * (kPer / 2) : 0);
-        constexpr int kC = DH / 4 < 32 ? DH / 4 : 32;  // columns per store
-        uint4 v[DH / 16];
+      const int row = first_row() + r;
+      const bool in = row < A.til.rows;
+      const uint4 *from = reinterpret_cast<const uint4 *>(A.q);
+      if (in) from += (queries(W.l, W.b, W.h) + query_of(row)) * kPer + hf * (kPer / 2);
+      constexpr int kC = DH / 4 < 32 ? DH / 4 : 32;  // columns per store
+      uint4 v[DH / 16];
 #pragma unroll
-        for (int e = 0; e < DH / 16; ++e) v[e] = in ? from[e] : none;
-        go_ahead();
+      for (int e = 0; e < DH / 16; ++e) v[e] = in ? from[e] : make_uint4(0u, 0u, 0u, 0u);
+      go_ahead();
 #pragma unroll
-        for (int c = 0; c < DH / 4; c += kC) {
-          uint32_t w[kC];
+      for (int c = 0; c < DH / 4; c += kC) {
+        uint32_t w[kC];
 #pragma unroll
-          for (int e = 0; e < kC / 4; ++e) {
-            const uint4 f = v[c / 4 + e];
-            w[4 * e] = f.x, w[4 * e + 1] = f.y, w[4 * e + 2] = f.z, w[4 * e + 3] = f.w;
-          }
-          if constexpr (kC == 32) ptx::tmem_st32(tq + Y::kColQ + hf * (DH / 4) + c, w);
-          else ptx::tmem_st16(tq + Y::kColQ + hf * (DH / 4) + c, w);
+        for (int e = 0; e < kC / 4; ++e) {
+          const uint4 f = v[c / 4 + e];
+          w[4 * e] = f.x, w[4 * e + 1] = f.y, w[4 * e + 2] = f.z, w[4 * e + 3] = f.w;
         }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-      } else {  // swizzled in shared memory, 16 bytes per lane
-        constexpr int kStep = kSoftmaxThreads / kPer, kLoads = kRows / kStep;
-        const int c = tid % kPer, r0 = tid / kPer;
-        uint4 v[kLoads];
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int row = first_row() + r0 + e * kStep;
-          v[e] = row < A.til.rows ? qg[query_of(row) * kPer + c] : none;
-        }
-        go_ahead();
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int rr = r0 + e * kStep;
-          *reinterpret_cast<uint4 *>(smem + Y::kSmemQ + (c / 8) * kRows * 128 + rr * 128 +
-                                     ((c & 7) ^ (rr & 7)) * 16) = v[e];
-        }
-        ptx::fence_proxy_async();
-        if constexpr (PAIR) ptx::fence_cluster();
+        if constexpr (kC == 32) ptx::tmem_st32(tq + Y::kColQ + hf * (DH / 4) + c, w);
+        else ptx::tmem_st16(tq + Y::kColQ + hf * (DH / 4) + c, w);
       }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
       tell(q_bar);
     };
-    // The next segment with a tile for this CTA.
-    auto advance = [&]() {
+    // What this row sees in the walk's segment: of the tree as bits, of the cache
+    // from a position on.  The masks of the request's tree, by doubling, are one
+    // warp's work.
+    uint64_t next_bits = 0;
+    int next_lo = 0;
+    auto look = [&]() {
+      if (A.fixed > 0) return;
+      if (W.b != req) {
+        req = W.b;
+        if (warp == 0) {
+          const int32_t *parent = A.parent + (size_t)req * A.N;
+          int up[2] = {lane < A.N ? parent[lane] : -1, lane + 32 < A.N ? parent[lane + 32] : -1};
+          uint64_t m[2] = {1ull << lane, 1ull << (lane + 32)};
 #pragma unroll 1
-      while (W.next())
-        if (W.live) return true;
-      return false;
+          for (int step = 0; step < 6; ++step) {
+            uint64_t add[2];
+            int to[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int a = up[e] & 31;
+              const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], a);
+              const uint64_t m1 = __shfl_sync(0xffffffffu, m[1], a);
+              const int u0 = __shfl_sync(0xffffffffu, up[0], a);
+              const int u1 = __shfl_sync(0xffffffffu, up[1], a);
+              add[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
+              to[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+            }
+            m[0] |= add[0], m[1] |= add[1], up[0] = to[0], up[1] = to[1];
+          }
+          anc[lane] = m[0], anc[lane + 32] = m[1];
+        }
+        ptx::named_sync(5, kSoftmaxThreads);
+      }
+      const int row = first_row() + r;
+      next_bits = 0, next_lo = 0;
+      if (row < A.til.rows) {
+        next_bits = anc[A.per.node(row)];
+        if (A.window > 0) {
+          next_lo = W.ctx + __popcll(next_bits) - A.window;  // ctx + depth - window + 1
+          uint64_t m = next_bits;
+#pragma unroll 1
+          for (int pos = W.ctx; m; ++pos, m &= m - 1)  // nodes of the path, root first
+            if (pos < next_lo && pos >= A.n_sink) next_bits &= ~(m & (0 - m));
+        }
+      }
     };
 
     bool have = advance();
-    // this thread's node's parent in the walk's request, ahead of its use
-    auto parent_of = [&]() {
-      return A.fixed <= 0 && tid < A.N ? A.parent[(size_t)W.b * A.N + tid] : -1;
-    };
-    int up_next = have ? parent_of() : -1;
-    if (have) load_q();
-    else go_ahead();
+    if (have) {
+      if constexpr (!PAIR) load_q();
+      look();
+    } else {
+      go_ahead();
+    }
 #pragma unroll 1
     while (have) {
       const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
-      const int nb = blk1 - blk0, ctx = W.ctx;
+      const int nb = blk1 - blk0;
       const int first = W.first;
       const int row0 = first_row(), row = row0 + r;
       const bool real = row < A.til.rows;
       const bool busy = row0 + quad * 32 < A.til.rows;  // the warp has rows
-      const int node = real ? row / A.G : 0;
-      // ancestor masks of the request's tree, by doubling
-      if (A.fixed <= 0 && b != req) {
-        int *ups = reinterpret_cast<int *>(red);  // not in use between segments
-        int up = up_next;
-        uint64_t m = 1ull << (tid & 63);
-        if (tid < kMaxNodes) anc[tid] = m, ups[tid] = up;
-#pragma unroll 1
-        for (int step = 0; step < 6; ++step) {
-          ptx::named_sync(5, kSoftmaxThreads);
-          const uint64_t add = tid < kMaxNodes && up >= 0 ? anc[up] : 0ull;
-          const int next_up = tid < kMaxNodes && up >= 0 ? ups[up] : -1;
-          ptx::named_sync(5, kSoftmaxThreads);
-          m |= add, up = next_up;
-          if (tid < kMaxNodes) anc[tid] = m, ups[tid] = up;
-        }
-        ptx::named_sync(5, kSoftmaxThreads);
-        req = b;
-      }
-      // what this row sees: of the tree as bits, of the cache from lo on
-      uint64_t tree_bits = 0;
-      int lo = 0;
-      if (A.fixed <= 0 && real) {
-        tree_bits = anc[node];
-        if (A.window > 0) {
-          lo = ctx + __popcll(tree_bits) - A.window;  // ctx + depth - window + 1
-          uint64_t m = tree_bits;
-#pragma unroll 1
-          for (int pos = ctx; m; ++pos, m &= m - 1)  // nodes of the path, root first
-            if (pos < lo && pos >= A.n_sink) tree_bits &= ~(m & (0 - m));
-        }
-      }
+      const uint64_t tree_bits = next_bits;
+      const int lo = next_lo;
 
       float m_run = -INFINITY, l_run = 0.f;  // the row's reference (raw); this half's sum
 #pragma unroll 1
@@ -524,9 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sc = tq + Y::kColS + (qi & 1) * Y::kBlk;
         float sv[Y::kMine], mh = -INFINITY;
         if (busy) {
-          ptx::tmem_ld32(sc + hf * Y::kMine, *reinterpret_cast<float(*)[32]>(sv));
+          // (a pair's columns: the lower halves of both units, then the upper)
+          constexpr int kFirst = PAIR ? 32 : Y::kMine, kThen = PAIR ? 64 : 32;
+          ptx::tmem_ld32(sc + hf * kFirst, *reinterpret_cast<float(*)[32]>(sv));
           if constexpr (Y::kMine == 64)
-            ptx::tmem_ld32(sc + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+            ptx::tmem_ld32(sc + hf * kFirst + kThen, *reinterpret_cast<float(*)[32]>(sv + 32));
         }
         // this thread's unit: its own, or the upper or lower half of the one
         constexpr bool kOne = Y::kBlkUnits == 1;
@@ -646,17 +717,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       piece += 2 * Y::kPieces * nb;
       q += nb;
-      // the next Q tile goes in while the last product runs: every score
-      // product of this segment is done
+      // what the next segment needs, while the last product runs (every score
+      // product of this segment is done: its Q tile may go)
       const int c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
       const int set = W.set;
       have = advance();
       if (have) {
-        up_next = parent_of();
-        load_q();
+        if constexpr (!PAIR) load_q();
+        look();
       }
 
       // ---- this segment's result: whole, or a partial ----
+      // A finished row of the stream in the prefix's results ([layer, KV head]
+      // [DH / 4][all rows] of four columns); the first columns are fetched ahead.
+      const size_t rows_all = (size_t)A.n_req * A.til.rows;
+      auto place_x = [&](int rw) {
+        return (size_t)(l * A.Hkv + h) * rows_all * (DH / 4) + (size_t)b * A.til.rows + rw;
+      };
+      float4 x[4];
+      auto fetch_x = [&](int col) {
+        const float4 *from =
+            reinterpret_cast<const float4 *>(A.x_o) + place_x(row) + col / 4 * rows_all;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __ldcg(from + e * rows_all);
+      };
+      if (A.x_o && real) fetch_x(hf * kHalf);
       wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
       ptx::tc_fence_after();
       ptx::named_sync(1 + quad, 64);  // the last maxima are read
@@ -666,30 +751,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = misc[2] == 0;
       float l_sum = red[r] + red[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
-      // A finished row of the stream: its place among all queries, and in the
-      // prefix's results ([layer, KV head][DH / 4][all rows] of four columns).
-      auto place = [&](int rw) {
-        const int nd = rw / A.G;
-        return (((size_t)l * A.n_req + b) * A.nodes + nd) * A.Hq + h * A.G + (rw - nd * A.G);
-      };
-      const size_t rows_all = (size_t)A.n_req * A.til.rows;
-      auto place_x = [&](int rw) {
-        return (size_t)(l * A.Hkv + h) * rows_all * (DH / 4) + (size_t)b * A.til.rows + rw;
-      };
+      // A finished row's place among all queries, and in the prefix's lse.
+      auto place = [&](int rw) { return queries(l, b, h) + query_of(rw); };
       auto place_xl = [&](int rw) {
         return (size_t)(l * A.Hkv + h) * rows_all + (size_t)b * A.til.rows + rw;
       };
       // The factors of this stream's O and of the prefix's o, and the row's lse.
       auto factors = [&](int rw, float m, float sum, float &w, float &wx) {
-        const float own = sum > 0.f ? m + log2f(sum) : -INFINITY;
+        const float own = sum > 0.f ? m + __log2f(sum) : -INFINITY;
         float all = own;
-        w = sum > 0.f ? 1.f / sum : 0.f, wx = 0.f;
+        w = sum > 0.f ? __fdividef(1.f, sum) : 0.f, wx = 0.f;
         if (A.x_o) {
           const float x = __ldcg(A.x_lse2 + place_xl(rw)), top = fmaxf(own, x);
           if (top != -INFINITY) {
-            const float eo = exp2f(own - top), ex = exp2f(x - top), inv = 1.f / (eo + ex);
+            const float eo = ptx::ex2(own - top), ex = ptx::ex2(x - top);
+            const float inv = __fdividef(1.f, eo + ex);
             w *= eo * inv, wx = ex * inv;
-            all = top + log2f(eo + ex);
+            all = top + __log2f(eo + ex);
           }
         }
         return all;
@@ -703,11 +781,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
       // Partial g of the stream: m and l per row, then O as [DH / 4][128] of
       // four columns.  Each CTA has two: its first segment's, and its last's.
-      auto partial = [&](int g) {
-        const int cta = ((c_first + g) * A.til.group + lane_of) * Y::kCtas + rank;
-        const int slot = g == 0 && W.begin_of(c_first) < first ? 1 : 0;
-        return A.part + (size_t)(2 * cta + slot) * part_floats(DH);
-      };
+      const size_t by = 2 * (size_t)A.til.group * Y::kCtas * part_floats(DH);
+      float *part0 = A.part + (size_t)(2 * ((c_first * A.til.group + lane_of) * Y::kCtas + rank)) *
+                                  part_floats(DH);
+      const int late = W.begin_of(c_first) < first ? (int)part_floats(DH) : 0;
+      auto partial = [&](int g) { return part0 + g * by + (g == 0 ? late : 0); };
       bool join = false;
       if (!whole && rows > 0) {
         float4 *to = reinterpret_cast<float4 *>(partial(W.cg - c_first) + 2 * kRows);
@@ -730,136 +808,185 @@ __global__ void __launch_bounds__(kThreads, 1)
           float *ml = partial(W.cg - c_first);
           ml[r] = m2, ml[kRows + r] = l_sum;
         }
-        __threadfence();
         ptx::named_sync(5, kSoftmaxThreads);
         const size_t counter =
             ((((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles + tile) * Y::kCtas + rank;
         if (tid == 0) {
+          __threadfence();  // the CTA's partial, before its arrival
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
           misc[1] = (int)prev == n_piece - 1 ? 1 : 0;
           if (misc[1]) A.counters[counter] = 0u;  // for the next call
+          __threadfence();
         }
         ptx::named_sync(5, kSoftmaxThreads);
         join = misc[1] != 0;
-        if (join) __threadfence();
       }
       if (join && rows <= kFewRows) {
-        // few rows, maybe many pieces: four columns of a row per thread, eight
-        // pieces in flight
+        // few rows, maybe many pieces: the pieces' weights, then four columns of a
+        // row per thread; as many rows at a time as `red` holds weights of
+        constexpr int kHeld = 4 * kRows - kFewRows;
+        float *wx_of = red + kHeld;
+        const int step = kHeld / n_piece < rows ? kHeld / n_piece : rows;
 #pragma unroll 1
-        for (int idx = tid; idx < rows * (DH / 4); idx += kSoftmaxThreads) {
-          const int rr = idx / (DH / 4), c4 = idx % (DH / 4);
-          float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int rr0 = 0; rr0 < rows; rr0 += step) {
+          const int here = rows - rr0 < step ? rows - rr0 : step;
+          ptx::named_sync(5, kSoftmaxThreads);  // the last weights are read
+          if (tid < here) {
+            const int rw = row0 + rr0 + tid;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+            for (int g = 0; g < n_piece; ++g) top = fmaxf(top, __ldcg(partial(g) + rr0 + tid));
+            if (top == -INFINITY) top = 0.f;
+#pragma unroll 4
+            for (int g = 0; g < n_piece; ++g) {
+              const float *pg = partial(g) + rr0 + tid;
+              const float e = ptx::ex2(__ldcg(pg) - top);
+              red[g * here + tid] = e;
+              sum = fmaf(e, __ldcg(pg + kRows), sum);
+            }
+            float w, wx;
+            put_lse(rw, factors(rw, top, sum, w, wx));
 #pragma unroll 1
-          for (int g0 = 0; g0 < n_piece; g0 += 8) {
-            float mg[8], lg[8];
-            float4 og[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float *pg = partial(g0 + e < n_piece ? g0 + e : 0);
-              mg[e] = g0 + e < n_piece ? __ldcg(pg + rr) : -INFINITY;
-              lg[e] = __ldcg(pg + kRows + rr);
-              og[e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) + c4 * kRows + rr);
-            }
-            float t8 = top;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t8 = fmaxf(t8, mg[e]);
-            if (t8 == -INFINITY) continue;
-            const float old = ptx::ex2(top - t8);
-            top = t8, sum *= old;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] *= old;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (mg[e] == -INFINITY) continue;  // an empty piece's O is not read
-              const float w = ptx::ex2(mg[e] - top);
-              sum = fmaf(w, lg[e], sum);
-              acc[0] = fmaf(w, og[e].x, acc[0]), acc[1] = fmaf(w, og[e].y, acc[1]);
-              acc[2] = fmaf(w, og[e].z, acc[2]), acc[3] = fmaf(w, og[e].w, acc[3]);
-            }
+            for (int g = 0; g < n_piece; ++g) red[g * here + tid] *= w;
+            wx_of[tid] = wx;
           }
-          const int rw = row0 + rr;
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (A.x_o)
-            f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);
-          float w, wx;
-          const float all = factors(rw, top, sum, w, wx);
-          f.x = fmaf(acc[0], w, wx * f.x), f.y = fmaf(acc[1], w, wx * f.y);
-          f.z = fmaf(acc[2], w, wx * f.z), f.w = fmaf(acc[3], w, wx * f.w);
-          if (A.o32)
-            reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;
-          else
-            reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] =
-                make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
-          if (c4 == 0) put_lse(rw, all);
+          ptx::named_sync(5, kSoftmaxThreads);
+#pragma unroll 1
+          for (int idx = tid; idx < here * (DH / 4); idx += kSoftmaxThreads) {
+            const int rr = idx / (DH / 4), c4 = idx % (DH / 4), rw = row0 + rr0 + rr;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (A.x_o) {
+              f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);
+              const float wx = wx_of[rr];
+              f.x *= wx, f.y *= wx, f.z *= wx, f.w *= wx;
+            }
+#pragma unroll 8
+            for (int g = 0; g < n_piece; ++g) {
+              const float e = red[g * here + rr];
+              const float4 y = __ldcg(reinterpret_cast<const float4 *>(partial(g) + 2 * kRows) +
+                                      c4 * kRows + rr0 + rr);
+              if (e > 0.f)  // (an empty piece's O holds nothing)
+                f.x = fmaf(e, y.x, f.x), f.y = fmaf(e, y.y, f.y), f.z = fmaf(e, y.z, f.z),
+                f.w = fmaf(e, y.w, f.w);
+            }
+            if (A.o32)
+              reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;
+            else
+              reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] =
+                  make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
+          }
         }
       } else if (busy && valid && (whole || join)) {
         // a row per two threads; this CTA's piece is still in tensor memory,
         // the others' (all but one, mostly) are read 32 columns at a time
-        float top = m2, sum = l_sum, w_own = 1.f;
+        float top = m2, sum = l_sum, w_own = 1.f, w_it = 0.f;
+        // the one other piece that most joins have: its columns come ahead
+        const int it = W.cg == c_first ? 1 : 0;
+        const float *other = partial(join ? it : 0);
+        float4 y[4];
+        auto fetch_y = [&](const float *pg, int col) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) +
+                          (col / 4 + e) * kRows + r);
+        };
         if (join) {
+          fetch_y(other, hf * kHalf);
+          const float m_it = __ldcg(other + r), l_it = __ldcg(other + kRows + r);
+          top = fmaxf(top, m_it);
 #pragma unroll 1
           for (int g = 0; g < n_piece; ++g)
-            if (c_first + g != W.cg) top = fmaxf(top, __ldcg(partial(g) + r));
+            if (c_first + g != W.cg && g != it) top = fmaxf(top, __ldcg(partial(g) + r));
           const float ref = top == -INFINITY ? 0.f : top;
-          w_own = ptx::ex2(m2 - ref), sum = l_sum * w_own;
+          w_own = ptx::ex2(m2 - ref), w_it = ptx::ex2(m_it - ref);
+          sum = l_sum * w_own + l_it * w_it;
 #pragma unroll 1
           for (int g = 0; g < n_piece; ++g)
-            if (c_first + g != W.cg)
+            if (c_first + g != W.cg && g != it)
               sum += ptx::ex2(__ldcg(partial(g) + r) - ref) * __ldcg(partial(g) + kRows + r);
           top = ref;
         }
         float w = 0.f, wx = 0.f, all = 0.f;
         if (real) all = factors(row, top, sum, w, wx);
         if (real && hf == 0) put_lse(row, all);
+        // where the four rows of this lane's group of lanes go
+        uint64_t to[4] = {};
+        if (A.o) {
+          const uint64_t mine = real ? reinterpret_cast<uint64_t>(A.o + place(row) * DH) : 0ull;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + k);
+        }
 #pragma unroll 1
         for (int c = 0; c < kHalf / 32; ++c) {
-          const int col = hf * kHalf + 32 * c;
-          float v[32];
-          ptx::tmem_ld32(tq + Y::kColO + (uint32_t)col, v);
-          ptx::tmem_wait_ld();
-          if (!real) continue;
+          uint32_t pc[4][4];  // 32 columns, 16 at a time
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= w * w_own;
-          // add f times 32 columns of this row in an array of four-column rows
-          auto add = [&](float f, const float4 *from, size_t stride) {
-            float4 x[8];
+          for (int j = 0; j < 2; ++j) {
+            const int col = hf * kHalf + 32 * c + 16 * j;
+            const bool more = j == 0 || c + 1 < kHalf / 32;
+            float v[16];
+            ptx::tmem_ld16(tq + Y::kColO + (uint32_t)col, v);
+            ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __ldcg(from + e * stride);
+            for (int e = 0; e < 16; ++e) v[e] *= w * w_own;
+            auto add = [&](float f, const float4(&z)[4]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[4 * e] = fmaf(f, x[e].x, v[4 * e]);
-              v[4 * e + 1] = fmaf(f, x[e].y, v[4 * e + 1]);
-              v[4 * e + 2] = fmaf(f, x[e].z, v[4 * e + 2]);
-              v[4 * e + 3] = fmaf(f, x[e].w, v[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) {
+                v[4 * e] = fmaf(f, z[e].x, v[4 * e]);
+                v[4 * e + 1] = fmaf(f, z[e].y, v[4 * e + 1]);
+                v[4 * e + 2] = fmaf(f, z[e].z, v[4 * e + 2]);
+                v[4 * e + 3] = fmaf(f, z[e].w, v[4 * e + 3]);
+              }
+            };
+            if (A.x_o && real) {
+              add(wx, x);
+              if (more) fetch_x(col + 16);
             }
-          };
-          if (join) {
+            if (join && real) {
+              // (an empty piece's O holds nothing)
+              if (w_it > 0.f) add(w * w_it, y);
 #pragma unroll 1
-            for (int g = 0; g < n_piece; ++g) {
-              const float *pg = partial(g);
-              const float mg = c_first + g != W.cg ? __ldcg(pg + r) : -INFINITY;
-              if (mg == -INFINITY) continue;  // an empty piece's O is not read
-              add(w * ptx::ex2(mg - top),
-                  reinterpret_cast<const float4 *>(pg + 2 * kRows) + col / 4 * kRows + r, kRows);
+              for (int g = 0; g < n_piece && n_piece > 2; ++g) {
+                if (c_first + g == W.cg || g == it) continue;
+                const float w_g = ptx::ex2(__ldcg(partial(g) + r) - top);
+                fetch_y(partial(g), col);
+                if (w_g > 0.f) add(w * w_g, y);
+              }
+              if (more) fetch_y(other, col + 16);
             }
+            if (A.o32) {
+              float4 *at = reinterpret_cast<float4 *>(A.o32) + place_x(row) + col / 4 * rows_all;
+              if (real) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  at[e * rows_all] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pc[2 * j + (e >> 2)][e & 3] = pack2<F16>(v[2 * e], v[2 * e + 1]);
           }
-          if (A.x_o)
-            add(wx, reinterpret_cast<const float4 *>(A.x_o) + place_x(row) + col / 4 * rows_all,
-                rows_all);
-          if (A.o32) {
-            float4 *to = reinterpret_cast<float4 *>(A.o32) + place_x(row) + col / 4 * rows_all;
+          if (A.o) {
+            // four lanes exchange 16-byte pieces, so that a store of the warp
+            // writes 64 bytes of eight rows instead of 16 of thirty-two
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              to[e * rows_all] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          } else {
-            uint4 *to = reinterpret_cast<uint4 *>(A.o + place(row) * DH + col);
+            for (int s = 1; s <= 2; s *= 2) {
+              const bool up = lane & s;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(pack2<F16>(v[8 * e], v[8 * e + 1]),
-                                 pack2<F16>(v[8 * e + 2], v[8 * e + 3]),
-                                 pack2<F16>(v[8 * e + 4], v[8 * e + 5]),
-                                 pack2<F16>(v[8 * e + 6], v[8 * e + 7]));
+              for (int k = 0; k < 4; ++k) {
+                if (k & s) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t got =
+                      __shfl_xor_sync(0xffffffffu, up ? pc[k][e] : pc[k + s][e], s);
+                  if (up) pc[k][e] = got;
+                  else pc[k + s][e] = got;
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (to[k])
+                reinterpret_cast<uint4 *>(to[k])[(hf * kHalf + 32 * c) / 8 + (lane & 3)] =
+                    make_uint4(pc[k][0], pc[k][1], pc[k][2], pc[k][3]);
           }
         }
       }
@@ -892,7 +1019,7 @@ cudaError_t launch_attn_of(const AttnMaps &maps, const AttnArgs &A, int grid,
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(Lay<DH, PAIR>::kThreads);
   cfg.dynamicSmemBytes = bytes, cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -31,6 +31,7 @@ struct MassArgs {
   int L, Hq, Hkv, G, n_req, fixed, Bq, N, T, window, n_sink;
   int cap, stages;  // rows per pass, ring stages
   float scale_log2;
+  PerGroup per;
   Tiling til;
   const int32_t *ctx_len, *parent, *accepted;
   const uint16_t *q;
@@ -125,13 +126,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the segment's queries into L2, ahead of its keys: loads of them would
       // wait for all the copies in flight
 #pragma unroll 1
-      for (uint64_t m = path; m; m &= m - 1) {
-        const size_t at = ((size_t)z * A.N + (__ffsll((long long)m) - 1)) * A.Hq + W.h * A.G;
-        const char *line = reinterpret_cast<const char *>(A.q + at * DH);
-#pragma unroll 1
-        for (int i = lane * 128; i < A.G * DH * 2; i += 32 * 128) ptx::prefetch_line(line + i);
-        if (lane == 0) ptx::prefetch_line(A.lse + at);
-      }
+      for (int n = lane; n < A.N; n += 32)
+        if (path >> n & 1)
+          ptx::prefetch_bytes(A.q + (((size_t)z * A.N + n) * A.Hq + W.h * A.G) * DH,
+                              (uint32_t)(A.G * DH * 2));
+      __syncwarp();
 #pragma unroll 1
       for (int r0 = 0; r0 < rows && lane == 0; r0 += A.cap)
 #pragma unroll 1
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::named_sync(5, 256);  // nodes are listed; the last pass is done everywhere
         constexpr int kPer = DH / 8;  // 16-byte pieces per row
         auto query = [&](int r) {  // row r of the pass among all queries
-          const int d = (r0 + r) / A.G;
+          const int d = A.per.node(r0 + r);
           return (lb * A.N + nodes[d]) * A.Hq + W.h * A.G + (r0 + r - d * A.G);
         };
 #pragma unroll 8
@@ -360,7 +359,8 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
     return LBX_EINVAL;
   if (c->T > 0 && (!aligned_to(k_cache, 16) || !aligned_to(score, 4))) return LBX_EINVAL;
   const int lists = c->L * c->Bq, G = c->Hq / c->Hkv;
-  // the block list's indexes are 32-bit
+  // 32-bit indexes of the block list, and of rows (see PerGroup)
+  if ((long long)c->N * G >= (1LL << 32) / G) return LBX_EINVAL;
   if ((long long)lists * c->Hkv >= (1LL << 31) / (c->T / kUnit + 3)) return LBX_EINVAL;
   const int grid = grid_limit();
   if (grid < 1) return LBX_ECUDA;
@@ -372,6 +372,7 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
   A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = G, A.n_req = c->Bq;
   A.Bq = c->Bq, A.N = c->N, A.T = c->T, A.window = c->window, A.n_sink = c->n_sink;
   A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.per = per_group(G);
   A.til = {c->N * G, 1, 1, 1, 1};
   A.ctx_len = ctx_len, A.parent = parent, A.accepted = accepted, A.q = q, A.lse = lse;
   A.score = score, A.score_tree = score_tree, A.status = d_status;

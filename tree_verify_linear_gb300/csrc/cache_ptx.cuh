@@ -17,9 +17,9 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
       : "memory");
 }
 
-// Bring the line at `p` into L2.
-__device__ __forceinline__ void prefetch_line(const void *p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+// Bring `bytes` at `p` into L2 (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void prefetch_bytes(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // One plain arrival (release of this thread's earlier memory operations).

@@ -53,6 +53,15 @@ struct Ring {
   }
 };
 
+// Division of a row number by the heads of a group: exact while row * G < 2^32.
+struct PerGroup {
+  uint64_t inv;  // 2^32 / G, rounded up
+  __device__ __forceinline__ int node(int row) const {
+    return (int)(((uint64_t)(uint32_t)row * inv) >> 32);
+  }
+};
+inline PerGroup per_group(int G) { return {((1ull << 32) + (unsigned)G - 1) / (unsigned)G}; }
+
 // The low k (0..64) bits.
 __device__ __forceinline__ uint64_t low_bits(int k) {
   return k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
