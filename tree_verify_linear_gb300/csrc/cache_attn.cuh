@@ -36,14 +36,15 @@
 // and half the reads of L2.  Each CTA's copies arrive on its own barriers; the
 // follower passes the news on to the leader, whose one thread issues all MMAs.
 //
-// Per CTA: warps 0-7 softmax, warp 8 issues the MMAs, warp 9 the copies.  K
+// Per CTA: warps 0-7 softmax, warp 8 issues the MMAs, warp 9 the copies, warps
+// 10 and 11 of a pair bring the Q tiles.  K
 // and V arrive by TMA in 16 KB pieces through one ring, in the order the MMAs
 // take them, so that all of the shared memory keeps copies in flight.  The Q
 // tile sits in tensor memory (in shared memory for a pair, whose 128-key
 // blocks need the columns).  S of a block and its P share one of two buffers.
-// Every wait is bounded; a CTA whose wait gives up reports LBX_ETIMEOUT, still
-// counts itself in with empty partials, drains its copies and frees its tensor
-// memory.
+// Every wait is bounded; a CTA whose wait gives up reports LBX_ETIMEOUT, counts
+// its segment in with an empty partial, drains its copies, frees its tensor
+// memory and leaves.
 #pragma once
 
 #include "cache_common.cuh"
@@ -79,6 +80,18 @@ struct AttnArgs {
   int32_t *status;
 };
 
+// A segment (a stream's blocks in the CTA's range) as the softmax threads see it:
+// one warp walks the list for them and publishes the segments in turn.
+struct Seg {
+  int have;          // 0: the range is done
+  int l, h, b;       // the stream
+  int row0;          // its first row of this CTA
+  int blk0, nb;      // blocks
+  int ctx, w0, s_eff, ns, nw;  // the key list's units
+  int slot, late;    // partials of the stream: the first one, and whether it is its CTA's second
+  int pieces, mine;  // how many, and which is this CTA's
+};
+
 template <int DH, bool PAIR>
 struct Lay {
   static constexpr int kCtas = PAIR ? 2 : 1;
@@ -104,11 +117,11 @@ struct Lay {
   static constexpr int kSmemQ = 0;
   static constexpr int kSmemRing = kSmemQ + kQBytes;
   static constexpr int kSmemRed = kSmemRing + kStages * kPiece;  // float [2][2][128]
-  static constexpr int kSmemAnc = kSmemRed + 4 * kRows * 4;      // uint64 [64]
-  static constexpr int kSmemMisc = kSmemAnc + kMaxNodes * 8;     // int [8]
+  static constexpr int kSmemSegs = kSmemRed + 4 * kRows * 4;     // Seg [4]
+  static constexpr int kSmemMisc = kSmemSegs + 4 * (int)sizeof(Seg);  // int [8]
   static constexpr int kSmemBars = kSmemMisc + 32;
-  // full, empty, peer (of a pair), s[2], p[2], o[2], lo[2], q, q free, end
-  static constexpr int kNBars = (PAIR ? 3 : 2) * kStages + 11;
+  // full, empty, peer (of a pair), s[2], p[2], o[2], lo[2], segs[4], q, q free, end
+  static constexpr int kNBars = (PAIR ? 3 : 2) * kStages + 15;
   static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
   static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0, "shared memory");
 
@@ -146,13 +159,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   unsigned char *smem = cache_smem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float *red = reinterpret_cast<float *>(smem + Y::kSmemRed);
-  uint64_t *anc = reinterpret_cast<uint64_t *>(smem + Y::kSmemAnc);
-  // [0] tensor memory base, [1] last of its row tile, [2] a wait gave up
+  Seg *segs = reinterpret_cast<Seg *>(smem + Y::kSmemSegs);
+  // [0] tensor memory base, [1] last of its row tile, [2] a wait gave up, [3] one
+  // of a softmax thread did
   volatile int *misc = reinterpret_cast<volatile int *>(smem + Y::kSmemMisc);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + Y::kSmemBars);
   uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
   uint64_t *s_bar = peer + (PAIR ? Y::kStages : 0), *p_bar = s_bar + 2;
-  uint64_t *o_bar = p_bar + 2, *lo_bar = o_bar + 2, *q_bar = lo_bar + 2, *qf_bar = q_bar + 1;
+  uint64_t *o_bar = p_bar + 2, *lo_bar = o_bar + 2, *seg_bar = lo_bar + 2;
+  uint64_t *q_bar = seg_bar + 4, *qf_bar = q_bar + 1;
   uint64_t *end_bar = qf_bar + 1;
 
   if (batch_bad(A.Bq, A.N, A.T, A.ctx_len, A.parent, nullptr)) {
@@ -166,7 +181,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
                                : full + i == q_bar ? Y::kCtas * Y::kLoaders / 32
                                                    : 1);
     ptx::fence_mbar_init();
-    misc[2] = 0;
+    misc[2] = misc[3] = 0;
   }
   if (warp == 8) {
     uint32_t *base = reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc);
@@ -184,7 +199,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
-  Walk<Y::kBlkUnits, kJoinBlocks, AttnArgs> W(A, lane);
+  using Walker = Walk<Y::kBlkUnits, kJoinBlocks, AttnArgs>;
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
@@ -199,19 +214,18 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     }
   };
   // Query rows of the walk's tile from this CTA's first on.
-  auto first_row = [&]() { return (W.tile * Y::kCtas + rank) * kRows; };
+  auto first_row = [&](const Walker &W) { return (W.tile * Y::kCtas + rank) * kRows; };
   // The place of a row of the stream among all queries: of its first one, and
   // of the row from there.
   auto queries = [&](int l, int b, int h) {
     return (size_t)(l * A.n_req + b) * A.nodes * A.Hq + h * A.G;
   };
   auto query_of = [&](int row) { return row + A.per.node(row) * (A.Hq - A.G); };
-  // The segment's queries into L2, ahead of its keys: loads of them would wait
-  // for all the copies in flight.
-  // A prefix's results that the segment will be joined with, too.
-  // A prefix's results that the segment will be joined with, too.  One warp.
-  auto prefetch_q = [&]() {
-    const int row = first_row(), rows = A.til.rows - row < kRows ? A.til.rows - row : kRows;
+  // The segment's queries into L2, ahead of its keys (loads of them would wait
+  // for all the copies in flight), and a prefix's results that it will be joined
+  // with.  One warp.
+  auto prefetch_q = [&](const Walker &W) {
+    const int row = first_row(W), rows = A.til.rows - row < kRows ? A.til.rows - row : kRows;
     if (rows <= 0) return;
     const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
 #pragma unroll 1
@@ -228,22 +242,41 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     }
   };
   // The next segment with a tile for this CTA.
-  auto advance = [&]() {
+  auto advance = [&](Walker &W) {
 #pragma unroll 1
     while (W.next())
       if (W.live) return true;
     return false;
   };
+  // Segment k for the softmax threads.  The warp that does this is at most three
+  // segments ahead of them (it has the last one's queries to load first, or its
+  // products to issue), so that four places do.
+  auto publish = [&](const Walker &W, bool have, uint32_t k) {
+    if (lane != 0) return;
+    Seg &s = segs[k & 3];
+    s.have = have;
+    if (have) {
+      const int c_first = W.owner(W.first), c_last = W.owner(W.first + W.entries() - 1);
+      s.l = W.l, s.h = W.h, s.b = W.b, s.row0 = first_row(W);
+      s.blk0 = W.blk0, s.nb = W.blk1 - W.blk0;
+      s.ctx = W.ctx, s.w0 = W.w0, s.s_eff = W.s_eff, s.ns = W.ns, s.nw = W.nw;
+      s.slot = 2 * ((c_first * A.til.group + W.slot_in_group) * Y::kCtas + rank);
+      s.late = W.begin_of(c_first) < W.first;
+      s.pieces = c_last - c_first + 1, s.mine = W.cg - c_first;
+    }
+    ptx::mbar_arrive(&seg_bar[k & 3]);
+  };
 
   if (warp == 9) {
     // ---- copies ----
+    Walker W(A, lane);
     Ring<Y::kStages> ring;
     int loads = 0;
     // behind the first Q tile's loads or prefetches
     ptx::named_sync(6, Y::kLoaders + 32);
 #pragma unroll 1
-    while (advance()) {
-      if (!PAIR) prefetch_q();
+    while (advance(W)) {
+      if (!PAIR) prefetch_q(W);
       if (lane != 0) continue;
       const int nb = W.blk1 - W.blk0;
       const int z = A.fixed > 0 ? W.l : W.l * A.n_req + W.b;
@@ -307,11 +340,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     // ---- Q rows of a pair, swizzled into shared memory, 16 bytes per lane ----
     constexpr int kPer = DH / 8, kStep = 64 / kPer, kBatch = 8;  // rows per load, loads in flight
     const int c = (tid & 63) % kPer, r0 = (tid & 63) / kPer;
+    Walker W(A, lane);
     bool ahead = true;
-    uint32_t seg = 0;
 #pragma unroll 1
-    for (bool have = advance(); have || ahead; have = advance(), ++seg) {
-      if (have && warp == 10) prefetch_q();
+    for (uint32_t seg = 0;; ++seg) {
+      const bool have = advance(W);
+      if (warp == 10) {
+        publish(W, have, seg);
+        if (have) prefetch_q(W);
+      }
       if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
       ahead = false;
       if (!have) break;
@@ -323,7 +360,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         uint4 v[kBatch];
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
-          const int row = first_row() + b0 + e * kStep;
+          const int row = first_row(W) + b0 + e * kStep;
           v[e] = make_uint4(0u, 0u, 0u, 0u);
           if (row < A.til.rows) v[e] = q0[(size_t)query_of(row) * kPer + c];
         }
@@ -341,6 +378,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     if (bad) misc[2] = 1;
   } else if (warp == 8 && rank == 1) {
     // ---- the follower tells the leader of each piece that has landed ----
+    Walker W(A, lane);
     Ring<Y::kStages> ring;
 #pragma unroll 1
     while (W.next()) {
@@ -354,6 +392,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     if (bad) misc[2] = 1;
   } else if (warp == 8) {
     // ---- MMAs: the warp walks and waits as one, one lane issues ----
+    Walker W(A, lane);
     Ring<Y::kStages> ring;
     uint32_t q = 0, seg = 0;
     const bool one = ptx::elect_one();
@@ -375,8 +414,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       return wait_all(&full[ring.st], ring.ph) && (!PAIR || wait_all(&peer[ring.st], ring.ph));
     };
 #pragma unroll 1
-    while (W.next()) {
-      if (!W.live) continue;
+    while (advance(W)) {
+      if (!PAIR) publish(W, true, seg);
       const int nb = W.blk1 - W.blk0;
       // S of block i into buffer (q + i) & 1, once the buffer's last P has been
       // multiplied (the first two blocks find it free).  A pair takes the keys in
@@ -470,6 +509,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       ++seg;
       if (bad) break;
     }
+    if (!PAIR) publish(W, false, seg);
     if (one) {
       if (bad) misc[2] = 1;
       commit(end_bar);
@@ -483,9 +523,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     const float sl2 = A.scale_log2;
     constexpr int kHalf = DH / 2;
     uint32_t q = 0, piece = 0;  // blocks and ring pieces so far
-    int req = -1;
 
-    // Without a pair: the Q tile of the walk's segment into tensor memory, half a
+    // Without a pair: the Q tile of a segment into tensor memory, half a
     // row per thread, pairs along dh, rows past the stream's zero.  The first
     // tile's loads go ahead of the first copies of K and V.
     bool ahead = !PAIR;
@@ -493,12 +532,12 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
       ahead = false;
     };
-    auto load_q = [&]() {
+    auto load_q = [&](const volatile Seg &s) {
       constexpr int kPer = DH / 8;  // 16-byte pieces per row
-      const int row = first_row() + r;
+      const int row = s.row0 + r;
       const bool in = row < A.til.rows;
       const uint4 *from = reinterpret_cast<const uint4 *>(A.q);
-      if (in) from += (queries(W.l, W.b, W.h) + query_of(row)) * kPer + hf * (kPer / 2);
+      if (in) from += (queries(s.l, s.b, s.h) + query_of(row)) * kPer + hf * (kPer / 2);
       constexpr int kC = DH / 4 < 32 ? DH / 4 : 32;  // columns per store
       uint4 v[DH / 16];
 #pragma unroll
@@ -519,68 +558,74 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       ptx::tc_fence_before();
       tell(q_bar);
     };
-    // What this row sees in the walk's segment: of the tree as bits, of the cache
-    // from a position on.  The masks of the request's tree, by doubling, are one
-    // warp's work.
+    // What this row sees in a segment: of the tree as bits, of the cache from a
+    // position on.  The ancestor masks of the request's tree, by doubling, are one
+    // warp's work; they lie where the last maxima were.
     uint64_t next_bits = 0;
     int next_lo = 0;
-    auto look = [&]() {
+    auto look = [&](const volatile Seg &s) {
       if (A.fixed > 0) return;
-      if (W.b != req) {
-        req = W.b;
-        if (warp == 0) {
-          const int32_t *parent = A.parent + (size_t)req * A.N;
-          int up[2] = {lane < A.N ? parent[lane] : -1, lane + 32 < A.N ? parent[lane + 32] : -1};
-          uint64_t m[2] = {1ull << lane, 1ull << (lane + 32)};
+      uint64_t *anc = reinterpret_cast<uint64_t *>(red);
+      if (warp == 0) {
+        const int32_t *parent = A.parent + (size_t)s.b * A.N;
+        int up[2] = {lane < A.N ? parent[lane] : -1, lane + 32 < A.N ? parent[lane + 32] : -1};
+        uint64_t m[2] = {1ull << lane, 1ull << (lane + 32)};
 #pragma unroll 1
-          for (int step = 0; step < 6; ++step) {
-            uint64_t add[2];
-            int to[2];
+        for (int step = 0; step < 6; ++step) {
+          uint64_t add[2];
+          int to[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int a = up[e] & 31;
-              const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], a);
-              const uint64_t m1 = __shfl_sync(0xffffffffu, m[1], a);
-              const int u0 = __shfl_sync(0xffffffffu, up[0], a);
-              const int u1 = __shfl_sync(0xffffffffu, up[1], a);
-              add[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
-              to[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
-            }
-            m[0] |= add[0], m[1] |= add[1], up[0] = to[0], up[1] = to[1];
+          for (int e = 0; e < 2; ++e) {
+            const int a = up[e] & 31;
+            const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], a);
+            const uint64_t m1 = __shfl_sync(0xffffffffu, m[1], a);
+            const int u0 = __shfl_sync(0xffffffffu, up[0], a);
+            const int u1 = __shfl_sync(0xffffffffu, up[1], a);
+            add[e] = up[e] < 0 ? 0ull : up[e] < 32 ? m0 : m1;
+            to[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
           }
-          anc[lane] = m[0], anc[lane + 32] = m[1];
+          m[0] |= add[0], m[1] |= add[1], up[0] = to[0], up[1] = to[1];
         }
-        ptx::named_sync(5, kSoftmaxThreads);
+        anc[lane] = m[0], anc[lane + 32] = m[1];
       }
-      const int row = first_row() + r;
+      ptx::named_sync(5, kSoftmaxThreads);
+      const int row = s.row0 + r;
       next_bits = 0, next_lo = 0;
       if (row < A.til.rows) {
         next_bits = anc[A.per.node(row)];
         if (A.window > 0) {
-          next_lo = W.ctx + __popcll(next_bits) - A.window;  // ctx + depth - window + 1
+          const int ctx = s.ctx;
+          next_lo = ctx + __popcll(next_bits) - A.window;  // ctx + depth - window + 1
           uint64_t m = next_bits;
 #pragma unroll 1
-          for (int pos = W.ctx; m; ++pos, m &= m - 1)  // nodes of the path, root first
+          for (int pos = ctx; m; ++pos, m &= m - 1)  // nodes of the path, root first
             if (pos < next_lo && pos >= A.n_sink) next_bits &= ~(m & (0 - m));
         }
       }
     };
 
-    bool have = advance();
-    if (have) {
-      if constexpr (!PAIR) load_q();
-      look();
+    // Segment k is published (and the last one's maxima are read); false in all
+    // threads if a wait of any of them gave up.
+    auto published = [&](uint32_t k) {
+      wait(&seg_bar[k & 3], (k >> 2) & 1);
+      if (bad) misc[3] = 1;
+      ptx::named_sync(5, kSoftmaxThreads);
+      return misc[3] == 0;
+    };
+    uint32_t k = 0;
+    const volatile Seg *g = segs;
+    bool more = published(0) && g->have;
+    if (more) {
+      if constexpr (!PAIR) load_q(*g);
+      look(*g);
     } else {
       go_ahead();
     }
 #pragma unroll 1
-    while (have) {
-      const int l = W.l, b = W.b, h = W.h, tile = W.tile, blk0 = W.blk0, blk1 = W.blk1;
-      const int nb = blk1 - blk0;
-      const int first = W.first;
-      const int row0 = first_row(), row = row0 + r;
+    while (more) {
+      const int nb = g->nb, row = g->row0 + r;
       const bool real = row < A.til.rows;
-      const bool busy = row0 + quad * 32 < A.til.rows;  // the warp has rows
+      const bool busy = row - lane < A.til.rows;  // the warp has rows
       const uint64_t tree_bits = next_bits;
       const int lo = next_lo;
 
@@ -603,7 +648,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         constexpr bool kOne = Y::kBlkUnits == 1;
         int start, cnt;
         bool tree;
-        W.unit((blk0 + i) * Y::kBlkUnits + (kOne ? 0 : hf), start, tree, cnt);
+        unit_of(*g, A.fixed > 0, A.N, (g->blk0 + i) * Y::kBlkUnits + (kOne ? 0 : hf), start, tree,
+                cnt);
         auto clear_unseen = [&]() {
           // values no query sees must not reach O through a zero weight
           if (!tree && cnt > 0 && cnt < kUnit) {
@@ -719,17 +765,18 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       q += nb;
       // what the next segment needs, while the last product runs (every score
       // product of this segment is done: its Q tile may go)
-      const int c_first = W.owner(first), c_last = W.owner(first + W.entries() - 1);
-      const int set = W.set;
-      have = advance();
-      if (have) {
-        if constexpr (!PAIR) load_q();
-        look();
+      ++k;
+      const volatile Seg *next = &segs[k & 3];
+      more = published(k) && next->have;
+      if (more) {
+        if constexpr (!PAIR) load_q(*next);
+        look(*next);
       }
 
       // ---- this segment's result: whole, or a partial ----
       // A finished row of the stream in the prefix's results ([layer, KV head]
       // [DH / 4][all rows] of four columns); the first columns are fetched ahead.
+      const int l = g->l, h = g->h, b = g->b, row0 = g->row0;
       const size_t rows_all = (size_t)A.n_req * A.til.rows;
       auto place_x = [&](int rw) {
         return (size_t)(l * A.Hkv + h) * rows_all * (DH / 4) + (size_t)b * A.til.rows + rw;
@@ -745,11 +792,12 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
       ptx::tc_fence_after();
       ptx::named_sync(1 + quad, 64);  // the last maxima are read
-      red[hf * kRows + r] = l_run;
-      if (bad) misc[2] = 1;
+      float *sums = red + 2 * kRows;  // clear of the masks
+      sums[hf * kRows + r] = l_run;
+      if (bad) misc[3] = 1;
       ptx::named_sync(5, kSoftmaxThreads);
-      const bool valid = misc[2] == 0;
-      float l_sum = red[r] + red[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
+      const bool valid = misc[3] == 0;
+      float l_sum = sums[r] + sums[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
       // A finished row's place among all queries, and in the prefix's lse.
       auto place = [&](int rw) { return queries(l, b, h) + query_of(rw); };
@@ -776,19 +824,18 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         if (A.lse2) A.lse2[place_xl(rw)] = all;
         if (A.lse) A.lse[place(rw)] = all * 0.6931471805599453f;
       };
-      const bool whole = c_first == c_last;
-      const int lane_of = tile - set * A.til.group, n_piece = c_last - c_first + 1;
+      const int n_piece = g->pieces, mine = g->mine;
+      const bool whole = n_piece == 1;
       const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
-      // Partial g of the stream: m and l per row, then O as [DH / 4][128] of
+      // Partial e of the stream: m and l per row, then O as [DH / 4][128] of
       // four columns.  Each CTA has two: its first segment's, and its last's.
       const size_t by = 2 * (size_t)A.til.group * Y::kCtas * part_floats(DH);
-      float *part0 = A.part + (size_t)(2 * ((c_first * A.til.group + lane_of) * Y::kCtas + rank)) *
-                                  part_floats(DH);
-      const int late = W.begin_of(c_first) < first ? (int)part_floats(DH) : 0;
-      auto partial = [&](int g) { return part0 + g * by + (g == 0 ? late : 0); };
+      float *part0 = A.part + (size_t)g->slot * part_floats(DH);
+      const int late = g->late ? (int)part_floats(DH) : 0;
+      auto partial = [&](int e) { return part0 + e * by + (e == 0 ? late : 0); };
       bool join = false;
       if (!whole && rows > 0) {
-        float4 *to = reinterpret_cast<float4 *>(partial(W.cg - c_first) + 2 * kRows);
+        float4 *to = reinterpret_cast<float4 *>(partial(mine) + 2 * kRows);
         if (busy && valid) {
 #pragma unroll 1
           for (int c = 0; c < kHalf / 32; ++c) {
@@ -805,12 +852,12 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           }
         }
         if (real && hf == 0) {
-          float *ml = partial(W.cg - c_first);
+          float *ml = partial(mine);
           ml[r] = m2, ml[kRows + r] = l_sum;
         }
         ptx::named_sync(5, kSoftmaxThreads);
-        const size_t counter =
-            ((((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles + tile) * Y::kCtas + rank;
+        const size_t counter =  // tiles of ctas x 128 rows
+            (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas + row0 / kRows;
         if (tid == 0) {
           __threadfence();  // the CTA's partial, before its arrival
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
@@ -881,7 +928,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         // the others' (all but one, mostly) are read 32 columns at a time
         float top = m2, sum = l_sum, w_own = 1.f, w_it = 0.f;
         // the one other piece that most joins have: its columns come ahead
-        const int it = W.cg == c_first ? 1 : 0;
+        const int it = mine == 0 ? 1 : 0;
         const float *other = partial(join ? it : 0);
         float4 y[4];
         auto fetch_y = [&](const float *pg, int col) {
@@ -895,15 +942,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           const float m_it = __ldcg(other + r), l_it = __ldcg(other + kRows + r);
           top = fmaxf(top, m_it);
 #pragma unroll 1
-          for (int g = 0; g < n_piece; ++g)
-            if (c_first + g != W.cg && g != it) top = fmaxf(top, __ldcg(partial(g) + r));
+          for (int e = 0; e < n_piece; ++e)
+            if (e != mine && e != it) top = fmaxf(top, __ldcg(partial(e) + r));
           const float ref = top == -INFINITY ? 0.f : top;
           w_own = ptx::ex2(m2 - ref), w_it = ptx::ex2(m_it - ref);
           sum = l_sum * w_own + l_it * w_it;
 #pragma unroll 1
-          for (int g = 0; g < n_piece; ++g)
-            if (c_first + g != W.cg && g != it)
-              sum += ptx::ex2(__ldcg(partial(g) + r) - ref) * __ldcg(partial(g) + kRows + r);
+          for (int e = 0; e < n_piece; ++e)
+            if (e != mine && e != it)
+              sum += ptx::ex2(__ldcg(partial(e) + r) - ref) * __ldcg(partial(e) + kRows + r);
           top = ref;
         }
         float w = 0.f, wx = 0.f, all = 0.f;
@@ -945,11 +992,11 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
               // (an empty piece's O holds nothing)
               if (w_it > 0.f) add(w * w_it, y);
 #pragma unroll 1
-              for (int g = 0; g < n_piece && n_piece > 2; ++g) {
-                if (c_first + g == W.cg || g == it) continue;
-                const float w_g = ptx::ex2(__ldcg(partial(g) + r) - top);
-                fetch_y(partial(g), col);
-                if (w_g > 0.f) add(w * w_g, y);
+              for (int e = 0; e < n_piece && n_piece > 2; ++e) {
+                if (e == mine || e == it) continue;
+                const float w_e = ptx::ex2(__ldcg(partial(e) + r) - top);
+                fetch_y(partial(e), col);
+                if (w_e > 0.f) add(w * w_e, y);
               }
               if (more) fetch_y(other, col + 16);
             }
@@ -992,14 +1039,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       }
       ptx::tc_fence_before();
       ptx::named_sync(5, kSoftmaxThreads);  // O and red are free again
+      g = next;
+      more = more && valid;
     }
-    if (bad) misc[2] = 1;
   }
 
   ptx::tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) ptx::cluster_sync();  // neither leaves while the other may reach it
-  if (tid == 0 && misc[2] && A.status) *A.status = LBX_ETIMEOUT;
+  if (tid == 0 && (misc[2] || misc[3]) && A.status) *A.status = LBX_ETIMEOUT;
   if (warp == 8) {
     ptx::tc_fence_after();
     if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, Y::kTmemCols);

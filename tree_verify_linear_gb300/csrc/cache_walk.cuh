@@ -67,6 +67,24 @@ __device__ __forceinline__ uint64_t low_bits(int k) {
   return k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
 }
 
+// Unit u of a key list (ctx, w0, s_eff, ns, nw of S): the position (or tree
+// node) of its first key, whether it is the tree's, and how many of its keys any
+// query sees.  A unit past the last is empty: a copy of it lies outside its
+// array and fills in zeros.
+template <class S>
+__device__ __forceinline__ void unit_of(const S &s, bool prefix, int N, int u, int &start,
+                                        bool &tree, int &cnt) {
+  const int ns = s.ns, first_tree = ns + s.nw;
+  tree = u >= first_tree && !prefix;
+  if (u >= first_tree + (prefix ? 0 : 1)) {
+    start = tree ? N : s.ctx, cnt = 0;
+    return;
+  }
+  start = u < ns ? u * kUnit : tree ? 0 : s.w0 + (u - ns) * kUnit;
+  const int end = u < ns ? s.s_eff : tree ? N : s.ctx;
+  cnt = end - start < kUnit ? end - start : kUnit;
+}
+
 // Walks a CTA's range of the block list (blocks of BU units).  Used by whole
 // warps, each lane alike; the CTAs of a pair walk alike.
 // Where whole streams per group come out within JOIN blocks (the price of
@@ -178,18 +196,8 @@ struct Walk {
     const int big = more * (each + 1);
     return at < big ? at / (each + 1) : more + (at - big) / each;
   }
-  // Unit u: the position (or tree node) of its first key, whether it is the
-  // tree's, and how many of its keys any query sees.  A unit past the last is
-  // empty: a copy of it lies outside its array and fills in zeros.
   __device__ __forceinline__ void unit(int u, int &start, bool &tree, int &cnt) const {
-    tree = u >= ns + nw && A.fixed <= 0;
-    if (u >= units) {
-      start = tree ? A.N : ctx, cnt = 0;
-      return;
-    }
-    start = u < ns ? u * kUnit : tree ? 0 : w0 + (u - ns) * kUnit;
-    const int end = u < ns ? s_eff : tree ? A.N : ctx;
-    cnt = end - start < kUnit ? end - start : kUnit;
+    unit_of(*this, A.fixed > 0, A.N, u, start, tree, cnt);
   }
 };
 
