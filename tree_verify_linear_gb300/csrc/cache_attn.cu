@@ -34,6 +34,24 @@ bool have_encode() {
 
 }  // namespace
 
+// Queries as (dh, Hq, nodes, lists); box: 64 columns of a KV head's G heads of as
+// many nodes as fit 128 rows.
+static bool encode_queries(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int nodes,
+                           int lists) {
+  if (!have_encode()) return false;
+  const int G = c->Hq / c->Hkv;
+  const cuuint64_t row = (cuuint64_t)c->Hq * c->dh * 2;
+  const cuuint64_t gdim[4] = {(cuuint64_t)c->dh, (cuuint64_t)c->Hq, (cuuint64_t)nodes,
+                              (cuuint64_t)lists};
+  const cuuint64_t gstride[3] = {(cuuint64_t)c->dh * 2, row, row * (cuuint64_t)nodes};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G), 1};
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), gdim, gstride,
+                  box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_list(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, int lists,
                  int keys) {
   if (!have_encode()) return false;
@@ -72,8 +90,8 @@ Space space_of(const lbx_attn_cfg *c) {
   const size_t part = up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
   const long long G = c->Hq / c->Hkv, rows = (long long)c->N * G;
   const size_t lists = (size_t)c->L * c->Hkv;
-  s.own = tiling(rows, c->dh);
-  s.pre = tiling(rows * c->Bq, c->dh);
+  s.own = tiling(rows, (int)G, c->dh);
+  s.pre = tiling(rows * c->Bq, (int)G, c->dh);
   s.count = part;
   s.pre_count = s.count + up256(lists * c->Bq * s.own.tiles * s.own.ctas * 4);
   s.x_o = s.pre_count, s.x_lse = s.x_o, s.bytes = s.x_lse;
@@ -141,6 +159,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     if (!encode_list(&maps.k, kp, c, c->P, c->L, kUnit) || !encode_list(&maps.v, vp, c, c->P, c->L, v_box(s.pre)))
       return LBX_ECUDA;
     maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
+    if (s.pre.ctas == 2 && !encode_queries(&maps.q, q, c, c->Bq * c->N, c->L)) return LBX_ECUDA;
     A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
     A.o32 = reinterpret_cast<float *>(base + s.x_o);
     A.lse2 = reinterpret_cast<float *>(base + s.x_lse);
@@ -155,6 +174,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if (c->T > 0 &&
       (!encode_list(&maps.k, kc, c, c->T, lists, kUnit) || !encode_list(&maps.v, vc, c, c->T, lists, v_box(s.own))))
     return LBX_ECUDA;
+  if (s.own.ctas == 2 && !encode_queries(&maps.q, q, c, c->N, lists)) return LBX_ECUDA;
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
   A.window = c->window, A.n_sink = c->n_sink;
   A.o = o, A.lse = lse;

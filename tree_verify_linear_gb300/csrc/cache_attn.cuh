@@ -36,8 +36,8 @@
 // and half the reads of L2.  Each CTA's copies arrive on its own barriers; the
 // follower passes the news on to the leader, whose one thread issues all MMAs.
 //
-// Per CTA: warps 0-7 softmax, warp 8 issues the MMAs, warp 9 the copies, warps
-// 10 and 11 of a pair bring the Q tiles.  K
+// Per CTA: warps 0-7 softmax, warp 8 issues the MMAs, warp 9 the copies, warp 10
+// of a pair brings the Q tiles.  K
 // and V arrive by TMA in 16 KB pieces through one ring, in the order the MMAs
 // take them, so that all of the shared memory keeps copies in flight.  The Q
 // tile sits in tensor memory (in shared memory for a pair, whose 128-key
@@ -96,9 +96,9 @@ template <int DH, bool PAIR>
 struct Lay {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr bool kQTmem = !PAIR;
+  static constexpr int kAtoms = DH / 64;
   static constexpr int kBlkUnits = DH == 256 && !PAIR ? 1 : 2;  // units per block
-  static constexpr int kLoaders = PAIR ? 64 : kSoftmaxThreads;   // threads that bring Q
-  static constexpr int kThreads = kSoftmaxThreads + (PAIR ? 128 : 64);
+  static constexpr int kThreads = kSoftmaxThreads + (PAIR ? 96 : 64);
   static constexpr int kBlk = kBlkUnits * kUnit;                 // keys per block
   static constexpr int kMine = kBlk / 2;                         // keys per softmax thread
   // what one CTA holds of a block: kKeys keys of K, kCols columns of V
@@ -120,8 +120,8 @@ struct Lay {
   static constexpr int kSmemSegs = kSmemRed + 4 * kRows * 4;     // Seg [4]
   static constexpr int kSmemMisc = kSmemSegs + 4 * (int)sizeof(Seg);  // int [8]
   static constexpr int kSmemBars = kSmemMisc + 32;
-  // full, empty, peer (of a pair), s[2], p[2], o[2], lo[2], segs[4], q, q free, end
-  static constexpr int kNBars = (PAIR ? 3 : 2) * kStages + 15;
+  // full, empty, peer (of a pair), s[2], p[2], o[2], lo[2], segs[4], q, q here, q free, end
+  static constexpr int kNBars = (PAIR ? 3 : 2) * kStages + 16;
   static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
   static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0, "shared memory");
 
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
   uint64_t *s_bar = peer + (PAIR ? Y::kStages : 0), *p_bar = s_bar + 2;
   uint64_t *o_bar = p_bar + 2, *lo_bar = o_bar + 2, *seg_bar = lo_bar + 2;
-  uint64_t *q_bar = seg_bar + 4, *qf_bar = q_bar + 1;
+  uint64_t *q_bar = seg_bar + 4, *qh_bar = q_bar + 1, *qf_bar = qh_bar + 1;
   uint64_t *end_bar = qf_bar + 1;
 
   if (batch_bad(A.Bq, A.N, A.T, A.ctx_len, A.parent, nullptr)) {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     for (int i = 0; i < Y::kNBars; ++i)
       ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1
                                    ? Y::kCtas * kSoftmaxThreads / 32
-                               : full + i == q_bar ? Y::kCtas * Y::kLoaders / 32
+                               : full + i == q_bar ? (PAIR ? 2 : kSoftmaxThreads / 32)
                                                    : 1);
     ptx::fence_mbar_init();
     misc[2] = misc[3] = 0;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     }
   };
   // Query rows of the walk's tile from this CTA's first on.
-  auto first_row = [&](const Walker &W) { return (W.tile * Y::kCtas + rank) * kRows; };
+  auto first_row = [&](const Walker &W) { return (W.tile * Y::kCtas + rank) * A.til.per_cta; };
   // The place of a row of the stream among all queries: of its first one, and
   // of the row from there.
   auto queries = [&](int l, int b, int h) {
@@ -225,12 +225,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   // for all the copies in flight), and a prefix's results that it will be joined
   // with.  One warp.
   auto prefetch_q = [&](const Walker &W) {
-    const int row = first_row(W), rows = A.til.rows - row < kRows ? A.til.rows - row : kRows;
+    const int row = first_row(W), left = A.til.rows - row;
+    const int rows = left < A.til.per_cta ? left : A.til.per_cta;
     if (rows <= 0) return;
-    const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
+    if constexpr (!PAIR) {
+      const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
 #pragma unroll 1
-    for (int n = A.per.node(row) + lane; n <= A.per.node(row + rows - 1); n += 32)
-      ptx::prefetch_bytes(q0 + (size_t)n * A.Hq * DH, (uint32_t)(A.G * DH * 2));
+      for (int n = A.per.node(row) + lane; n <= A.per.node(row + rows - 1); n += 32)
+        ptx::prefetch_bytes(q0 + (size_t)n * A.Hq * DH, (uint32_t)(A.G * DH * 2));
+    }
     if (A.x_o) {
       const size_t rows_all = (size_t)A.n_req * A.til.rows;
       const float4 *x0 = reinterpret_cast<const float4 *>(A.x_o) +
@@ -272,8 +275,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     Walker W(A, lane);
     Ring<Y::kStages> ring;
     int loads = 0;
-    // behind the first Q tile's loads or prefetches
-    ptx::named_sync(6, Y::kLoaders + 32);
+    // behind the first Q tile's loads
+    if constexpr (!PAIR) ptx::named_sync(6, kSoftmaxThreads + 32);
 #pragma unroll 1
     while (advance(W)) {
       if (!PAIR) prefetch_q(W);
@@ -336,46 +339,33 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       for (int i = loads > Y::kStages ? loads - Y::kStages : 0; i < loads; ++i)
         (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
     }
-  } else if (PAIR && warp >= 10) {
-    // ---- Q rows of a pair, swizzled into shared memory, 16 bytes per lane ----
-    constexpr int kPer = DH / 8, kStep = 64 / kPer, kBatch = 8;  // rows per load, loads in flight
-    const int c = (tid & 63) % kPer, r0 = (tid & 63) / kPer;
+  } else if (PAIR && warp == 10) {
+    // ---- Q tiles of a pair, by tensor copies (nodes past the last read as zeros) ----
     Walker W(A, lane);
-    bool ahead = true;
+    const uint32_t bytes = (uint32_t)(A.til.per_cta * DH * 2);
 #pragma unroll 1
     for (uint32_t seg = 0;; ++seg) {
       const bool have = advance(W);
-      if (warp == 10) {
-        publish(W, have, seg);
-        if (have) prefetch_q(W);
-      }
-      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
-      ahead = false;
+      publish(W, have, seg);
       if (!have) break;
-      const uint4 *q0 = reinterpret_cast<const uint4 *>(A.q) + queries(W.l, W.b, W.h) * kPer;
+      prefetch_q(W);
       // the last segment's score products are done
-      if (seg > 0 && !wait(qf_bar, (seg - 1) & 1)) break;
+      if (lane == 0 && (seg == 0 || wait(qf_bar, (seg - 1) & 1))) {
+        ptx::mbar_arrive_expect_tx(qh_bar, bytes);
 #pragma unroll 1
-      for (int b0 = r0; b0 < kRows; b0 += kBatch * kStep) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int row = first_row(W) + b0 + e * kStep;
-          v[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (row < A.til.rows) v[e] = q0[(size_t)query_of(row) * kPer + c];
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int rr = b0 + e * kStep;
-          *reinterpret_cast<uint4 *>(smem + Y::kSmemQ + (c / 8) * kRows * 128 + rr * 128 +
-                                     ((c & 7) ^ (rr & 7)) * 16) = v[e];
-        }
+        for (int a = 0; a < Y::kAtoms; ++a)
+          ptx::tma_load_4d(smem + Y::kSmemQ + a * kRows * 128, &maps.q, a * 64, W.h * A.G,
+                           A.per.node(first_row(W)), A.fixed > 0 ? W.l : W.l * A.n_req + W.b,
+                           qh_bar);
+        if (wait(qh_bar, seg & 1)) ptx::mbar_arrive_at(q_bar, 0);
       }
-      ptx::fence_proxy_async();
-      ptx::fence_cluster();
-      tell(q_bar);
+      if (__any_sync(0xffffffffu, bad)) break;
     }
-    if (bad) misc[2] = 1;
+    if (bad) {
+      misc[2] = 1;
+      (void)ptx::mbar_wait(qh_bar, 0);  // no copy is left behind
+      (void)ptx::mbar_wait(qh_bar, 1);
+    }
   } else if (warp == 8 && rank == 1) {
     // ---- the follower tells the leader of each piece that has landed ----
     Walker W(A, lane);
@@ -529,7 +519,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     // tile's loads go ahead of the first copies of K and V.
     bool ahead = !PAIR;
     auto go_ahead = [&]() {
-      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(Y::kLoaders + 32) : "memory");
+      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(kSoftmaxThreads + 32) : "memory");
       ahead = false;
     };
     auto load_q = [&](const volatile Seg &s) {
@@ -591,7 +581,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       ptx::named_sync(5, kSoftmaxThreads);
       const int row = s.row0 + r;
       next_bits = 0, next_lo = 0;
-      if (row < A.til.rows) {
+      if (r < A.til.per_cta && row < A.til.rows) {
         next_bits = anc[A.per.node(row)];
         if (A.window > 0) {
           const int ctx = s.ctx;
@@ -624,8 +614,9 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
 #pragma unroll 1
     while (more) {
       const int nb = g->nb, row = g->row0 + r;
-      const bool real = row < A.til.rows;
-      const bool busy = row - lane < A.til.rows;  // the warp has rows
+      const bool real = r < A.til.per_cta && row < A.til.rows;
+      // the warp has rows
+      const bool busy = quad * 32 < A.til.per_cta && row - lane < A.til.rows;
       const uint64_t tree_bits = next_bits;
       const int lo = next_lo;
 
@@ -656,17 +647,23 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
             // the stage's earlier pieces have been multiplied, so that its barrier
             // is in the phase that ends with this one's arrival
             if (i > 0) wait(&o_bar[(qi - 1) & 1], ((qi - 1) >> 1) & 1);
-            // V comes after K of the next block
+            // V comes after K of the next block; the unit's keys lie in one piece or
+            // several, or in a half of one
             const uint32_t v_piece = piece + Y::kPieces * ((i + 1 < nb ? i + 2 : nb) + i);
             constexpr int kWide = Y::kCols / 8, kBy = kOne ? 256 : 128;
-#pragma unroll 1
-            for (int idx = tid % kBy; idx < (kUnit - cnt) * kWide; idx += kBy) {
-              const int c = idx % kWide, at = (kOne ? 0 : hf * kUnit) + cnt + idx / kWide;
-              const uint32_t pc = v_piece + at / Y::kVKeys, st = pc % Y::kStages;
-              wait(&full[st], (pc / Y::kStages) & 1);
-              *reinterpret_cast<uint4 *>(smem + Y::kSmemRing + st * kPiece + (c / 8) * Y::kVAtom +
-                                         (at % Y::kVKeys) * 128 + (c & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+            constexpr int kIn = Y::kVKeys < kUnit ? Y::kVKeys : kUnit;  // keys of it in a piece
+#pragma unroll
+            for (int part = 0; part < kUnit / kIn; ++part) {
+              const int at0 = (kOne ? 0 : hf * kUnit) + part * kIn;  // key of the block
+              const uint32_t pc = v_piece + at0 / Y::kVKeys, st = pc % Y::kStages;
+              const int from = cnt - part * kIn > 0 ? cnt - part * kIn : 0;
+              if (from < kIn) wait(&full[st], (pc / Y::kStages) & 1);
+              unsigned char *v0 = smem + Y::kSmemRing + st * kPiece + (at0 % Y::kVKeys) * 128;
+#pragma unroll 2
+              for (int idx = from * kWide + tid % kBy; idx < kIn * kWide; idx += kBy)
+                *reinterpret_cast<uint4 *>(v0 + (idx % kWide / 8) * Y::kVAtom +
+                                           idx / kWide * 128 + (idx & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
             }
             ptx::fence_proxy_async();
             if constexpr (PAIR) ptx::fence_cluster();
@@ -826,7 +823,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       };
       const int n_piece = g->pieces, mine = g->mine;
       const bool whole = n_piece == 1;
-      const int rows = A.til.rows - row0 < kRows ? A.til.rows - row0 : kRows;
+      const int left = A.til.rows - row0, rows = left < A.til.per_cta ? left : A.til.per_cta;
       // Partial e of the stream: m and l per row, then O as [DH / 4][128] of
       // four columns.  Each CTA has two: its first segment's, and its last's.
       const size_t by = 2 * (size_t)A.til.group * Y::kCtas * part_floats(DH);
@@ -856,8 +853,9 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           ml[r] = m2, ml[kRows + r] = l_sum;
         }
         ptx::named_sync(5, kSoftmaxThreads);
-        const size_t counter =  // tiles of ctas x 128 rows
-            (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas + row0 / kRows;
+        const size_t counter =
+            (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas +
+            row0 / A.til.per_cta;
         if (tid == 0) {
           __threadfence();  // the CTA's partial, before its arrival
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
@@ -871,30 +869,34 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       if (join && rows <= kFewRows) {
         // few rows, maybe many pieces: the pieces' weights, then four columns of a
         // row per thread; as many rows at a time as `red` holds weights of
-        constexpr int kHeld = 4 * kRows - kFewRows;
-        float *wx_of = red + kHeld;
+        constexpr int kHeld = (4 * kRows - kFewRows) / 2;
+        float *l_of = red + kHeld, *wx_of = l_of + kHeld;
         const int step = kHeld / n_piece < rows ? kHeld / n_piece : rows;
 #pragma unroll 1
         for (int rr0 = 0; rr0 < rows; rr0 += step) {
           const int here = rows - rr0 < step ? rows - rr0 : step;
           ptx::named_sync(5, kSoftmaxThreads);  // the last weights are read
+          if (tid < here * n_piece) {
+            const float *pg = partial(tid / here) + rr0 + tid % here;
+            red[tid] = __ldcg(pg), l_of[tid] = __ldcg(pg + kRows);
+          }
+          ptx::named_sync(5, kSoftmaxThreads);
           if (tid < here) {
             const int rw = row0 + rr0 + tid;
             float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-            for (int g = 0; g < n_piece; ++g) top = fmaxf(top, __ldcg(partial(g) + rr0 + tid));
+#pragma unroll 1
+            for (int e = tid; e < here * n_piece; e += here) top = fmaxf(top, red[e]);
             if (top == -INFINITY) top = 0.f;
-#pragma unroll 4
-            for (int g = 0; g < n_piece; ++g) {
-              const float *pg = partial(g) + rr0 + tid;
-              const float e = ptx::ex2(__ldcg(pg) - top);
-              red[g * here + tid] = e;
-              sum = fmaf(e, __ldcg(pg + kRows), sum);
+#pragma unroll 1
+            for (int e = tid; e < here * n_piece; e += here) {
+              const float w_e = ptx::ex2(red[e] - top);
+              red[e] = w_e;
+              sum = fmaf(w_e, l_of[e], sum);
             }
             float w, wx;
             put_lse(rw, factors(rw, top, sum, w, wx));
 #pragma unroll 1
-            for (int g = 0; g < n_piece; ++g) red[g * here + tid] *= w;
+            for (int e = tid; e < here * n_piece; e += here) red[e] *= w;
             wx_of[tid] = wx;
           }
           ptx::named_sync(5, kSoftmaxThreads);
@@ -907,14 +909,22 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
               const float wx = wx_of[rr];
               f.x *= wx, f.y *= wx, f.z *= wx, f.w *= wx;
             }
-#pragma unroll 8
-            for (int g = 0; g < n_piece; ++g) {
-              const float e = red[g * here + rr];
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(partial(g) + 2 * kRows) +
-                                      c4 * kRows + rr0 + rr);
-              if (e > 0.f)  // (an empty piece's O holds nothing)
-                f.x = fmaf(e, y.x, f.x), f.y = fmaf(e, y.y, f.y), f.z = fmaf(e, y.z, f.z),
-                f.w = fmaf(e, y.w, f.w);
+            // ten pieces' loads in flight
+#pragma unroll 1
+            for (int e0 = 0; e0 < n_piece; e0 += 10) {
+              float4 y[10];
+#pragma unroll
+              for (int e = 0; e < 10; ++e)
+                y[e] = __ldcg(reinterpret_cast<const float4 *>(
+                                  partial(e0 + e < n_piece ? e0 + e : e0) + 2 * kRows) +
+                              c4 * kRows + rr0 + rr);
+#pragma unroll
+              for (int e = 0; e < 10; ++e) {
+                const float w_e = e0 + e < n_piece ? red[(e0 + e) * here + rr] : 0.f;
+                if (w_e > 0.f)  // (an empty piece's O holds nothing)
+                  f.x = fmaf(w_e, y[e].x, f.x), f.y = fmaf(w_e, y[e].y, f.y),
+                  f.z = fmaf(w_e, y[e].z, f.z), f.w = fmaf(w_e, y[e].w, f.w);
+              }
             }
             if (A.o32)
               reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;

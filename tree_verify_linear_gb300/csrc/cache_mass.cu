@@ -373,7 +373,7 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
   A.Bq = c->Bq, A.N = c->N, A.T = c->T, A.window = c->window, A.n_sink = c->n_sink;
   A.scale_log2 = c->scale * 1.4426950408889634f;
   A.per = per_group(G);
-  A.til = {c->N * G, 1, 1, 1, 1};
+  A.til = {c->N * G, 1, 1, 1, 1, kRows};
   A.ctx_len = ctx_len, A.parent = parent, A.accepted = accepted, A.q = q, A.lse = lse;
   A.score = score, A.score_tree = score_tree, A.status = d_status;
   // 64 KB of Q rows at most; the ring takes what they leave

@@ -16,16 +16,18 @@ constexpr int kMaxCtas = 160;      // largest grid
 constexpr int kRows = 128;         // query rows per CTA
 constexpr int kMaxGroup = 8;       // most row tiles that run side by side
 
-// Row tiles of a stream, of 128 rows (256 for pairs of CTAs): `sets` sets of up
-// to `group` tiles each.
+// Row tiles of a stream: `sets` sets of up to `group` tiles each, a tile of one
+// CTA's 128 rows, or of a pair's whole nodes (whose queries one tensor copy
+// brings: G heads of 128 / G nodes per CTA).
 struct Tiling {
-  int rows, tiles, sets, group, ctas;  // ctas: per tile
+  int rows, tiles, sets, group, ctas, per_cta;  // ctas: per tile; per_cta: rows
 };
-inline Tiling tiling(long long rows, int dh) {
+inline Tiling tiling(long long rows, int G, int dh) {
   Tiling t;
   t.rows = (int)rows;
-  t.ctas = rows > kRows && dh >= 128 ? 2 : 1;
-  t.tiles = (int)((rows + t.ctas * kRows - 1) / (t.ctas * kRows));
+  t.ctas = rows > kRows && dh >= 128 && G <= kRows ? 2 : 1;
+  t.per_cta = t.ctas == 2 ? kRows / G * G : kRows;
+  t.tiles = (int)((rows + t.ctas * t.per_cta - 1) / (t.ctas * t.per_cta));
   t.sets = (t.tiles + kMaxGroup - 1) / kMaxGroup;
   t.group = (t.tiles + t.sets - 1) / t.sets;
   return t;
@@ -34,6 +36,7 @@ inline Tiling tiling(long long rows, int dh) {
 struct AttnMaps {
   CUtensorMap k, v;    // (dh, Hkv, positions, layer x request), boxes of 64 columns
   CUtensorMap kt, vt;  // the tree's
+  CUtensorMap q;       // (dh, Hq, nodes, lists), boxes of 64 columns of a pair's Q rows
 };
 
 // (dh, Hkv, len, lists) view of a [lists][len][Hkv][dh] array of 16-bit values;
