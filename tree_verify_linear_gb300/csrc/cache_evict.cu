@@ -1,7 +1,8 @@
 // cache_evict.cu -- append the accepted path to the cache and keep the best
 // `budget` entries per (layer, request, KV head): lbx_cache_evict.
 //
-// One CTA per (layer, request, KV head).  The candidates' scores become 32-bit
+// One CTA per (layer, request, KV head), or a cluster of CTAs that all make the
+// same selection and share the moves.  The candidates' scores become 32-bit
 // keys of the same order (protected entries above all, NaN below all).  A
 // radix selection finds the key of the last entry that stays, eight bits at a
 // time: a histogram of the digit among the keys that share the digits found
@@ -10,8 +11,10 @@
 // lowest indexes), with running counts per 64 of them, from which the r-th
 // entry to move and the r-th free place follow by a binary search.  Entries
 // that move come from at or past min(ctx, size) and go below size into places
-// that nothing is read from, so that all rows move at once, in place.
+// that nothing is read from, so that all rows move at once, in place; only the
+// selection has to be done everywhere before the first move.
 #include "cache_common.cuh"
+#include "cache_ptx.cuh"
 
 namespace lbx {
 namespace cache {
@@ -23,10 +26,11 @@ constexpr int kBatch = 1024;  // rows whose source and place are listed at a tim
 // keys are kept in shared memory when this many bytes hold them (two CTAs per
 // SM), else made again from the scores and positions in each pass
 constexpr size_t kKeyBytes = 96 * 1024;
+constexpr int kFly = 8;  // 16-byte pieces of rows in flight per thread
 
 struct Args {
   lbx_attn_cfg c;
-  int budget, n_recent, keep_keys;
+  int budget, n_recent, keep_keys, share;  // share: CTAs per selection
   const int32_t *ctx_len, *seen, *parent, *accepted;
   const uint16_t *kt, *vt;
   const float *score_tree;
@@ -63,7 +67,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long lbg = blockIdx.x;
+  const int rank = A.share > 1 ? (int)ptx::cluster_rank() : 0;
+  const long long lbg = blockIdx.x / A.share;
   const int g = (int)(lbg % c.Hkv);
   const long long lb = lbg / c.Hkv;
   const int b = (int)(lb % c.Bq);
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
   const int low = ctx < size ? ctx : size;  // entries below do not move
   const int seen_out = seen + n - ctx, recent = seen_out - A.n_recent;
   if (tid < c.N && (path >> tid & 1)) node_at[__popcll(path & ((1ull << tid) - 1))] = tid;
-  if (tid == 0 && lb == b && g == 0) A.ctx_out[b] = size, A.seen_out[b] = seen_out;
+  if (tid == 0 && rank == 0 && lb == b && g == 0) A.ctx_out[b] = size, A.seen_out[b] = seen_out;
 
   float *score = A.score + lbg * c.T;
   int32_t *pos = A.pos + lbg * c.T;
@@ -177,9 +182,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
                           : before[low >> 6] + __popcll(stay[low >> 6] & below(low & 63));
   const int moves = size - (int)stay_low;
 
+  if (A.share > 1) ptx::cluster_sync();  // every score and position is read
+
   // ---- move: batches of listed rows ----
-  const int upr = c.dh / 8;  // 16-byte pieces per row
-  for (int m0 = 0; m0 < moves; m0 += kBatch) {
+  const int shift = c.dh == 256 ? 6 : c.dh == 128 ? 5 : 4;  // 16-byte pieces of K and V: 2^shift
+  for (int m0 = rank * kBatch; m0 < moves; m0 += A.share * kBatch) {
     const int cnt = moves - m0 < kBatch ? moves - m0 : kBatch;
     for (int t = tid; t < cnt; t += kThreads) {
       const uint32_t rs = stay_low + (uint32_t)(m0 + t);  // number among those that stay
@@ -210,17 +217,28 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
       score[d] = s < ctx ? score[s] : score_tree[node_at[s - ctx]];
       pos[d] = s < ctx ? pos[s] : seen + (s - ctx);
     }
-    for (int u = tid; u < cnt * 2 * upr; u += kThreads) {
-      const int t = u / (2 * upr), e = u - t * 2 * upr;
-      const int s = src[t];
-      const bool is_v = e >= upr;
-      const int piece = is_v ? e - upr : e;
-      const uint16_t *from =
-          s < ctx ? (is_v ? A.vc : A.kc) + (((size_t)lb * c.T + s) * c.Hkv + g) * c.dh
-                  : (is_v ? A.vt : A.kt) +
-                        (((size_t)lb * c.N + node_at[s - ctx]) * c.Hkv + g) * c.dh;
-      uint16_t *to = (is_v ? A.vc : A.kc) + (((size_t)lb * c.T + dst[t]) * c.Hkv + g) * c.dh;
-      reinterpret_cast<uint4 *>(to)[piece] = reinterpret_cast<const uint4 *>(from)[piece];
+    for (int u0 = tid; u0 < cnt << shift; u0 += kFly * kThreads) {
+      uint4 piece[kFly];
+      // piece u of the batch: half of a row's are K's, half V's
+      auto place = [&](int u, bool from) -> uint4 * {
+        const int e = u & ((1 << shift) - 1), half = 1 << (shift - 1), t = u >> shift;
+        const int s = src[t], i = from ? s : dst[t];
+        const bool is_v = e >= half, old = !from || s < ctx;
+        const uint16_t *base = old ? (is_v ? A.vc : A.kc) : (is_v ? A.vt : A.kt);
+        const size_t row = old ? (size_t)lb * c.T + i : (size_t)lb * c.N + node_at[s - ctx];
+        return reinterpret_cast<uint4 *>(const_cast<uint16_t *>(base)) +
+               (row * c.Hkv + g) * half + (e & (half - 1));
+      };
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int u = u0 + k * kThreads;
+        if (u < cnt << shift) piece[k] = __ldcs(place(u, true));
+      }
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int u = u0 + k * kThreads;
+        if (u < cnt << shift) *place(u, false) = piece[k];
+      }
     }
     __syncthreads();
   }
@@ -251,9 +269,22 @@ extern "C" int lbx_cache_evict(const lbx_attn_cfg *c, int budget, int n_recent,
   if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)shared) != cudaSuccess)
     return LBX_ECUDA;
-  const Args A = {*c,    budget, n_recent,   keep_keys, ctx_len, seen,  parent, accepted,
-                  k_tree, v_tree, score_tree, k_cache,   v_cache, score, pos,    ctx_out,
-                  seen_out, d_status};
-  evict_kernel<<<(unsigned)(c->L * c->Bq * c->Hkv), kThreads, shared, stream>>>(A);
-  return cudaGetLastError() == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  // A cache larger than its budget may have many rows to move: CTAs share each
+  // selection until the GPU has about four of them per SM.  A full cache moves a
+  // few rows per step, and one CTA does.
+  const long long lists = (long long)c->L * c->Bq * c->Hkv;
+  int share = 1;
+  if (c->T > budget + c->N)
+    while (share < 8 && lists * share * 2 <= 4 * 152) share *= 2;
+  const Args A = {*c,     budget, n_recent,   keep_keys, share,   ctx_len, seen, parent,  accepted,
+                  k_tree, v_tree, score_tree, k_cache,   v_cache, score,   pos,  ctx_out, seen_out,
+                  d_status};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(lists * share)), cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = shared, cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)share, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = share > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_kernel, A) == cudaSuccess ? LBX_OK : LBX_ECUDA;
 }

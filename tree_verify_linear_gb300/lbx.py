@@ -291,31 +291,33 @@ def make_attn_cfg(L, Bq, N, Hq, Hkv, dh, T, P=0, window=0, n_sink=0, dtype=LBX_B
                         n_sink=n_sink, dtype=dtype, scale=dh ** -0.5 if scale is None else scale)
 
 
-def _elem(cfg):
-    """A check for the arrays of the config's element type."""
-    return _bf if cfg.dtype == LBX_BF16 else _f16
+_ELEM = {LBX_BF16: torch.bfloat16, LBX_F16: torch.float16}
 
 
-def _f16(t, name):
-    return _ptr(t, (torch.float16,), name)
-
-
-def _sized(t, shape, name):
-    if t is not None and tuple(t.shape) != shape:
+def _refuse(t, shape, dtype, name):
+    """What _at refused, said in _ptr's words."""
+    ok = _BF16_OK if dtype is torch.bfloat16 else (dtype,)
+    p = _ptr(t, ok, name)
+    if tuple(t.shape) != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return p
 
 
-def _attn_shapes(cfg, **arrays):
-    """Check the shapes of the named arrays against the config."""
-    L, Bq, N, Hq, Hkv, dh, T = cfg.L, cfg.Bq, cfg.N, cfg.Hq, cfg.Hkv, cfg.dh, cfg.T
-    shapes = {"q": (L, Bq, N, Hq, dh), "o": (L, Bq, N, Hq, dh), "lse": (L, Bq, N, Hq),
-              "k_cache": (L, Bq, T, Hkv, dh), "v_cache": (L, Bq, T, Hkv, dh),
-              "k_tree": (L, Bq, N, Hkv, dh), "v_tree": (L, Bq, N, Hkv, dh),
-              "k_prefix": (L, cfg.P, Hkv, dh), "v_prefix": (L, cfg.P, Hkv, dh),
-              "score": (L, Bq, Hkv, T), "pos": (L, Bq, Hkv, T), "score_tree": (L, Bq, Hkv, N),
-              "parent": (Bq, N)}
-    for name, t in arrays.items():
-        _sized(t, shapes.get(name, (Bq,)), name)
+def _at(t, shape, dtype, name):
+    """The address of a contiguous CUDA tensor of this shape and type (the calls
+    below check a dozen of them, which for a small call costs as much as the
+    kernel: one line for the ordinary case)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _refuse(t, shape, dtype, name)
+
+
+def _stream_of(t, stream):
+    """The given stream, or the current one of the tensor's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def lbx_cache_attn_workspace_size(cfg: lbx_attn_cfg) -> int:
@@ -330,60 +332,68 @@ def new_cache_attn_workspace(cfg: lbx_attn_cfg, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def _attention_arrays(cfg, ctx_len, parent, q, prefix, k_cache, v_cache, k_tree, v_tree, o, lse):
+    """Addresses of the attention calls' arrays in the C order."""
+    L, Bq, N, Hq, Hkv, dh, T = cfg.L, cfg.Bq, cfg.N, cfg.Hq, cfg.Hkv, cfg.dh, cfg.T
+    el, i32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32
+    qs, cs, ts = (L, Bq, N, Hq, dh), (L, Bq, T, Hkv, dh), (L, Bq, N, Hkv, dh)
+    return (_at(ctx_len, (Bq,), i32, "ctx_len"), _at(parent, (Bq, N), i32, "parent"),
+            _at(q, qs, el, "q"), *prefix, _at(k_cache, cs, el, "k_cache"),
+            _at(v_cache, cs, el, "v_cache"), _at(k_tree, ts, el, "k_tree"),
+            _at(v_tree, ts, el, "v_tree"), _at(o, qs, el, "o"),
+            None if lse is None else _at(lse, (L, Bq, N, Hq), torch.float32, "lse"))
+
+
 def lbx_window_attention(cfg, ctx_len, parent, q, k_cache, v_cache, k_tree, v_tree, o, workspace,
                          lse=None, d_status=None, stream=None):
     """Tree attention with a sliding window and visible first positions."""
-    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, q=q, k_cache=k_cache, v_cache=v_cache,
-                 k_tree=k_tree, v_tree=v_tree, o=o, lse=lse)
-    el = _elem(cfg)
     _check("lbx_window_attention", load().lbx_window_attention(
-        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"), el(q, "q"),
-        el(k_cache, "k_cache"), el(v_cache, "v_cache"), el(k_tree, "k_tree"),
-        el(v_tree, "v_tree"), el(o, "o"), _f32(lse, "lse"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _i32(d_status, "d_status"),
-        _stream(stream)))
+        ctypes.byref(cfg), *_attention_arrays(cfg, ctx_len, parent, q, (), k_cache, v_cache,
+                                              k_tree, v_tree, o, lse),
+        _ptr(workspace, None, "workspace"), workspace.nbytes, _i32(d_status, "d_status"),
+        _stream_of(q, stream)))
 
 
 def lbx_prefix_attention(cfg, ctx_len, parent, q, k_prefix, v_prefix, k_cache, v_cache, k_tree,
                          v_tree, o, workspace, lse=None, d_status=None, stream=None):
     """Attention of a batch over one shared prefix, its own caches and trees."""
-    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, q=q, k_prefix=k_prefix, v_prefix=v_prefix,
-                 k_cache=k_cache, v_cache=v_cache, k_tree=k_tree, v_tree=v_tree, o=o, lse=lse)
-    el = _elem(cfg)
+    el, ps = _ELEM.get(cfg.dtype, torch.bfloat16), (cfg.L, cfg.P, cfg.Hkv, cfg.dh)
+    prefix = _at(k_prefix, ps, el, "k_prefix"), _at(v_prefix, ps, el, "v_prefix")
     _check("lbx_prefix_attention", load().lbx_prefix_attention(
-        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"), el(q, "q"),
-        el(k_prefix, "k_prefix"), el(v_prefix, "v_prefix"), el(k_cache, "k_cache"),
-        el(v_cache, "v_cache"), el(k_tree, "k_tree"), el(v_tree, "v_tree"), el(o, "o"),
-        _f32(lse, "lse"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _i32(d_status, "d_status"),
-        _stream(stream)))
+        ctypes.byref(cfg), *_attention_arrays(cfg, ctx_len, parent, q, prefix, k_cache, v_cache,
+                                              k_tree, v_tree, o, lse),
+        _ptr(workspace, None, "workspace"), workspace.nbytes, _i32(d_status, "d_status"),
+        _stream_of(q, stream)))
 
 
 def lbx_attention_mass(cfg, ctx_len, parent, accepted, q, lse, k_cache, k_tree, score, score_tree,
                        d_status=None, stream=None):
     """Accumulate the accepted path's attention weights per key."""
-    _attn_shapes(cfg, ctx_len=ctx_len, parent=parent, accepted=accepted, q=q, lse=lse,
-                 k_cache=k_cache, k_tree=k_tree, score=score, score_tree=score_tree)
-    el = _elem(cfg)
+    L, Bq, N, Hq, Hkv, dh, T = cfg.L, cfg.Bq, cfg.N, cfg.Hq, cfg.Hkv, cfg.dh, cfg.T
+    el, i32, f32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, torch.float32
     _check("lbx_attention_mass", load().lbx_attention_mass(
-        ctypes.byref(cfg), _i32(ctx_len, "ctx_len"), _i32(parent, "parent"),
-        _i32(accepted, "accepted"), el(q, "q"), _f32(lse, "lse"), el(k_cache, "k_cache"),
-        el(k_tree, "k_tree"), _f32(score, "score"), _f32(score_tree, "score_tree"),
-        _i32(d_status, "d_status"), _stream(stream)))
+        ctypes.byref(cfg), _at(ctx_len, (Bq,), i32, "ctx_len"),
+        _at(parent, (Bq, N), i32, "parent"), _at(accepted, (Bq,), i32, "accepted"),
+        _at(q, (L, Bq, N, Hq, dh), el, "q"), _at(lse, (L, Bq, N, Hq), f32, "lse"),
+        _at(k_cache, (L, Bq, T, Hkv, dh), el, "k_cache"),
+        _at(k_tree, (L, Bq, N, Hkv, dh), el, "k_tree"), _at(score, (L, Bq, Hkv, T), f32, "score"),
+        _at(score_tree, (L, Bq, Hkv, N), f32, "score_tree"), _i32(d_status, "d_status"),
+        _stream_of(q, stream)))
 
 
 def lbx_cache_evict(cfg, budget, n_recent, ctx_len, seen, parent, accepted, k_tree, v_tree,
                     score_tree, k_cache, v_cache, score, pos, ctx_out, seen_out, d_status=None,
                     stream=None):
     """Append the accepted path to the cache and keep its `budget` best entries."""
-    _attn_shapes(cfg, ctx_len=ctx_len, seen=seen, parent=parent, accepted=accepted, k_tree=k_tree,
-                 v_tree=v_tree, score_tree=score_tree, k_cache=k_cache, v_cache=v_cache,
-                 score=score, pos=pos, ctx_out=ctx_out, seen_out=seen_out)
-    el = _elem(cfg)
+    L, Bq, N, Hkv, dh, T = cfg.L, cfg.Bq, cfg.N, cfg.Hkv, cfg.dh, cfg.T
+    el, i32, f32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, torch.float32
+    cs, ts, per = (L, Bq, T, Hkv, dh), (L, Bq, N, Hkv, dh), (Bq,)
     _check("lbx_cache_evict", load().lbx_cache_evict(
-        ctypes.byref(cfg), int(budget), int(n_recent), _i32(ctx_len, "ctx_len"),
-        _i32(seen, "seen"), _i32(parent, "parent"), _i32(accepted, "accepted"),
-        el(k_tree, "k_tree"), el(v_tree, "v_tree"), _f32(score_tree, "score_tree"),
-        el(k_cache, "k_cache"), el(v_cache, "v_cache"), _f32(score, "score"), _i32(pos, "pos"),
-        _i32(ctx_out, "ctx_out"), _i32(seen_out, "seen_out"), _i32(d_status, "d_status"),
-        _stream(stream)))
+        ctypes.byref(cfg), int(budget), int(n_recent), _at(ctx_len, per, i32, "ctx_len"),
+        _at(seen, per, i32, "seen"), _at(parent, (Bq, N), i32, "parent"),
+        _at(accepted, per, i32, "accepted"), _at(k_tree, ts, el, "k_tree"),
+        _at(v_tree, ts, el, "v_tree"), _at(score_tree, (L, Bq, Hkv, N), f32, "score_tree"),
+        _at(k_cache, cs, el, "k_cache"), _at(v_cache, cs, el, "v_cache"),
+        _at(score, (L, Bq, Hkv, T), f32, "score"), _at(pos, (L, Bq, Hkv, T), i32, "pos"),
+        _at(ctx_out, per, i32, "ctx_out"), _at(seen_out, per, i32, "seen_out"),
+        _i32(d_status, "d_status"), _stream_of(score, stream)))
