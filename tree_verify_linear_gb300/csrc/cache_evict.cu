@@ -15,6 +15,7 @@
 // selection has to be done everywhere before the first move.
 #include "cache_common.cuh"
 #include "cache_ptx.cuh"
+#include "cache_walk.cuh"
 
 namespace lbx {
 namespace cache {
@@ -22,9 +23,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 1024;  // rows whose source and place are listed at a time
+constexpr int kBatch = 512;  // rows whose source and place are listed at a time
 // keys are kept in shared memory when this many bytes hold them (two CTAs per
-// SM), else made again from the scores and positions in each pass
+// SM, three at 16384 entries), else made again from the scores and positions in each pass
 constexpr size_t kKeyBytes = 96 * 1024;
 constexpr int kFly = 8;  // 16-byte pieces of rows in flight per thread
 
@@ -99,8 +100,10 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
   // ---- the key of the last entry that stays, and how many equal ones do ----
   uint32_t last = 0, equal = 0;
   if (n > size) {
-    if (A.keep_keys)
+    if (A.keep_keys) {
+#pragma unroll 8
       for (int i = tid; i < n; i += kThreads) keys[i] = make_key(i);
+    }
     uint32_t want = (uint32_t)size;  // how many of the keys that match so far stay
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
@@ -270,12 +273,15 @@ extern "C" int lbx_cache_evict(const lbx_attn_cfg *c, int budget, int n_recent,
                            (int)shared) != cudaSuccess)
     return LBX_ECUDA;
   // A cache larger than its budget may have many rows to move: CTAs share each
-  // selection until the GPU has about four of them per SM.  A full cache moves a
-  // few rows per step, and one CTA does.
+  // selection as long as all of them run at once (two waves of clusters would
+  // take twice the time).  A full cache moves a few rows per step, and one does.
   const long long lists = (long long)c->L * c->Bq * c->Hkv;
-  int share = 1;
+  int share = 1, per_sm = 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, evict_kernel, kThreads, shared) !=
+      cudaSuccess)
+    return LBX_ECUDA;
   if (c->T > budget + c->N)
-    while (share < 8 && lists * share * 2 <= 4 * 152) share *= 2;
+    while (share < 8 && lists * share * 2 <= (long long)per_sm * grid_limit()) share *= 2;
   const Args A = {*c,     budget, n_recent,   keep_keys, share,   ctx_len, seen, parent,  accepted,
                   k_tree, v_tree, score_tree, k_cache,   v_cache, score,   pos,  ctx_out, seen_out,
                   d_status};
