@@ -57,28 +57,19 @@ __device__ __forceinline__ int batch_bad(int Bq, int N, int T, const int32_t *ct
   return __syncthreads_or(bad);
 }
 
-// Node n's ancestors and itself, as a bit mask (its depth is the number of
-// set bits less one).
-__device__ __forceinline__ uint64_t path_mask(const int32_t *parent, int n) {
+// The path from the root to `node` as a bit mask (its depth is the number of
+// set bits less one).  The warp holds two parents per lane: following them one
+// load after the other would take a trip to memory per step.
+__device__ __forceinline__ uint64_t warp_path(const int32_t *parent, int N, int node, int lane) {
+  const int p0 = lane < N ? parent[lane] : -1, p1 = lane + 32 < N ? parent[lane + 32] : -1;
   uint64_t m = 0;
-  for (int s = 0; s < kMaxNodes && n >= 0; ++s) {
-    m |= 1ull << n;
-    n = parent[n];
+#pragma unroll 1
+  for (int s = 0; s < kMaxNodes && node >= 0; ++s) {
+    m |= 1ull << node;
+    const int a = __shfl_sync(0xffffffffu, p0, node & 31), b = __shfl_sync(0xffffffffu, p1, node & 31);
+    node = node < 32 ? a : b;
   }
   return m;
-}
-
-// Whether the query at position `at` sees position j <= at.
-__device__ __forceinline__ bool sees(int at, int j, int window, int n_sink) {
-  return window == 0 || at - j < window || j < n_sink;
-}
-
-__device__ __forceinline__ float to_f32(uint16_t x, int dtype) {
-  return dtype == LBX_BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
-}
-__device__ __forceinline__ uint16_t from_f32(float x, int dtype) {
-  return dtype == LBX_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
-                           : __half_as_ushort(__float2half_rn(x));
 }
 
 }  // namespace cache

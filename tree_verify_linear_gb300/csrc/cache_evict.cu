@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
   const long long lb = lbg / c.Hkv;
   const int b = (int)(lb % c.Bq);
   const int ctx = A.ctx_len[b], seen = A.seen[b];
-  const uint64_t path = path_mask(A.parent + (size_t)b * c.N, A.accepted[b]);
+  const uint64_t path = warp_path(A.parent + (size_t)b * c.N, c.N, A.accepted[b], lane);
   const int n = ctx + __popcll(path), size = n < A.budget ? n : A.budget;
   const int low = ctx < size ? ctx : size;  // entries below do not move
   const int seen_out = seen + n - ctx, recent = seen_out - A.n_recent;
@@ -87,13 +87,16 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
   const int words = (n + 63) / 64, cap_words = (c.T + c.N + 63) / 64;
   uint64_t *stay = reinterpret_cast<uint64_t *>(smem);  // one bit per candidate
   uint32_t *before = reinterpret_cast<uint32_t *>(stay + cap_words);  // set in earlier words
-  uint32_t *keys = before + cap_words;                                // only with keep_keys
+  // only with keep_keys
+  uint32_t *keys = reinterpret_cast<uint32_t *>(smem + ((cap_words * 12 + 15) & ~15));
   __syncthreads();
 
+  auto rank_of = [&](int p, float s) {
+    return p < c.n_sink || p >= recent ? kSafe : key_of(s);
+  };
   auto make_key = [&](int i) -> uint32_t {
-    const int p = i < ctx ? pos[i] : seen + (i - ctx);
-    if (p < c.n_sink || p >= recent) return kSafe;
-    return key_of(i < ctx ? score[i] : score_tree[node_at[i - ctx]]);
+    return i < ctx ? rank_of(pos[i], score[i])
+                   : rank_of(seen + (i - ctx), score_tree[node_at[i - ctx]]);
   };
   auto key = [&](int i) -> uint32_t { return A.keep_keys ? keys[i] : make_key(i); };
 
@@ -101,8 +104,19 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Args A) {
   uint32_t last = 0, equal = 0;
   if (n > size) {
     if (A.keep_keys) {
-#pragma unroll 8
-      for (int i = tid; i < n; i += kThreads) keys[i] = make_key(i);
+      // four entries at a time where the rows are aligned, then the rest
+      const bool wide = ((reinterpret_cast<uintptr_t>(score) | reinterpret_cast<uintptr_t>(pos)) &
+                         15) == 0;
+      const int quads = wide ? ctx / 4 : 0;
+#pragma unroll 4
+      for (int i = tid; i < quads; i += kThreads) {
+        const int4 p = reinterpret_cast<const int4 *>(pos)[i];
+        const float4 s = reinterpret_cast<const float4 *>(score)[i];
+        reinterpret_cast<uint4 *>(keys)[i] = make_uint4(rank_of(p.x, s.x), rank_of(p.y, s.y),
+                                                        rank_of(p.z, s.z), rank_of(p.w, s.w));
+      }
+#pragma unroll 2
+      for (int i = quads * 4 + tid; i < n; i += kThreads) keys[i] = make_key(i);
     }
     uint32_t want = (uint32_t)size;  // how many of the keys that match so far stay
     for (int shift = 24; shift >= 0; shift -= 8) {
@@ -266,7 +280,7 @@ extern "C" int lbx_cache_evict(const lbx_attn_cfg *c, int budget, int n_recent,
       !aligned_to(score, 4) || !aligned_to(pos, 4) || !aligned_to(ctx_out, 4) ||
       !aligned_to(seen_out, 4) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
-  const size_t n = (size_t)c->T + c->N, bits = (n + 63) / 64 * 12;
+  const size_t n = (size_t)c->T + c->N, bits = ((n + 63) / 64 * 12 + 15) & ~(size_t)15;
   const int keep_keys = n * 4 + bits <= kKeyBytes;
   const size_t shared = bits + (keep_keys ? n * 4 : 0);
   if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

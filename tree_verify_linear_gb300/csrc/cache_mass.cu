@@ -51,20 +51,6 @@ constexpr int kTailBars = kTailMisc + 16;                // full, empty, s[2], f
 constexpr int kTail = kTailBars + (2 * kMaxStages + 6) * 8;
 static_assert(kTail <= 3072, "shared memory");
 
-// The path from the root to `node` as a bit mask: the warp holds two parents
-// per lane.
-__device__ __forceinline__ uint64_t warp_path(const int32_t *parent, int N, int node, int lane) {
-  const int p0 = lane < N ? parent[lane] : -1, p1 = lane + 32 < N ? parent[lane + 32] : -1;
-  uint64_t m = 0;
-#pragma unroll 1
-  for (int s = 0; s < kMaxNodes && node >= 0; ++s) {
-    m |= 1ull << node;
-    const int a = __shfl_sync(0xffffffffu, p0, node & 31), b = __shfl_sync(0xffffffffu, p1, node & 31);
-    node = node < 32 ? a : b;
-  }
-  return m;
-}
-
 template <int DH, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     mass_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ MassArgs A) {
