@@ -5,7 +5,8 @@
 // The window call is one launch over the requests' key lists.  The prefix call
 // is two: the queries of all requests over the prefix, whose normalised result
 // and base-2 lse go to the workspace in fp32, then the requests' own keys,
-// whose last step joins the two by their lse.
+// whose last step joins the two by their lse.  The second begins on the SMs that
+// the first one's CTAs leave and waits for its results only there.
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -81,23 +82,27 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The workspace: partials and counters of the requests' launch; with a prefix
 // also the prefix launch's, its results and their lse.
+size_t part_bytes(const lbx_attn_cfg *c) {
+  return up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
+}
 struct Space {
   Tiling own, pre;
-  size_t count, pre_count, x_o, x_lse, bytes;  // offsets after the partials
+  size_t count, pre_part, pre_count, x_o, x_lse, bytes;  // offsets after the partials
 };
 Space space_of(const lbx_attn_cfg *c) {
   Space s;
-  const size_t part = up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
+  const size_t part = part_bytes(c);
   const long long G = c->Hq / c->Hkv, rows = (long long)c->N * G;
   const size_t lists = (size_t)c->L * c->Hkv;
   s.own = tiling(rows, (int)G, c->dh);
   s.pre = tiling(rows * c->Bq, (int)G, c->dh);
   s.count = part;
-  s.pre_count = s.count + up256(lists * c->Bq * s.own.tiles * s.own.ctas * 4);
-  s.x_o = s.pre_count, s.x_lse = s.x_o, s.bytes = s.x_lse;
-  if (c->P > 0) {
+  s.pre_part = s.count + up256(lists * c->Bq * s.own.tiles * s.own.ctas * 4);
+  s.pre_count = s.x_o = s.x_lse = s.bytes = s.pre_part;
+  if (c->P > 0) {  // the two launches overlap: nothing is shared
     const size_t queries = (size_t)c->L * c->Bq * c->N * c->Hq;
-    s.x_o += up256(lists * s.pre.tiles * s.pre.ctas * 4);
+    s.pre_count = s.pre_part + part;
+    s.x_o = s.pre_count + up256(lists * s.pre.tiles * s.pre.ctas * 4);
     s.x_lse = s.x_o + up256(queries * c->dh * 4);
     s.bytes = s.x_lse + up256(queries * 4);
   }
@@ -107,7 +112,7 @@ Space space_of(const lbx_attn_cfg *c) {
 // The block list's indexes are 32-bit.
 bool list_ok(const lbx_attn_cfg *c, const Space &s) {
   auto fits = [&](const Tiling &t, long long lists, long long len) {
-    return lists * t.sets < (1LL << 31) / (len / kUnit + 3);
+    return lists * t.sets < (1LL << 31) / (len / kUnit + 3 + kLeadBlocks);
   };
   const long long lists = (long long)c->L * c->Hkv, G = c->Hq / c->Hkv;
   if ((long long)c->Bq * c->N * G >= (1LL << 32) / G) return false;  // see PerGroup
@@ -161,6 +166,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
     if (s.pre.ctas == 2 && !encode_queries(&maps.q, q, c, c->Bq * c->N, c->L)) return LBX_ECUDA;
     A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
+    A.part = reinterpret_cast<float *>(base + s.pre_part);
     A.o32 = reinterpret_cast<float *>(base + s.x_o);
     A.lse2 = reinterpret_cast<float *>(base + s.x_lse);
     A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count);
@@ -178,6 +184,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
   A.window = c->window, A.n_sink = c->n_sink;
   A.o = o, A.lse = lse;
+  A.part = reinterpret_cast<float *>(base);
   A.counters = reinterpret_cast<unsigned int *>(base + s.count);
   return launch(maps) ? LBX_OK : LBX_ECUDA;
 }

@@ -133,8 +133,9 @@ struct Lay {
 
 // Most rows whose pieces are joined by columns instead of by rows.
 constexpr int kFewRows = 32;
-// What joining the pieces of a cut stream costs, in blocks.
-constexpr int kJoinBlocks = 3;
+// What a stream costs beside its blocks, and joining the pieces of a cut one
+// (measured about 13000 and 10000 cycles; a block takes 2200 to 3400).
+constexpr int kLeadBlocks = 4, kJoinBlocks = 3;
 
 // Parts of P: f16 once, bf16 hi + lo.
 template <bool F16>
@@ -199,7 +200,9 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
-  using Walker = Walk<Y::kBlkUnits, kJoinBlocks, AttnArgs>;
+  // the requests' launch may take the SMs that this one leaves
+  if (A.o32) ptx::launch_dependents();
+  using Walker = Walk<Y::kBlkUnits, kLeadBlocks, kJoinBlocks, AttnArgs>;
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
@@ -221,28 +224,16 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     return (size_t)(l * A.n_req + b) * A.nodes * A.Hq + h * A.G;
   };
   auto query_of = [&](int row) { return row + A.per.node(row) * (A.Hq - A.G); };
-  // The segment's queries into L2, ahead of its keys (loads of them would wait
-  // for all the copies in flight), and a prefix's results that it will be joined
-  // with.  One warp.
+  // Without a pair: the segment's queries into L2, ahead of its keys (loads of
+  // them would wait for all the copies in flight).  One warp.
   auto prefetch_q = [&](const Walker &W) {
     const int row = first_row(W), left = A.til.rows - row;
     const int rows = left < A.til.per_cta ? left : A.til.per_cta;
     if (rows <= 0) return;
-    if constexpr (!PAIR) {
-      const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
+    const uint16_t *q0 = A.q + queries(W.l, W.b, W.h) * DH;
 #pragma unroll 1
-      for (int n = A.per.node(row) + lane; n <= A.per.node(row + rows - 1); n += 32)
-        ptx::prefetch_bytes(q0 + (size_t)n * A.Hq * DH, (uint32_t)(A.G * DH * 2));
-    }
-    if (A.x_o) {
-      const size_t rows_all = (size_t)A.n_req * A.til.rows;
-      const float4 *x0 = reinterpret_cast<const float4 *>(A.x_o) +
-                         (size_t)(W.l * A.Hkv + W.h) * rows_all * (DH / 4) +
-                         (size_t)W.b * A.til.rows + row;
-#pragma unroll 1
-      for (int c = lane; c < DH / 4; c += 32)
-        ptx::prefetch_bytes(x0 + c * rows_all, (uint32_t)(rows * 16));
-    }
+    for (int n = A.per.node(row) + lane; n <= A.per.node(row + rows - 1); n += 32)
+      ptx::prefetch_bytes(q0 + (size_t)n * A.Hq * DH, (uint32_t)(A.G * DH * 2));
   };
   // The next segment with a tile for this CTA.
   auto advance = [&](Walker &W) {
@@ -259,7 +250,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     Seg &s = segs[k & 3];
     s.have = have;
     if (have) {
-      const int c_first = W.owner(W.first), c_last = W.owner(W.first + W.entries() - 1);
+      const int c_first = W.owner(W.first), c_last = W.owner(W.last);
       s.l = W.l, s.h = W.h, s.b = W.b, s.row0 = first_row(W);
       s.blk0 = W.blk0, s.nb = W.blk1 - W.blk0;
       s.ctx = W.ctx, s.w0 = W.w0, s.s_eff = W.s_eff, s.ns = W.ns, s.nw = W.nw;
@@ -348,7 +339,6 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       const bool have = advance(W);
       publish(W, have, seg);
       if (!have) break;
-      prefetch_q(W);
       // the last segment's score products are done
       if (lane == 0 && (seg == 0 || wait(qf_bar, (seg - 1) & 1))) {
         ptx::mbar_arrive_expect_tx(qh_bar, bytes);
@@ -553,12 +543,16 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     // warp's work; they lie where the last maxima were.
     uint64_t next_bits = 0;
     int next_lo = 0;
+    int up[2] = {-1, -1};
+    auto parents = [&](const volatile Seg &s) {  // ahead of look()
+      if (A.fixed > 0 || warp != 0) return;
+      const int32_t *parent = A.parent + (size_t)s.b * A.N;
+      up[0] = lane < A.N ? parent[lane] : -1, up[1] = lane + 32 < A.N ? parent[lane + 32] : -1;
+    };
     auto look = [&](const volatile Seg &s) {
       if (A.fixed > 0) return;
       uint64_t *anc = reinterpret_cast<uint64_t *>(red);
       if (warp == 0) {
-        const int32_t *parent = A.parent + (size_t)s.b * A.N;
-        int up[2] = {lane < A.N ? parent[lane] : -1, lane + 32 < A.N ? parent[lane + 32] : -1};
         uint64_t m[2] = {1ull << lane, 1ull << (lane + 32)};
 #pragma unroll 1
         for (int step = 0; step < 6; ++step) {
@@ -606,6 +600,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     const volatile Seg *g = segs;
     bool more = published(0) && g->have;
     if (more) {
+      parents(*g);
       if constexpr (!PAIR) load_q(*g);
       look(*g);
     } else {
@@ -766,6 +761,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       const volatile Seg *next = &segs[k & 3];
       more = published(k) && next->have;
       if (more) {
+        parents(*next);
         if constexpr (!PAIR) load_q(*next);
         look(*next);
       }
@@ -778,14 +774,15 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       auto place_x = [&](int rw) {
         return (size_t)(l * A.Hkv + h) * rows_all * (DH / 4) + (size_t)b * A.til.rows + rw;
       };
-      float4 x[4];
-      auto fetch_x = [&](int col) {
+      float4 x[2][4];
+      auto fetch_x = [&](float4(&to)[4], int col) {
         const float4 *from =
             reinterpret_cast<const float4 *>(A.x_o) + place_x(row) + col / 4 * rows_all;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __ldcg(from + e * rows_all);
+        for (int e = 0; e < 4; ++e) to[e] = __ldcg(from + e * rows_all);
       };
-      if (A.x_o && real) fetch_x(hf * kHalf);
+      if (A.x_o) ptx::wait_prerequisite_grid();  // that launch is complete
+      if (A.x_o && real) fetch_x(x[0], hf * kHalf), fetch_x(x[1], hf * kHalf + 16);
       wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
       ptx::tc_fence_after();
       ptx::named_sync(1 + quad, 64);  // the last maxima are read
@@ -936,7 +933,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       } else if (busy && valid && (whole || join)) {
         // a row per two threads; this CTA's piece is still in tensor memory,
         // the others' (all but one, mostly) are read 32 columns at a time
-        float top = m2, sum = l_sum, w_own = 1.f, w_it = 0.f;
+        float top = m2, sum = l_sum;
         // the one other piece that most joins have: its columns come ahead
         const int it = mine == 0 ? 1 : 0;
         const float *other = partial(join ? it : 0);
@@ -949,19 +946,18 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         };
         if (join) {
           fetch_y(other, hf * kHalf);
-          const float m_it = __ldcg(other + r), l_it = __ldcg(other + kRows + r);
-          top = fmaxf(top, m_it);
+          // (everything in the pieces' order, whichever CTA joins them)
 #pragma unroll 1
           for (int e = 0; e < n_piece; ++e)
-            if (e != mine && e != it) top = fmaxf(top, __ldcg(partial(e) + r));
-          const float ref = top == -INFINITY ? 0.f : top;
-          w_own = ptx::ex2(m2 - ref), w_it = ptx::ex2(m_it - ref);
-          sum = l_sum * w_own + l_it * w_it;
+            if (e != mine) top = fmaxf(top, __ldcg(partial(e) + r));
+          if (top == -INFINITY) top = 0.f;
+          sum = 0.f;
 #pragma unroll 1
-          for (int e = 0; e < n_piece; ++e)
-            if (e != mine && e != it)
-              sum += ptx::ex2(__ldcg(partial(e) + r) - ref) * __ldcg(partial(e) + kRows + r);
-          top = ref;
+          for (int e = 0; e < n_piece; ++e) {
+            const float m_e = e == mine ? m2 : __ldcg(partial(e) + r);
+            const float l_e = e == mine ? l_sum : __ldcg(partial(e) + kRows + r);
+            sum = fmaf(ptx::ex2(m_e - top), l_e, sum);
+          }
         }
         float w = 0.f, wx = 0.f, all = 0.f;
         if (real) all = factors(row, top, sum, w, wx);
@@ -983,8 +979,10 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
             float v[16];
             ptx::tmem_ld16(tq + Y::kColO + (uint32_t)col, v);
             ptx::tmem_wait_ld();
+            if (!join) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= w * w_own;
+              for (int e = 0; e < 16; ++e) v[e] *= w;
+            }
             auto add = [&](float f, const float4(&z)[4]) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -994,21 +992,27 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
                 v[4 * e + 3] = fmaf(f, z[e].w, v[4 * e + 3]);
               }
             };
-            if (A.x_o && real) {
-              add(wx, x);
-              if (more) fetch_x(col + 16);
-            }
             if (join && real) {
-              // (an empty piece's O holds nothing)
-              if (w_it > 0.f) add(w * w_it, y);
+              float u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = v[e], v[e] = 0.f;
 #pragma unroll 1
-              for (int e = 0; e < n_piece && n_piece > 2; ++e) {
-                if (e == mine || e == it) continue;
-                const float w_e = ptx::ex2(__ldcg(partial(e) + r) - top);
-                fetch_y(partial(e), col);
-                if (w_e > 0.f) add(w * w_e, y);
+              for (int e = 0; e < n_piece; ++e) {
+                const float m_e = e == mine ? m2 : __ldcg(partial(e) + r);
+                const float f = w * ptx::ex2(m_e - top);
+                if (e == mine) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i] = fmaf(f, u[i], v[i]);
+                } else {
+                  if (e != it) fetch_y(partial(e), col);
+                  if (f > 0.f) add(f, y);  // (an empty piece's O holds nothing)
+                }
               }
               if (more) fetch_y(other, col + 16);
+            }
+            if (A.x_o && real) {
+              add(wx, x[j]);
+              if (c + 1 < kHalf / 32) fetch_x(x[j], col + 32);
             }
             if (A.o32) {
               float4 *at = reinterpret_cast<float4 *>(A.o32) + place_x(row) + col / 4 * rows_all;
@@ -1079,10 +1083,14 @@ cudaError_t launch_attn_of(const AttnMaps &maps, const AttnArgs &A, int grid,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(Lay<DH, PAIR>::kThreads);
   cfg.dynamicSmemBytes = bytes, cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = PAIR ? 2 : 1, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at, cfg.numAttrs = PAIR ? 1 : 0;
+  // behind a prefix: begins where that launch's CTAs end, waits for its results
+  // where it joins them
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = A.x_o ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, A);
 }
 

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-  Walk<2, 0, MassArgs> W(A, lane);
+  Walk<2, 3, 0, MassArgs> W(A, lane);
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
@@ -347,7 +347,7 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
   const int lists = c->L * c->Bq, G = c->Hq / c->Hkv;
   // 32-bit indexes of the block list, and of rows (see PerGroup)
   if ((long long)c->N * G >= (1LL << 32) / G) return LBX_EINVAL;
-  if ((long long)lists * c->Hkv >= (1LL << 31) / (c->T / kUnit + 3)) return LBX_EINVAL;
+  if ((long long)lists * c->Hkv >= (1LL << 31) / (c->T / kUnit + 6)) return LBX_EINVAL;
   const int grid = grid_limit();
   if (grid < 1) return LBX_ECUDA;
   AttnMaps maps = {};

@@ -90,11 +90,12 @@ __device__ __forceinline__ void unit_of(const S &s, bool prefix, int N, int u, i
 
 // Walks a CTA's range of the block list (blocks of BU units).  Used by whole
 // warps, each lane alike; the CTAs of a pair walk alike.
-// Where whole streams per group come out within JOIN blocks (the price of
-// joining the pieces of a cut stream) of equal ranges of blocks, a stream
-// counts as one entry of the list and is not cut.  Args has the shapes: L, Hkv,
-// N, n_req, fixed, window, n_sink, ctx_len and til.
-template <int BU, int JOIN, class Args>
+// A stream also costs what it takes to begin and end it, LEAD blocks that come
+// before its own in the list.  Where whole streams per group come out within
+// JOIN blocks (the price of joining the pieces of a cut stream) of equal ranges,
+// a stream counts as one entry of the list and is not cut.  Args has the shapes:
+// L, Hkv, N, n_req, fixed, window, n_sink, ctx_len and til.
+template <int BU, int LEAD, int JOIN, class Args>
 struct Walk {
   const Args &A;
   // the list's entries and how they are cut: `more` ranges of each + 1 entries,
@@ -104,7 +105,7 @@ struct Walk {
   bool uncut;
   // the current segment
   int l, h, set, tile, blk0, blk1;
-  int first;  // the stream's first entry
+  int first, last;  // its entries: of the stream's first and last block
   bool live;  // this CTA has a tile of the stream
 
   // units of a request's key list
@@ -125,13 +126,13 @@ struct Walk {
   }
   // Streams per request; entries of each of the current request's in the list.
   __device__ __forceinline__ int streams() const { return A.L * A.Hkv * A.til.sets; }
-  __device__ __forceinline__ int entries() const { return uncut ? 1 : nblk; }
+  __device__ __forceinline__ int entries() const { return uncut ? 1 : nblk + LEAD; }
 
   __device__ __forceinline__ Walk(const Args &a, int lane) : A(a), uncut(false) {
     int sum = 0, most = 0;
 #pragma unroll 1
     for (int r = lane; r < A.n_req; r += 32) {
-      sum += blocks_of(r);
+      sum += blocks_of(r) + LEAD;
       most = nblk > most ? nblk : most;
     }
     sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
@@ -139,7 +140,7 @@ struct Walk {
     total = sum * streams();
     groups = (int)(gridDim.x / (unsigned)(A.til.group * A.til.ctas));
     const long long all = (long long)streams() * A.n_req;
-    uncut = (all + groups - 1) / groups * most <= (total + groups - 1) / groups + JOIN;
+    uncut = (all + groups - 1) / groups * (most + LEAD) <= (total + groups - 1) / groups + JOIN;
     if (uncut) total = (int)all;
     if (groups > total) groups = total;
     each = total / groups, more = total - each * groups;
@@ -176,23 +177,26 @@ struct Walk {
 
   // Take the next segment; false at the end of the range.
   __device__ __forceinline__ bool next() {
-    if (x >= x_end) return false;
 #pragma unroll 1
-    while (x - per_b_base >= entries() * streams()) {
-      per_b_base += entries() * streams();
-      blocks_of(++b);
+    while (x < x_end) {
+#pragma unroll 1
+      while (x - per_b_base >= entries() * streams()) {
+        per_b_base += entries() * streams();
+        blocks_of(++b);
+      }
+      const int in_b = x - per_b_base, s = in_b / entries(), at = x - (in_b - s * entries());
+      const int lh = A.til.sets > 1 ? s / A.til.sets : s;
+      set = s - lh * A.til.sets;
+      l = lh / A.Hkv, h = lh - l * A.Hkv;
+      first = uncut ? at : at + LEAD, last = uncut ? at : first + nblk - 1;
+      blk0 = uncut || x < first ? 0 : x - first;
+      blk1 = uncut || x_end > last ? nblk : x_end - first;
+      x = at + entries();
+      tile = set * A.til.group + slot_in_group;
+      live = tile < A.til.tiles;
+      if (blk1 > blk0) return true;  // else the range ends before the stream's blocks
     }
-    const int in_b = x - per_b_base, s = in_b / entries();
-    blk0 = in_b - s * entries();
-    first = x - blk0;
-    const int lh = A.til.sets > 1 ? s / A.til.sets : s;
-    set = s - lh * A.til.sets;
-    l = lh / A.Hkv, h = lh - l * A.Hkv;
-    blk1 = uncut || x_end - first >= nblk ? nblk : x_end - first;
-    x = uncut ? x + 1 : first + blk1;
-    tile = set * A.til.group + slot_in_group;
-    live = tile < A.til.tiles;
-    return true;
+    return false;
   }
   __device__ __forceinline__ int begin_of(int g) const { return g * each + (g < more ? g : more); }
   __device__ __forceinline__ int owner(int at) const {
