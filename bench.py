@@ -100,7 +100,7 @@ def read_peaks():
 # Sources of kernels that the verify step never launches; a change to them
 # leaves the recorded traffic of the verify workloads valid.
 OTHER_OPS = ("accept_walk.cu", "ddtree_build.cu", "tree_attn.cu", "cache_common.cuh",
-             "cache_attn.cu", "cache_attn.cuh", "cache_attn_64.cu", "cache_attn_128.cu",
+             "cache_attn.cu", "cache_attn.cuh", "cache_few.cu", "cache_attn_64.cu", "cache_attn_128.cu",
              "cache_attn_256.cu", "cache_ptx.cuh", "cache_walk.cuh", "cache_mass.cu", "cache_evict.cu")
 
 

@@ -131,6 +131,14 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if ((lse && !aligned_to(lse, 4)) || (status && !aligned_to(status, 4))) return LBX_EINVAL;
   const Space s = space_of(c);
   if (!list_ok(c, s) || ws_bytes < s.bytes) return LBX_EINVAL;
+  unsigned char *base = static_cast<unsigned char *>(ws);
+  if (const int chunks = few_chunks(c)) {
+    const FewArgs F = {*c, chunks, c->scale * 1.4426950408889634f, ctx_len, parent, q, kp, vp, kc,
+                       vc, kt, vt, o, lse, reinterpret_cast<float *>(base),
+                       reinterpret_cast<unsigned int *>(base + s.count), status};
+    return launch_few(F, stream) == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  }
+
   // rows of a box of V: a piece of it may hold fewer keys than a unit
   static_assert(Lay<128, false>::kVBox == kUnit && Lay<64, false>::kVBox == kUnit &&
                     Lay<128, true>::kVBox == kUnit && Lay<256, true>::kVBox == kUnit,
@@ -141,7 +149,6 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
 
   const int nsm = grid_limit();
   if (nsm < 1) return LBX_ECUDA;
-  unsigned char *base = static_cast<unsigned char *>(ws);
   AttnArgs A = {};
   A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = c->Hq / c->Hkv;
   A.Bq = c->Bq, A.N = c->N, A.T = c->T;

@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       } else if (busy && valid && (whole || join)) {
         // a row per two threads; this CTA's piece is still in tensor memory,
         // the others' (all but one, mostly) are read 32 columns at a time
-        float top = m2, sum = l_sum;
+        float top = m2, sum = l_sum, f_it = 0.f, f_mine = 1.f;
         // the one other piece that most joins have: its columns come ahead
         const int it = mine == 0 ? 1 : 0;
         const float *other = partial(join ? it : 0);
@@ -956,12 +956,16 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           for (int e = 0; e < n_piece; ++e) {
             const float m_e = e == mine ? m2 : __ldcg(partial(e) + r);
             const float l_e = e == mine ? l_sum : __ldcg(partial(e) + kRows + r);
-            sum = fmaf(ptx::ex2(m_e - top), l_e, sum);
+            const float f = ptx::ex2(m_e - top);
+            sum = fmaf(f, l_e, sum);
+            if (e == mine) f_mine = f;
+            if (e == it) f_it = f;
           }
         }
         float w = 0.f, wx = 0.f, all = 0.f;
         if (real) all = factors(row, top, sum, w, wx);
         if (real && hf == 0) put_lse(row, all);
+        f_mine *= w, f_it *= w;
         // where the four rows of this lane's group of lanes go
         uint64_t to[4] = {};
         if (A.o) {
@@ -998,15 +1002,17 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
               for (int e = 0; e < 16; ++e) u[e] = v[e], v[e] = 0.f;
 #pragma unroll 1
               for (int e = 0; e < n_piece; ++e) {
-                const float m_e = e == mine ? m2 : __ldcg(partial(e) + r);
-                const float f = w * ptx::ex2(m_e - top);
                 if (e == mine) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) v[i] = fmaf(f, u[i], v[i]);
-                } else {
-                  if (e != it) fetch_y(partial(e), col);
-                  if (f > 0.f) add(f, y);  // (an empty piece's O holds nothing)
+                  for (int i = 0; i < 16; ++i) v[i] = fmaf(f_mine, u[i], v[i]);
+                  continue;
                 }
+                float f = f_it;
+                if (e != it) {
+                  f = ptx::ex2(__ldcg(partial(e) + r) - top) * w;
+                  fetch_y(partial(e), col);
+                }
+                if (f > 0.f) add(f, y);  // (an empty piece's O holds nothing)
               }
               if (more) fetch_y(other, col + 16);
             }
@@ -1068,6 +1074,24 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
     else ptx::tmem_dealloc(tmem, Y::kTmemCols);
   }
 }
+
+// The small kernel of cache_few.cu.
+struct FewArgs {
+  lbx_attn_cfg c;
+  int chunks;  // units a stream can have
+  float scale_log2;
+  const int32_t *ctx_len, *parent;
+  const uint16_t *q, *kp, *vp, *kc, *vc, *kt, *vt;
+  uint16_t *o;
+  float *lse, *part;
+  unsigned int *counters;
+  int32_t *status;
+};
+// Most units of all streams it takes (see few_chunks).
+constexpr int kFewUnits = 1024;
+// Units per stream, or 0 where the call is not one for the small kernel.
+int few_chunks(const lbx_attn_cfg *c);
+cudaError_t launch_few(const FewArgs &A, cudaStream_t stream);
 
 // Launches of one head dimension and type (instances in cache_attn_*.cu).
 template <int DH>
