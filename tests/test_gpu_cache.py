@@ -121,6 +121,12 @@ BUSY = {
     "dh64_three_tiles": (dict(L=3, Bq=4, N=64, Hq=30, Hkv=5, dh=64, T=2000, ctx=[2000, 77, 1231, 640]), 0, 0),
     "dh64_f16_window": (dict(L=9, Bq=5, N=3, Hq=16, Hkv=8, dh=64, T=3000, dtype="f16",
                              ctx=[3000, 2900, 511, 1025, 2001]), 1500, 3),
+    # one or two streams over the whole GPU: joins of many pieces
+    "one_stream_pair": (dict(L=1, Bq=1, N=22, Hq=6, Hkv=1, dh=256, T=9000, ctx=[8990]), 0, 0),
+    "one_stream_few_rows": (dict(L=1, Bq=1, N=3, Hq=6, Hkv=1, dh=256, T=9000, dtype="f16", ctx=[9000]), 0, 0),
+    "two_streams_dh128": (dict(L=1, Bq=2, N=40, Hq=7, Hkv=1, dh=128, T=7000, ctx=[7000, 5001]), 0, 0),
+    "one_stream_dh64": (dict(L=1, Bq=1, N=12, Hq=4, Hkv=1, dh=64, T=20000, ctx=[19999]), 0, 0),
+    "one_prefix": (dict(L=1, Bq=7, N=22, Hq=5, Hkv=1, dh=128, T=60, P=9001, dtype="f16"), 0, 0),
     "prefix_dh256": (dict(L=3, Bq=5, N=22, Hq=12, Hkv=2, dh=256, T=700, P=3001, ctx=[700, 3, 501, 258, 640]), 0, 0),
     "prefix_dh128_f16": (dict(L=3, Bq=9, N=7, Hq=32, Hkv=4, dh=128, T=900, P=4000, dtype="f16"), 0, 0),
     "prefix_dh64": (dict(L=4, Bq=40, N=2, Hq=16, Hkv=4, dh=64, T=300, P=2049), 0, 0),
@@ -153,9 +159,15 @@ def test_lse_may_be_left_out():
     assert status == 0 and torch.equal(o, o2)
 
 
-@pytest.mark.parametrize("P", [0, 140])
-def test_calls_in_a_row_and_on_another_stream_agree(P):
-    inp = R.make_inputs(2, 3, 22, 12, 2, 256, 400, P=P, ctx=[400, 20, 333], seed=9)
+@pytest.mark.parametrize("P,sizes", [
+    (0, dict(L=2, Bq=3, N=22, Hq=12, Hkv=2, dh=256, T=400, ctx=[400, 20, 333])),
+    (140, dict(L=2, Bq=3, N=22, Hq=12, Hkv=2, dh=256, T=400, ctx=[400, 20, 333])),
+    (0, dict(L=1, Bq=2, N=22, Hq=6, Hkv=1, dh=128, T=9000, ctx=[9000, 8001])),
+    (0, dict(L=3, Bq=5, N=9, Hq=8, Hkv=4, dh=256, T=3000, dtype="f16")),
+    (5000, dict(L=1, Bq=6, N=5, Hq=8, Hkv=2, dh=64, T=700)),
+])
+def test_calls_in_a_row_and_on_another_stream_agree(P, sizes):
+    inp = R.make_inputs(**sizes, P=P, seed=9)
     a, al, _ = run_attention(inp)
     b, bl, _ = run_attention(inp, calls=3)
     c, cl, status = run_attention(inp, calls=2, stream=torch.cuda.Stream())

@@ -88,6 +88,7 @@ size_t part_bytes(const lbx_attn_cfg *c) {
 struct Space {
   Tiling own, pre;
   size_t count, pre_part, pre_count, x_o, x_lse, bytes;  // offsets after the partials
+  size_t own_n, pre_n;                                      // counters of each kind
 };
 Space space_of(const lbx_attn_cfg *c) {
   Space s;
@@ -97,12 +98,13 @@ Space space_of(const lbx_attn_cfg *c) {
   s.own = tiling(rows, (int)G, c->dh);
   s.pre = tiling(rows * c->Bq, (int)G, c->dh);
   s.count = part;
-  s.pre_part = s.count + up256(lists * c->Bq * s.own.tiles * s.own.ctas * 4);
+  s.own_n = lists * c->Bq * s.own.tiles * s.own.ctas, s.pre_n = lists * s.pre.tiles * s.pre.ctas;
+  s.pre_part = s.count + up256(2 * s.own_n * 4);
   s.pre_count = s.x_o = s.x_lse = s.bytes = s.pre_part;
   if (c->P > 0) {  // the two launches overlap: nothing is shared
     const size_t queries = (size_t)c->L * c->Bq * c->N * c->Hq;
     s.pre_count = s.pre_part + part;
-    s.x_o = s.pre_count + up256(lists * s.pre.tiles * s.pre.ctas * 4);
+    s.x_o = s.pre_count + up256(2 * s.pre_n * 4);
     s.x_lse = s.x_o + up256(queries * c->dh * 4);
     s.bytes = s.x_lse + up256(queries * 4);
   }
@@ -176,7 +178,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     A.part = reinterpret_cast<float *>(base + s.pre_part);
     A.o32 = reinterpret_cast<float *>(base + s.x_o);
     A.lse2 = reinterpret_cast<float *>(base + s.x_lse);
-    A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count);
+    A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count), A.n_counters = s.pre_n;
     if (!launch(maps)) return LBX_ECUDA;
     A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr, A.fixed = 0;
   }
@@ -192,7 +194,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   A.window = c->window, A.n_sink = c->n_sink;
   A.o = o, A.lse = lse;
   A.part = reinterpret_cast<float *>(base);
-  A.counters = reinterpret_cast<unsigned int *>(base + s.count);
+  A.counters = reinterpret_cast<unsigned int *>(base + s.count), A.n_counters = s.own_n;
   return launch(maps) ? LBX_OK : LBX_ECUDA;
 }
 

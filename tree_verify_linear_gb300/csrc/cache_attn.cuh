@@ -28,7 +28,9 @@
 // group of them, one for each row tile of the stream, which then read the same
 // keys at the same time): one CTA per SM, whatever the lengths.  Streams that
 // a range does not cover whole leave partials (m, l, O) in the workspace, at
-// most two per CTA, and the last CTA of a row tile to finish joins them.
+// most two per CTA.  Of two pieces the CTA that finishes last joins both (its own
+// from tensor memory); of more, all but the last piece's CTAs, whose ranges end
+// there, wait for each other and join some of the rows each.
 //
 // Streams of more than 128 rows (head dimensions 128 and 256) run on pairs of
 // CTAs that share one product of 256 rows: each CTA keeps half of the block's
@@ -76,7 +78,8 @@ struct AttnArgs {
   float *lse;                  // natural lse or NULL
   const float *x_o, *x_lse2;   // a prefix's results to join, or NULL
   float *part;
-  unsigned int *counters;      // one per (stream, tile, CTA of the pair)
+  unsigned int *counters;      // pieces written, per (stream, tile, CTA of the pair) ...
+  size_t n_counters;           // ... and, behind as many, pieces that have joined
   int32_t *status;
 };
 
@@ -828,6 +831,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       const int late = g->late ? (int)part_floats(DH) : 0;
       auto partial = [&](int e) { return part0 + e * by + (e == 0 ? late : 0); };
       bool join = false;
+      const size_t counter = (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas +
+                             row0 / A.til.per_cta;
       if (!whole && rows > 0) {
         float4 *to = reinterpret_cast<float4 *>(partial(mine) + 2 * kRows);
         if (busy && valid) {
@@ -850,28 +855,31 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           ml[r] = m2, ml[kRows + r] = l_sum;
         }
         ptx::named_sync(5, kSoftmaxThreads);
-        const size_t counter =
-            (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas +
-            row0 / A.til.per_cta;
         if (tid == 0) {
           __threadfence();  // the CTA's partial, before its arrival
           const unsigned prev = atomicAdd(&A.counters[counter], 1u);
-          misc[1] = (int)prev == n_piece - 1 ? 1 : 0;
-          if (misc[1]) A.counters[counter] = 0u;  // for the next call
+          int go = n_piece == 2 ? prev == 1 : mine < n_piece - 1;
+          if (n_piece == 2 && go) A.counters[counter] = 0u;  // for the next call
+          if (n_piece > 2 && go && !ptx::wait_count(&A.counters[counter], (unsigned)n_piece))
+            go = 0, misc[3] = 1;
+          misc[1] = go;
           __threadfence();
         }
         ptx::named_sync(5, kSoftmaxThreads);
         join = misc[1] != 0;
       }
-      if (join && rows <= kFewRows) {
-        // few rows, maybe many pieces: the pieces' weights, then four columns of a
-        // row per thread; as many rows at a time as `red` holds weights of
+      if (join && (n_piece > 2 || rows <= kFewRows)) {
+        // few rows, or this CTA's share of them: the pieces' weights, then four
+        // columns of a row per thread; as many rows at a time as `red` holds
+        // weights of
+        const int from = n_piece > 2 ? rows * mine / (n_piece - 1) : 0;
+        const int to = n_piece > 2 ? rows * (mine + 1) / (n_piece - 1) : rows;
         constexpr int kHeld = (4 * kRows - kFewRows) / 2;
         float *l_of = red + kHeld, *wx_of = l_of + kHeld;
-        const int step = kHeld / n_piece < rows ? kHeld / n_piece : rows;
+        const int step = kHeld / n_piece < kFewRows ? kHeld / n_piece : kFewRows;
 #pragma unroll 1
-        for (int rr0 = 0; rr0 < rows; rr0 += step) {
-          const int here = rows - rr0 < step ? rows - rr0 : step;
+        for (int rr0 = from; rr0 < to; rr0 += step) {
+          const int here = to - rr0 < step ? to - rr0 : step;
           ptx::named_sync(5, kSoftmaxThreads);  // the last weights are read
           if (tid < here * n_piece) {
             const float *pg = partial(tid / here) + rr0 + tid % here;
@@ -930,37 +938,32 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
                   make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
           }
         }
+        if (n_piece > 2) {
+          ptx::named_sync(5, kSoftmaxThreads);
+          if (tid == 0 &&
+              atomicAdd(&A.counters[A.n_counters + counter], 1u) == (unsigned)n_piece - 2)
+            A.counters[counter] = A.counters[A.n_counters + counter] = 0u;  // for the next call
+        }
       } else if (busy && valid && (whole || join)) {
-        // a row per two threads; this CTA's piece is still in tensor memory,
-        // the others' (all but one, mostly) are read 32 columns at a time
+        // a row per two threads; this CTA's piece is still in tensor memory, the
+        // other one's columns come ahead
         float top = m2, sum = l_sum, f_it = 0.f, f_mine = 1.f;
-        // the one other piece that most joins have: its columns come ahead
-        const int it = mine == 0 ? 1 : 0;
-        const float *other = partial(join ? it : 0);
+        const float *other = partial(join ? 1 - mine : 0);
         float4 y[4];
-        auto fetch_y = [&](const float *pg, int col) {
+        auto fetch_y = [&](int col) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            y[e] = __ldcg(reinterpret_cast<const float4 *>(pg + 2 * kRows) +
+            y[e] = __ldcg(reinterpret_cast<const float4 *>(other + 2 * kRows) +
                           (col / 4 + e) * kRows + r);
         };
         if (join) {
-          fetch_y(other, hf * kHalf);
-          // (everything in the pieces' order, whichever CTA joins them)
-#pragma unroll 1
-          for (int e = 0; e < n_piece; ++e)
-            if (e != mine) top = fmaxf(top, __ldcg(partial(e) + r));
+          fetch_y(hf * kHalf);
+          const float m_it = __ldcg(other + r), l_it = __ldcg(other + kRows + r);
+          top = fmaxf(top, m_it);
           if (top == -INFINITY) top = 0.f;
-          sum = 0.f;
-#pragma unroll 1
-          for (int e = 0; e < n_piece; ++e) {
-            const float m_e = e == mine ? m2 : __ldcg(partial(e) + r);
-            const float l_e = e == mine ? l_sum : __ldcg(partial(e) + kRows + r);
-            const float f = ptx::ex2(m_e - top);
-            sum = fmaf(f, l_e, sum);
-            if (e == mine) f_mine = f;
-            if (e == it) f_it = f;
-          }
+          f_mine = ptx::ex2(m2 - top), f_it = ptx::ex2(m_it - top);
+          // (in the pieces' order, whichever CTA joins them)
+          sum = mine == 0 ? fmaf(f_it, l_it, f_mine * l_sum) : fmaf(f_mine, l_sum, f_it * l_it);
         }
         float w = 0.f, wx = 0.f, all = 0.f;
         if (real) all = factors(row, top, sum, w, wx);
@@ -997,24 +1000,19 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
               }
             };
             if (join && real) {
-              float u[16];
+              if (!(f_it > 0.f)) {  // an empty piece's O holds nothing
 #pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = v[e], v[e] = 0.f;
-#pragma unroll 1
-              for (int e = 0; e < n_piece; ++e) {
-                if (e == mine) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) v[i] = fmaf(f_mine, u[i], v[i]);
-                  continue;
-                }
-                float f = f_it;
-                if (e != it) {
-                  f = ptx::ex2(__ldcg(partial(e) + r) - top) * w;
-                  fetch_y(partial(e), col);
-                }
-                if (f > 0.f) add(f, y);  // (an empty piece's O holds nothing)
+                for (int e = 0; e < 4; ++e) y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
               }
-              if (more) fetch_y(other, col + 16);
+              const float *z = reinterpret_cast<const float *>(y);
+              if (mine == 0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = fmaf(f_it, z[e], f_mine * v[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = fmaf(f_mine, v[e], f_it * z[e]);
+              }
+              if (more) fetch_y(col + 16);
             }
             if (A.x_o && real) {
               add(wx, x[j]);

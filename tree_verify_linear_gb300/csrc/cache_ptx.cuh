@@ -52,6 +52,21 @@ __host__ __device__ constexpr uint32_t idesc_16(bool f16, int M, int N, bool b_m
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Wait until other CTAs of the launch have brought a counter up to n; false after
+// four seconds (they run already, or as soon as the SMs are free of other
+// launches).
+__device__ __forceinline__ bool wait_count(const unsigned int *count, unsigned int n) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    unsigned int c;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(c) : "l"(count) : "memory");
+    if (c >= n) return true;
+    if (globaltimer_ns() - t0 > 4 * kWaitNs) return false;
+    __nanosleep(100);
+  }
+  return false;
+}
+
 // ---- a pair of CTAs (a cluster of two, rank 0 the leader) ------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
