@@ -74,9 +74,9 @@ struct AttnArgs {
   const int32_t *ctx_len, *parent;
   const uint16_t *q;
   uint16_t *o;                 // results in the 16-bit type ...
-  float *o32, *lse2;           // ... or normalised in fp32 with the base-2 lse (prefix)
+  float *o32, *lse2;           // ... or normalised in fp32 with the base-2 lse
   float *lse;                  // natural lse or NULL
-  const float *x_o, *x_lse2;   // a prefix's results to join, or NULL
+  const float *x_o, *x_lse2;   // the first launch's results to join, or NULL
   float *part;
   unsigned int *counters;      // pieces written, per (stream, tile, CTA of the pair) ...
   size_t n_counters;           // ... and, behind as many, pieces that have joined
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
-  // the requests' launch may take the SMs that this one leaves
+  // the prefix's launch may take the SMs that this one leaves
   if (A.o32) ptx::launch_dependents();
   using Walker = Walk<Y::kBlkUnits, kLeadBlocks, kJoinBlocks, AttnArgs>;
   bool bad = false;  // a wait of this thread gave up: it waits no more
@@ -351,6 +351,19 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
                            A.per.node(first_row(W)), A.fixed > 0 ? W.l : W.l * A.n_req + W.b,
                            qh_bar);
         if (wait(qh_bar, seg & 1)) ptx::mbar_arrive_at(q_bar, 0);
+      }
+      __syncwarp();
+      if (A.x_o) {  // what the segment will be joined with, into L2
+        ptx::wait_prerequisite_grid();
+        const int row = first_row(W), left = A.til.rows - row;
+        const int rows = left < A.til.per_cta ? left : A.til.per_cta;
+        const size_t rows_all = (size_t)A.n_req * A.til.rows;
+        const float4 *x0 = reinterpret_cast<const float4 *>(A.x_o) +
+                           (size_t)(W.l * A.Hkv + W.h) * rows_all * (DH / 4) +
+                           (size_t)W.b * A.til.rows + row;
+#pragma unroll 1
+        for (int c = lane; c < DH / 4 && rows > 0; c += 32)
+          ptx::prefetch_bytes(x0 + c * rows_all, (uint32_t)(rows * 16));
       }
       if (__any_sync(0xffffffffu, bad)) break;
     }
@@ -770,7 +783,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       }
 
       // ---- this segment's result: whole, or a partial ----
-      // A finished row of the stream in the prefix's results ([layer, KV head]
+      // A finished row of the stream in the first launch's results ([layer, KV head]
       // [DH / 4][all rows] of four columns); the first columns are fetched ahead.
       const int l = g->l, h = g->h, b = g->b, row0 = g->row0;
       const size_t rows_all = (size_t)A.n_req * A.til.rows;
@@ -796,12 +809,12 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       const bool valid = misc[3] == 0;
       float l_sum = sums[r] + sums[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
-      // A finished row's place among all queries, and in the prefix's lse.
+      // A finished row's place among all queries, and in the first launch's lse.
       auto place = [&](int rw) { return queries(l, b, h) + query_of(rw); };
       auto place_xl = [&](int rw) {
         return (size_t)(l * A.Hkv + h) * rows_all + (size_t)b * A.til.rows + rw;
       };
-      // The factors of this stream's O and of the prefix's o, and the row's lse.
+      // The factors of this stream's O and of the first launch's o, and the row's lse.
       auto factors = [&](int rw, float m, float sum, float &w, float &wx) {
         const float own = sum > 0.f ? m + __log2f(sum) : -INFINITY;
         float all = own;
@@ -1108,8 +1121,8 @@ cudaError_t launch_attn_of(const AttnMaps &maps, const AttnArgs &A, int grid,
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = PAIR ? 2 : 1, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  // behind a prefix: begins where that launch's CTAs end, waits for its results
-  // where it joins them
+  // the second launch of a call begins where the first one's CTAs end and waits for
+  // its results where it joins them
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at, cfg.numAttrs = A.x_o ? 2 : 1;
