@@ -149,6 +149,34 @@ def mass(inp, lse, score, window=0, n_sink=0, scale=None):
     return out, tree, tol + 1e-30, tree_tol + 1e-30
 
 
+def mass_dense(inp, lse, score):
+    """mass() for long caches without a window, as dense products in fp64 on the GPU."""
+    q = inp["q"].cuda().double()
+    L, Bq, N, Hq, dh = q.shape
+    Hkv, T = inp["k_tree"].shape[3], inp["k_cache"].shape[2]
+    G = Hq // Hkv
+    out, tree = score.astype(np.float64), np.zeros((L, Bq, Hkv, N))
+    tol, tree_tol = 2.0 ** -22 * np.abs(out) + 1e-30, np.full(tree.shape, 1e-30)
+    for b in range(Bq):
+        ctx = int(inp["ctx_len"][b])
+        path = root_path(inp["parent"][b].tolist(), int(inp["accepted"][b]))
+        seen = torch.ones(len(path), G, ctx + len(path), dtype=torch.bool)
+        seen[:, :, ctx:] = torch.ones(len(path), len(path), dtype=torch.bool).tril()[:, None]
+        for l in range(L):
+            for g in range(Hkv):
+                k = torch.cat([inp["k_cache"][l, b, :ctx, g], inp["k_tree"][l, b, path, g]]).cuda().double()
+                qp = q[l, b, path, g * G:(g + 1) * G]
+                z = torch.from_numpy(lse[l, b, path, g * G:(g + 1) * G]).cuda().double()[..., None]
+                w = (qp @ k.T * dh ** -0.5 - z).exp().masked_fill(~seen.cuda(), 0)
+                e = (qp.abs() @ k.abs().T).amax(-1, keepdim=True) * (dh ** -0.5 * (dh + 2) * 2.0 ** -24)
+                t = (w * (e + (z.abs() + 4) * 2.0 ** -21 + N * G * 2.0 ** -24)).sum((0, 1)).cpu().numpy()
+                w = w.sum((0, 1)).cpu().numpy()
+                out[l, b, g, :ctx] += w[:ctx]
+                tol[l, b, g, :ctx] += t[:ctx]
+                tree[l, b, g, path], tree_tol[l, b, g, path] = w[ctx:], t[ctx:] + 1e-30
+    return out, tree, tol, tree_tol
+
+
 def evict(inp, score, score_tree, pos, seen, budget, n_sink, n_recent):
     """New copies of k_cache, v_cache, score, pos, and ctx_out, seen_out."""
     kc, vc = inp["k_cache"].clone(), inp["v_cache"].clone()

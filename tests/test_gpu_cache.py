@@ -312,6 +312,29 @@ def test_attention_mass(name):
         assert np.array_equal(got[:, b, :, ctx:], score[:, b, :, ctx:])
 
 
+@pytest.mark.parametrize("sizes", [
+    dict(L=4, Bq=4, N=22, Hq=12, Hkv=2, dh=256, T=3000, ctx=[3000, 1, 1501, 2111]),
+    dict(L=6, Bq=5, N=64, Hq=32, Hkv=8, dh=128, T=1500, dtype="f16", tree="chain"),
+    dict(L=9, Bq=6, N=5, Hq=16, Hkv=4, dh=64, T=2500),
+    dict(L=1, Bq=1, N=40, Hq=8, Hkv=1, dh=256, T=20000, ctx=[19999], tree="chain"),
+])
+def test_mass_of_long_ragged_batches(sizes):
+    """Every CTA walks many blocks and several streams; paths longer than a pass."""
+    inp = R.make_inputs(**sizes, seed=31)
+    if sizes.get("tree") == "chain":
+        inp["accepted"][:] = sizes["N"] - 1
+    _, ref_lse, _, _ = R.attention_dense(inp)
+    lse = torch.from_numpy(ref_lse.astype(np.float32))
+    L, Bq, T, Hkv = inp["k_cache"].shape[:4]
+    score = np.random.default_rng(2).random((L, Bq, Hkv, T)).astype(np.float32)
+    got, tree, status = run_mass(inp, lse, score)
+    ref, ref_tree, tol, tree_tol = R.mass_dense(inp, lse.numpy(), score)
+    assert status == 0
+    assert (np.abs(got - ref) <= tol).all() and (np.abs(tree - ref_tree) <= tree_tol).all()
+    again, tree2, _ = run_mass(inp, lse, score)
+    assert np.array_equal(got, again) and np.array_equal(tree, tree2)
+
+
 @pytest.mark.parametrize("dh", [64, 128, 256])
 def test_mass_of_a_long_path_and_unseen_garbage(dh):
     """64 nodes on the path (512 query rows); NaN where no query looks; a query

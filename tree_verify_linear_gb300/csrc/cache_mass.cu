@@ -11,6 +11,13 @@
 // is 2 dh operations per row and key, far below what the tensor cores do in
 // the time a key takes to arrive: the kernel is bound by reading K.
 //
+// The tensor cores truncate as they accumulate, about half a unit in the 24th bit
+// of the running sum per 16 columns; a weight takes the score's absolute error as
+// its relative one.  Up to 128 rows each half of the head dimension has an
+// accumulator of its own and the two are added here, which halves that error
+// (1.5e-6 to 0.7e-6 of a path key's sum at dimension 256); with more rows the
+// columns of tensor memory do not allow it.
+//
 // The path's nodes are taken root first, so row d G + h belongs to the node of
 // depth d, and the rows that see a key are one range of rows.  Up to 128 rows
 // (256 for head dimensions below 256) are multiplied at a time; longer paths
@@ -30,7 +37,7 @@ namespace {
 struct MassArgs {
   int L, Hq, Hkv, G, n_req, fixed, Bq, N, T, window, n_sink;
   int cap, stages;  // rows per pass, ring stages
-  float scale_log2;
+  float scale;
   PerGroup per;
   Tiling til;
   const int32_t *ctx_len, *parent, *accepted;
@@ -57,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kPieces = DH / 64;  // per block of 128 keys
   extern __shared__ __align__(1024) unsigned char cache_smem[];
   unsigned char *ring_mem = cache_smem + A.cap * DH * 2, *tail = ring_mem + A.stages * kPiece;
-  float *lse2 = reinterpret_cast<float *>(tail + kTailLse);
+  float *lse_of = reinterpret_cast<float *>(tail + kTailLse);
   int *nodes = reinterpret_cast<int *>(tail + kTailNodes);
   volatile int *misc = reinterpret_cast<volatile int *>(tail + kTailMisc);  // TMEM base, gave up
   uint64_t *full = reinterpret_cast<uint64_t *>(tail + kTailBars);
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- copies ----
     int st = 0, loads = 0;
     uint32_t ph = 0;
+    ptx::named_sync(6, 256 + 32);  // behind the first queries' loads
 #pragma unroll 1
     while (W.next()) {
       const int rows = rows_of(), z = W.l * A.n_req + W.b;
@@ -165,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r0 = 0; r0 < rows && !bad; r0 += A.cap, ++seg) {
         const int nr = (rows - r0 < A.cap ? rows - r0 + 31 : A.cap) & ~31;
         const uint32_t idesc = ptx::idesc_16(F16, 128, nr, false);
+        const bool two = nr <= 128;  // accumulators
         if (!wait_all(q_bar, seg & 1)) break;
 #pragma unroll 1
         for (int i = 0; i < W.blk1 - W.blk0 && !bad; ++i) {
@@ -178,9 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t qd = qdesc + (uint64_t)(a * A.cap * (128 >> 4));
             if (one) {
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
-                ptx::mma_bf16_ss(tmem + buf * 256, kd + 2 * s, qd + 2 * s, idesc,
-                                 a + s > 0 ? 1u : 0u);
+              for (int s = 0; s < 4; ++s) {
+                const int step = a * 4 + s, mid = two ? DH / 32 : DH / 16;
+                ptx::mma_bf16_ss(tmem + buf * 256 + (step >= mid ? 128 : 0), kd + 2 * s, qd + 2 * s,
+                                 idesc, step > 0 && step != mid ? 1u : 0u);
+              }
               ptx::mma_commit(&empty[st]);
               if (a == kPieces - 1) ptx::mma_commit(&s_bar[buf]);
             }
@@ -202,6 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = (warp & 3) * 32 + lane;  // of a block: its lane of tensor memory
     const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * 256;
     uint32_t used = 0;
+    bool ahead = true;
+    auto go_ahead = [&]() {
+      if (ahead) asm volatile("bar.arrive 6, %0;" ::"n"(256 + 32) : "memory");
+      ahead = false;
+    };
 #pragma unroll 1
     while (W.next()) {
       const int rows = rows_of(), len = rows / A.G;
@@ -217,18 +233,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int d = A.per.node(r0 + r);
           return (lb * A.N + nodes[d]) * A.Hq + W.h * A.G + (r0 + r - d * A.G);
         };
-#pragma unroll 8
-        for (int i = tid; i < nr * kPer; i += 256) {
-          const int r = i / kPer, c = i % kPer;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (r < in) v = reinterpret_cast<const uint4 *>(A.q)[query(r) * kPer + c];
-          *reinterpret_cast<uint4 *>(cache_smem + (c / 8) * A.cap * 128 + r * 128 +
-                                     ((c & 7) ^ (r & 7)) * 16) = v;
+        // all of a thread's loads in flight, the first tile's ahead of the copies
+        constexpr int kStep = 256 / kPer, kLoads = (DH == 256 ? 128 : kMaxRows) / kStep;
+        const int piece = tid % kPer, r1 = tid / kPer;
+        uint4 v[kLoads];
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int r = r1 + e * kStep;
+          v[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < in) v[e] = reinterpret_cast<const uint4 *>(A.q)[query(r) * kPer + piece];
+        }
+        go_ahead();
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int r = r1 + e * kStep;
+          if (r < nr)
+            *reinterpret_cast<uint4 *>(cache_smem + (piece / 8) * A.cap * 128 + r * 128 +
+                                       ((piece & 7) ^ (r & 7)) * 16) = v[e];
         }
         if (tid < nr) {
           // rows past the last, and those without a finite score, weigh nothing
           const float z = tid < in ? A.lse[query(tid)] : -INFINITY;
-          lse2[tid] = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;
+          lse_of[tid] = z == -INFINITY ? INFINITY : z;
         }
         ptx::fence_proxy_async();
         ptx::named_sync(5, 256);
@@ -266,16 +292,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           const bool all = __all_sync(0xffffffffu, !to || (lo <= 0 && hi >= in));
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          // 32 columns at a time, the next ones on their way meanwhile
+          // 32 columns at a time, the next ones on their way meanwhile.  The lse
+          // is taken off before the change of base: the difference is small where
+          // a weight is not, and so is its rounding.
+          constexpr float kLog2e = 1.4426950408889634f;
           auto weigh = [&](const float(&s)[32], int c) {
             float p[32];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 z = *reinterpret_cast<const float4 *>(lse2 + c + e);
-              p[e] = ptx::ex2(fmaf(s[e], A.scale_log2, -z.x));
-              p[e + 1] = ptx::ex2(fmaf(s[e + 1], A.scale_log2, -z.y));
-              p[e + 2] = ptx::ex2(fmaf(s[e + 2], A.scale_log2, -z.z));
-              p[e + 3] = ptx::ex2(fmaf(s[e + 3], A.scale_log2, -z.w));
+              const float4 z = *reinterpret_cast<const float4 *>(lse_of + c + e);
+              p[e] = ptx::ex2(fmaf(s[e], A.scale, -z.x) * kLog2e);
+              p[e + 1] = ptx::ex2(fmaf(s[e + 1], A.scale, -z.y) * kLog2e);
+              p[e + 2] = ptx::ex2(fmaf(s[e + 2], A.scale, -z.z) * kLog2e);
+              p[e + 3] = ptx::ex2(fmaf(s[e + 3], A.scale, -z.w) * kLog2e);
             }
             if (!all) {
 #pragma unroll
@@ -287,15 +316,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           float s0[32], s1[32];
           ptx::tmem_ld32(tq, s0);
+          if (nr <= 128) {  // two accumulators
 #pragma unroll 1
-          for (int c = 0; c < nr; c += 64) {
-            ptx::tmem_wait_ld();
-            if (c + 32 < nr) ptx::tmem_ld32(tq + c + 32, s1);
-            weigh(s0, c);
-            if (c + 32 < nr) {
+            for (int c = 0; c < nr; c += 32) {
+              ptx::tmem_ld32(tq + 128 + c, s1);
               ptx::tmem_wait_ld();
-              if (c + 64 < nr) ptx::tmem_ld32(tq + c + 64, s0);
-              weigh(s1, c + 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s1[e] += s0[e];
+              if (c + 32 < nr) ptx::tmem_ld32(tq + c + 32, s0);
+              weigh(s1, c);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < nr; c += 64) {
+              ptx::tmem_wait_ld();
+              if (c + 32 < nr) ptx::tmem_ld32(tq + c + 32, s1);
+              weigh(s0, c);
+              if (c + 32 < nr) {
+                ptx::tmem_wait_ld();
+                if (c + 64 < nr) ptx::tmem_ld32(tq + c + 64, s0);
+                weigh(s1, c + 32);
+              }
             }
           }
           ptx::tc_fence_before();
@@ -306,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::named_sync(5, 256);  // nodes and lse are read
     }
+    go_ahead();
     if (bad) misc[1] = 1;
   }
 
@@ -357,7 +399,7 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
   MassArgs A = {};
   A.L = c->L, A.Hq = c->Hq, A.Hkv = c->Hkv, A.G = G, A.n_req = c->Bq;
   A.Bq = c->Bq, A.N = c->N, A.T = c->T, A.window = c->window, A.n_sink = c->n_sink;
-  A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.scale = c->scale;
   A.per = per_group(G);
   A.til = {c->N * G, 1, 1, 1, 1, kRows};
   A.ctx_len = ctx_len, A.parent = parent, A.accepted = accepted, A.q = q, A.lse = lse;
