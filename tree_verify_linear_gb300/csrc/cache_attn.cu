@@ -184,7 +184,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     return LBX_ECUDA;
   if (s.own.ctas == 2 && !encode_queries(&maps.q, q, c, c->N, lists)) return LBX_ECUDA;
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
-  A.window = c->window, A.n_sink = c->n_sink;
+  A.window = c->window, A.n_sink = c->n_sink, A.join = kJoinBlocks;
   A.part = reinterpret_cast<float *>(base);
   A.counters = reinterpret_cast<unsigned int *>(base + s.count), A.n_counters = s.own_n;
   if (prefix)
@@ -199,7 +199,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
     return LBX_ECUDA;
   maps.kt = maps.k, maps.vt = maps.v;  // a prefix has no tree: never read
   if (s.pre.ctas == 2 && !encode_queries(&maps.q, q, c, c->Bq * c->N, c->L)) return LBX_ECUDA;
-  A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre;
+  A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre, A.join = kJoinPrefixBlocks;
   A.part = reinterpret_cast<float *>(base + s.pre_part);
   A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count), A.n_counters = s.pre_n;
   A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr;

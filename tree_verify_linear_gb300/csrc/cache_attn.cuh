@@ -68,6 +68,7 @@ struct AttnArgs {
   int fixed;      // length of every key list if > 0 (the prefix), else ctx_len
   int Bq, N, T;   // of the batch (its check, the trees)
   int window, n_sink;
+  int join;       // what joining the pieces of a cut stream costs, in blocks
   float scale_log2;
   PerGroup per;
   Tiling til;
@@ -136,9 +137,13 @@ struct Lay {
 
 // Most rows whose pieces are joined by columns instead of by rows.
 constexpr int kFewRows = 32;
-// What a stream costs beside its blocks, and joining the pieces of a cut one
-// (measured about 13000 and 10000 cycles; a block takes 2200 to 3400).
-constexpr int kLeadBlocks = 4, kJoinBlocks = 3;
+// In blocks (of 2200 to 3400 cycles): what a stream costs beside its own, and what
+// cutting streams and joining the pieces costs, the requests' and a prefix's
+// (whose rows are more, and joined with the requests' results too).  Measured
+// against 3 for both joins: five requests of 22 nodes, 24/4 heads of dimension
+// 256, 2 layers over 1000 shared keys 71 -> 42 us, 4 layers over 4096 118 -> 100 us;
+// of 3 nodes, 5 layers of 1024 keys 54 -> 38 us; where they lose, it is up to 5%.
+constexpr int kLeadBlocks = 4, kJoinBlocks = 8, kJoinPrefixBlocks = 13;
 
 // Parts of P: f16 once, bf16 hi + lo.
 template <bool F16>
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   // the prefix's launch may take the SMs that this one leaves
   if (A.o32) ptx::launch_dependents();
-  using Walker = Walk<Y::kBlkUnits, kLeadBlocks, kJoinBlocks, AttnArgs>;
+  using Walker = Walk<Y::kBlkUnits, kLeadBlocks, AttnArgs>;
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
@@ -919,8 +924,10 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           }
           ptx::named_sync(5, kSoftmaxThreads);
 #pragma unroll 1
-          for (int idx = tid; idx < here * (DH / 4); idx += kSoftmaxThreads) {
-            const int rr = idx / (DH / 4), c4 = idx % (DH / 4), rw = row0 + rr0 + rr;
+          for (int idx = tid; idx < (here + 7) / 8 * 8 * (DH / 4); idx += kSoftmaxThreads) {
+            const int rr = idx / (2 * DH) * 8 + idx % 8, c4 = idx / 8 % (DH / 4);
+            const int rw = row0 + rr0 + rr;
+            if (rr >= here) continue;
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (A.x_o) {
               f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);

@@ -37,6 +37,7 @@ namespace {
 struct MassArgs {
   int L, Hq, Hkv, G, n_req, fixed, Bq, N, T, window, n_sink;
   int cap, stages;  // rows per pass, ring stages
+  static constexpr int join = 0;  // pieces of a stream need no joining
   float scale;
   PerGroup per;
   Tiling til;
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-  Walk<2, 3, 0, MassArgs> W(A, lane);
+  Walk<2, 3, MassArgs> W(A, lane);
   bool bad = false;  // a wait of this thread gave up: it waits no more
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;

@@ -92,10 +92,10 @@ __device__ __forceinline__ void unit_of(const S &s, bool prefix, int N, int u, i
 // warps, each lane alike; the CTAs of a pair walk alike.
 // A stream also costs what it takes to begin and end it, LEAD blocks that come
 // before its own in the list.  Where whole streams per group come out within
-// JOIN blocks (the price of joining the pieces of a cut stream) of equal ranges,
-// a stream counts as one entry of the list and is not cut.  Args has the shapes:
-// L, Hkv, N, n_req, fixed, window, n_sink, ctx_len and til.
-template <int BU, int LEAD, int JOIN, class Args>
+// Args::join blocks (the price of joining the pieces of a cut stream) of equal
+// ranges, a stream counts as one entry of the list and is not cut.  Args also has
+// the shapes: L, Hkv, N, n_req, fixed, window, n_sink, ctx_len and til.
+template <int BU, int LEAD, class Args>
 struct Walk {
   const Args &A;
   // the list's entries and how they are cut: `more` ranges of each + 1 entries,
@@ -140,7 +140,7 @@ struct Walk {
     total = sum * streams();
     groups = (int)(gridDim.x / (unsigned)(A.til.group * A.til.ctas));
     const long long all = (long long)streams() * A.n_req;
-    uncut = (all + groups - 1) / groups * (most + LEAD) <= (total + groups - 1) / groups + JOIN;
+    uncut = (all + groups - 1) / groups * (most + LEAD) <= (total + groups - 1) / groups + A.join;
     if (uncut) total = (int)all;
     if (groups > total) groups = total;
     each = total / groups, more = total - each * groups;
