@@ -76,6 +76,8 @@ ATTN = {
     "chain_64": (dict(L=1, Bq=2, N=64, Hq=2, Hkv=2, dh=64, T=100, tree="chain"), 30, 2),
     "star_64": (dict(L=1, Bq=2, N=64, Hq=2, Hkv=1, dh=256, T=64, tree="star", ctx=[64, 1]), 0, 0),
     "group_of_48": (dict(L=1, Bq=1, N=3, Hq=48, Hkv=1, dh=64, T=77), 0, 0),
+    "group_of_130": (dict(L=1, Bq=1, N=2, Hq=130, Hkv=1, dh=128, T=90, ctx=[81]), 0, 0),
+    "group_of_65": (dict(L=1, Bq=2, N=3, Hq=130, Hkv=2, dh=256, T=70, dtype="f16"), 40, 2),
     "many_heads": (dict(L=1, Bq=2, N=1, Hq=64, Hkv=64, dh=64, T=50), 20, 1),
     "ragged_f16": (dict(L=2, Bq=5, N=4, Hq=8, Hkv=2, dh=128, T=333, dtype="f16",
                         ctx=[333, 0, 1, 64, 128]), 0, 0),
@@ -512,3 +514,15 @@ def test_the_binding_refuses_other_shapes_types_and_layouts():
     with pytest.raises(TypeError):
         call(ctx_len=d["ctx_len"].long())
     torch.cuda.synchronize()
+
+
+def test_the_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples", "bounded_cache.py")
+    spec = importlib.util.spec_from_file_location("bounded_cache", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    seen, ctx, o, o_win = ex.main(["--rounds", "40", "--budget", "64"])
+    assert (ctx <= 64).all() and (ctx == torch.minimum(seen, torch.full_like(seen, 64))).all()
+    assert (seen >= 40).all() and torch.isfinite(o).all() and torch.isfinite(o_win).all()
