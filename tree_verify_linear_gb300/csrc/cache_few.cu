@@ -343,14 +343,18 @@ int few_chunks(const lbx_attn_cfg *c) {
   const long long n = units(c->P) + own + 1, all = n * c->L * c->Bq * c->Hkv;
   // Up to about one wave of CTAs it is the faster one, beyond the other is: us per
   // call here / there, bf16, 24 query heads over 4 of dimension 256,
-  //   9 units per stream, 4 streams    9.3 / 17.2
-  //   17 units, 16 streams            12.9 / 19.3
-  //   63 units, 16 streams            35.8 / 25.3
+  //   9 units per stream, 4 streams    9.3 / 15.4
+  //   17 units, 16 streams            13.1 / 17.6
+  //   64 units, 4 streams             21.9 / 28.5
+  //   42 units, 12 streams            24.7 / 21.3
+  //   64 units, 8 streams             28.4 / 23.4
   // and, with a prefix (two launches there),
-  //   21 units, 20 streams            19.8 / 68.1
-  //   29 units, 32 streams (dh 128)   17.6 / 45.0
+  //   21 units, 20 streams            20.3 / 26.4
+  //   29 units, 32 streams (dh 128)   17.4 / 23.5
+  //   63 units, 16 streams            37.8 / 42.8
+  //   32 units, 32 streams            31.7 / 30.6
   // The join's weights fit in K's place up to 64 units.
-  return n <= 64 && all <= (c->P > 0 ? kFewUnits : kFewUnits / 2) ? (int)n : 0;
+  return n <= 64 && all <= (c->P > 0 ? kFewUnits : kFewUnits * 3 / 8) ? (int)n : 0;
 }
 
 cudaError_t launch_few(const FewArgs &A, cudaStream_t stream) {
