@@ -1,0 +1,23 @@
+"""GPU tests of the bounded cache's operators at their edges: full windows,
+shared workspaces, calls side by side, NaN, the longest windows."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as R
+from test_gpu_cache import built, check_attention, run_attention  # noqa: F401 (built: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- a window as long as a full cache ---------------------------------------
+
+@pytest.mark.parametrize("T,n_sink", [(2, 1), (64, 1), (64, 64), (65, 4), (100, 4), (128, 70), (512, 4), (1024, 1)])
+@pytest.mark.parametrize("dh,dtype,N,Hq", [(64, "f16", 1, 1), (128, "bf16", 1, 4), (256, "bf16", 3, 5)])
+def test_window_as_long_as_a_full_cache(T, n_sink, dh, dtype, N, Hq):
+    """Its first position is past the window and a first position that stays
+    visible; twice on one workspace."""
+    inp = R.make_inputs(1, 2, N, Hq, 1, dh, T, dtype=dtype, ctx=[T, T - 1], seed=T + n_sink)
+    o, lse = check_attention(inp, window=T, n_sink=n_sink)
+    o2, lse2, status = run_attention(inp, calls=2, window=T, n_sink=n_sink)
+    assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)

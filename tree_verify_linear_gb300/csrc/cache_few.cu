@@ -336,9 +336,12 @@ int few_chunks(const lbx_attn_cfg *c) {
   const long long rows = (long long)c->N * (c->Hq / c->Hkv);
   if (rows > kTile) return 0;
   auto units = [](long long n) { return (n + kUnit - 1) / kUnit; };
-  // the most a request can have: a window with its sinks, or the whole cache
-  const long long own = c->window > 0 && c->window < c->T
-                            ? units(c->window) + units(c->n_sink < c->T ? c->n_sink : c->T)
+  // the most a request can have, over all context lengths up to T: once the
+  // context is as long as the window its first position is on its own, W - 1
+  // cached positions are in the window and the others, up to n_sink, before it
+  const long long W = c->window, before = c->T - (W - 1);
+  const long long own = W > 0 && before > 0
+                            ? units(W - 1) + units(c->n_sink < before ? c->n_sink : before)
                             : units(c->T);
   const long long n = units(c->P) + own + 1, all = n * c->L * c->Bq * c->Hkv;
   // Up to about one wave of CTAs it is the faster one, beyond the other is: us per
