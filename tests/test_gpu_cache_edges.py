@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import cache_ref as R
-from test_gpu_cache import built, check_attention, run_attention  # noqa: F401 (built: a fixture)
+from test_gpu_cache import built, check_attention, run_attention, run_mass  # noqa: F401 (built: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +21,19 @@ def test_window_as_long_as_a_full_cache(T, n_sink, dh, dtype, N, Hq):
     o, lse = check_attention(inp, window=T, n_sink=n_sink)
     o2, lse2, status = run_attention(inp, calls=2, window=T, n_sink=n_sink)
     assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---- the longest windows ------------------------------------------------------
+
+@pytest.mark.parametrize("dh,T", [(64, 30), (128, 2000), (256, 70)])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 40])
+def test_the_longest_windows_are_no_window(dh, T, window):
+    inp = R.make_inputs(1, 2, 40, 4, 2, dh, T, ctx=[T, T // 2], tree="chain", seed=dh)
+    inp["accepted"][:] = 39
+    o, lse, _ = run_attention(inp)
+    o2, lse2, status = run_attention(inp, window=window)
+    assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    score = np.zeros((1, 2, 2, T), np.float32)
+    s, tree, _ = run_mass(inp, lse, score)
+    s2, tree2, status = run_mass(inp, lse, score, window=window)
+    assert status == 0 and np.array_equal(s, s2) and np.array_equal(tree, tree2)

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (off < cnt) {
             const int d = __popcll(path & ((2ull << off) - 1)) - 1;
             lo = d * A.G;
-            if (A.window > 0 && W.ctx + d >= A.n_sink && d + A.window < len)
+            if (A.window > 0 && W.ctx + d >= A.n_sink && A.window < len - d)
               hi = (d + A.window) * A.G;
             if (!(path >> off & 1)) hi = 0;
             to = A.score_tree + lbg * A.N + off;
