@@ -37,3 +37,19 @@ def test_the_longest_windows_are_no_window(dh, T, window):
     s, tree, _ = run_mass(inp, lse, score)
     s2, tree2, status = run_mass(inp, lse, score, window=window)
     assert status == 0 and np.array_equal(s, s2) and np.array_equal(tree, tree2)
+
+
+# ---- the first segment of a block of threads -----------------------------------
+
+@pytest.mark.parametrize("dh,N,Hq,T,dtype", [(256, 22, 6, 0, "bf16"), (128, 64, 4, 1, "f16"), (64, 40, 3, 0, "bf16")])
+def test_every_request_reads_its_own_tree(dh, N, Hq, T, dtype):
+    """As many requests as multiprocessors, each with a tree of its own and next to
+    no cache: every block of threads begins with another tree's masks."""
+    inp = R.make_inputs(1, 152, N, Hq, 1, dh, T, dtype=dtype, seed=dh + N)
+    o, lse, status = run_attention(inp)
+    assert status == 0
+    ref_o, ref_lse, o_tol, lse_tol = R.attention_dense(inp)
+    assert (np.abs(o.double().numpy() - ref_o) <= o_tol).all()
+    assert (np.abs(lse.double().numpy() - ref_lse) <= lse_tol).all()
+    o2, lse2, status = run_attention(inp, calls=200)
+    assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)

@@ -632,6 +632,9 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       parents(*g);
       if constexpr (!PAIR) load_q(*g);
       look(*g);
+      // the masks are read before the first block's maxima take their place (for
+      // later segments the barrier at a segment's end sees to it)
+      ptx::named_sync(5, kSoftmaxThreads);
     } else {
       go_ahead();
     }
