@@ -375,8 +375,10 @@ typedef struct lbx_attn_cfg {
 /* Bytes of workspace lbx_window_attention (cfg->P == 0) or
  * lbx_prefix_attention (cfg->P > 0) needs (0 on a bad cfg).  It must be
  * zero-filled once before its first use (and after a call that reported
- * LBX_ETIMEOUT); every call that runs to completion leaves its counters at zero;
- * two calls that run at the same time must not share it. */
+ * LBX_ETIMEOUT); every call that runs to completion leaves its counters at zero.
+ * Calls of any configurations, of either function, may take turns on one
+ * workspace that is large enough for each; two calls that run at the same time
+ * must not share it. */
 size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *cfg);
 
 /*

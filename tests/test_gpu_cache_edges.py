@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import cache_ref as R
-from test_gpu_cache import built, check_attention, run_attention, run_mass  # noqa: F401 (built: a fixture)
+from test_gpu_cache import built, cfg_of, check_attention, run_attention, run_mass  # noqa: F401 (built: a fixture)
+from tree_verify_linear_gb300 import lbx
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,33 @@ def test_every_request_reads_its_own_tree(dh, N, Hq, T, dtype):
     assert (np.abs(lse.double().numpy() - ref_lse) <= lse_tol).all()
     o2, lse2, status = run_attention(inp, calls=200)
     assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---- one workspace for many configurations ---------------------------------------
+
+def test_calls_of_every_kind_take_turns_on_one_workspace():
+    """Batch sizes, head dimensions, with and without a prefix, streams in many
+    pieces and the small kernel: each call gives what it gives on a workspace of its own."""
+    kinds = [(dict(L=4, Bq=b, N=22, Hq=12, Hkv=2, dh=256, T=700, P=p, dtype=t), {})
+             for b, p, t in ((4, 900, "bf16"), (5, 900, "bf16"), (3, 0, "f16"), (6, 0, "bf16"))]
+    kinds += [(dict(L=1, Bq=b, N=12, Hq=4, Hkv=1, dh=dh, T=9000, P=p), {})
+              for b, dh, p in ((1, 64, 0), (2, 128, 0), (7, 64, 5000), (1, 256, 3000))]
+    kinds += [(dict(L=1, Bq=2, N=1, Hq=8, Hkv=4, dh=dh, T=500, P=p), {}) for dh, p in ((64, 0), (256, 100))]
+    kinds += [(dict(L=2, Bq=3, N=5, Hq=8, Hkv=2, dh=128, T=3000), dict(window=900, n_sink=4))]
+    calls = []
+    for i, (sizes, kw) in enumerate(kinds):
+        inp = R.make_inputs(**sizes, seed=600 + i)
+        o, lse, status = run_attention(inp, **kw)
+        assert status == 0
+        calls.append((cfg_of(inp, **kw), {k: v.cuda() for k, v in inp.items()}, o.cuda(), lse.cuda()))
+    ws = torch.zeros(max(lbx.lbx_cache_attn_workspace_size(c[0]) for c in calls), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for step in range(3 * len(calls)):
+        cfg, d, o, lse = calls[step * 5 % len(calls)]
+        got, got_lse = torch.full_like(o, float("nan")), torch.full_like(lse, float("nan"))
+        pre = (d["k_prefix"], d["v_prefix"]) if cfg.P else ()
+        (lbx.lbx_prefix_attention if cfg.P else lbx.lbx_window_attention)(
+            cfg, d["ctx_len"], d["parent"], d["q"], *pre, d["k_cache"], d["v_cache"], d["k_tree"],
+            d["v_tree"], got, ws, lse=got_lse, d_status=status)
+        assert torch.equal(got, o) and torch.equal(got_lse, lse), step
+    assert int(status.item()) == 0 and not ws[:4096].any()

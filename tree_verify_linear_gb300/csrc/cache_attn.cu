@@ -83,31 +83,29 @@ namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// The workspace: partials and counters of the requests' launch; with a prefix
-// also the prefix launch's, its results and their lse.
+// The workspace: counters, at the same places whatever the configuration, so that
+// calls of any kind may take turns on one; then the partials of the requests' launch;
+// with a prefix also the prefix launch's, and the first launch's results and lse.
+constexpr size_t kCounterBytes = 4 * kFewUnits;
+constexpr int kPrefixCounters = 2 * kMaxCtas;  // the first of the prefix launch's
+static_assert(2 * kPrefixCounters <= kFewUnits, "counters of two launches, or of the small kernel");
 size_t part_bytes(const lbx_attn_cfg *c) {
   return up256((size_t)kMaxCtas * 2 * part_floats(c->dh) * 4);
 }
 struct Space {
   Tiling own, pre;
-  size_t count, pre_part, pre_count, x_o, x_lse, bytes;  // offsets after the partials
-  size_t own_n, pre_n;                                      // counters of each kind
+  size_t part, pre_part, x_o, x_lse, bytes;  // offsets, and the end
 };
 Space space_of(const lbx_attn_cfg *c) {
   Space s;
-  const size_t part = part_bytes(c);
   const long long G = c->Hq / c->Hkv, rows = (long long)c->N * G;
-  const size_t lists = (size_t)c->L * c->Hkv;
   s.own = tiling(rows, (int)G, c->dh);
   s.pre = tiling(rows * c->Bq, (int)G, c->dh);
-  s.count = part;
-  s.own_n = lists * c->Bq * s.own.tiles * s.own.ctas, s.pre_n = lists * s.pre.tiles * s.pre.ctas;
-  s.pre_part = s.count + up256(2 * s.own_n * 4);
-  s.pre_count = s.x_o = s.x_lse = s.bytes = s.pre_part;
+  s.part = kCounterBytes;
+  s.pre_part = s.x_o = s.x_lse = s.bytes = s.part + part_bytes(c);
   if (c->P > 0) {  // the two launches overlap: nothing is shared
     const size_t queries = (size_t)c->L * c->Bq * c->N * c->Hq;
-    s.pre_count = s.pre_part + part;
-    s.x_o = s.pre_count + up256(2 * s.pre_n * 4);
+    s.x_o = s.pre_part + part_bytes(c);
     s.x_lse = s.x_o + up256(queries * c->dh * 4);
     s.bytes = s.x_lse + up256(queries * 4);
   }
@@ -139,8 +137,8 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   unsigned char *base = static_cast<unsigned char *>(ws);
   if (const int chunks = few_chunks(c)) {
     const FewArgs F = {*c, chunks, c->scale * 1.4426950408889634f, ctx_len, parent, q, kp, vp, kc,
-                       vc, kt, vt, o, lse, reinterpret_cast<float *>(base),
-                       reinterpret_cast<unsigned int *>(base + s.count), status};
+                       vc, kt, vt, o, lse, reinterpret_cast<float *>(base + s.part),
+                       reinterpret_cast<unsigned int *>(base), status};
     return launch_few(F, stream) == cudaSuccess ? LBX_OK : LBX_ECUDA;
   }
 
@@ -160,7 +158,6 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   A.scale_log2 = c->scale * 1.4426950408889634f;
   A.per = per_group(A.G);
   A.ctx_len = ctx_len, A.parent = parent, A.q = q, A.status = status;
-  A.part = reinterpret_cast<float *>(base);
   const bool f16 = c->dtype == LBX_F16;
   auto launch = [&](const AttnMaps &maps) {
     const int by = A.til.group * A.til.ctas;  // at most 16: fewer than SMs
@@ -185,8 +182,8 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if (s.own.ctas == 2 && !encode_queries(&maps.q, q, c, c->N, lists)) return LBX_ECUDA;
   A.n_req = c->Bq, A.nodes = c->N, A.til = s.own;
   A.window = c->window, A.n_sink = c->n_sink, A.join = kJoinBlocks;
-  A.part = reinterpret_cast<float *>(base);
-  A.counters = reinterpret_cast<unsigned int *>(base + s.count), A.n_counters = s.own_n;
+  A.part = reinterpret_cast<float *>(base + s.part);
+  A.counters = reinterpret_cast<unsigned int *>(base);
   if (prefix)
     A.o32 = reinterpret_cast<float *>(base + s.x_o), A.lse2 = reinterpret_cast<float *>(base + s.x_lse);
   else
@@ -201,7 +198,7 @@ int attention(const lbx_attn_cfg *c, const int32_t *ctx_len, const int32_t *pare
   if (s.pre.ctas == 2 && !encode_queries(&maps.q, q, c, c->Bq * c->N, c->L)) return LBX_ECUDA;
   A.n_req = 1, A.nodes = c->Bq * c->N, A.fixed = c->P, A.til = s.pre, A.join = kJoinPrefixBlocks;
   A.part = reinterpret_cast<float *>(base + s.pre_part);
-  A.counters = reinterpret_cast<unsigned int *>(base + s.pre_count), A.n_counters = s.pre_n;
+  A.counters += kPrefixCounters;
   A.x_o = A.o32, A.x_lse2 = A.lse2, A.o32 = nullptr, A.lse2 = nullptr;
   A.o = o, A.lse = lse;
   return launch(maps) ? LBX_OK : LBX_ECUDA;

@@ -87,8 +87,9 @@ struct AttnArgs {
   float *lse;                  // natural lse or NULL
   const float *x_o, *x_lse2;   // the first launch's results to join, or NULL
   float *part;
-  unsigned int *counters;      // pieces written, per (stream, tile, CTA of the pair) ...
-  size_t n_counters;           // ... and, behind as many, pieces that have joined
+  // pieces written, per CTA: of the stream that begins in its range and ends beyond it
+  // (one at most) ...
+  unsigned int *counters;      // ... and, kMaxCtas further on, pieces that have joined
   int32_t *status;
 };
 
@@ -860,8 +861,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       const int late = g->late ? (int)part_floats(DH) : 0;
       auto partial = [&](int e) { return part0 + e * by + (e == 0 ? late : 0); };
       bool join = false;
-      const size_t counter = (((size_t)b * A.L + l) * A.Hkv + h) * A.til.tiles * Y::kCtas +
-                             row0 / A.til.per_cta;
+      const int counter = g->slot >> 1;
       if (!whole && rows > 0) {
         float4 *to = reinterpret_cast<float4 *>(partial(mine) + 2 * kRows);
         if (busy && valid) {
@@ -972,8 +972,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         if (n_piece > 2) {
           ptx::named_sync(5, kSoftmaxThreads);
           if (tid == 0 &&
-              atomicAdd(&A.counters[A.n_counters + counter], 1u) == (unsigned)n_piece - 2)
-            A.counters[counter] = A.counters[A.n_counters + counter] = 0u;  // for the next call
+              atomicAdd(&A.counters[kMaxCtas + counter], 1u) == (unsigned)n_piece - 2)
+            A.counters[counter] = A.counters[kMaxCtas + counter] = 0u;  // for the next call
         }
       } else if (busy && valid && (whole || join)) {
         // a row per two threads; this CTA's piece is still in tensor memory, the
