@@ -84,3 +84,41 @@ def test_calls_of_every_kind_take_turns_on_one_workspace():
             d["v_tree"], got, ws, lse=got_lse, d_status=status)
         assert torch.equal(got, o) and torch.equal(got_lse, lse), step
     assert int(status.item()) == 0 and not ws[:4096].any()
+
+
+# ---- calls side by side ------------------------------------------------------------
+
+@pytest.mark.parametrize("P", [0, 9000])
+def test_calls_on_streams_of_two_priorities(P):
+    """Streams cut into pieces for every multiprocessor, two calls at a time: the
+    one of higher priority takes the multiprocessors that the other's blocks wait for.
+    Neither may depend on a block that is not running."""
+    inps = [R.make_inputs(L=1, Bq=2, N=22, Hq=6, Hkv=1, dh=256, T=500 if P else 9000, P=P,
+                          ctx=[500, 0] if P else [9000, 7000], seed=700),
+            R.make_inputs(L=1, Bq=1, N=3, Hq=8, Hkv=1, dh=128, T=20000, dtype="f16", ctx=[19999], seed=701)]
+    calls = []
+    for inp, priority in zip(inps, (0, -1)):
+        o, lse, status = run_attention(inp)
+        assert status == 0
+        cfg = cfg_of(inp)
+        calls.append((cfg, {k: v.cuda() for k, v in inp.items()}, o.cuda(), lse.cuda(),
+                      lbx.new_cache_attn_workspace(cfg), torch.cuda.Stream(priority=priority)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [[(torch.full_like(c[2], float("nan")), torch.empty_like(c[3])) for c in calls] for _ in range(20)]
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    begin.record()
+    for turn in outs:
+        for (cfg, d, _, _, ws, stream), (o, lse) in zip(calls, turn):
+            pre = (d["k_prefix"], d["v_prefix"]) if cfg.P else ()
+            (lbx.lbx_prefix_attention if cfg.P else lbx.lbx_window_attention)(
+                cfg, d["ctx_len"], d["parent"], d["q"], *pre, d["k_cache"], d["v_cache"], d["k_tree"],
+                d["v_tree"], o, ws, lse=lse, d_status=status, stream=stream)
+    torch.cuda.synchronize()
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for turn in outs:
+        for (_, _, o, lse, _, _), (got, got_lse) in zip(calls, turn):
+            assert torch.equal(got, o) and torch.equal(got_lse, lse)
+    assert begin.elapsed_time(end) < 1000  # a wait for a block that cannot run would take seconds

@@ -29,8 +29,12 @@
 // keys at the same time): one CTA per SM, whatever the lengths.  Streams that
 // a range does not cover whole leave partials (m, l, O) in the workspace, at
 // most two per CTA.  Of two pieces the CTA that finishes last joins both (its own
-// from tensor memory); of more, all but the last piece's CTAs, whose ranges end
-// there, wait for each other and join some of the rows each.
+// from tensor memory).  Of more, the rows are joined in shares, one fewer than pieces:
+// the CTAs of all but the last piece, whose ranges end there, wait a little for the
+// others (they finish at about the same time) and take a share each; the one that
+// finishes last takes what shares are left.  Where other work holds the SMs and CTAs
+// of the launch run one after the other, the waits run out and that one takes all:
+// no result depends on a CTA that may not be running.
 //
 // Streams of more than 128 rows (head dimensions 128 and 256) run on pairs of
 // CTAs that share one product of 256 rows: each CTA keeps half of the block's
@@ -87,9 +91,10 @@ struct AttnArgs {
   float *lse;                  // natural lse or NULL
   const float *x_o, *x_lse2;   // the first launch's results to join, or NULL
   float *part;
-  // pieces written, per CTA: of the stream that begins in its range and ends beyond it
-  // (one at most) ...
-  unsigned int *counters;      // ... and, kMaxCtas further on, pieces that have joined
+  // Per CTA, of the stream that begins in its range and ends beyond it (one at most):
+  // pieces written, and in the upper half the CTAs that are done with the stream; and,
+  // kMaxCtas further on, the shares of its rows that are taken.
+  unsigned int *counters;
   int32_t *status;
 };
 
@@ -146,6 +151,11 @@ struct Lay {
 
 // Most rows whose pieces are joined by columns instead of by rows.
 constexpr int kFewRows = 32;
+// How long a CTA waits for the other pieces of a stream before it leaves them to the
+// last: some times the spread of the ends of equal ranges; and an SM that other work
+// waits for is kept no longer than that.  (64 requests of one row over 32001 shared keys,
+// 16/2 heads of dimension 128: 84 us, 136 us where the last joins alone.)
+constexpr uint64_t kJoinWaitNs = 50000;
 // In blocks (of 2200 to 3400 cycles): what a stream costs beside its own, and what
 // cutting streams and joining the pieces costs, the requests' and a prefix's
 // (whose rows are more, and joined with the requests' results too).  Measured
@@ -885,12 +895,18 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         }
         ptx::named_sync(5, kSoftmaxThreads);
         if (tid == 0) {
+          int share = 0;
           __threadfence();  // the CTA's partial, before its arrival
-          const unsigned prev = atomicAdd(&A.counters[counter], 1u);
-          int go = n_piece == 2 ? prev == 1 : mine < n_piece - 1;
+          const unsigned prev = atomicAdd(&A.counters[counter], 1u) & 0xffffu;
+          const bool last = prev == (unsigned)n_piece - 1;
+          int go = last;
           if (n_piece == 2 && go) A.counters[counter] = 0u;  // for the next call
-          if (n_piece > 2 && go && !ptx::wait_count(&A.counters[counter], (unsigned)n_piece))
-            go = 0, misc[3] = 1;
+          if (n_piece > 2) {
+            if (!last && mine < n_piece - 1)
+              go = ptx::wait_count(&A.counters[counter], (unsigned)n_piece, kJoinWaitNs);
+            if (go) share = (int)atomicAdd(&A.counters[kMaxCtas + counter], 1u);
+            misc[4] = share, misc[5] = last;
+          }
           misc[1] = go;
           __threadfence();
         }
@@ -898,82 +914,85 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         join = misc[1] != 0;
       }
       if (join && (n_piece > 2 || rows <= kFewRows)) {
-        // few rows, or this CTA's share of them: the pieces' weights, then four
-        // columns of a row per thread; as many rows at a time as `red` holds
-        // weights of
-        const int from = n_piece > 2 ? rows * mine / (n_piece - 1) : 0;
-        const int to = n_piece > 2 ? rows * (mine + 1) / (n_piece - 1) : rows;
+        // few rows, or a share of them: the pieces' weights, then four columns of a
+        // row per thread; as many rows at a time as `red` holds weights of
+        const int shares = n_piece == 2 ? 1 : rows < n_piece - 1 ? rows : n_piece - 1;
+        const bool last = n_piece > 2 && misc[5] != 0;
         constexpr int kHeld = (4 * kRows - kFewRows) / 2;
         float *l_of = red + kHeld, *wx_of = l_of + kHeld;
         const int step = kHeld / n_piece < kFewRows ? kHeld / n_piece : kFewRows;
+        int share = n_piece > 2 ? misc[4] : 0;
 #pragma unroll 1
-        for (int rr0 = from; rr0 < to; rr0 += step) {
-          const int here = to - rr0 < step ? to - rr0 : step;
-          ptx::named_sync(5, kSoftmaxThreads);  // the last weights are read
-          if (tid < here * n_piece) {
-            const float *pg = partial(tid / here) + rr0 + tid % here;
-            red[tid] = __ldcg(pg), l_of[tid] = __ldcg(pg + kRows);
-          }
-          ptx::named_sync(5, kSoftmaxThreads);
-          if (tid < here) {
-            const int rw = row0 + rr0 + tid;
-            float top = -INFINITY, sum = 0.f;
+        while (share < shares) {
+          const int from = rows * share / shares, to = rows * (share + 1) / shares;
 #pragma unroll 1
-            for (int e = tid; e < here * n_piece; e += here) top = fmaxf(top, red[e]);
-            if (top == -INFINITY) top = 0.f;
-#pragma unroll 1
-            for (int e = tid; e < here * n_piece; e += here) {
-              const float w_e = ptx::ex2(red[e] - top);
-              red[e] = w_e;
-              sum = fmaf(w_e, l_of[e], sum);
+          for (int rr0 = from; rr0 < to; rr0 += step) {
+            const int here = to - rr0 < step ? to - rr0 : step;
+            ptx::named_sync(5, kSoftmaxThreads);  // the last weights are read
+            if (tid < here * n_piece) {
+              const float *pg = partial(tid / here) + rr0 + tid % here;
+              red[tid] = __ldcg(pg), l_of[tid] = __ldcg(pg + kRows);
             }
-            float w, wx;
-            put_lse(rw, factors(rw, top, sum, w, wx));
+            ptx::named_sync(5, kSoftmaxThreads);
+            if (tid < here) {
+              const int rw = row0 + rr0 + tid;
+              float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-            for (int e = tid; e < here * n_piece; e += here) red[e] *= w;
-            wx_of[tid] = wx;
-          }
-          ptx::named_sync(5, kSoftmaxThreads);
+              for (int e = tid; e < here * n_piece; e += here) top = fmaxf(top, red[e]);
+              if (top == -INFINITY) top = 0.f;
 #pragma unroll 1
-          for (int idx = tid; idx < (here + 7) / 8 * 8 * (DH / 4); idx += kSoftmaxThreads) {
-            const int rr = idx / (2 * DH) * 8 + idx % 8, c4 = idx / 8 % (DH / 4);
-            const int rw = row0 + rr0 + rr;
-            if (rr >= here) continue;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (A.x_o) {
-              f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);
-              const float wx = wx_of[rr];
-              f.x *= wx, f.y *= wx, f.z *= wx, f.w *= wx;
-            }
-            // ten pieces' loads in flight
-#pragma unroll 1
-            for (int e0 = 0; e0 < n_piece; e0 += 10) {
-              float4 y[10];
-#pragma unroll
-              for (int e = 0; e < 10; ++e)
-                y[e] = __ldcg(reinterpret_cast<const float4 *>(
-                                  partial(e0 + e < n_piece ? e0 + e : e0) + 2 * kRows) +
-                              c4 * kRows + rr0 + rr);
-#pragma unroll
-              for (int e = 0; e < 10; ++e) {
-                const float w_e = e0 + e < n_piece ? red[(e0 + e) * here + rr] : 0.f;
-                if (w_e > 0.f)  // (an empty piece's O holds nothing)
-                  f.x = fmaf(w_e, y[e].x, f.x), f.y = fmaf(w_e, y[e].y, f.y),
-                  f.z = fmaf(w_e, y[e].z, f.z), f.w = fmaf(w_e, y[e].w, f.w);
+              for (int e = tid; e < here * n_piece; e += here) {
+                const float w_e = ptx::ex2(red[e] - top);
+                red[e] = w_e;
+                sum = fmaf(w_e, l_of[e], sum);
               }
+              float w, wx;
+              put_lse(rw, factors(rw, top, sum, w, wx));
+#pragma unroll 1
+              for (int e = tid; e < here * n_piece; e += here) red[e] *= w;
+              wx_of[tid] = wx;
             }
-            if (A.o32)
-              reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;
-            else
-              reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] =
-                  make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
+            ptx::named_sync(5, kSoftmaxThreads);
+#pragma unroll 1
+            for (int idx = tid; idx < (here + 7) / 8 * 8 * (DH / 4); idx += kSoftmaxThreads) {
+              const int rr = idx / (2 * DH) * 8 + idx % 8, c4 = idx / 8 % (DH / 4);
+              const int rw = row0 + rr0 + rr;
+              if (rr >= here) continue;
+              float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (A.x_o) {
+                f = __ldcg(reinterpret_cast<const float4 *>(A.x_o) + place_x(rw) + c4 * rows_all);
+                const float wx = wx_of[rr];
+                f.x *= wx, f.y *= wx, f.z *= wx, f.w *= wx;
+              }
+              // ten pieces' loads in flight
+#pragma unroll 1
+              for (int e0 = 0; e0 < n_piece; e0 += 10) {
+                float4 y[10];
+#pragma unroll
+                for (int e = 0; e < 10; ++e)
+                  y[e] = __ldcg(reinterpret_cast<const float4 *>(
+                                    partial(e0 + e < n_piece ? e0 + e : e0) + 2 * kRows) +
+                                c4 * kRows + rr0 + rr);
+#pragma unroll
+                for (int e = 0; e < 10; ++e) {
+                  const float w_e = e0 + e < n_piece ? red[(e0 + e) * here + rr] : 0.f;
+                  if (w_e > 0.f)  // (an empty piece's O holds nothing)
+                    f.x = fmaf(w_e, y[e].x, f.x), f.y = fmaf(w_e, y[e].y, f.y),
+                    f.z = fmaf(w_e, y[e].z, f.z), f.w = fmaf(w_e, y[e].w, f.w);
+                }
+              }
+              if (A.o32)
+                reinterpret_cast<float4 *>(A.o32)[place_x(rw) + c4 * rows_all] = f;
+              else
+                reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] =
+                    make_uint2(pack2<F16>(f.x, f.y), pack2<F16>(f.z, f.w));
+            }
           }
-        }
-        if (n_piece > 2) {
+          if (!last) break;  // those that are left are the last one's
+          ptx::named_sync(5, kSoftmaxThreads);  // the share's number is read
+          if (tid == 0) misc[4] = (int)atomicAdd(&A.counters[kMaxCtas + counter], 1u);
           ptx::named_sync(5, kSoftmaxThreads);
-          if (tid == 0 &&
-              atomicAdd(&A.counters[kMaxCtas + counter], 1u) == (unsigned)n_piece - 2)
-            A.counters[counter] = A.counters[kMaxCtas + counter] = 0u;  // for the next call
+          share = misc[4];
         }
       } else if (busy && valid && (whole || join)) {
         // a row per two threads; this CTA's piece is still in tensor memory, the
@@ -1085,6 +1104,12 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
                     make_uint4(pc[k][0], pc[k][1], pc[k][2], pc[k][3]);
           }
         }
+      }
+      if (tid == 0 && rows > 0 && n_piece > 2) {
+        // done with the stream's counters; the last that is clears them for the next call
+        __threadfence();
+        if (atomicAdd(&A.counters[counter], 1u << 16) >> 16 == (unsigned)n_piece - 1)
+          A.counters[counter] = A.counters[kMaxCtas + counter] = 0u;
       }
       ptx::tc_fence_before();
       ptx::named_sync(5, kSoftmaxThreads);  // O and red are free again

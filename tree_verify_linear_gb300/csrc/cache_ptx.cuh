@@ -52,16 +52,17 @@ __host__ __device__ constexpr uint32_t idesc_16(bool f16, int M, int N, bool b_m
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Wait until other CTAs of the launch have brought a counter up to n; false after
-// four seconds (they run already, or as soon as the SMs are free of other
-// launches).
-__device__ __forceinline__ bool wait_count(const unsigned int *count, unsigned int n) {
+// Wait until other CTAs of the launch have brought the low 16 bits of a counter up to
+// n; false after `limit` ns.  Nothing says that those CTAs are running: the caller must
+// do without them then.
+__device__ __forceinline__ bool wait_count(const unsigned int *count, unsigned int n,
+                                           uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     unsigned int c;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(c) : "l"(count) : "memory");
-    if (c >= n) return true;
-    if (globaltimer_ns() - t0 > 4 * kWaitNs) return false;
+    if ((c & 0xffffu) >= n) return true;
+    if (globaltimer_ns() - t0 > limit) return false;
     __nanosleep(100);
   }
   return false;
