@@ -396,7 +396,8 @@ size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *cfg);
  * ctx_len, before every window) may hold anything, NaN included.  A key that
  * one query of a request sees and another does not has to have a finite
  * value: it enters the other's sum with weight 0.  A query all of whose
- * scores are -inf gets o = 0 and lse = -inf.
+ * scores are -inf gets o = 0 and lse = -inf; one with a NaN among its scores
+ * gets NaN for both.
  * cfg->P must be 0.  Returns LBX_EINVAL for unsupported shapes, NULL or
  * misaligned pointers (16 bytes for the 16-bit arrays and the workspace, 4 for
  * the others) or a short workspace, LBX_ECUDA if a launch fails; an invalid
@@ -430,7 +431,8 @@ int lbx_prefix_attention(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const 
  * with w = exp(scale q.k - lse) for visible keys (visible as in
  * lbx_window_attention), else 0.  lse is what the attention call gave; with a
  * shared prefix it covers the prefix, whose keys are not scored; a query with
- * lse = -inf adds nothing.
+ * lse = -inf adds nothing; one with a NaN lse makes the sums of the keys it sees
+ * NaN.
  *   accepted [Bq] int32 in 0..N-1; q, k_cache, k_tree, lse as above;
  *   score [L][Bq][Hkv][T] fp32, in/out (entries j >= ctx_len are not touched;
  *   may be NULL when T == 0); score_tree [L][Bq][Hkv][N] fp32 out.

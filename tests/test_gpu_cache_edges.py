@@ -122,3 +122,83 @@ def test_calls_on_streams_of_two_priorities(P):
         for (_, _, o, lse, _, _), (got, got_lse) in zip(calls, turn):
             assert torch.equal(got, o) and torch.equal(got_lse, lse)
     assert begin.elapsed_time(end) < 1000  # a wait for a block that cannot run would take seconds
+
+
+# ---- NaN that a query does see -------------------------------------------------------
+
+NAN = {  # streams whole, in two pieces, in many, joined with a prefix's; the small kernel
+    "whole_pair": dict(L=16, Bq=6, N=22, Hq=12, Hkv=2, dh=256, T=200, ctx=[200] * 6),
+    "whole": dict(L=16, Bq=12, N=5, Hq=4, Hkv=1, dh=64, T=300, dtype="f16", ctx=[300] * 12),
+    "two_pieces": dict(L=1, Bq=1, N=22, Hq=48, Hkv=8, dh=256, T=4500, ctx=[4500]),
+    "many_pieces_pair": dict(L=1, Bq=2, N=22, Hq=6, Hkv=1, dh=256, T=9000, ctx=[9000, 8000]),
+    "many_pieces": dict(L=1, Bq=2, N=12, Hq=4, Hkv=1, dh=64, T=20000, ctx=[19999, 7000]),
+    "prefix_pair": dict(L=2, Bq=5, N=22, Hq=12, Hkv=2, dh=128, T=300, P=3001, dtype="f16", ctx=[300] * 5),
+    "prefix": dict(L=1, Bq=40, N=2, Hq=16, Hkv=4, dh=64, T=300, P=2049, ctx=[300] * 40),
+    "few_one_unit": dict(L=1, Bq=2, N=3, Hq=4, Hkv=2, dh=128, T=0),
+    "few_units": dict(L=1, Bq=2, N=1, Hq=8, Hkv=2, dh=256, T=700, ctx=[700, 650]),
+    "few_prefix": dict(L=1, Bq=2, N=2, Hq=4, Hkv=2, dh=64, T=90, P=150, dtype="f16", ctx=[90, 90]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(NAN))
+def test_a_nan_score_makes_its_query_nan(name):
+    inp = R.make_inputs(**NAN[name], seed=800 + len(name))
+    o, lse, _ = run_attention(inp)
+    nan = float("nan")
+    L, Bq, N, Hq = lse.shape
+    G, T = Hq // inp["k_tree"].shape[3], inp["k_cache"].shape[2]
+
+    def check(change, rows, lse_too=True):
+        bad = {k: v.clone() for k, v in inp.items()}
+        change(bad)
+        o2, lse2, status = run_attention(bad)
+        assert status == 0
+        hit = torch.zeros(lse.shape, dtype=torch.bool)
+        hit[rows] = True
+        assert o2[hit].isnan().all() and torch.equal(o2[~hit], o[~hit])
+        want = torch.where(hit, torch.full_like(lse, nan), lse) if lse_too else lse
+        assert torch.equal(torch.nan_to_num(lse2, nan=1e30), torch.nan_to_num(want, nan=1e30))
+
+    def one(bad, key, *at):
+        bad[key][at] = nan
+    # a query; the root's key; a cached key, the first and the last; one of the prefix; a value
+    check(lambda d: one(d, "q", L - 1, Bq - 1, N - 1, Hq - 1, 3), (L - 1, Bq - 1, N - 1, Hq - 1))
+    check(lambda d: one(d, "k_tree", 0, 0, 0, 0, 0), (0, 0, slice(None), slice(G)))
+    if T:
+        for j in (0, int(inp["ctx_len"][0]) - 1):
+            check(lambda d: one(d, "k_cache", 0, 0, j, 0, 1), (0, 0, slice(None), slice(G)))
+        check(lambda d: one(d, "v_cache", 0, 0, T // 3, 0), (0, 0, slice(None), slice(G)), lse_too=False)
+    if "k_prefix" in inp:
+        check(lambda d: one(d, "k_prefix", 0, 77, 0, 0), (0, slice(None), slice(None), slice(G)))
+
+
+def test_nan_beside_a_prefix_without_a_finite_score():
+    """Neither side's -inf hides the other's NaN."""
+    inp = R.make_inputs(1, 40, 2, 16, 4, 64, 30, P=2049, ctx=[30] * 40, seed=31)
+    inp["q"] = inp["q"].abs() + 1
+    for finite, hidden in ((("k_prefix",), ("k_cache", "k_tree")), (("k_cache", "k_tree"), ("k_prefix",))):
+        bad = {k: v.clone() for k, v in inp.items()}
+        for k in finite:
+            bad[k][:] = -float("inf")
+        for k in hidden:
+            bad[k][:] = float("nan")
+        o, lse, status = run_attention(bad)
+        assert status == 0 and o.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_a_nan_lse_reaches_the_weights_of_the_keys_it_sees(dh):
+    inp = R.make_inputs(1, 2, 8, 4, 2, dh, 150, ctx=[150, 90], tree="chain", seed=32)
+    inp["accepted"][:] = 7
+    _, ref_lse, _, _ = R.attention(inp, window=40, n_sink=2)
+    lse = torch.from_numpy(ref_lse.astype(np.float32))
+    score = np.zeros((1, 2, 2, 150), np.float32)
+    clean, clean_tree, _ = run_mass(inp, lse, score, window=40, n_sink=2)
+    lse[0, 0, 5, 0] = float("nan")
+    got, tree, status = run_mass(inp, lse, score, window=40, n_sink=2)
+    assert status == 0
+    js, ms = R.visible(inp["parent"][0].tolist(), 5, 150, 40, 2)
+    hit, hit_tree = np.zeros(got.shape, bool), np.zeros(tree.shape, bool)
+    hit[0, 0, 0, js], hit_tree[0, 0, 0, ms] = True, True
+    assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], clean[~hit])
+    assert np.isnan(tree[hit_tree]).all() and np.array_equal(tree[~hit_tree], clean_tree[~hit_tree])

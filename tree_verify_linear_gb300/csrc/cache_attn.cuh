@@ -842,13 +842,14 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
         return (size_t)(l * A.Hkv + h) * rows_all + (size_t)b * A.til.rows + rw;
       };
       // The factors of this stream's O and of the first launch's o, and the row's lse.
+      // (A NaN among a row's scores makes its sum one, and the row with it.)
       auto factors = [&](int rw, float m, float sum, float &w, float &wx) {
-        const float own = sum > 0.f ? m + __log2f(sum) : -INFINITY;
+        const float own = sum == 0.f ? -INFINITY : m + __log2f(sum);
         float all = own;
-        w = sum > 0.f ? __fdividef(1.f, sum) : 0.f, wx = 0.f;
+        w = sum == 0.f ? 0.f : __fdividef(1.f, sum), wx = 0.f;
         if (A.x_o) {
           const float x = __ldcg(A.x_lse2 + place_xl(rw)), top = fmaxf(own, x);
-          if (top != -INFINITY) {
+          if (own != -INFINITY || x != -INFINITY) {
             const float eo = ptx::ex2(own - top), ex = ptx::ex2(x - top);
             const float inv = __fdividef(1.f, eo + ex);
             w *= eo * inv, wx = ex * inv;
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 10; ++e) {
                   const float w_e = e0 + e < n_piece ? red[(e0 + e) * here + rr] : 0.f;
-                  if (w_e > 0.f)  // (an empty piece's O holds nothing)
+                  if (w_e != 0.f)  // (an empty piece's O holds nothing)
                     f.x = fmaf(w_e, y[e].x, f.x), f.y = fmaf(w_e, y[e].y, f.y),
                     f.z = fmaf(w_e, y[e].z, f.z), f.w = fmaf(w_e, y[e].w, f.w);
                 }

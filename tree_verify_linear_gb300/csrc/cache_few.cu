@@ -242,14 +242,14 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewArgs A) 
     return ((size_t)lb * c.N + node) * c.Hq + h * G + (r - node * G);
   };
   auto put_lse = [&](int r, float m2, float sum1) {
-    if (A.lse) A.lse[query(r)] = sum1 > 0.f ? (m2 + __log2f(sum1)) * 0.6931471805599453f : -INFINITY;
+    if (A.lse) A.lse[query(r)] = sum1 == 0.f ? -INFINITY : (m2 + __log2f(sum1)) * 0.6931471805599453f;
   };
   if (units == 1) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = row + e * 8;
       if (r >= rows) continue;
-      const float w = total[e] > 0.f ? __fdividef(1.f, total[e]) : 0.f;
+      const float w = total[e] == 0.f ? 0.f : __fdividef(1.f, total[e]);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
         reinterpret_cast<uint32_t *>(A.o + query(r) * DH)[(warp * kTiles + t) * 4 + (lane & 3)] =
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewArgs A) 
       w_of[i] = w, sum1 = fmaf(w, s_of[i], sum1);
     }
     put_lse(tid, ref, sum1);
-    s_of[tid] = sum1 > 0.f ? __fdividef(1.f, sum1) : 0.f;
+    s_of[tid] = sum1 == 0.f ? 0.f : __fdividef(1.f, sum1);
   }
   __syncthreads();
 #pragma unroll 1
