@@ -386,7 +386,10 @@ size_t lbx_cache_attn_workspace_size(const lbx_attn_cfg *cfg);
  * visible.  Cached position j < ctx_len[b] is visible to node n if
  *     window == 0  or  ctx_len[b] + depth(n) - j < window  or  j < n_sink,
  * and tree node m on n's root path (itself included) if the same holds for
- * m's position ctx_len[b] + depth(m).  Over the visible keys of each query
+ * m's position ctx_len[b] + depth(m).  A window counts places in the cache: it
+ * needs one that holds every position in order, as an append-only cache does.
+ * Where lbx_cache_evict has dropped entries, window must be 0 here and in
+ * lbx_attention_mass.  Over the visible keys of each query
  *     o = sum_j exp(scale q.k_j - lse) v_j,  lse = log sum_j exp(scale q.k_j).
  *   q [L][Bq][N][Hq][dh], k_cache, v_cache [L][Bq][T][Hkv][dh] (may be NULL
  *   when T == 0), k_tree, v_tree [L][Bq][N][Hkv][dh], o [L][Bq][N][Hq][dh]
@@ -454,8 +457,9 @@ int lbx_attention_mass(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const in
  * (NaN below every number, -0 equal to 0); ties go to the lowest index.
  * Cached entries that stay at an index below size do not move; the others
  * that stay, in order of their index, fill the free places below size, in
- * order.  The order of the cache's entries is thus not that of their
- * positions, which pos keeps; keys carry their position encoding with them.
+ * order.  Once entries have been dropped the order of those in the cache is
+ * not that of their positions, which pos keeps; keys carry their position
+ * encoding with them.  Until then (seen <= budget) the call appends in order.
  * Places at or past size keep what they held.
  *   k_cache, v_cache [L][Bq][T][Hkv][dh], score fp32 and pos int32
  *   [L][Bq][Hkv][T]: in/out; k_tree, v_tree [L][Bq][N][Hkv][dh], score_tree

@@ -202,3 +202,25 @@ def test_a_nan_lse_reaches_the_weights_of_the_keys_it_sees(dh):
     hit[0, 0, 0, js], hit_tree[0, 0, 0, ms] = True, True
     assert np.isnan(got[hit]).all() and np.array_equal(got[~hit], clean[~hit])
     assert np.isnan(tree[hit_tree]).all() and np.array_equal(tree[~hit_tree], clean_tree[~hit_tree])
+
+
+# ---- windows and eviction ----------------------------------------------------------
+
+def test_the_example_windows_see_the_last_positions():
+    """Its windowed queries see the positions up to their own, of a cache that
+    holds them all in order, while the other cache drops entries."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples", "bounded_cache.py")
+    spec = importlib.util.spec_from_file_location("bounded_cache", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    s = ex.serve(60, 64)
+    n = s["seen"].tolist()
+    assert s["len_all"].tolist() == n and (s["ctx"] == 64).all() and min(n) > ex.WINDOW
+    for b in range(ex.BQ):
+        assert (s["pos_all"][:, b, :, :n[b]].cpu() == torch.arange(n[b])).all()
+    inp = {k: s[k].cpu() for k in ("parent", "q", "k_tree", "v_tree", "ctx_len")}
+    inp.update(k_cache=s["k_all"].cpu(), v_cache=s["v_all"].cpu())
+    ref, _, tol, _ = R.attention_dense(inp, window=ex.WINDOW, n_sink=ex.SINKS)
+    assert (np.abs(s["o_win"].cpu().double().numpy() - ref) <= tol).all()
