@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import cache_ref as R
-from test_gpu_cache import built, cfg_of, check_attention, run_attention, run_mass  # noqa: F401 (built: a fixture)
+from test_gpu_cache import (built, cfg_of, check_attention, run_attention, run_evict,  # noqa: F401
+                            run_mass)  # (built: a fixture)
 from tree_verify_linear_gb300 import lbx
 
 pytestmark = pytest.mark.gpu
@@ -224,3 +225,52 @@ def test_the_example_windows_see_the_last_positions():
     inp.update(k_cache=s["k_all"].cpu(), v_cache=s["v_all"].cpu())
     ref, _, tol, _ = R.attention_dense(inp, window=ex.WINDOW, n_sink=ex.SINKS)
     assert (np.abs(s["o_win"].cpu().double().numpy() - ref) <= tol).all()
+
+
+# ---- host threads --------------------------------------------------------------------
+
+def test_host_threads_call_with_different_sizes():
+    """Two threads, small and large calls of the operators whose shared memory goes
+    by their sizes; the library lets them run at the same time."""
+    import threading
+    ok, failed = [], []
+
+    def work(T, N):
+        try:
+            inp = R.make_inputs(1, 1, N, 8, 1, 64, T, ctx=[T], seed=T)
+            d = {k: v.cuda() for k, v in inp.items()}
+            cfg, stream = cfg_of(inp), torch.cuda.Stream()
+            f32, i32 = {"device": "cuda"}, {"dtype": torch.int32, "device": "cuda"}
+            lse, score, tree = torch.zeros(1, 1, N, 8, **f32), torch.zeros(1, 1, 1, T, **f32), torch.zeros(1, 1, 1, N, **f32)
+            pos, outs = torch.zeros(1, 1, 1, T, **i32), [torch.zeros(1, **i32) for _ in range(2)]
+            torch.cuda.synchronize()
+            for _ in range(1500):
+                lbx.lbx_attention_mass(cfg, d["ctx_len"], d["parent"], d["accepted"], d["q"], lse,
+                                       d["k_cache"], d["k_tree"], score, tree, stream=stream)
+                lbx.lbx_cache_evict(cfg, T, 0, d["ctx_len"], d["ctx_len"], d["parent"], d["accepted"],
+                                    d["k_tree"], d["v_tree"], tree, d["k_cache"], d["v_cache"], score,
+                                    pos, *outs, stream=stream)
+            stream.synchronize()
+            ok.append(T)
+        except Exception as e:  # noqa: BLE001 (told to the test's own thread)
+            failed.append(repr(e))
+    threads = [threading.Thread(target=work, args=a) for a in ((70, 1), (15000, 30), (1000, 8))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and len(ok) == 3, failed
+
+
+def test_the_longest_cache_evict_takes():
+    T = lbx.LBX_EVICT_MAX_T
+    inp = R.make_inputs(1, 1, 64, 1, 1, 64, T, ctx=[T], tree="chain", seed=33)
+    inp["accepted"][:] = 63
+    score = np.arange(T, dtype=np.float32).reshape(1, 1, 1, T)
+    pos = np.arange(T, dtype=np.int32).reshape(1, 1, 1, T)
+    tree = np.full((1, 1, 1, 64), 2.0 * T, np.float32)
+    (k, v, s, p, ctx, seen), status = run_evict(inp, score, tree, pos, [T], T, 0, 0)
+    # the 64 lowest leave, the path takes their places in order
+    assert status == 0 and ctx.tolist() == [T] and seen.tolist() == [T + 64]
+    assert p[0, 0, 0, :64].tolist() == list(range(T, T + 64)) and np.array_equal(p[..., 64:], pos[..., 64:])
+    assert torch.equal(k[0, 0, :64], inp["k_tree"][0, 0]) and torch.equal(v[:, :, 64:], inp["v_cache"][:, :, 64:])

@@ -34,6 +34,12 @@ constexpr int kBatch = 512;  // rows whose source and place are listed at a time
 constexpr size_t kKeyBytes = 96 * 1024;
 constexpr int kFly = 8;  // 16-byte pieces of rows in flight per thread
 
+// Bytes of the bits and counts of n candidates.
+constexpr size_t bit_bytes(size_t n) { return ((n + 63) / 64 * 12 + 15) & ~(size_t)15; }
+// The most shared memory a call asks for.
+constexpr size_t kMostBytes = bit_bytes((size_t)LBX_EVICT_MAX_T + kMaxNodes);
+static_assert(kMostBytes >= kKeyBytes && kMostBytes <= 220 * 1024, "shared memory");
+
 struct Args {
   lbx_attn_cfg c;
   int budget, n_recent, keep_keys, share;  // share: CTAs per selection
@@ -285,11 +291,13 @@ extern "C" int lbx_cache_evict(const lbx_attn_cfg *c, int budget, int n_recent,
       !aligned_to(score, 4) || !aligned_to(pos, 4) || !aligned_to(ctx_out, 4) ||
       !aligned_to(seen_out, 4) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
-  const size_t n = (size_t)c->T + c->N, bits = ((n + 63) / 64 * 12 + 15) & ~(size_t)15;
+  const size_t n = (size_t)c->T + c->N, bits = bit_bytes(n);
   const int keep_keys = n * 4 + bits <= kKeyBytes;
   const size_t shared = bits + (keep_keys ? n * 4 : 0);
+  // the limit is the function's, not the call's: the same for all, since another host
+  // thread may set it between this and the launch
   if (cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)shared) != cudaSuccess)
+                           (int)kMostBytes) != cudaSuccess)
     return LBX_ECUDA;
   // A cache larger than its budget may have many rows to move: CTAs share each
   // selection as long as all of them run at once (two waves of clusters would

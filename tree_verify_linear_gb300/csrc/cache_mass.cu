@@ -63,6 +63,7 @@ constexpr int kTailMisc = kTailNodes + kMaxNodes * 4;    // int [4]
 constexpr int kTailBars = kTailMisc + 16;                // full, empty, s[2], free[2], q, end
 constexpr int kTail = kTailBars + (2 * kMaxStages + 6) * 8;
 static_assert(kTail <= 3072, "shared memory");
+constexpr int kMostBytes = 227 * 1024;
 
 template <int DH, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -370,7 +371,9 @@ template <int DH>
 cudaError_t launch_mass(bool f16, const AttnMaps &maps, const MassArgs &A, int grid, int bytes,
                         cudaStream_t stream) {
   auto kernel = f16 ? mass_kernel<DH, true> : mass_kernel<DH, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // (the same limit for all calls: another host thread may set it before this launch)
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, kThreads, (size_t)bytes, stream>>>(maps, A);
   return cudaGetLastError();
@@ -414,7 +417,7 @@ extern "C" int lbx_attention_mass(const lbx_attn_cfg *c, const int32_t *ctx_len,
   const int most = c->dh == 256 ? 128 : kMaxRows;
   A.cap = c->N * G < most ? (c->N * G + 31) & ~31 : most;
   const int q_bytes = A.cap * c->dh * 2;
-  A.stages = (227 * 1024 - kTail - q_bytes) / kPiece;
+  A.stages = (kMostBytes - kTail - q_bytes) / kPiece;
   if (A.stages > kMaxStages) A.stages = kMaxStages;
   const int bytes = q_bytes + A.stages * kPiece + kTail;
   const bool f16 = c->dtype == LBX_F16;
