@@ -465,7 +465,8 @@ int lbx_attention_mass(const lbx_attn_cfg *cfg, const int32_t *ctx_len, const in
  *   [L][Bq][Hkv][T]: in/out; k_tree, v_tree [L][Bq][N][Hkv][dh], score_tree
  *   [L][Bq][Hkv][N]; ctx_len, seen, accepted [Bq], parent [Bq][N]: in;
  *   ctx_out [Bq] = size and seen_out [Bq] = seen + nodes of the path: out
- *   (no overlap with the inputs; they are the next step's ctx_len and seen).
+ *   (LBX_EINVAL if they overlap each other, ctx_len, seen, parent or accepted;
+ *   they are the next step's ctx_len and seen).
  * 1 <= budget <= T <= LBX_EVICT_MAX_T, n_sink >= 0, n_recent >= 0.  cfg->P, window and scale are
  * not read.  Errors as in lbx_attention_mass.
  */

@@ -38,3 +38,15 @@ def test_the_small_kernel_has_a_block_for_every_unit(lib):
                 got = chunks(ctypes.byref(cfg))
                 most = max(units_of(ctx, window, n_sink) for ctx in range(T + 1))
                 assert got == most, (T, window, n_sink)
+
+
+@pytest.mark.parametrize("out,on", [(o, i) for o in (11, 12) for i in (0, 1, 2, 3)] + [(11, 12)])
+@pytest.mark.parametrize("at", [-60, 0, 60])
+def test_eviction_refuses_outputs_over_its_inputs(lib, out, on, at):
+    """Arguments 11 and 12 are ctx_out and seen_out, 0 to 3 ctx_len, seen, parent
+    and accepted, 16 requests each (nothing is read: the call is refused first)."""
+    from tree_verify_linear_gb300 import lbx
+    cfg = lbx.make_attn_cfg(L=1, Bq=16, N=4, Hq=4, Hkv=2, dh=64, T=8)
+    args = [(i + 1) << 20 for i in range(13)]
+    args[out] = args[on] + at
+    assert lib.lbx_cache_evict(ctypes.byref(cfg), 4, 0, *args, None, None) == lbx.LBX_EINVAL

@@ -274,3 +274,22 @@ def test_the_longest_cache_evict_takes():
     assert status == 0 and ctx.tolist() == [T] and seen.tolist() == [T + 64]
     assert p[0, 0, 0, :64].tolist() == list(range(T, T + 64)) and np.array_equal(p[..., 64:], pos[..., 64:])
     assert torch.equal(k[0, 0, :64], inp["k_tree"][0, 0]) and torch.equal(v[:, :, 64:], inp["v_cache"][:, :, 64:])
+
+
+def test_eviction_takes_outputs_beside_its_inputs():
+    """ctx_len, seen, accepted and the outputs as rows of one array."""
+    Bq = 16
+    inp = R.make_inputs(1, Bq, 3, 2, 2, 64, 40, seed=34)
+    d = {k: v.cuda() for k, v in inp.items()}
+    rows = torch.zeros(5, Bq, dtype=torch.int32, device="cuda")
+    rows[0], rows[1], rows[2] = d["ctx_len"], 50, d["accepted"]
+    score = torch.rand(1, Bq, 2, 40, device="cuda")
+    pos = torch.zeros(1, Bq, 2, 40, dtype=torch.int32, device="cuda")
+    args = (d["parent"], rows[2], d["k_tree"], d["v_tree"], torch.rand(1, Bq, 2, 3, device="cuda"),
+            d["k_cache"], d["v_cache"], score, pos)
+    lbx.lbx_cache_evict(cfg_of(inp), 30, 0, rows[0], rows[1], *args, rows[3], rows[4])
+    for b in range(Bq):
+        path = len(R.root_path(inp["parent"][b].tolist(), int(inp["accepted"][b])))
+        assert rows[3, b] == min(30, int(inp["ctx_len"][b]) + path) and rows[4, b] == 50 + path
+    with pytest.raises(lbx.LbxError):
+        lbx.lbx_cache_evict(cfg_of(inp), 30, 0, rows[0], rows[1], *args, rows[0], rows[4])

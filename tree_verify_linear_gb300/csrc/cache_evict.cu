@@ -18,6 +18,8 @@
 // the copies that put scores and positions back, 4.9 TB/s while rows of 512 bytes
 // move, 15 us for the selection; a full cache of 4096 that takes six entries, 64
 // lists: 14.3 us, the latency of the selection's passes.
+#include <initializer_list>
+
 #include "cache_common.cuh"
 #include "cache_ptx.cuh"
 #include "cache_walk.cuh"
@@ -291,6 +293,17 @@ extern "C" int lbx_cache_evict(const lbx_attn_cfg *c, int budget, int n_recent,
       !aligned_to(score, 4) || !aligned_to(pos, 4) || !aligned_to(ctx_out, 4) ||
       !aligned_to(seen_out, 4) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
+  // CTAs read the inputs while one writes the outputs
+  const size_t per = (size_t)c->Bq * 4;
+  auto apart = [](const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x + na <= y || y + nb <= x;
+  };
+  for (const void *out : {ctx_out, seen_out})
+    if (!apart(out, per, ctx_len, per) || !apart(out, per, seen, per) ||
+        !apart(out, per, accepted, per) || !apart(out, per, parent, per * c->N))
+      return LBX_EINVAL;
+  if (!apart(ctx_out, per, seen_out, per)) return LBX_EINVAL;
   const size_t n = (size_t)c->T + c->N, bits = bit_bytes(n);
   const int keep_keys = n * 4 + bits <= kKeyBytes;
   const size_t shared = bits + (keep_keys ? n * 4 : 0);
