@@ -293,3 +293,32 @@ def test_eviction_takes_outputs_beside_its_inputs():
         assert rows[3, b] == min(30, int(inp["ctx_len"][b]) + path) and rows[4, b] == 50 + path
     with pytest.raises(lbx.LbxError):
         lbx.lbx_cache_evict(cfg_of(inp), 30, 0, rows[0], rows[1], *args, rows[0], rows[4])
+
+
+# ---- many small weights beside a large one ---------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dh,N,Hq,Bq,T", [(64, 1, 1, 160, 8192), (128, 44, 3, 80, 4096), (256, 1, 1, 160, 4096)])
+def test_many_small_weights_beside_a_large_one(dtype, dh, N, Hq, Bq, T):
+    """The first key scores 17.75 above all others, whose weights (2^-25.6) are below
+    the smallest f16: together they are all there is of o, whose error is the
+    roundings of o and of the weights (u each) and, in f16, 2^-32 for each key."""
+    el = R.DTYPE[dtype]
+    q = torch.zeros(1, Bq, N, Hq, dh, dtype=el, device="cuda")
+    q[..., 0] = 8
+    kc, vc = (torch.zeros(1, Bq, T, 1, dh, dtype=el, device="cuda") for _ in range(2))
+    kc[:, :, 0, :, 0], vc[:, :, 1:] = 17.75, 1
+    kt, vt = (torch.zeros(1, Bq, N, 1, dh, dtype=el, device="cuda") for _ in range(2))
+    kt[..., 0] = -100
+    parent = torch.zeros(Bq, N, dtype=torch.int32, device="cuda")
+    parent[:, 0] = -1
+    ctx, status = torch.full((Bq,), T, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cfg = lbx.make_attn_cfg(1, Bq, N, Hq, 1, dh, T, dtype=lbx.LBX_F16 if dtype == "f16" else lbx.LBX_BF16, scale=0.125)
+    o, lse = torch.empty_like(q), torch.empty(1, Bq, N, Hq, device="cuda")
+    lbx.lbx_window_attention(cfg, ctx, parent, q, kc, vc, kt, vt, o, lbx.new_cache_attn_workspace(cfg), lse=lse,
+                             d_status=status)
+    small = (T - 1) * np.exp(-17.75)
+    want, u = small / (1 + small), 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
+    tol = 2 * u * want + (T * 2.0 ** -32 if dtype == "f16" else 0)
+    assert int(status.item()) == 0 and float((o.double() - want).abs().max()) <= tol
+    assert float((lse.double() - 17.75 - np.log1p(small)).abs().max()) <= 2.0 ** -20 * 20

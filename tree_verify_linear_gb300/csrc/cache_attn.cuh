@@ -17,7 +17,10 @@
 // (2^-17 of a weight): with hi alone the weights' rounding (2^-8 each) would
 // add as much error as the rounding of o to bf16, the only one left otherwise.
 // In f16 a weight's rounding (2^-11) is as small as that of o in f16, and one
-// product serves.
+// product serves (the error of o is 1.4 times that of weights in fp32).  f16 ends
+// at 2^-25, which many small weights beside one large one add up to: weights are
+// taken 2^7 times as large there (2^15 at most), so that what falls below is 2^-32 of
+// the reference.
 //
 // The key list is cut into units of 64 keys from one array: the visible first
 // positions before the window, the window, the tree's own keys.  A block is
@@ -167,6 +170,10 @@ constexpr int kLeadBlocks = 4, kJoinBlocks = 8, kJoinPrefixBlocks = 13;
 // Parts of P: f16 once, bf16 hi + lo.
 template <bool F16>
 constexpr int kParts = F16 ? 1 : 2;
+
+// What f16 weights are raised by, as a power of two.
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
           l_run *= alpha;
           m_run = mb;
         }
-        const float ref = m_run == -INFINITY ? 0.f : m_run * sl2;
+        const float ref = m_run == -INFINITY ? 0.f : fmaf(m_run, sl2, -kLift<F16>);
         {
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t pk[Y::kMine / 2];
@@ -834,7 +841,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       if (bad) misc[3] = 1;
       ptx::named_sync(5, kSoftmaxThreads);
       const bool valid = misc[3] == 0;
-      float l_sum = sums[r] + sums[kRows + r], m2 = m_run == -INFINITY ? -INFINITY : m_run * sl2;
+      float l_sum = sums[r] + sums[kRows + r];
+      float m2 = m_run == -INFINITY ? -INFINITY : fmaf(m_run, sl2, -kLift<F16>);
       if (!valid) l_sum = 0.f, m2 = -INFINITY;
       // A finished row's place among all queries, and in the first launch's lse.
       auto place = [&](int rw) { return queries(l, b, h) + query_of(rw); };
@@ -844,7 +852,8 @@ __global__ void __launch_bounds__(Lay<DH, PAIR>::kThreads, 1)
       // The factors of this stream's O and of the first launch's o, and the row's lse.
       // (A NaN among a row's scores makes its sum one, and the row with it.)
       auto factors = [&](int rw, float m, float sum, float &w, float &wx) {
-        const float own = sum == 0.f ? -INFINITY : m + __log2f(sum);
+        constexpr float kDown = F16 ? 1.f / 128.f : 1.f;  // 2^-kLift
+        const float own = sum == 0.f ? -INFINITY : m + kLift<F16> + __log2f(sum * kDown);
         float all = own;
         w = sum == 0.f ? 0.f : __fdividef(1.f, sum), wx = 0.f;
         if (A.x_o) {
