@@ -13,10 +13,11 @@
 //
 // The tensor cores truncate as they accumulate, about half a unit in the 24th bit
 // of the running sum per 16 columns; a weight takes the score's absolute error as
-// its relative one.  Up to 128 rows each half of the head dimension has an
-// accumulator of its own and the two are added here, which halves that error
-// (1.5e-6 to 0.7e-6 of a path key's sum at dimension 256); with more rows the
-// columns of tensor memory do not allow it.
+// its relative one.  So parts of the head dimension have accumulators of their own,
+// as many as the columns of tensor memory allow, and are added here: four up to 64
+// rows per pass, two up to 128, else one.  Error of the path keys' sums against 64 bits
+// (2-norms): 0.4e-6 at most with four (dimension 256, where two gave 0.75e-6 and
+// operations in fp32 give 0.5e-6), 0.95e-6 with one (dimension 128; fp32: 0.6e-6).
 //
 // The path's nodes are taken root first, so row d G + h belongs to the node of
 // depth d, and the rows that see a key are one range of rows.  Up to 128 rows
@@ -29,9 +30,9 @@
 // columns).  Waits are bounded as in the attention kernel.
 //
 // Measured: 16 layers, five requests of 4097 to 8192 keys, paths of 6 nodes, 24/4
-// heads of dimension 256: 168 us, 6.1 TB/s (91% of a copy's rate); one layer, one
+// heads of dimension 256: 167 us, 6.2 TB/s (91% of a copy's rate); one layer, one
 // token, 3001 keys: 10.3 us, launch and host call.  Paths of 40 nodes at 4 heads per
-// group: 72 us, 45%: 160 exponentials per key.
+// group: 74 us, 45%: 160 exponentials per key.
 #include "cache_ptx.cuh"
 #include "cache_walk.cuh"
 
@@ -64,6 +65,10 @@ constexpr int kTailBars = kTailMisc + 16;                // full, empty, s[2], f
 constexpr int kTail = kTailBars + (2 * kMaxStages + 6) * 8;
 static_assert(kTail <= 3072, "shared memory");
 constexpr int kMostBytes = 227 * 1024;
+
+// Accumulators of a score buffer's 256 columns for a pass of nr rows: parts of the head
+// dimension, each with its own.
+__device__ __forceinline__ int accumulators(int nr) { return nr <= 64 ? 4 : nr <= 128 ? 2 : 1; }
 
 template <int DH, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r0 = 0; r0 < rows && !bad; r0 += A.cap, ++seg) {
         const int nr = (rows - r0 < A.cap ? rows - r0 + 31 : A.cap) & ~31;
         const uint32_t idesc = ptx::idesc_16(F16, 128, nr, false);
-        const bool two = nr <= 128;  // accumulators
+        const int acc = accumulators(nr), per = DH / 16 / acc;
         if (!wait_all(q_bar, seg & 1)) break;
 #pragma unroll 1
         for (int i = 0; i < W.blk1 - W.blk0 && !bad; ++i) {
@@ -195,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one) {
 #pragma unroll
               for (int s = 0; s < 4; ++s) {
-                const int step = a * 4 + s, mid = two ? DH / 32 : DH / 16;
-                ptx::mma_bf16_ss(tmem + buf * 256 + (step >= mid ? 128 : 0), kd + 2 * s, qd + 2 * s,
-                                 idesc, step > 0 && step != mid ? 1u : 0u);
+                const int step = a * 4 + s, at = step / per;
+                ptx::mma_bf16_ss(tmem + buf * 256 + at * (256 / acc), kd + 2 * s, qd + 2 * s, idesc,
+                                 step > at * per ? 1u : 0u);
               }
               ptx::mma_commit(&empty[st]);
               if (a == kPieces - 1) ptx::mma_commit(&s_bar[buf]);
@@ -323,13 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           float s0[32], s1[32];
           ptx::tmem_ld32(tq, s0);
-          if (nr <= 128) {  // two accumulators
+          const int acc = accumulators(nr);
+          if (acc > 1) {
 #pragma unroll 1
             for (int c = 0; c < nr; c += 32) {
-              ptx::tmem_ld32(tq + 128 + c, s1);
+              ptx::tmem_ld32(tq + 256 / acc + c, s1);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e) s1[e] += s0[e];
+#pragma unroll 1
+              for (int k = 2; k < acc; ++k) {
+                ptx::tmem_ld32(tq + k * (256 / acc) + c, s0);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s1[e] += s0[e];
+              }
               if (c + 32 < nr) ptx::tmem_ld32(tq + c + 32, s0);
               weigh(s1, c);
             }
