@@ -322,3 +322,23 @@ def test_many_small_weights_beside_a_large_one(dtype, dh, N, Hq, Bq, T):
     tol = 2 * u * want + (T * 2.0 ** -32 if dtype == "f16" else 0)
     assert int(status.item()) == 0 and float((o.double() - want).abs().max()) <= tol
     assert float((lse.double() - 17.75 - np.log1p(small)).abs().max()) <= 2.0 ** -20 * 20
+
+
+# ---- full-context tree attention ---------------------------------------------------------
+
+def test_tree_attention_gives_the_same_bits_every_time():
+    """Its halves of a row exchange every block's maxima: two buffers, so that one
+    may run ahead of the other; 200 calls of 64 blocks per block of threads agree."""
+    L, Bq, N, Hq, Hkv, dh, T = 2, 3, 22, 12, 2, 256, 20000
+    inp = R.make_inputs(L, Bq, N, Hq, Hkv, dh, T, ctx=[20000, 17001, 19], seed=35)
+    d = {k: v.cuda() for k, v in inp.items()}
+    ws = lbx.new_attn_workspace(L, Bq, N, Hq, Hkv, dh, T)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.empty(L, Bq, N, Hq, dh, device="cuda") for _ in range(2)]
+    for i in range(200):
+        lbx.lbx_tree_attention(dh ** -0.5, d["ctx_len"], d["parent"], d["q"], d["k_cache"], d["v_cache"],
+                               d["k_tree"], d["v_tree"], outs[min(i, 1)], ws, status)
+        if i:
+            assert torch.equal(outs[0], outs[1]), i
+    ref, _, tol, _ = R.attention_dense(inp)
+    assert int(status.item()) == 0 and (np.abs(outs[0].cpu().double().numpy() - ref) <= tol).all()

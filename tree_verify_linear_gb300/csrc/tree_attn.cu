@@ -74,8 +74,8 @@ constexpr int kKBytes = (kDh / 64) * kKVAtom;      // 32 KB: one K (or V) block
 constexpr int kSmemK = 0;
 constexpr int kSmemV = kSmemK + kKStages * kKBytes;
 constexpr int kSmemAnc = kSmemV + kVStages * kKBytes;      // uint64 [64]
-constexpr int kSmemRed = kSmemAnc + kMaxNodes * 8;        // float [2][128]
-constexpr int kSmemMisc = kSmemRed + 2 * kRows * 4;       // int [16]
+constexpr int kSmemRed = kSmemAnc + kMaxNodes * 8;        // float [2][2][128]
+constexpr int kSmemMisc = kSmemRed + 4 * kRows * 4;       // int [16]
 constexpr int kNBars = kKStages + kVStages + 6;           // k, v, s[2], o[2], p[2]
 constexpr int kSmemBars = kSmemMisc + 64;                 // uint64 [kNBars]
 constexpr int kSmemTotal = kSmemBars + kNBars * 8;
@@ -183,7 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int N = A.N, Bq = A.Bq, Hkv = A.Hkv, tiles = g.tiles;
   int *misc = reinterpret_cast<int *>(smem + kSmemMisc);  // [0] TMEM base, [1] last CTA
   uint64_t *anc = reinterpret_cast<uint64_t *>(smem + kSmemAnc);
-  float *red = reinterpret_cast<float *>(smem + kSmemRed);  // [2][kRows] per-half values
+  // [2][2][kRows] per-half values: the maxima of block q in buffer q & 1 (a half may be
+  // a block ahead of its reader), then the sums
+  float *red = reinterpret_cast<float *>(smem + kSmemRed);
   uint64_t *k_bar = reinterpret_cast<uint64_t *>(smem + kSmemBars);  // [kKStages]
   uint64_t *v_bar = k_bar + kKStages;                                 // [kVStages]
   uint64_t *s_bar = v_bar + kVStages;                                 // [2]
@@ -459,7 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], mx[e + 4]);
         const float mh = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        red[hf * kRows + r] = mh;
+        float *max_of = red + (q & 1) * 2 * kRows;
+        max_of[hf * kRows + r] = mh;
         // context keys past the cache's end: their V rows are zeroed, so that a
         // non-finite value there cannot reach O through a zero weight
         const int vrows = kend - key0;
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::fence_proxy_async();
         }
         ptx::named_sync(1, kSoftmaxThreads);  // ---------------- both halves' maxima
-        const float mb = fmaxf(mh, red[(1 - hf) * kRows + r]);
+        const float mb = fmaxf(mh, max_of[(1 - hf) * kRows + r]);
         float alpha = 1.f;
         bool need = false;
         if (mb > m_run + 8.f) {  // move the reference maximum (also the first time)
