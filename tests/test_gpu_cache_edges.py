@@ -342,3 +342,51 @@ def test_tree_attention_gives_the_same_bits_every_time():
             assert torch.equal(outs[0], outs[1]), i
     ref, _, tol, _ = R.attention_dense(inp)
     assert int(status.item()) == 0 and (np.abs(outs[0].cpu().double().numpy() - ref) <= tol).all()
+
+
+# ---- precision of the weights ---------------------------------------------------------
+
+@pytest.mark.parametrize("dh,N,Hq,Bq", [(64, 1, 1, 100), (64, 1, 1, 400), (128, 1, 2, 400), (128, 43, 3, 200),
+                                        (256, 1, 1, 100), (256, 1, 1, 400), (256, 22, 6, 200)])
+def test_bf16_weights_are_not_rounded_to_bf16(dh, N, Hq, Bq):
+    """Two keys whose values nearly cancel: o is what the rounding of the second value
+    leaves, 2^-8 of a weight at most.  Weights in bf16 would be off by as much; as hi + lo
+    they are good to 2^-17, and o's own rounding is 2^-8 of o.  (e: of a score, as in
+    cache_ref; every row of a request asks the same.)"""
+    g = torch.Generator().manual_seed(dh + N)
+    q0 = torch.randn(Bq, dh, generator=g).bfloat16()
+    k = torch.randn(Bq, 2, dh, generator=g).bfloat16()
+    q0[:, 0], k[:, :, 0] = 8, 0
+    s = torch.einsum("bd,bjd->bj", q0.double(), k.double()) * dh ** -0.5
+    w = s.softmax(-1)
+    v1 = (-(w[:, 0] / w[:, 1])).bfloat16()
+    want = w[:, 0] + w[:, 1] * v1.double()
+    e = (dh + 2) * 2.0 ** -24 * dh ** -0.5 * torch.einsum("bd,bjd->bj", q0.double().abs(), k.double().abs()).amax(-1)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -17 + 2 * e + 2.0 ** -20) * 2 * w[:, 0]
+    inp = {"q": q0[None, :, None, None].expand(1, Bq, N, Hq, dh).contiguous(), "k_cache": k[None, :, :, None],
+           "v_cache": torch.stack([torch.ones_like(v1), v1], 1)[None, :, :, None, None].expand(1, Bq, 2, 1, dh).contiguous(),
+           "k_tree": torch.zeros(1, Bq, N, 1, dh).bfloat16(), "v_tree": torch.zeros(1, Bq, N, 1, dh).bfloat16(),
+           "ctx_len": torch.full((Bq,), 2, dtype=torch.int32), "parent": torch.zeros(Bq, N, dtype=torch.int32)}
+    inp["k_tree"][..., 0] = -1000
+    inp["parent"][:, 0] = -1
+    o, _, status = run_attention(inp)
+    over = (o[0].double() - want[:, None, None, None]).abs() / tol[:, None, None, None]
+    assert status == 0 and float(over.max()) <= 1
+
+
+# ---- single tokens in f16 ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("Bq,T,window", [(2, 1, 0), (2, 65, 0), (3, 300, 100), (16, 2100, 0), (16, 2500, 700)])
+def test_single_tokens_in_f16(dh, Bq, T, window):
+    """Attention and weights of plain decode steps, the small kernel's and the large one's."""
+    inp = R.make_inputs(2, Bq, 1, 8, 4, dh, T, dtype="f16", seed=dh + T)
+    o, lse, status = run_attention(inp, window=window, n_sink=3)
+    assert status == 0
+    ref_o, ref_lse, o_tol, lse_tol = R.attention_dense(inp, window=window, n_sink=3)
+    assert (np.abs(o.double().numpy() - ref_o) <= o_tol).all()
+    assert (np.abs(lse.double().numpy() - ref_lse) <= lse_tol).all()
+    score = np.random.default_rng(3).random((2, Bq, 4, T)).astype(np.float32)
+    got, tree, status = run_mass(inp, lse, score, window=window, n_sink=3)
+    ref, ref_tree, tol, tree_tol = R.mass(inp, lse.numpy(), score, window=window, n_sink=3)
+    assert status == 0 and (np.abs(got - ref) <= tol).all() and (np.abs(tree - ref_tree) <= tree_tol).all()
