@@ -390,3 +390,22 @@ def test_single_tokens_in_f16(dh, Bq, T, window):
     got, tree, status = run_mass(inp, lse, score, window=window, n_sink=3)
     ref, ref_tree, tol, tree_tol = R.mass(inp, lse.numpy(), score, window=window, n_sink=3)
     assert status == 0 and (np.abs(got - ref) <= tol).all() and (np.abs(tree - ref_tree) <= tree_tol).all()
+
+
+# ---- the current stream --------------------------------------------------------------------
+
+def test_calls_go_to_the_current_stream(monkeypatch):
+    """With torch's quick way to its handle, and without it."""
+    t, side = torch.zeros(1, device="cuda"), torch.cuda.Stream()
+    for quick in (True, False):
+        if not quick:
+            monkeypatch.setattr(lbx, "_raw_stream", lbx._public_raw_stream)
+        assert lbx._stream_of(t, None) == torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert lbx._stream_of(t, None) == side.cuda_stream
+        assert lbx._stream_of(t, side) == side.cuda_stream
+    inp = R.make_inputs(1, 2, 3, 4, 2, 64, 50, seed=36)
+    o, lse, _ = run_attention(inp)
+    with torch.cuda.stream(side):
+        o2, lse2, status = run_attention(inp)
+    assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
