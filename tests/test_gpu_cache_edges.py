@@ -409,3 +409,56 @@ def test_calls_go_to_the_current_stream(monkeypatch):
     with torch.cuda.stream(side):
         o2, lse2, status = run_attention(inp)
     assert status == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---- graphs --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("sizes", [dict(L=1, Bq=2, N=1, Hq=8, Hkv=2, dh=128, T=200),
+                                   dict(L=2, Bq=3, N=22, Hq=12, Hkv=2, dh=256, T=700),
+                                   dict(L=1, Bq=6, N=22, Hq=6, Hkv=1, dh=256, T=300, P=9000),
+                                   dict(L=1, Bq=40, N=2, Hq=16, Hkv=4, dh=64, T=300, P=2049, dtype="f16")])
+def test_a_round_of_calls_replays_from_a_graph(sizes):
+    """Attention, weights and eviction captured together, replayed on new lengths."""
+    inp = R.make_inputs(**sizes, seed=37)
+    cfg = cfg_of(inp)
+    d = {k: v.cuda() for k, v in inp.items()}
+    L, Bq, N, Hq, T = *inp["q"].shape[:4], cfg.T
+    ws, status = lbx.new_cache_attn_workspace(cfg), torch.zeros(1, dtype=torch.int32, device="cuda")
+    seen = torch.full((Bq,), 3 * T, dtype=torch.int32, device="cuda")
+    pre = (d["k_prefix"], d["v_prefix"]) if cfg.P else ()
+    start = {"k_cache": d["k_cache"].clone(), "v_cache": d["v_cache"].clone(),
+             "score": torch.rand(L, Bq, cfg.Hkv, T, device="cuda"),
+             "pos": torch.randint(3 * T, (L, Bq, cfg.Hkv, T), dtype=torch.int32, device="cuda")}
+    s = {k: v.clone() for k, v in start.items()}
+    s.update(o=torch.empty_like(d["q"]), lse=torch.empty(L, Bq, N, Hq, device="cuda"),
+             tree=torch.empty(L, Bq, cfg.Hkv, N, device="cuda"), ctx_out=torch.empty_like(seen), seen_out=torch.empty_like(seen))
+
+    def calls():
+        (lbx.lbx_prefix_attention if cfg.P else lbx.lbx_window_attention)(
+            cfg, d["ctx_len"], d["parent"], d["q"], *pre, s["k_cache"], s["v_cache"], d["k_tree"], d["v_tree"],
+            s["o"], ws, lse=s["lse"], d_status=status)
+        lbx.lbx_attention_mass(cfg, d["ctx_len"], d["parent"], d["accepted"], d["q"], s["lse"], s["k_cache"],
+                               d["k_tree"], s["score"], s["tree"], d_status=status)
+        lbx.lbx_cache_evict(cfg, T // 2, 5, d["ctx_len"], seen, d["parent"], d["accepted"], d["k_tree"], d["v_tree"],
+                            s["tree"], s["k_cache"], s["v_cache"], s["score"], s["pos"], s["ctx_out"], s["seen_out"],
+                            d_status=status)
+
+    def reset():
+        for k, v in start.items():
+            s[k].copy_(v)
+    calls()
+    reset()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for ctx in ([T] * Bq, [b * T // Bq for b in range(Bq)], [0] * Bq):
+        d["ctx_len"].copy_(torch.tensor(ctx, dtype=torch.int32))
+        reset()
+        calls()
+        want = {k: v.clone() for k, v in s.items()}
+        reset()
+        graph.replay()
+        for k, v in s.items():
+            assert torch.equal(v, want[k]), (k, ctx)
+    assert int(status.item()) == 0

@@ -344,8 +344,9 @@ int few_chunks(const lbx_attn_cfg *c) {
                             ? units(W - 1) + units(c->n_sink < before ? c->n_sink : before)
                             : units(c->T);
   const long long n = units(c->P) + own + 1, all = n * c->L * c->Bq * c->Hkv;
-  // Up to about one wave of CTAs it is the faster one, beyond the other is: us per
-  // call here / there, bf16, 24 query heads over 4 of dimension 256,
+  // Up to about one wave of CTAs it is the faster one, beyond the other is (at
+  // dimensions 64 and 128, whose units are smaller, some way beyond): us per call here /
+  // there, bf16, 24 query heads over 4 of dimension 256,
   //   9 units per stream, 4 streams    9.3 / 15.4
   //   17 units, 16 streams            13.1 / 17.6
   //   64 units, 4 streams             21.9 / 28.5
@@ -356,6 +357,17 @@ int few_chunks(const lbx_attn_cfg *c) {
   //   29 units, 32 streams (dh 128)   17.4 / 23.5
   //   63 units, 16 streams            37.8 / 42.8
   //   32 units, 32 streams            31.7 / 30.6
+  // Four heads per KV head, one token, from a graph (dimension 64 f16; 128 bf16; 256 f16):
+  //   24 units, 4 streams              9.9 / 14.5     8.9 / 16.7    10.0 / 21.1
+  //   62 units, 4 streams             18.7 / 18.2    16.2 / 20.9    18.9 / 31.7
+  //   24 units, 16 streams            11.7 / 15.7    11.3 / 17.8    18.3 / 19.9
+  //   12 units, 32 streams            10.0 / 14.1    10.6 / 16.7    17.1 / 18.8
+  //   48 units, 16 streams            18.9 / 17.2    18.2 / 19.8    28.5 / 24.2
+  //   12 units, 64 streams            12.1 / 14.4    15.0 / 16.9    23.7 / 23.3
+  // and, with a prefix,
+  //   20 units, 16 streams            10.8 / 18.1    11.1 / 22.6    15.2 / 25.0
+  //   60 units, 16 streams            22.0 / 22.1    21.7 / 24.9    33.6 / 40.9
+  //   32 units, 32 streams            17.1 / 22.5    18.2 / 24.7    29.0 / 33.3
   // The join's weights fit in K's place up to 64 units.
   return n <= 64 && all <= (c->P > 0 ? kFewUnits : kFewUnits * 3 / 8) ? (int)n : 0;
 }
