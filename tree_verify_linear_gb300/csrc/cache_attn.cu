@@ -8,7 +8,7 @@
 // last step joins the two by their lse.  (In this order because the second's
 // streams are the fewer and longer ones, and a stream's end costs 9 us with the
 // joining and 3 us without: five requests of 22 nodes over 4096 shared keys take
-// 312 us; the other way round cost 14 us more.)  The second launch begins on the SMs that
+// 311 us; the other way round cost 14 us more.)  The second launch begins on the SMs that
 // the first one's CTAs leave and waits for its results only there.
 #include <cudaTypedefs.h>
 

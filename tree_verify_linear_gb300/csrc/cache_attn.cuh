@@ -57,9 +57,9 @@
 //
 // What bounds it, measured on one GB300 (copies reach 6.77 TB/s).  One row per KV
 // head's group, 16 requests of 8001 to 16384 keys, 4 layers, 32/8 heads of dimension
-// 128, f16: 517 us, 91% of that bandwidth.  Trees of 22 nodes in bf16 at
+// 128, f16: 500 to 511 us, 92 to 94% of that bandwidth.  Trees of 22 nodes in bf16 at
 // 24/4 heads of dimension 256: the tensor pipe, 1.8 us per block and pair for
-// Q K^T and two products with V; five requests, 16 layers, 4096 keys each: 335 us (on
+// Q K^T and two products with V; five requests, 16 layers, 4096 keys each: 322 to 334 us (on
 // single CTAs, which read K and V for 128 rows each, 618 us).  Short lists: the
 // 7 us that a stream takes to begin and end.
 #pragma once

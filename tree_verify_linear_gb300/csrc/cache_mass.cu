@@ -17,7 +17,7 @@
 // as many as the columns of tensor memory allow, and are added here: four up to 64
 // rows per pass, two up to 128, else one.  Error of the path keys' sums against 64 bits
 // (2-norms): 0.4e-6 at most with four (dimension 256, where two gave 0.75e-6 and
-// operations in fp32 give 0.5e-6), 0.95e-6 with one (dimension 128; fp32: 0.6e-6).
+// operations in fp32 give 0.5e-6), 1.0e-6 with one (dimension 128; fp32: 0.6e-6 to 0.8e-6).
 //
 // The path's nodes are taken root first, so row d G + h belongs to the node of
 // depth d, and the rows that see a key are one range of rows.  Up to 128 rows
