@@ -60,6 +60,7 @@ extern "C" {
 #define LBX_ECUDA (-2)  /* a CUDA call or kernel launch failed               */
 #define LBX_ETREE (-3)  /* invalid tree (device-detected, via d_status)      */
 #define LBX_ETIMEOUT (-4) /* a bounded in-kernel wait gave up (via d_status) */
+#define LBX_EPAGES (-5)  /* the page pool has too few free pages (via d_status) */
 
 /* Limits. */
 #define LBX_MAX_TREE_NODES 64 /* tree mode: N <= 64 nodes per request          */
@@ -475,6 +476,155 @@ int lbx_cache_evict(const lbx_attn_cfg *cfg, int budget, int n_recent, const int
                     const uint16_t *k_tree, const uint16_t *v_tree, const float *score_tree,
                     uint16_t *k_cache, uint16_t *v_cache, float *score, int32_t *pos,
                     int32_t *ctx_out, int32_t *seen_out, int32_t *d_status, cudaStream_t stream);
+
+/*
+ * ---- The paged KV cache of the full-attention layers -----------------------
+ *
+ * Four operators for serving with a cache whose positions lie in pages of one
+ * pool: lbx_page_tables gives the requests of a step the pages that their
+ * lengths need, lbx_qk_norm_rope puts the new tokens' keys and values there,
+ * lbx_paged_attention reads them, and lbx_page_commit keeps a verified path.
+ * The new tokens of a batch are rows 0 .. start[Bq]-1 of M, request after
+ * request (request b's are start[b] .. start[b+1]-1, any number of them, none
+ * included); rows from start[Bq] on are padding: nothing is read from them and
+ * what is written per row keeps what it held (slot and pos: -1).  Position p of
+ * request b lies in page block_table[b][p / page] at p % page; of layer l's pool
+ * [n_pages][page][Hkv][dh] that is row slot = block_table[b][p / page] * page +
+ * p % page.  Layers are a batch dimension sharing lengths, tables and positions.
+ */
+#define LBX_PAGE_MAX_REQUESTS 2048
+#define LBX_PAGED_MAX_GROUP 128 /* lbx_paged_attention: Hq / Hkv */
+
+typedef struct lbx_page_cfg {
+  int L, Bq;      /* layers, requests (Bq <= LBX_PAGE_MAX_REQUESTS)             */
+  int M;          /* rows of new tokens, padding included (>= 1)                */
+  int Hq, Hkv;    /* query / KV heads, Hq % Hkv == 0                            */
+  int dh;         /* head dimension: 64, 128 or 256                             */
+  int page;       /* positions per page: 16, 32, 64, 128 or 256                 */
+  int n_pages;    /* pages of each layer's pool; L * n_pages * page < 2^31      */
+  int max_pages;  /* columns of the block table; max_pages * page <= 2^30       */
+  int dtype;      /* LBX_BF16 or LBX_F16                                        */
+  float scale;    /* scale of q . k (> 0, finite)                               */
+} lbx_page_cfg;
+
+/*
+ * Block tables and slot maps of a step, from the requests' lengths.  Request b
+ * has ctx_len[b] positions, gets new_len[b] more and holds its first held[b]
+ * pages.  It leaves with exactly held_out[b] = ceil((ctx_len + new_len) / page):
+ * the pages it holds beyond that go onto the free stack (request after request,
+ * in order of position), then missing ones come off the stack's top (the same
+ * order).  So an ended request (both lengths 0) gives its pages back, and one
+ * whose draft was rejected those that only the draft had needed.
+ *   ctx_len, new_len, held [Bq], n_free [1] int32: in
+ *   block_table [Bq][max_pages], free_list [n_pages] int32: in/out; entries past
+ *     held_out, and places of the stack at or past its top, keep what they held
+ *     or get what passed through them
+ *   held_out [Bq], n_free_out [1] int32 out: the next step's held and n_free.
+ *     They may not overlap the inputs (LBX_EINVAL)
+ *   start [Bq + 1], slot [M], pos [M] int32 out
+ * Of cfg, Bq, M, page, n_pages and max_pages matter.  Reported through d_status,
+ * with nothing written: LBX_EPAGES if the pool has too few pages; LBX_EINVAL if a
+ * length or count is negative, more tokens come than M, more pages are needed or
+ * held than max_pages, or the stack would outgrow n_pages.  A page outside the pool
+ * gives slot -1 for its positions, and LBX_EINVAL.  The call may be repeated
+ * on the same inputs, with the same results.
+ */
+int lbx_page_tables(const lbx_page_cfg *cfg, const int32_t *ctx_len, const int32_t *new_len,
+                    const int32_t *held, const int32_t *n_free, int32_t *block_table,
+                    int32_t *free_list, int32_t *held_out, int32_t *n_free_out, int32_t *start,
+                    int32_t *slot, int32_t *pos, int32_t *d_status, cudaStream_t stream);
+
+/* How lbx_qk_norm_rope pairs the first `rot` dimensions of a head. */
+#define LBX_ROPE_HALVES 0   /* pair i: dimensions i and i + rot/2 */
+#define LBX_ROPE_ADJACENT 1 /* pair i: dimensions 2i and 2i + 1   */
+#define LBX_ROPE_MAX_AXES 4
+
+typedef struct lbx_rope_cfg {
+  int rot;   /* dimensions that turn, even, 0 .. dh                              */
+  int axes;  /* position axes, 1 .. LBX_ROPE_MAX_AXES                            */
+  int section[LBX_ROPE_MAX_AXES]; /* pairs that turn with each axis, in order of the
+                pairs; they add up to rot/2 (unused axes: 0)                     */
+  int pairing; /* LBX_ROPE_*                                                     */
+  float eps; /* of the norms (>= 0, finite)                                      */
+} lbx_rope_cfg;
+
+/*
+ * Norms of queries and keys per head and their rotation by the tokens'
+ * positions, in one pass that puts keys and values into their pages:
+ *     y = x / sqrt(mean x^2 + eps) * weight       (x itself without a weight),
+ *     (a, b) <- (a cos t - b sin t, b cos t + a sin t),  t = pos[axis(i)] inv_freq[i]
+ * for every pair i of the first rot dimensions; values are copied.
+ *   qkv [L][M][Hq + 2 Hkv][dh] of cfg->dtype: each row's query, key and value heads
+ *   q_weight, k_weight [L][dh] fp32 (NULL: no norm)
+ *   inv_freq [rot/2] fp32 (may be NULL when rot == 0; finite): any scaling of
+ *     positions is in them.  t is exact to 2^-30 of a turn at every position
+ *   pos [axes][M] int32, any values; slot [M] int32: a row's place in every layer's
+ *     pool; a negative one marks a row that is skipped (padding)
+ *   q_out [L][M][Hq][dh] out; k_pages, v_pages [L][n_pages][page][Hkv][dh]: the rows'
+ *     slots are written, nothing else is touched
+ * Sums and products are fp32, results rounded once.  A slot at or past
+ * n_pages * page is reported as LBX_EINVAL through d_status and its row skipped.  Two
+ * rows must not name one slot.  q_out must not overlap the other arrays.
+ */
+int lbx_qk_norm_rope(const lbx_page_cfg *cfg, const lbx_rope_cfg *rope, const uint16_t *qkv,
+                     const float *q_weight, const float *k_weight, const float *inv_freq,
+                     const int32_t *pos, const int32_t *slot, uint16_t *q_out, uint16_t *k_pages,
+                     uint16_t *v_pages, int32_t *d_status, cudaStream_t stream);
+
+/* Bytes of workspace lbx_paged_attention needs (0 on a bad cfg).  It must be
+ * zero-filled once before its first use (and after a call that reported
+ * LBX_ETIMEOUT); every call that runs to completion leaves its counters at zero.
+ * Calls of any configurations may take turns on one workspace that is large
+ * enough for each; two calls that run at the same time must not share it. */
+size_t lbx_paged_workspace_size(const lbx_page_cfg *cfg);
+
+/*
+ * Attention of each request's new tokens over its pages.  Request b's tokens are at
+ * positions ctx_len[b], ctx_len[b] + 1, .. of its cache, which holds their keys and
+ * values already.  Token i sees the positions before ctx_len[b] and
+ *     parent == NULL: its own and those of the tokens before it (a prompt's
+ *                     chunk; with one token, the plain decode step);
+ *     otherwise:      those of the tokens on its root path, itself included (a draft
+ *                     tree, at most LBX_ATTN_MAX_NODES tokens per request):
+ *                     parent[start[b]] == -1, 0 <= parent[start[b] + i] < i.
+ *     o = sum_j exp(scale q.k_j - lse) v_j,  lse = log sum_j exp(scale q.k_j).
+ *   start [Bq + 1], ctx_len [Bq], block_table [Bq][max_pages] int32; parent [M] int32
+ *   or NULL; q [L][M][Hq][dh], k_pages, v_pages [L][n_pages][page][Hkv][dh] of
+ *   cfg->dtype; o [L][M][Hq][dh] out of cfg->dtype, lse [L][M][Hq] fp32 out (may be
+ *   NULL).
+ * Sums and softmax statistics are fp32; the weights meet V in its type, rounded once.
+ * What a request's pages hold past its last token, and other pages, may be
+ * anything, NaN included; a key that one query of a request sees and another
+ * does not has to have a finite value.  A query all of whose scores are -inf gets o = 0
+ * and lse = -inf; one with a NaN among its scores gets NaN for both.
+ * Hq / Hkv <= LBX_PAGED_MAX_GROUP.  Returns as lbx_window_attention.  Through
+ * d_status, with nothing written: LBX_ETREE if start does not rise from 0 to at
+ * most M, a length is negative or beyond the table, or a tree breaks its rules.  A
+ * page outside the pool is not read: LBX_EINVAL through d_status, and the outputs of
+ * that request hold nothing of use.
+ */
+int lbx_paged_attention(const lbx_page_cfg *cfg, const int32_t *start, const int32_t *ctx_len,
+                        const int32_t *block_table, const int32_t *parent, const uint16_t *q,
+                        const uint16_t *k_pages, const uint16_t *v_pages, uint16_t *o, float *lse,
+                        void *workspace, size_t workspace_bytes, int32_t *d_status,
+                        cudaStream_t stream);
+
+/*
+ * Keep the verified path of each request's draft tree: the keys and values of the
+ * path's nodes, from the root to accepted[b], move to positions ctx_len[b],
+ * ctx_len[b] + 1, .. (in place; a node's index is never below its depth), and
+ * ctx_out[b] = ctx_len[b] + nodes of the path.  The positions behind hold what they
+ * held.  A request without tokens keeps its length (accepted is not read).
+ *   start, ctx_len, block_table, parent as in lbx_paged_attention (parent not
+ *   NULL); accepted [Bq] int32, a node of the tree; k_pages, v_pages in/out;
+ *   ctx_out [Bq] int32 out (LBX_EINVAL if it overlaps an int32 input).
+ * Errors as in lbx_paged_attention; an accepted index out of range is reported
+ * like an invalid tree, and a path through a page outside the pool does not move.
+ */
+int lbx_page_commit(const lbx_page_cfg *cfg, const int32_t *start, const int32_t *ctx_len,
+                    const int32_t *block_table, const int32_t *parent, const int32_t *accepted,
+                    uint16_t *k_pages, uint16_t *v_pages, int32_t *ctx_out, int32_t *d_status,
+                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -72,6 +72,7 @@ const char *lbx_strerror(int status) {
     case LBX_ECUDA: return "CUDA launch or runtime error";
     case LBX_ETREE: return "invalid draft tree (parent array is not a topologically numbered tree, or not a chain in chunked mode)";
     case LBX_ETIMEOUT: return "a bounded wait inside a kernel gave up (reported through d_status)";
+    case LBX_EPAGES: return "the page pool has too few free pages";
   }
   return "unknown status";
 }

@@ -18,7 +18,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblbx.so")
 
-LBX_OK, LBX_EINVAL, LBX_ECUDA, LBX_ETREE, LBX_ETIMEOUT = 0, -1, -2, -3, -4
+LBX_OK, LBX_EINVAL, LBX_ECUDA, LBX_ETREE, LBX_ETIMEOUT, LBX_EPAGES = 0, -1, -2, -3, -4, -5
 LBX_MAX_TREE_NODES = 64
 LBX_CHAIN_CHUNK = 64
 LBX_MAX_CONV_WIDTH = 4
@@ -30,13 +30,16 @@ EXPORTS = ("lbx_strerror", "lbx_workspace_size", "lbx_tree_conv", "lbx_tree_delt
            "lbx_accept_workspace_size", "lbx_accept_walk", "lbx_ddtree_build",
            "lbx_attn_workspace_size", "lbx_tree_attention", "lbx_cache_attn_workspace_size",
            "lbx_window_attention", "lbx_prefix_attention", "lbx_attention_mass",
-           "lbx_cache_evict")
+           "lbx_cache_evict", "lbx_page_tables", "lbx_qk_norm_rope", "lbx_paged_workspace_size",
+           "lbx_paged_attention", "lbx_page_commit")
 LBX_ACCEPT_MAX_NODES = 4096
 LBX_DDTREE_MAX_K, LBX_DDTREE_MAX_DEPTH = 8, 64
 LBX_NOALLOC_MAX_GROUPS = 65536
 LBX_ATTN_HEAD_DIM, LBX_ATTN_MAX_NODES = 256, 64
 LBX_BF16, LBX_F16 = 0, 1
 LBX_EVICT_MAX_T = 1 << 20
+LBX_PAGE_MAX_REQUESTS, LBX_PAGED_MAX_GROUP = 2048, 128
+LBX_ROPE_HALVES, LBX_ROPE_ADJACENT, LBX_ROPE_MAX_AXES = 0, 1, 4
 
 
 class LbxError(RuntimeError):
@@ -57,6 +60,19 @@ class lbx_attn_cfg(ctypes.Structure):
                 ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("dh", ctypes.c_int),
                 ("T", ctypes.c_int), ("P", ctypes.c_int), ("window", ctypes.c_int),
                 ("n_sink", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class lbx_page_cfg(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("Bq", ctypes.c_int), ("M", ctypes.c_int),
+                ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("dh", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class lbx_rope_cfg(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("axes", ctypes.c_int),
+                ("section", ctypes.c_int * LBX_ROPE_MAX_AXES), ("pairing", ctypes.c_int),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -105,6 +121,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.lbx_attention_mass.argtypes = [vp] * 12
         lib.lbx_cache_evict.restype = i32
         lib.lbx_cache_evict.argtypes = [vp, i32, i32] + [vp] * 15
+        lib.lbx_page_tables.restype = i32
+        lib.lbx_page_tables.argtypes = [vp] * 14
+        lib.lbx_qk_norm_rope.restype = i32
+        lib.lbx_qk_norm_rope.argtypes = [vp] * 13
+        lib.lbx_paged_workspace_size.restype = ctypes.c_size_t
+        lib.lbx_paged_workspace_size.argtypes = [vp]
+        lib.lbx_paged_attention.restype = i32
+        lib.lbx_paged_attention.argtypes = [vp] * 10 + [vp, ctypes.c_size_t, vp, vp]
+        lib.lbx_page_commit.restype = i32
+        lib.lbx_page_commit.argtypes = [vp] * 11
         _lib = lib
     return _lib
 
@@ -406,3 +432,93 @@ def lbx_cache_evict(cfg, budget, n_recent, ctx_len, seen, parent, accepted, k_tr
         _at(score, (L, Bq, Hkv, T), f32, "score"), _at(pos, (L, Bq, Hkv, T), i32, "pos"),
         _at(ctx_out, per, i32, "ctx_out"), _at(seen_out, per, i32, "seen_out"),
         _i32(d_status, "d_status"), _stream_of(score, stream)))
+
+
+def make_page_cfg(L, Bq, M, Hq, Hkv, dh, page, n_pages, max_pages, dtype=LBX_BF16,
+                  scale=None) -> lbx_page_cfg:
+    """Config of the paged cache's operators; scale defaults to 1/sqrt(dh)."""
+    return lbx_page_cfg(L=L, Bq=Bq, M=M, Hq=Hq, Hkv=Hkv, dh=dh, page=page, n_pages=n_pages,
+                        max_pages=max_pages, dtype=dtype, scale=dh ** -0.5 if scale is None else scale)
+
+
+def make_rope_cfg(sections, eps=1e-6, pairing=LBX_ROPE_HALVES) -> lbx_rope_cfg:
+    """Rotation of 2 * sum(sections) dimensions; sections[a] pairs turn with axis a."""
+    if len(sections) > LBX_ROPE_MAX_AXES:
+        raise ValueError(f"sections: {len(sections)} axes, at most {LBX_ROPE_MAX_AXES}")
+    return lbx_rope_cfg(rot=2 * sum(sections), axes=len(sections),
+                        section=(ctypes.c_int * LBX_ROPE_MAX_AXES)(*sections), pairing=pairing,
+                        eps=eps)
+
+
+def lbx_page_tables(cfg, ctx_len, new_len, held, n_free, block_table, free_list, held_out, n_free_out,
+                    start, slot, pos, d_status=None, stream=None):
+    """Block tables and slot maps of a step from the requests' lengths."""
+    i32, per = torch.int32, (cfg.Bq,)
+    _check("lbx_page_tables", load().lbx_page_tables(
+        ctypes.byref(cfg), _at(ctx_len, per, i32, "ctx_len"), _at(new_len, per, i32, "new_len"),
+        _at(held, per, i32, "held"), _at(n_free, (1,), i32, "n_free"),
+        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
+        _at(free_list, (cfg.n_pages,), i32, "free_list"), _at(held_out, per, i32, "held_out"),
+        _at(n_free_out, (1,), i32, "n_free_out"), _at(start, (cfg.Bq + 1,), i32, "start"),
+        _at(slot, (cfg.M,), i32, "slot"), _at(pos, (cfg.M,), i32, "pos"),
+        _i32(d_status, "d_status"), _stream_of(slot, stream)))
+
+
+def _pages(cfg, k_pages, v_pages, el):
+    shape = (cfg.L, cfg.n_pages, cfg.page, cfg.Hkv, cfg.dh)
+    return _at(k_pages, shape, el, "k_pages"), _at(v_pages, shape, el, "v_pages")
+
+
+def lbx_qk_norm_rope(cfg, rope, qkv, inv_freq, pos, slot, q_out, k_pages, v_pages, q_weight=None,
+                     k_weight=None, d_status=None, stream=None):
+    """Norms of queries and keys per head and their rotation; keys and values
+    go to their pages."""
+    el, i32, f32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, torch.float32
+    weights = [None if w is None else _at(w, (cfg.L, cfg.dh), f32, name)
+               for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    _check("lbx_qk_norm_rope", load().lbx_qk_norm_rope(
+        ctypes.byref(cfg), ctypes.byref(rope),
+        _at(qkv, (cfg.L, cfg.M, cfg.Hq + 2 * cfg.Hkv, cfg.dh), el, "qkv"), *weights,
+        None if inv_freq is None else _at(inv_freq, (rope.rot // 2,), f32, "inv_freq"),
+        _at(pos, (rope.axes, cfg.M), i32, "pos"), _at(slot, (cfg.M,), i32, "slot"),
+        _at(q_out, (cfg.L, cfg.M, cfg.Hq, cfg.dh), el, "q_out"), *_pages(cfg, k_pages, v_pages, el),
+        _i32(d_status, "d_status"), _stream_of(qkv, stream)))
+
+
+def lbx_paged_workspace_size(cfg: lbx_page_cfg) -> int:
+    return int(load().lbx_paged_workspace_size(ctypes.byref(cfg)))
+
+
+def new_paged_workspace(cfg: lbx_page_cfg, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of lbx_paged_workspace_size(cfg) bytes."""
+    n = lbx_paged_workspace_size(cfg)
+    if n == 0:
+        raise LbxError("lbx_paged_workspace_size", LBX_EINVAL)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def lbx_paged_attention(cfg, start, ctx_len, block_table, q, k_pages, v_pages, o, workspace,
+                        parent=None, lse=None, d_status=None, stream=None):
+    """Attention of each request's new tokens (a chunk, a tree, one token) over its pages."""
+    el, i32, qs = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, (cfg.L, cfg.M, cfg.Hq, cfg.dh)
+    _check("lbx_paged_attention", load().lbx_paged_attention(
+        ctypes.byref(cfg), _at(start, (cfg.Bq + 1,), i32, "start"),
+        _at(ctx_len, (cfg.Bq,), i32, "ctx_len"),
+        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
+        None if parent is None else _at(parent, (cfg.M,), i32, "parent"), _at(q, qs, el, "q"),
+        *_pages(cfg, k_pages, v_pages, el), _at(o, qs, el, "o"),
+        None if lse is None else _at(lse, qs[:3], torch.float32, "lse"),
+        _ptr(workspace, None, "workspace"), workspace.nbytes, _i32(d_status, "d_status"),
+        _stream_of(q, stream)))
+
+
+def lbx_page_commit(cfg, start, ctx_len, block_table, parent, accepted, k_pages, v_pages, ctx_out,
+                    d_status=None, stream=None):
+    """Move the accepted path's keys and values to the positions behind the context."""
+    el, i32, per = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, (cfg.Bq,)
+    _check("lbx_page_commit", load().lbx_page_commit(
+        ctypes.byref(cfg), _at(start, (cfg.Bq + 1,), i32, "start"), _at(ctx_len, per, i32, "ctx_len"),
+        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
+        _at(parent, (cfg.M,), i32, "parent"), _at(accepted, per, i32, "accepted"),
+        *_pages(cfg, k_pages, v_pages, el), _at(ctx_out, per, i32, "ctx_out"),
+        _i32(d_status, "d_status"), _stream_of(k_pages, stream)))
