@@ -38,6 +38,19 @@ bool have_encode() {
 
 }  // namespace
 
+bool encode_16bit(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                  const uint64_t *strides, const uint32_t *box) {
+  if (!have_encode()) return false;
+  cuuint64_t gdim[5], gstride[4];
+  cuuint32_t gbox[5], estride[5];
+  for (int i = 0; i < rank; ++i) gdim[i] = dims[i], gbox[i] = box[i], estride[i] = 1;
+  for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides[i];
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank, const_cast<void *>(base),
+                  gdim, gstride, gbox, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Queries as (dh, Hq, nodes, lists); box: 64 columns of a KV head's G heads of as
 // many nodes as fit 128 rows.
 static bool encode_queries(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int nodes,

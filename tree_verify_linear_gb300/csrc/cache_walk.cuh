@@ -43,6 +43,10 @@ struct AttnMaps {
 // box: 64 columns of one head's `keys` consecutive positions.
 bool encode_list(CUtensorMap *map, const void *base, const lbx_attn_cfg *c, int len, int lists,
                  int keys);
+// A dense array of 16-bit values (dims innermost first, strides in bytes of all but the
+// first), boxes of 64 columns in the 128-byte swizzle.
+bool encode_16bit(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                  const uint64_t *strides, const uint32_t *box);
 // SMs of the current device, at most kMaxCtas (0 if a CUDA call fails).
 int grid_limit();
 

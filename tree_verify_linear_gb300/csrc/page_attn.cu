@@ -1,101 +1,20 @@
 // page_attn.cu -- attention of each request's new tokens over its pages:
-// lbx_paged_attention.
-//
-// The simplest form: a warp per (row, query head), the head's dimensions over its
-// lanes, one key after another with the running maximum and sum of the softmax.
-#include "page_common.cuh"
+// lbx_paged_attention (host side; the kernel is in page_attn.cuh).
+#include "page_attn.cuh"
 
 namespace lbx {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr size_t kCounterBytes = (2 * kMaxCtas * 4 + 255) & ~255;
 
-struct PlainArgs {
-  lbx_page_cfg c;
-  int shift;
-  const int32_t *start, *ctx_len, *table, *parent;
-  const uint16_t *q, *k, *v;
-  uint16_t *o;
-  float *lse;
-  int32_t *status;
-};
-
-template <bool F16>
-__device__ __forceinline__ float value(uint16_t u) {
-  if constexpr (F16) return __half2float(__ushort_as_half(u));
-  else return __uint_as_float((uint32_t)u << 16);
-}
-
-template <int DH, bool F16>
-__global__ void __launch_bounds__(kThreads) plain_kernel(const PlainArgs A) {
-  const lbx_page_cfg &c = A.c;
-  if (batch_bad(c, A.start, A.ctx_len, A.parent, nullptr)) {
-    if (threadIdx.x == 0 && A.status) *A.status = LBX_ETREE;
-    return;
-  }
-  const int lane = threadIdx.x & 31, rows = A.start[c.Bq];
-  const long long n = (long long)c.L * rows * c.Hq, warps = (long long)gridDim.x * (kThreads / 32);
-#pragma unroll 1
-  for (long long w = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < n; w += warps) {
-    const int h = (int)(w % c.Hq), r = (int)(w / c.Hq % rows), l = (int)(w / c.Hq / rows);
-    int a = 0, z = c.Bq - 1;  // the last request that starts at r or before
-    while (a < z) {
-      const int m = (a + z + 1) >> 1;
-      if (A.start[m] <= r) a = m;
-      else z = m - 1;
-    }
-    const int s = A.start[a], i = r - s, ctx = A.ctx_len[a];
-    const int end = A.parent ? ctx + i + 1 : ctx + i + 1;
-    const uint64_t path =
-        A.parent ? cache::warp_path(A.parent + s, A.start[a + 1] - s, i, lane) : ~0ull;
-    const size_t at = ((size_t)l * c.M + r) * c.Hq + h;
-    constexpr int kE = DH / 32;
-    float q[kE], acc[kE], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) q[e] = value<F16>(A.q[at * DH + lane + 32 * e]), acc[e] = 0.f;
-#pragma unroll 1
-    for (int p = 0; p < end; ++p) {
-      if (A.parent && p >= ctx && !(path >> (p - ctx) & 1)) continue;
-      const int id = A.table[(size_t)a * c.max_pages + (p >> A.shift)];
-      if (id < 0 || id >= c.n_pages) {
-        if (A.status) *A.status = LBX_EINVAL;
-        break;
-      }
-      const size_t row = (((size_t)l * c.n_pages + id) * c.page + (p & (c.page - 1))) * c.Hkv +
-                         h / (c.Hq / c.Hkv);
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) x = fmaf(q[e], value<F16>(A.k[row * DH + lane + 32 * e]), x);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x *= c.scale;
-      const float top = x > m ? x : m;  // (a NaN stays out of it and reaches the sum)
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float alpha = expf(m - ref), weight = expf(x - ref);
-      m = top;
-      sum = fmaf(sum, alpha, weight);
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        acc[e] = fmaf(acc[e], alpha, weight * value<F16>(A.v[row * DH + lane + 32 * e]));
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const float y = sum == 0.f ? 0.f : acc[e] * inv;
-      uint16_t u;
-      if constexpr (F16) u = __half_as_ushort(__float2half_rn(y));
-      else u = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-      A.o[at * DH + lane + 32 * e] = u;
-    }
-    if (lane == 0 && A.lse) A.lse[at] = sum == 0.f ? -INFINITY : m + logf(sum);
-  }
-}
-
-template <int DH>
-void launch(bool f16, const PlainArgs &A, cudaStream_t stream) {
-  if (f16) plain_kernel<DH, true><<<152 * 8, kThreads, 0, stream>>>(A);
-  else plain_kernel<DH, false><<<152 * 8, kThreads, 0, stream>>>(A);
+bool encode_pool(CUtensorMap *map, const void *base, const lbx_page_cfg *c, int box) {
+  const uint64_t row = (uint64_t)c->Hkv * c->dh * 2;
+  const uint64_t dims[3] = {(uint64_t)c->dh, (uint64_t)c->Hkv,
+                            (uint64_t)c->L * c->n_pages * c->page};
+  const uint64_t strides[2] = {(uint64_t)c->dh * 2, row};
+  const uint32_t boxes[3] = {64, 1, (uint32_t)box};
+  return cache::encode_16bit(map, base, 3, dims, strides, boxes);
 }
 
 }  // namespace
@@ -105,7 +24,9 @@ void launch(bool f16, const PlainArgs &A, cudaStream_t stream) {
 extern "C" size_t lbx_paged_workspace_size(const lbx_page_cfg *c) {
   using namespace lbx::paged;
   if (!cfg_ok(c) || c->Hq / c->Hkv > LBX_PAGED_MAX_GROUP) return 0;
-  return 256;
+  // per CTA a tile's first piece and another one, two subtiles each (of a pair one per CTA)
+  const size_t parts = c->dh == 256 ? 2 * kMaxCtas : 4 * kMaxCtas;
+  return kCounterBytes + parts * part_floats(c->dh) * 4;
 }
 
 extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
@@ -124,11 +45,31 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   if ((parent && !aligned_to(parent, 4)) || (lse && !aligned_to(lse, 4)) ||
       !aligned_to(workspace, 16) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
-  PlainArgs A = {*c, 0, start, ctx_len, block_table, parent, q, k_pages, v_pages, o, lse, d_status};
+  PageArgs A = {};
+  A.c = *c;
+  A.G = c->Hq / c->Hkv, A.tp = kRows / A.G, A.box = c->page < 64 ? c->page : 64;
   while (1 << A.shift < c->page) ++A.shift;
+  A.shape = shape_of(A.G, parent != nullptr);
+  A.scale_log2 = c->scale * 1.4426950408889634f;
+  A.start = start, A.ctx_len = ctx_len, A.table = block_table, A.parent = parent;
+  A.o = o, A.lse = lse, A.status = d_status;
+  A.counters = static_cast<unsigned int *>(workspace);
+  A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kCounterBytes);
+
+  PageMaps maps;
+  const uint64_t row = (uint64_t)c->Hq * c->dh * 2;
+  const uint64_t dims[4] = {(uint64_t)c->dh, (uint64_t)c->Hq, (uint64_t)c->M, (uint64_t)c->L};
+  const uint64_t strides[3] = {(uint64_t)c->dh * 2, row, row * (uint64_t)c->M};
+  const uint32_t box[4] = {64, (uint32_t)A.G, (uint32_t)A.tp, 1};
+  if (!lbx::cache::encode_16bit(&maps.q, q, 4, dims, strides, box) ||
+      !encode_pool(&maps.k, k_pages, c, A.box) || !encode_pool(&maps.v, v_pages, c, A.box))
+    return LBX_ECUDA;
+  const int nsm = lbx::cache::grid_limit();
+  if (nsm < 2) return LBX_ECUDA;
+  const int grid = nsm / 2 * 2;
   const bool f16 = c->dtype == LBX_F16;
-  if (c->dh == 64) launch<64>(f16, A, stream);
-  else if (c->dh == 128) launch<128>(f16, A, stream);
-  else launch<256>(f16, A, stream);
-  return cudaGetLastError() == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  const cudaError_t e = c->dh == 64    ? launch_page_attn<64>(f16, maps, A, grid, stream)
+                        : c->dh == 128 ? launch_page_attn<128>(f16, maps, A, grid, stream)
+                                       : launch_page_attn<256>(f16, maps, A, grid, stream);
+  return e == cudaSuccess ? LBX_OK : LBX_ECUDA;
 }

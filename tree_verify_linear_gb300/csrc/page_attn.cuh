@@ -1,0 +1,885 @@
+// page_attn.cuh -- attention of each request's new tokens over its pages on the
+// tensor cores (sm_103a): the kernel behind lbx_paged_attention.
+//
+// Rows are (token, head of the group) pairs of one KV head, 128 to a subtile, two
+// subtiles to a tile.  Per block of 128 keys and subtile
+//   S = Q K^T          tensor cores, operands in shared memory
+//   softmax            online, base 2, statistics in fp32
+//   O += P V           tensor cores, P from tensor memory, in V's type
+// The running reference of a row moves only when a block's maximum exceeds it by more
+// than 2^8, so that O is rescaled rarely; the result is the same softmax taken from
+// another reference.  P is rounded to the 16-bit type once (2^-8 of a weight in bf16,
+// 2^-11 in f16), which adds about as much error as the rounding of o; f16 weights are
+// taken 2^7 times as large, so that what falls below its range is 2^-32 of the
+// reference.
+//
+// Head dimensions 64 and 128: a CTA holds both subtiles of a tile, each with its own
+// softmax warps (a row per thread), so that the tensor cores work on one while the
+// other's softmax runs, and K and V are read once for 256 rows.  Head dimension 256: O
+// takes half of tensor memory, so that a CTA holds one subtile, with two buffers of
+// S; a pair of CTAs shares products of 256 rows, each with half of the keys and half of
+// V's columns in its shared memory; two threads share a row, 64 keys each.  P lies over
+// its S.  The products of a CTA run in the order they are issued.
+//
+// K and V come by tensor copies of whole page rows (boxes of at most 64 positions of
+// one head), a lane per box; a box past the request's last position is aimed outside the
+// array, which fills zeros without reading.  Rows of a last page behind the last
+// position are cleared before the product with V (a weight of 0 times NaN is NaN).
+//
+// The work is cut as page_walk.cuh says.  A tile cut into pieces leaves partials (m,
+// l, O) in the workspace; the CTA that finishes a tile's last piece joins them in
+// the pieces' order.
+//
+// Warps 0-7 softmax, 8 issues the products, 9 walks the list and copies K and V, 10
+// brings the queries.  Every wait is bounded; a thread whose wait gives up waits no
+// more, the call reports LBX_ETIMEOUT, and the CTA leaves after its copies have landed.
+#pragma once
+
+#include "cache_ptx.cuh"
+#include "cache_walk.cuh"
+#include "page_walk.cuh"
+
+namespace lbx {
+namespace paged {
+
+using cache::Ring;
+
+constexpr int kThreads = 352;
+constexpr int kMaxCtas = cache::kMaxCtas;
+
+// Floats of one partial: m (base 2) and l per row, then O as [dh / 4][128] of four.
+__host__ __device__ constexpr size_t part_floats(int dh) { return 2 * kRows + (size_t)kRows * dh; }
+
+struct PageMaps {
+  CUtensorMap q;     // (dh, Hq, M, L), boxes of 64 columns of whole tokens' heads
+  CUtensorMap k, v;  // (dh, Hkv, positions of all layers' pools), boxes of 64 columns
+};
+
+struct PageArgs {
+  lbx_page_cfg c;
+  int G, tp, box, shift;  // heads per group, tokens per subtile, positions per box
+  Shape shape;
+  float scale_log2;
+  const int32_t *start, *ctx_len, *table, *parent;
+  uint16_t *o;
+  float *lse, *part;
+  unsigned int *counters;  // per CTA and subtile: pieces of the tile that begins its cut there
+  int32_t *status;
+};
+
+// A CTA's share of a tile, as the walking warp publishes it.
+struct Seg {
+  int have, l, h, b;
+  int row0, n, tok0, ctx;  // first row of the request, its tokens, the tile's first token
+  int blk0, nb;
+  int subs;                // subtiles with rows
+  int pieces, mine, owner;
+};
+
+template <int DH>
+struct Lay {
+  static constexpr bool kPair = DH == 256;
+  static constexpr int kCtas = kPair ? 2 : 1, kSubs = kPair ? 1 : 2;
+  static constexpr int kKeys = kBlk / kCtas, kCols = DH / kCtas;  // of a block, per CTA
+  static constexpr int kMine = kPair ? 64 : 128;                  // keys per softmax thread
+  static constexpr int kGroup = kPair ? 256 : 128;                // threads of a subtile
+  static constexpr int kOut = kPair ? DH / 2 : DH;                // O's columns per thread
+  static constexpr int kStage = kKeys * DH * 2;
+  static_assert(kStage == kBlk * kCols * 2, "K and V take the same place");
+  static constexpr int kQSub = kRows * DH * 2, kQBytes = kSubs * kQSub;
+  static constexpr int kStages = (227 * 1024 - 3072 - kQBytes) / kStage;
+  static_assert(kStages >= 4, "the next block's K beside this one's V");
+  static constexpr int kSmemRing = kQBytes;
+  static constexpr int kSmemRed = kSmemRing + kStages * kStage;  // float [4][128]
+  static constexpr int kSmemSegs = kSmemRed + 4 * kRows * 4;     // Seg [4]
+  static constexpr int kSmemMisc = kSmemSegs + 4 * (int)sizeof(Seg);  // int [16]
+  static constexpr int kSmemBars = kSmemMisc + 64;
+  static constexpr int kNBars = 3 * kStages + 18;
+  static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
+  static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0 && kSmemBars % 8 == 0, "shared");
+  // tensor memory: two buffers of S / P, O of each subtile
+  static constexpr uint32_t kColO = 2 * kBlk, kTmemCols = 512;
+  static_assert(kColO + kSubs * DH <= kTmemCols, "tensor memory");
+};
+
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+}
+
+// Whether p holds in any of the threads that share a named barrier.
+__device__ __forceinline__ bool any_of(uint32_t id, uint32_t nthreads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+// Where a CTA's range of the list begins.
+struct Begin {
+  i64 total, per_lh;  // entries of the whole list, of one (layer, KV head)
+  i64 X;              // entry of the first tile
+  int lh, b, t;
+};
+
+// The sums over the requests: every thread takes consecutive ones.  Finds range
+// `me` of `ctas`; false if the batch breaks the rules (in every thread).  `scratch`:
+// 8 (kThreads + 64) bytes of shared memory and 4 (Bq + 1) for a tree's check.
+__device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, void *scratch,
+                                           Begin *out) {
+  const lbx_page_cfg &c = A.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  i64 *sums = static_cast<i64 *>(scratch), *warps = sums + kThreads;
+  int *starts = reinterpret_cast<int *>(warps + 64);
+  const int per = (c.Bq + kThreads - 1) / kThreads;
+  const i64 room = (i64)c.max_pages * c.page;
+  int bad = 0;
+  i64 sum = 0;
+#pragma unroll 1
+  for (int b = tid * per; b < (tid + 1) * per && b < c.Bq; ++b) {
+    const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
+    if ((b == 0 && s != 0) || s < 0 || e < s || e > c.M || ctx < 0 || (i64)ctx + e - s > room ||
+        (A.parent && e - s > LBX_ATTN_MAX_NODES)) {
+      bad = 1;
+      break;
+    }
+    sum += entries_of(A.shape, ctx, e - s);
+  }
+  if (A.parent)
+    for (int b = tid; b <= c.Bq; b += kThreads) starts[b] = A.start[b];
+  i64 upto = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const i64 o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) warps[warp] = upto;
+  if (__syncthreads_or(bad)) return false;
+  i64 total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += warps[w];
+    total += warps[w];
+  }
+  sums[tid] = upto;  // through this thread's requests
+  if (A.parent) {
+    const int rows = starts[c.Bq];
+#pragma unroll 1
+    for (int r = tid; r < rows; r += kThreads) {
+      const int p = A.parent[r];
+      int a = 0, z = c.Bq - 1;
+      while (a < z) {
+        const int h = (a + z + 1) >> 1;
+        if (starts[h] <= r) a = h;
+        else z = h - 1;
+      }
+      const int i = r - starts[a];
+      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
+    }
+  }
+  if (__syncthreads_or(bad)) return false;
+  if (tid == 0) {
+    Begin g;
+    g.per_lh = total, g.total = total * c.L * c.Hkv;
+    g.lh = g.b = g.t = 0, g.X = 0;
+    const Cut cut = cut_of(g.total, ctas);
+    if (total > 0 && me < cut.n) {
+      const i64 x = cut.at(me);
+      g.lh = (int)(x / total);
+      i64 y = x - g.lh * total;
+      int a = 0, z = kThreads - 1;  // the first thread whose requests reach past y
+      while (a < z) {
+        const int h = (a + z) >> 1;
+        if (sums[h] > y) z = h;
+        else a = h + 1;
+      }
+      if (a > 0) y -= sums[a - 1];
+      int b = a * per;
+      for (;; ++b) {
+        const i64 e = entries_of(A.shape, A.ctx_len[b], A.start[b + 1] - A.start[b]);
+        if (y < e) break;
+        y -= e;
+      }
+      i64 before;
+      g.b = b;
+      g.t = tile_at(A.shape, A.ctx_len[b], A.start[b + 1] - A.start[b], y, before);
+      g.X = x - (y - before);
+    }
+    *out = g;
+  }
+  __syncthreads();
+  return true;
+}
+
+template <int DH, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    page_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ PageArgs A) {
+  using Y = Lay<DH>;
+  constexpr bool PAIR = Y::kPair;
+  extern __shared__ __align__(1024) unsigned char page_smem[];
+  unsigned char *smem = page_smem;
+  const lbx_page_cfg &c = A.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float *red = reinterpret_cast<float *>(smem + Y::kSmemRed);
+  volatile Seg *segs = reinterpret_cast<volatile Seg *>(smem + Y::kSmemSegs);
+  // [0] tensor memory base, [1] a wait gave up, [2] a page outside the pool, [4 + sub]
+  // last of its tile's pieces
+  volatile int *misc = reinterpret_cast<volatile int *>(smem + Y::kSmemMisc);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + Y::kSmemBars);
+  uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
+  uint64_t *s_bar = peer + Y::kStages, *p_bar = s_bar + 2, *o_bar = p_bar + 2;
+  uint64_t *seg_bar = o_bar + 2, *seg_free = seg_bar + 4;
+  uint64_t *q_bar = seg_free + 4, *qh_bar = q_bar + 1, *q_free = qh_bar + 1, *end_bar = q_free + 1;
+
+  const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
+  const int me = blockIdx.x / Y::kCtas, ctas = gridDim.x / Y::kCtas;
+  Begin *begin = reinterpret_cast<Begin *>(smem + Y::kSmemSegs);  // read before the first segment
+  if (!find_begin(A, me, ctas, smem, begin)) {
+    if (tid == 0 && A.status) *A.status = LBX_ETREE;
+    return;
+  }
+  const Begin g = *begin;
+  if (g.total == 0) return;  // no tokens: every CTA alike
+  if (tid == 0) {
+    for (int i = 0; i < Y::kNBars; ++i)
+      ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1
+                                   ? Y::kCtas * Y::kGroup / 32
+                               : full + i >= seg_free && full + i < seg_free + 4 ? 10
+                               : full + i == q_bar ? Y::kCtas
+                                                   : 1);
+    ptx::fence_mbar_init();
+    misc[1] = misc[2] = 0;
+  }
+  if (warp == 8) {
+    uint32_t *base = reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc);
+    if constexpr (PAIR) {
+      ptx::tmem_alloc_pair(base, Y::kTmemCols);
+    } else {
+      ptx::tmem_alloc(base, Y::kTmemCols);
+      ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+  }
+  ptx::fence_proxy_async();  // the scratch of the sums lies where copies will land
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // the other CTA's barriers are set up
+  ptx::tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+
+  bool bad = false;  // a wait of this thread gave up: it waits no more
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!bad && !ptx::mbar_wait(bar, parity)) bad = true;
+    return !bad;
+  };
+  // Segment k, for every warp but the walking one; false when the list is done (or a
+  // wait gave up).
+  auto next_seg = [&](uint32_t k, Seg &s) {
+    bool ok = wait(&seg_bar[k & 3], (k >> 2) & 1);
+    if (ok) {
+      const volatile Seg &f = segs[k & 3];
+      s.have = f.have, s.l = f.l, s.h = f.h, s.b = f.b, s.row0 = f.row0, s.n = f.n;
+      s.tok0 = f.tok0, s.ctx = f.ctx, s.blk0 = f.blk0, s.nb = f.nb, s.subs = f.subs;
+      s.pieces = f.pieces, s.mine = f.mine, s.owner = f.owner;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&seg_free[k & 3]);
+    return ok && s.have != 0;
+  };
+
+  if (warp == 9) {
+    // ---- the walk, and copies of K and V ----
+    const Cut cut = cut_of(g.total, ctas);
+    int lh = g.lh, b = g.b, t = g.t, s0 = 0, n = 0, ctx = 0;
+    i64 X = g.X;
+    const int n_lh = c.L * c.Hkv;
+    auto request = [&]() { s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b]; };
+    auto step = [&]() {  // to the next tile of the list
+      X += kLead + blocks_of(A.shape, ctx, n, t);
+      ++t;
+#pragma unroll 1
+      while (t >= tiles_of(A.shape, n)) {
+        t = 0;
+        if (++b == c.Bq) {
+          b = 0;
+          if (++lh == n_lh) return;
+        }
+        request();
+      }
+    };
+    bool more = me < cut.n;
+    if (more) {
+      request();
+      const int nb = blocks_of(A.shape, ctx, n, t);
+      const i64 y = cut.at(me) - X;
+      if (y >= kLead + kLeast && y > kLead + nb - kLeast) step();
+    }
+    Ring<Y::kStages> ring;
+    int loads = 0, outside = 0;
+    const uint32_t none = (uint32_t)(c.L * c.n_pages) * (uint32_t)c.page;  // past the pools' end
+#pragma unroll 1
+    for (uint32_t k = 0;; ++k) {
+      Piece p;
+      const int nb_all = more && lh < n_lh ? blocks_of(A.shape, ctx, n, t) : 0;
+      more = more && lh < n_lh && piece_of(cut, me, X, nb_all, p) && !__any_sync(0xffffffffu, bad);
+      if (k >= 4) wait(&seg_free[k & 3], ((k >> 2) & 1) ^ 1u);
+      const int l = lh / c.Hkv, h = lh - l * c.Hkv, nb = p.blk1 - p.blk0;
+      const int tok0 = t * A.shape.W;
+      if (lane == 0) {
+        volatile Seg &s = segs[k & 3];
+        s.have = more;
+        if (more) {
+          s.l = l, s.h = h, s.b = b, s.row0 = s0, s.n = n, s.tok0 = tok0, s.ctx = ctx;
+          s.blk0 = p.blk0, s.nb = nb, s.subs = n - tok0 > A.tp ? 2 : 1;
+          s.pieces = p.pieces, s.mine = p.mine, s.owner = p.owner;
+        }
+        ptx::mbar_arrive(&seg_bar[k & 3]);
+      }
+      if (!more) break;
+      // Lane e brings box e of a block: `box` positions of one head, 64 columns.
+      // The rows of its boxes come from the table one block ahead.
+      const int kv_len = ctx + n;
+      constexpr int kKA = DH / 64, kVA = Y::kCols / 64;
+      const int k_boxes = Y::kKeys / A.box * kKA, v_boxes = kBlk / A.box * kVA;
+      const int32_t *row = A.table + (size_t)b * c.max_pages;
+      auto place = [&](int blk, int off) -> uint32_t {
+        const int pos = blk * kBlk + off;
+        if (pos >= kv_len) return none;
+        const int id = row[pos >> A.shift];
+        if (id < 0 || id >= c.n_pages) {
+          outside = 1;
+          return none;
+        }
+        return (uint32_t)(l * c.n_pages + id) * (uint32_t)c.page + (uint32_t)(pos & (c.page - 1));
+      };
+      const int k_off = lane / kKA * A.box + rank * Y::kKeys, v_off = lane / kVA * A.box;
+      auto k_row = [&](int blk) { return lane < k_boxes ? place(blk, k_off) : none; };
+      auto v_row = [&](int blk) { return lane < v_boxes ? place(blk, v_off) : none; };
+      auto take = [&]() {
+        // the first round finds every stage free
+        const bool ok = __all_sync(0xffffffffu, wait(&empty[ring.st], ring.ph ^ 1u));
+        if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&full[ring.st], (uint32_t)Y::kStage);
+        __syncwarp();
+        loads += ok;
+        return ok;
+      };
+      auto load_k = [&](uint32_t at) {
+        if (take() && lane < k_boxes)
+          ptx::tma_load_3d(smem + Y::kSmemRing + ring.st * Y::kStage + lane % kKA * (Y::kKeys * 128) +
+                               lane / kKA * A.box * 128,
+                           &maps.k, lane % kKA * 64, h, (int)at, &full[ring.st]);
+        ring.step();
+      };
+      auto load_v = [&](uint32_t at) {
+        if (take() && lane < v_boxes)
+          ptx::tma_load_3d(smem + Y::kSmemRing + ring.st * Y::kStage + lane % kVA * (kBlk * 128) +
+                               lane / kVA * A.box * 128,
+                           &maps.v, rank * Y::kCols + lane % kVA * 64, h, (int)at, &full[ring.st]);
+        ring.step();
+      };
+      uint32_t k_at = k_row(p.blk0), v_at = v_row(p.blk0);
+#pragma unroll 1
+      for (int i = 0; i < nb; ++i) {
+        // K of block i; V of block i goes before K of block i + 1 where one CTA has both
+        // subtiles, behind it in a pair, as the products take them
+        const int ahead = p.blk0 + (i + 1 < nb ? i + 1 : i);
+        const uint32_t k_next = k_row(ahead), v_next = v_row(ahead);
+        if (!PAIR || i == 0) load_k(k_at);
+        if (PAIR && i + 1 < nb) load_k(k_next);
+        load_v(v_at);
+        k_at = k_next, v_at = v_next;
+      }
+      if (p.last) more = false;
+      else step();
+    }
+    outside = __any_sync(0xffffffffu, outside);
+    if (lane == 0 && outside) misc[2] = 1;
+    if (bad) misc[1] = 1;
+    // every copy has landed before the CTA may leave (long since, unless a wait gave up)
+    if (lane == 0) {
+#pragma unroll 1
+      for (int i = loads > Y::kStages ? loads - Y::kStages : 0; i < loads; ++i)
+        (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
+    }
+  } else if (warp == 10) {
+    // ---- queries, by tensor copies (tokens past the last row read as zeros) ----
+    Seg s;
+    uint32_t k = 0;
+    uint64_t *here = PAIR ? qh_bar : q_bar;
+#pragma unroll 1
+    for (; next_seg(k, s); ++k) {
+      if (k > 0) wait(q_free, (k - 1) & 1);  // the last segment's score products are done
+      if (lane == 0 && !bad) {
+        const int live = PAIR ? 1 : s.subs;
+        ptx::mbar_arrive_expect_tx(here, (uint32_t)(live * A.tp * A.G * DH * 2));
+#pragma unroll 1
+        for (int e = 0; e < live; ++e)
+#pragma unroll 1
+          for (int a = 0; a < DH / 64; ++a)
+            ptx::tma_load_4d(smem + e * Y::kQSub + a * kRows * 128, &maps.q, a * 64, s.h * A.G,
+                             s.row0 + s.tok0 + (PAIR ? rank : e) * A.tp, s.l, here);
+        if constexpr (PAIR) {
+          if (wait(qh_bar, k & 1)) ptx::mbar_arrive_at(q_bar, 0);
+        }
+      }
+      __syncwarp();
+    }
+    if (bad) misc[1] = 1;
+    // no copy is left behind
+    if (lane == 0 && k > 0) (void)ptx::mbar_wait(here, (k - 1) & 1);
+  } else if (warp == 8) {
+    // ---- products: the warp waits as one, one lane issues ----
+    Ring<Y::kStages> ring;
+    uint32_t qs[2] = {0, 0};  // blocks so far, of each subtile (of a pair: in [0])
+    const bool one = ptx::elect_one();
+    const uint64_t qdesc = ptx::sdesc_sw128(ptx::smem_u32(smem));
+    const uint64_t kdesc = ptx::sdesc_sw128(ptx::smem_u32(smem + Y::kSmemRing));
+    const uint64_t vdesc = ptx::sdesc(ptx::smem_u32(smem + Y::kSmemRing), kBlk * 128, 1024u, 2u);
+    auto commit = [&](uint64_t *bar) {
+      if constexpr (PAIR) ptx::mma_commit_pair(bar);
+      else ptx::mma_commit(bar);
+    };
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+      bad = !__all_sync(0xffffffffu, wait(bar, parity));
+      return !bad;
+    };
+    // Clear V's rows of the block in `stage` behind the request's last position, up to
+    // the end of their box (boxes past it are zeros).
+    auto clear = [&](const Seg &s, int blk, int stage) {
+      const int from = s.ctx + s.n - blk * kBlk;
+      if (from >= kBlk || from % A.box == 0) return;
+      const int rows = (from + A.box - 1) / A.box * A.box - from;
+      unsigned char *v0 = smem + Y::kSmemRing + stage * Y::kStage + from * 128;
+      constexpr int kWide = Y::kCols / 8;  // 16-byte pieces of a row
+#pragma unroll 1
+      for (int i = lane; i < rows * kWide; i += 32)
+        *reinterpret_cast<uint4 *>(v0 + (i % kWide / 8) * (kBlk * 128) + i / kWide * 128 +
+                                   (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      ptx::fence_proxy_async();
+      if constexpr (PAIR) ptx::fence_cluster();
+      __syncwarp();
+    };
+    Seg s;
+    uint32_t k = 0;
+    if (rank == 1) {
+      // the follower tells the leader of each stage that has landed
+#pragma unroll 1
+      for (; next_seg(k, s); ++k) {
+#pragma unroll 1
+        for (int i = 0; i < 2 * s.nb; ++i, ring.step()) {
+          // K 0, K 1, V 0, K 2, V 1, .., V nb - 1
+          const bool is_v = i == 2 * s.nb - 1 || (i > 0 && i % 2 == 0);
+          if (!wait_all(&full[ring.st], ring.ph)) break;
+          if (is_v) clear(s, s.blk0 + (i == 2 * s.nb - 1 ? s.nb - 1 : i / 2 - 1), ring.st);
+          if (lane == 0) ptx::mbar_arrive_at(&peer[ring.st], 0);
+        }
+      }
+      if (bad) misc[1] = 1;
+    } else {
+      constexpr uint32_t idesc_s = ptx::idesc_16(F16, kRows * Y::kCtas, kBlk, false);
+      constexpr uint32_t idesc_o = ptx::idesc_16(F16, kRows * Y::kCtas, DH, true);
+      auto arrived = [&](const Ring<Y::kStages> &r) {
+        const bool ok = wait_all(&full[r.st], r.ph) && (!PAIR || wait_all(&peer[r.st], r.ph));
+        ptx::tc_fence_after();
+        return ok;
+      };
+      // S of subtile e (in a pair 0) into buffer `buf`
+      auto scores = [&](int e, int buf, int stage) {
+        const uint64_t kd = kdesc + (uint64_t)(stage * (Y::kStage >> 4));
+        const uint64_t qd = qdesc + (uint64_t)(e * (Y::kQSub >> 4));
+        if (one) {
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i) {
+            const uint64_t qa = qd + (uint64_t)((i >> 2) * (kRows * 128 >> 4) + 2 * (i & 3));
+            const uint64_t kb = kd + (uint64_t)((i >> 2) * (Y::kKeys * 128 >> 4) + 2 * (i & 3));
+            if constexpr (PAIR) ptx::mma_16_ss_pair(tmem + buf * kBlk, qa, kb, idesc_s, i > 0);
+            else ptx::mma_bf16_ss(tmem + buf * kBlk, qa, kb, idesc_s, i > 0);
+          }
+          commit(&s_bar[buf]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int e, int buf, int stage, uint32_t later) {
+        const uint64_t vd = vdesc + (uint64_t)(stage * (Y::kStage >> 4));
+        if (one) {
+#pragma unroll
+          for (int i = 0; i < kBlk / 16; ++i) {
+            const uint32_t pa = tmem + buf * kBlk + 8 * i, d = tmem + Y::kColO + e * DH;
+            const uint64_t vb = vd + (uint64_t)(i * (2048 >> 4));
+            const uint32_t acc = i > 0 ? 1u : later;
+            if constexpr (PAIR) ptx::mma_16_ts_pair(d, pa, vb, idesc_o, acc);
+            else ptx::mma_bf16_ts(d, pa, vb, idesc_o, acc);
+          }
+          commit(&o_bar[PAIR ? buf : e]);
+        }
+        __syncwarp();
+      };
+      auto done = [&](uint64_t *bar) {
+        if (one) commit(bar);
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (; !bad && next_seg(k, s); ++k) {
+        if (!wait_all(q_bar, k & 1) || !arrived(ring)) break;
+        const int live = PAIR ? 1 : s.subs;
+#pragma unroll 1
+        for (int e = 0; e < live; ++e) scores(e, PAIR ? qs[0] & 1 : e, ring.st);
+        done(&empty[ring.st]);
+        if (s.nb == 1) done(q_free);
+        ring.step();
+#pragma unroll 1
+        for (int i = 0; i < s.nb; ++i) {
+          const bool next = i + 1 < s.nb;
+          if constexpr (PAIR) {
+            if (next) {
+              if (!arrived(ring)) break;
+              scores(0, (qs[0] + 1) & 1, ring.st);
+              done(&empty[ring.st]);
+              if (i + 2 == s.nb) done(q_free);
+              ring.step();
+            }
+            if (!arrived(ring)) break;
+            clear(s, s.blk0 + i, ring.st);
+            if (!wait_all(&p_bar[qs[0] & 1], (qs[0] >> 1) & 1)) break;
+            ptx::tc_fence_after();
+            values(0, qs[0] & 1, ring.st, i > 0);
+            done(&empty[ring.st]);
+            ring.step();
+            ++qs[0];
+          } else {
+            if (!arrived(ring)) break;
+            clear(s, s.blk0 + i, ring.st);
+            Ring<Y::kStages> ahead = ring;
+            ahead.step();
+#pragma unroll 1
+            for (int e = 0; e < live; ++e) {
+              if (!wait_all(&p_bar[e], qs[e] & 1)) break;
+              ptx::tc_fence_after();
+              values(e, e, ring.st, i > 0);
+              if (e == live - 1) done(&empty[ring.st]);
+              if (next) {
+                if (e == 0 && !arrived(ahead)) break;
+                scores(e, e, ahead.st);
+              }
+              ++qs[e];
+            }
+            if (bad) break;
+            if (next) {
+              done(&empty[ahead.st]);
+              if (i + 2 == s.nb) done(q_free);
+              ring = ahead;
+            }
+            ring.step();
+          }
+        }
+      }
+      if (one) {
+        if (bad) misc[1] = 1;
+        commit(end_bar);
+        (void)ptx::mbar_wait(end_bar, 0);
+      }
+    }
+  } else {
+    // ---- softmax ----
+    const int quad = warp & 3, hf = warp >> 2;  // hf: the subtile, or a pair's half of the row
+    const int sub = PAIR ? rank : hf;           // subtile of the tile
+    const int gt = PAIR ? tid : tid & 127;      // thread of the subtile's group
+    const uint32_t bar_id = PAIR ? 5 : 5 + hf;
+    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t to = tq + Y::kColO + (PAIR ? hf * Y::kOut : hf * DH);  // this thread's O
+    const int r = quad * 32 + lane;             // row of the subtile
+    const float sl2 = A.scale_log2;
+    auto tell = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) ptx::mbar_arrive_at(bar, 0);
+        else ptx::mbar_arrive(bar);
+      }
+    };
+    uint32_t q = 0, k = 0;
+    Seg s;
+#pragma unroll 1
+    for (;; ++k) {
+      // (all of a group's threads go on, or none)
+      const bool over = !next_seg(k, s);
+      if (any_of(bar_id, Y::kGroup, over)) break;
+      if (!PAIR && sub >= s.subs) continue;
+      const int left = s.n - s.tok0 - sub * A.tp;  // tokens from the subtile's first on
+      const int rows = (left < A.tp ? left : A.tp) * A.G;
+      const int tok = s.tok0 + sub * A.tp + r / A.G, head = s.h * A.G + r % A.G;
+      const bool real = r < rows, busy = quad * 32 < rows;
+      // what the row sees: positions below `lim`, and of a tree the nodes in `path`
+      int lim = real ? s.ctx + tok + 1 : 0x40000000;
+      uint64_t path = 0;
+      if (A.parent && real) {
+        lim = s.ctx;
+        const int32_t *up = A.parent + s.row0;
+#pragma unroll 1
+        for (int m = tok, d = 0; m >= 0 && d < LBX_ATTN_MAX_NODES; ++d) {
+          path |= 1ull << m;
+          m = up[m];
+        }
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < s.nb; ++i, ++q) {
+        const int ch = PAIR ? (int)(q & 1) : hf;
+        const uint32_t ph = PAIR ? (q >> 1) & 1 : q & 1;
+        wait(&s_bar[ch], ph);
+        ptx::tc_fence_after();
+        if (!busy) {  // no rows: keep step with the others
+          tell(&p_bar[ch]);
+          continue;
+        }
+        const uint32_t sc = tq + ch * kBlk;
+        float sv[Y::kMine];
+#pragma unroll
+        for (int e = 0; e < Y::kMine; e += 32)
+          ptx::tmem_ld32(sc + (PAIR ? hf * 64 : 0) + e, *reinterpret_cast<float(*)[32]>(sv + e));
+        ptx::tmem_wait_ld();
+        const int k0 = (s.blk0 + i) * kBlk + (PAIR ? hf * 64 : 0);
+        if (!__all_sync(0xffffffffu, lim - k0 >= Y::kMine)) {
+#pragma unroll
+          for (int w = 0; w < Y::kMine / 64; ++w) {
+            uint64_t ok = cache::low_bits(lim - k0 - 64 * w);
+            const int by = k0 + 64 * w - lim;  // of a tree: the word's first key, from its root
+            if (by >= 0) ok |= by < 64 ? path >> by : 0ull;
+            else if (by > -64) ok |= path << -by;
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (!((uint32_t)(ok >> (e & 32)) >> (e & 31) & 1)) sv[64 * w + e] = -INFINITY;
+          }
+        }
+        float mb;
+        {
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = sv[e];
+#pragma unroll
+          for (int e = 8; e < Y::kMine; ++e) mx[e & 7] = fmaxf(mx[e & 7], sv[e]);
+          mb = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        }
+        if constexpr (PAIR) {
+          // (two buffers: the other half may not have read the last block's yet)
+          float *max_of = red + (q & 1) * 2 * kRows;
+          max_of[hf * kRows + r] = mb;
+          ptx::tc_fence_before();
+          ptx::named_sync(1 + quad, 64);  // the row's other half: maxima out, scores read
+          ptx::tc_fence_after();
+          mb = fmaxf(mb, max_of[(1 - hf) * kRows + r]);
+        }
+        float alpha = 1.f;
+        bool need = false;
+        if ((mb - m_run) * sl2 > 8.f) {  // the first time too
+          alpha = ptx::ex2((m_run - mb) * sl2);
+          need = i > 0 && real;
+          l_run *= alpha;
+          m_run = mb;
+        }
+        const float ref = m_run == -INFINITY ? 0.f : fmaf(m_run, sl2, -kLift<F16>);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e0 = 0; e0 < Y::kMine; e0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ptx::ex2(fmaf(sv[e0 + 2 * e], sl2, -ref));
+            const float p1 = ptx::ex2(fmaf(sv[e0 + 2 * e + 1], sl2, -ref));
+            sum[e & 3] += p0 + p1;
+            pk[e] = pack2<F16>(p0, p1);
+          }
+          ptx::tmem_st16(sc + (PAIR ? hf * 32 : 0) + e0 / 2, pk);
+        }
+        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // rows whose reference moved rescale O, once the previous product is done
+        if (__any_sync(0xffffffffu, need)) {
+          if constexpr (PAIR) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
+          else wait(&o_bar[hf], (q - 1) & 1);
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
+            float ov[32];
+            uint32_t w[32];
+            ptx::tmem_ld32(to + e0, ov);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(ov[e] * alpha);
+            ptx::tmem_st32(to + e0, w);
+          }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        tell(&p_bar[ch]);
+      }
+
+      // ---- the segment's result: whole, or a partial ----
+      if constexpr (PAIR) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
+      else wait(&o_bar[hf], (q - 1) & 1);
+      ptx::tc_fence_after();
+      float l_sum = l_run;
+      if constexpr (PAIR) {
+        ptx::named_sync(1 + quad, 64);  // the last maxima are read
+        red[hf * kRows + r] = l_run;
+        ptx::named_sync(1 + quad, 64);
+        l_sum = red[r] + red[kRows + r];
+      }
+      const float m2 = m_run == -INFINITY ? -INFINITY : fmaf(m_run, sl2, -kLift<F16>);
+      const bool valid = !any_of(bar_id, Y::kGroup, bad);
+      // The row's place among the outputs, and what its O is multiplied with.  (A NaN
+      // among a row's scores makes its sum one, and the row with it.)
+      auto place = [&](int rw) {
+        const int token = s.tok0 + sub * A.tp + rw / A.G;
+        return ((size_t)s.l * c.M + s.row0 + token) * c.Hq + s.h * A.G + rw % A.G;
+      };
+      auto finish = [&](int rw, float m, float sum) {
+        if (A.lse) A.lse[place(rw)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      };
+      if (s.pieces == 1) {
+        if (busy && valid) {
+          const float w = l_sum == 0.f ? 0.f : 1.f / l_sum;
+          if (real && (!PAIR || hf == 0)) finish(r, m2, l_sum);
+          uint4 *out = reinterpret_cast<uint4 *>(
+              A.o + (((size_t)s.l * c.M + s.row0 + tok) * c.Hq + head) * DH + (PAIR ? hf * Y::kOut : 0));
+#pragma unroll 1
+          for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
+            float ov[32];
+            ptx::tmem_ld32(to + e0, ov);
+            ptx::tmem_wait_ld();
+            if (!real) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const float a = ov[8 * e + 2 * f], b = ov[8 * e + 2 * f + 1];
+                u[f] = l_sum == 0.f ? 0u : pack2<F16>(a * w, b * w);
+              }
+              out[e0 / 8 + e] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        }
+      } else if (rows > 0) {
+        // Piece e > 0 lies at its range's first place, the first piece at its second.
+        auto partial = [&](int e) {
+          const int at = 2 * (s.owner + e) + (e == 0 ? 1 : 0);
+          return A.part + (size_t)(2 * at + sub) * part_floats(DH);
+        };
+        float *mine = partial(s.mine);
+        if (busy && valid) {
+#pragma unroll 1
+          for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
+            float ov[32];
+            ptx::tmem_ld32(to + e0, ov);
+            ptx::tmem_wait_ld();
+            if (!real) continue;
+            float4 *at = reinterpret_cast<float4 *>(mine + 2 * kRows) +
+                         (size_t)((PAIR ? hf * Y::kOut : 0) + e0) / 4 * kRows + r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              at[e * kRows] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          }
+          if (real && (!PAIR || hf == 0)) mine[r] = m2, mine[kRows + r] = l_sum;
+        }
+        ptx::named_sync(bar_id, Y::kGroup);
+        if (gt == 0) {
+          __threadfence();  // the group's partial, before its arrival
+          unsigned int *count = A.counters + 2 * s.owner + sub;
+          const bool last = atomicAdd(count, 1u) == (unsigned)s.pieces - 1;
+          if (last) *count = 0u;  // for the next call
+          misc[4 + sub] = last;
+          __threadfence();
+        }
+        ptx::named_sync(bar_id, Y::kGroup);
+        if (misc[4 + sub] && valid) {
+          // each row's largest reference and sum, then four columns of a row per thread
+          float *top_of = red + (PAIR ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
+          if (gt < rows) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+            for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + gt));
+            if (top == -INFINITY) top = 0.f;
+#pragma unroll 4
+            for (int e = 0; e < s.pieces; ++e) {
+              const float *f = partial(e) + gt;
+              sum = fmaf(ptx::ex2(__ldcg(f) - top), __ldcg(f + kRows), sum);
+            }
+            top_of[gt] = top, inv_of[gt] = sum == 0.f ? 0.f : 1.f / sum;
+            finish(gt, top, sum);
+          }
+          ptx::named_sync(bar_id, Y::kGroup);
+#pragma unroll 1
+          for (int idx = gt; idx < rows * (DH / 4); idx += Y::kGroup) {
+            const int rw = idx % rows, c4 = idx / rows;
+            const float top = top_of[rw], inv = inv_of[rw];
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int e = 0; e < s.pieces; ++e) {
+              const float *from = partial(e);
+              const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) +
+                                      (size_t)c4 * kRows + rw);
+              const float w = ptx::ex2(__ldcg(from + rw) - top);
+              f.x = fmaf(w, y.x, f.x), f.y = fmaf(w, y.y, f.y);
+              f.z = fmaf(w, y.z, f.z), f.w = fmaf(w, y.w, f.w);
+            }
+            const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
+            reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = inv == 0.f ? make_uint2(0u, 0u) : u;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::named_sync(bar_id, Y::kGroup);  // red is free again
+    }
+    if (bad) misc[1] = 1;
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();  // neither leaves while the other may reach it
+  if (tid == 0 && A.status) {
+    if (misc[1]) *A.status = LBX_ETIMEOUT;
+    else if (misc[2]) *A.status = LBX_EINVAL;
+  }
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, Y::kTmemCols);
+    else ptx::tmem_dealloc(tmem, Y::kTmemCols);
+  }
+}
+
+// Launches of one head dimension (instances in page_attn_*.cu).
+template <int DH>
+cudaError_t launch_page_attn(bool f16, const PageMaps &maps, const PageArgs &A, int grid,
+                             cudaStream_t stream);
+template <int DH, bool F16>
+cudaError_t launch_page_attn_of(const PageMaps &maps, const PageArgs &A, int grid,
+                                cudaStream_t stream) {
+  auto kernel = page_attn_kernel<DH, F16>;
+  constexpr int bytes = Lay<DH>::kSmemTotal;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes, cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = Lay<DH>::kCtas, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, A);
+}
+
+}  // namespace paged
+}  // namespace lbx

@@ -1,0 +1,128 @@
+// page_walk.cuh -- how lbx_paged_attention shares out its work: tiles of a request's
+// query rows, blocks of keys, one list of the blocks of all tiles cut into equal
+// ranges, one per CTA (or pair).
+//
+// A tile is two subtiles of whole tokens, as many as fit 128 rows of G heads each.
+// Its keys are the positions up to its last token's (all of a tree's), in blocks of
+// 128; a chunk's tiles are as much longer as they stand later.  The list runs over
+// (layer, KV head), request, tile, block; every tile begins with kLead blocks that
+// stand for what beginning and ending it costs.  Range c starts at c * total / n: where
+// that leaves a piece of fewer than kLeast blocks of a tile on either side, at the tile's
+// edge.  All is derived from the requests' lengths by every CTA for itself; only
+// the sums over the requests are shared.
+#pragma once
+
+#include "page_common.cuh"
+
+namespace lbx {
+namespace paged {
+
+constexpr int kBlk = 128;   // keys per block
+constexpr int kRows = 128;  // rows per subtile
+constexpr int kLead = 2, kLeast = 2;
+constexpr int kMinRange = 4;  // entries of the list per CTA, at least
+
+typedef long long i64;
+
+struct Shape {
+  int W;       // tokens per tile
+  int period;  // tiles after which (position mod kBlk) repeats; a power of two
+  int tree;
+};
+
+__host__ __device__ inline Shape shape_of(int G, bool tree) {
+  Shape s;
+  s.W = 2 * (kRows / G);
+  const int low = s.W & -s.W;  // gcd with kBlk, a power of two
+  s.period = low >= kBlk ? 1 : kBlk / low;
+  s.tree = tree;
+  return s;
+}
+
+__host__ __device__ inline int tiles_of(const Shape &s, int n) { return (n + s.W - 1) / s.W; }
+
+// Blocks of tile t of a request of ctx cached and n new tokens.
+__host__ __device__ inline int blocks_of(const Shape &s, int ctx, int n, int t) {
+  const i64 end = s.tree || (i64)(t + 1) * s.W >= n ? (i64)ctx + n : (i64)ctx + (i64)(t + 1) * s.W;
+  return (int)((end + kBlk - 1) / kBlk);
+}
+
+// Entries of the list of a request's first k tiles, none of them its last (unless k is
+// all of them).  With x_i = c + i W the sum of floor(x_i / 128) over whole periods
+// is (sum of x_i - sum of x_i mod 128) / 128, where the remainders of a period are
+// c mod g, c mod g + g, .. (g = 128 / period); the rest is added one by one.
+__host__ __device__ inline i64 entries_upto(const Shape &s, int ctx, int n, int k) {
+  if (s.tree) return (i64)k * (kLead + blocks_of(s, ctx, n, 0));
+  const int all = tiles_of(s, n), m = k < all ? k : all - 1;  // tiles that are not the last
+  i64 sum = (i64)k * kLead;
+  if (k >= all && all > 0) sum += blocks_of(s, ctx, n, all - 1);
+  if (m <= 0) return sum;
+  const i64 c = (i64)ctx + s.W + kBlk - 1, whole = m / s.period * s.period;
+  const int g = kBlk / s.period;
+  const i64 x = whole * c + whole * (whole - 1) / 2 * s.W;
+  const i64 rest = whole * (c % g) + whole / s.period * ((i64)g * s.period * (s.period - 1) / 2);
+  sum += (x - rest) / kBlk;
+  for (i64 i = whole; i < m; ++i) sum += (c + i * s.W) / kBlk;
+  return sum;
+}
+
+__host__ __device__ inline i64 entries_of(const Shape &s, int ctx, int n) {
+  return n > 0 ? entries_upto(s, ctx, n, tiles_of(s, n)) : 0;
+}
+
+// The tile of a request that entry y of its own lies in; `before`: the entries before it.
+__host__ __device__ inline int tile_at(const Shape &s, int ctx, int n, i64 y, i64 &before) {
+  int a = 0, z = tiles_of(s, n) - 1;
+  while (a < z) {
+    const int h = (a + z + 1) >> 1;
+    if (entries_upto(s, ctx, n, h) <= y) a = h;
+    else z = h - 1;
+  }
+  before = entries_upto(s, ctx, n, a);
+  return a;
+}
+
+// How the list is cut: n ranges of `total` entries.
+struct Cut {
+  i64 total;
+  int n;
+  __host__ __device__ i64 at(int c) const { return (i64)c * total / n; }
+  // the first boundary at or past x, and the last one at or before it
+  __host__ __device__ int first(i64 x) const { return (int)((x * n + total - 1) / total); }
+  __host__ __device__ int last(i64 x) const { return (int)(((x + 1) * n + total - 1) / total) - 1; }
+};
+
+__host__ __device__ inline Cut cut_of(i64 total, int ctas) {
+  const i64 n = total / kMinRange;
+  return {total, n < 1 ? 1 : n < ctas ? (int)n : ctas};
+}
+
+// A tile's share of range `me`: its blocks, and the tile's pieces.  X: the tile's first
+// entry, nb: its blocks.
+struct Piece {
+  int blk0, blk1;
+  int pieces, mine, owner;  // owner: the range of the first piece
+  bool last;                // the range ends in this tile
+};
+__host__ __device__ inline bool piece_of(const Cut &c, int me, i64 X, int nb, Piece &p) {
+  const i64 lo = X + kLead + kLeast, hi = X + kLead + nb - kLeast;
+  int a = 1, z = 0;  // the boundaries inside the tile
+  if (lo <= hi) {
+    a = c.first(lo), z = c.last(hi);
+    if (a < 1) a = 1;
+    if (z > c.n - 1) z = c.n - 1;
+  }
+  const bool any = a <= z;
+  // the range ends before the tile, or goes to the tile's edge
+  if (me + 1 < c.n && c.at(me + 1) < lo && c.at(me + 1) < X + kLead + nb) return false;
+  p.pieces = any ? z - a + 2 : 1;
+  p.owner = any ? a - 1 : me;
+  p.mine = any && me >= a ? me - a + 1 : 0;
+  p.blk0 = any && me >= a ? (int)(c.at(me) - X - kLead) : 0;
+  p.last = any && me + 1 >= a && me + 1 <= z;
+  p.blk1 = p.last ? (int)(c.at(me + 1) - X - kLead) : nb;
+  return true;
+}
+
+}  // namespace paged
+}  // namespace lbx
