@@ -46,6 +46,8 @@ using cache::Ring;
 
 constexpr int kThreads = 352;
 constexpr int kMaxCtas = cache::kMaxCtas;
+// Most rows whose pieces are joined by columns instead of by rows.
+constexpr int kFewRows = 32;
 
 // Floats of one partial: m (base 2) and l per row, then O as [dh / 4][128] of four.
 __host__ __device__ constexpr size_t part_floats(int dh) { return 2 * kRows + (size_t)kRows * dh; }
@@ -94,7 +96,7 @@ struct Lay {
   static constexpr int kSmemSegs = kSmemRed + 4 * kRows * 4;     // Seg [4]
   static constexpr int kSmemMisc = kSmemSegs + 4 * (int)sizeof(Seg);  // int [16]
   static constexpr int kSmemBars = kSmemMisc + 64;
-  static constexpr int kNBars = 3 * kStages + 18;
+  static constexpr int kNBars = 3 * kStages + 20;
   static constexpr int kSmemTotal = kSmemBars + kNBars * 8;
   static_assert(kSmemTotal <= 227 * 1024 && kSmemRing % 1024 == 0 && kSmemBars % 8 == 0, "shared");
   // tensor memory: two buffers of S / P, O of each subtile
@@ -132,24 +134,39 @@ __device__ __forceinline__ bool any_of(uint32_t id, uint32_t nthreads, bool p) {
 
 // Where a CTA's range of the list begins.
 struct Begin {
-  i64 total, per_lh;  // entries of the whole list, of one (layer, KV head)
-  i64 X;              // entry of the first tile
+  Cut cut;
+  i64 from, X;  // the range's first entry, that of the tile it lies in
   int lh, b, t;
 };
 
-// The sums over the requests: every thread takes consecutive ones.  Finds range
-// `me` of `ctas`; false if the batch breaks the rules (in every thread).  `scratch`:
-// 8 (kThreads + 64) bytes of shared memory and 4 (Bq + 1) for a tree's check.
-__device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, void *scratch,
-                                           Begin *out) {
+// Finds range `me` of the list for one of `ctas` CTAs (or pairs): sums over the requests,
+// consecutive ones per thread, then the request and the tile by counting. 1: there is
+// work for this range, 0: there is none, -1: the batch breaks the rules (in every
+// thread alike, and in every block).  `scratch`: shared memory.
+__device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i64 *scratch,
+                                          Begin &g) {
   const lbx_page_cfg &c = A.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  i64 *sums = static_cast<i64 *>(scratch), *warps = sums + kThreads;
-  int *starts = reinterpret_cast<int *>(warps + 64);
-  const int per = (c.Bq + kThreads - 1) / kThreads;
+  i64 *warps = scratch + 4;
+  const int per = c.Bq <= kThreads ? 1 : (c.Bq + kThreads - 1) / kThreads;
   const i64 room = (i64)c.max_pages * c.page;
   int bad = 0;
   i64 sum = 0;
+  if (A.parent) {  // the trees, a row per thread
+    const int rows = A.start[c.Bq];
+#pragma unroll 1
+    for (int r = tid; r < rows && r < c.M; r += kThreads) {
+      const int p = A.parent[r];
+      int a = 0, z = c.Bq - 1;
+      while (a < z) {
+        const int h = (a + z + 1) >> 1;
+        if (A.start[h] <= r) a = h;
+        else z = h - 1;
+      }
+      const int i = r - A.start[a];
+      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
+    }
+  }
 #pragma unroll 1
   for (int b = tid * per; b < (tid + 1) * per && b < c.Bq; ++b) {
     const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
@@ -160,8 +177,6 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
     }
     sum += entries_of(A.shape, ctx, e - s);
   }
-  if (A.parent)
-    for (int b = tid; b <= c.Bq; b += kThreads) starts[b] = A.start[b];
   i64 upto = sum;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -169,60 +184,77 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
     if (lane >= d) upto += o;
   }
   if (lane == 31) warps[warp] = upto;
-  if (__syncthreads_or(bad)) return false;
+  if (__syncthreads_or(bad)) return -1;
   i64 total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) upto += warps[w];
     total += warps[w];
   }
-  sums[tid] = upto;  // through this thread's requests
-  if (A.parent) {
-    const int rows = starts[c.Bq];
-#pragma unroll 1
-    for (int r = tid; r < rows; r += kThreads) {
-      const int p = A.parent[r];
-      int a = 0, z = c.Bq - 1;
-      while (a < z) {
-        const int h = (a + z + 1) >> 1;
-        if (starts[h] <= r) a = h;
-        else z = h - 1;
-      }
-      const int i = r - starts[a];
-      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
-    }
-  }
-  if (__syncthreads_or(bad)) return false;
-  if (tid == 0) {
-    Begin g;
-    g.per_lh = total, g.total = total * c.L * c.Hkv;
-    g.lh = g.b = g.t = 0, g.X = 0;
-    const Cut cut = cut_of(g.total, ctas);
-    if (total > 0 && me < cut.n) {
-      const i64 x = cut.at(me);
-      g.lh = (int)(x / total);
-      i64 y = x - g.lh * total;
-      int a = 0, z = kThreads - 1;  // the first thread whose requests reach past y
-      while (a < z) {
-        const int h = (a + z) >> 1;
-        if (sums[h] > y) z = h;
-        else a = h + 1;
-      }
-      if (a > 0) y -= sums[a - 1];
-      int b = a * per;
+  g.cut = cut_of(total * c.L * c.Hkv, ctas);
+  if (total == 0 || me >= g.cut.n) return 0;
+  g.from = g.cut.at(me);
+  g.lh = (int)(g.from / total);
+  i64 y = g.from - g.lh * total;
+  const int owner = __syncthreads_count(upto <= y);  // the thread that has the request
+  if (tid == owner) {
+    y -= upto - sum;
+    int b = tid * per;
+    if (per > 1)
       for (;; ++b) {
         const i64 e = entries_of(A.shape, A.ctx_len[b], A.start[b + 1] - A.start[b]);
         if (y < e) break;
         y -= e;
       }
-      i64 before;
-      g.b = b;
-      g.t = tile_at(A.shape, A.ctx_len[b], A.start[b + 1] - A.start[b], y, before);
-      g.X = x - (y - before);
-    }
-    *out = g;
+    scratch[0] = y, scratch[1] = b;
   }
   __syncthreads();
-  return true;
+  y = scratch[0], g.b = (int)scratch[1];
+  const int ctx = A.ctx_len[g.b], n = A.start[g.b + 1] - A.start[g.b];
+  g.t = 0;
+  i64 before = 0;
+#pragma unroll 1
+  for (int size = tiles_of(A.shape, n); size > 1;) {  // the last tile that begins at y or before
+    const int step = (size + kThreads - 1) / kThreads;
+    const bool in = (i64)tid * step < size;
+    const i64 e = in ? entries_upto(A.shape, ctx, n, g.t + tid * step) : 0;
+    const int k = __syncthreads_count(in && e <= y) - 1;
+    if (tid == k) scratch[2] = e;
+    __syncthreads();
+    before = scratch[2];
+    g.t += k * step;
+    size = size - k * step < step ? size - k * step : step;
+  }
+  g.X = g.from - (y - before);
+  return 1;
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 apart2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three (a NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 template <int DH, bool F16>
@@ -241,22 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *misc = reinterpret_cast<volatile int *>(smem + Y::kSmemMisc);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + Y::kSmemBars);
   uint64_t *empty = full + Y::kStages, *peer = empty + Y::kStages;
-  uint64_t *s_bar = peer + Y::kStages, *p_bar = s_bar + 2, *o_bar = p_bar + 2;
+  uint64_t *s_bar = peer + Y::kStages, *p_bar = s_bar + 2, *p2_bar = p_bar + 2, *o_bar = p2_bar + 2;
   uint64_t *seg_bar = o_bar + 2, *seg_free = seg_bar + 4;
   uint64_t *q_bar = seg_free + 4, *qh_bar = q_bar + 1, *q_free = qh_bar + 1, *end_bar = q_free + 1;
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int me = blockIdx.x / Y::kCtas, ctas = gridDim.x / Y::kCtas;
-  Begin *begin = reinterpret_cast<Begin *>(smem + Y::kSmemSegs);  // read before the first segment
-  if (!find_begin(A, me, ctas, smem, begin)) {
-    if (tid == 0 && A.status) *A.status = LBX_ETREE;
-    return;
-  }
-  const Begin g = *begin;
-  if (g.total == 0) return;  // no tokens: every CTA alike
   if (tid == 0) {
     for (int i = 0; i < Y::kNBars; ++i)
-      ptx::mbar_init(full + i, full + i == p_bar || full + i == p_bar + 1
+      ptx::mbar_init(full + i, full + i >= p_bar && full + i < p_bar + 4
                                    ? Y::kCtas * Y::kGroup / 32
                                : full + i >= seg_free && full + i < seg_free + 4 ? 10
                                : full + i == q_bar ? Y::kCtas
@@ -274,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::tc_fence_before();
   }
-  ptx::fence_proxy_async();  // the scratch of the sums lies where copies will land
+  Begin g;
+  const int work = find_begin(A, me, ctas, reinterpret_cast<i64 *>(red), g);
   __syncthreads();
   if constexpr (PAIR) ptx::cluster_sync();  // the other CTA's barriers are set up
   ptx::tc_fence_after();
@@ -300,13 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ok && s.have != 0;
   };
 
-  if (warp == 9) {
+  if (work <= 0) {
+    // nothing for this range (of a pair: for both)
+    if (work < 0 && tid == 0 && A.status) *A.status = LBX_ETREE;
+  } else if (warp == 9) {
     // ---- the walk, and copies of K and V ----
-    const Cut cut = cut_of(g.total, ctas);
-    int lh = g.lh, b = g.b, t = g.t, s0 = 0, n = 0, ctx = 0;
+    const Cut cut = g.cut;
+    int lh = g.lh, b = g.b, t = g.t, s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
     i64 X = g.X;
+    const i64 to = cut.at(me + 1);
     const int n_lh = c.L * c.Hkv;
-    auto request = [&]() { s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b]; };
+    bool more = true;
     auto step = [&]() {  // to the next tile of the list
       X += kLead + blocks_of(A.shape, ctx, n, t);
       ++t;
@@ -317,44 +347,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           b = 0;
           if (++lh == n_lh) return;
         }
-        request();
+        s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
       }
     };
-    bool more = me < cut.n;
-    if (more) {
-      request();
-      const int nb = blocks_of(A.shape, ctx, n, t);
-      const i64 y = cut.at(me) - X;
-      if (y >= kLead + kLeast && y > kLead + nb - kLeast) step();
+    {
+      const i64 y = g.from - X;
+      if (y >= kLead + kLeast && y > kLead + blocks_of(A.shape, ctx, n, t) - kLeast) step();
     }
+    // The range's next tile.
+    auto advance = [&](Seg &s) {
+      Piece p;
+      const int nb = more && lh < n_lh ? blocks_of(A.shape, ctx, n, t) : 0;
+      s.have = nb > 0 && piece_of(cut, me, g.from, to, X, nb, p);
+      if (!s.have) return;
+      s.l = lh / c.Hkv, s.h = lh - s.l * c.Hkv, s.b = b, s.row0 = s0, s.n = n, s.ctx = ctx;
+      s.tok0 = t * A.shape.W, s.subs = n - s.tok0 > A.tp ? 2 : 1;
+      s.blk0 = p.blk0, s.nb = p.blk1 - p.blk0;
+      s.pieces = p.pieces, s.mine = p.mine, s.owner = p.owner;
+      if (p.last) more = false;
+      else step();
+    };
+    auto publish = [&](const Seg &s, uint32_t k) {
+      if (k >= 4) wait(&seg_free[k & 3], ((k >> 2) & 1) ^ 1u);
+      if (lane == 0) {
+        volatile Seg &f = segs[k & 3];
+        f.have = s.have;
+        f.l = s.l, f.h = s.h, f.b = s.b, f.row0 = s.row0, f.n = s.n, f.ctx = s.ctx;
+        f.tok0 = s.tok0, f.subs = s.subs, f.blk0 = s.blk0, f.nb = s.nb;
+        f.pieces = s.pieces, f.mine = s.mine, f.owner = s.owner;
+        ptx::mbar_arrive(&seg_bar[k & 3]);
+      }
+      __syncwarp();
+    };
     Ring<Y::kStages> ring;
     int loads = 0, outside = 0;
     const uint32_t none = (uint32_t)(c.L * c.n_pages) * (uint32_t)c.page;  // past the pools' end
+    Seg s, next;
+    advance(s);
+    publish(s, 0);
+    // (a segment is published before the copies of the one before it, so that its
+    // queries can come as soon as their place is free)
 #pragma unroll 1
-    for (uint32_t k = 0;; ++k) {
-      Piece p;
-      const int nb_all = more && lh < n_lh ? blocks_of(A.shape, ctx, n, t) : 0;
-      more = more && lh < n_lh && piece_of(cut, me, X, nb_all, p) && !__any_sync(0xffffffffu, bad);
-      if (k >= 4) wait(&seg_free[k & 3], ((k >> 2) & 1) ^ 1u);
-      const int l = lh / c.Hkv, h = lh - l * c.Hkv, nb = p.blk1 - p.blk0;
-      const int tok0 = t * A.shape.W;
-      if (lane == 0) {
-        volatile Seg &s = segs[k & 3];
-        s.have = more;
-        if (more) {
-          s.l = l, s.h = h, s.b = b, s.row0 = s0, s.n = n, s.tok0 = tok0, s.ctx = ctx;
-          s.blk0 = p.blk0, s.nb = nb, s.subs = n - tok0 > A.tp ? 2 : 1;
-          s.pieces = p.pieces, s.mine = p.mine, s.owner = p.owner;
-        }
-        ptx::mbar_arrive(&seg_bar[k & 3]);
-      }
-      if (!more) break;
+    for (uint32_t k = 0; s.have; ++k, s = next) {
+      advance(next);
+      if (__any_sync(0xffffffffu, bad)) next.have = 0;
+      publish(next, k + 1);
+      const int nb = s.nb;
       // Lane e brings box e of a block: `box` positions of one head, 64 columns.
       // The rows of its boxes come from the table one block ahead.
-      const int kv_len = ctx + n;
+      const int kv_len = s.ctx + s.n;
       constexpr int kKA = DH / 64, kVA = Y::kCols / 64;
       const int k_boxes = Y::kKeys / A.box * kKA, v_boxes = kBlk / A.box * kVA;
-      const int32_t *row = A.table + (size_t)b * c.max_pages;
+      const int32_t *row = A.table + (size_t)s.b * c.max_pages;
       auto place = [&](int blk, int off) -> uint32_t {
         const int pos = blk * kBlk + off;
         if (pos >= kv_len) return none;
@@ -363,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           outside = 1;
           return none;
         }
-        return (uint32_t)(l * c.n_pages + id) * (uint32_t)c.page + (uint32_t)(pos & (c.page - 1));
+        return (uint32_t)(s.l * c.n_pages + id) * (uint32_t)c.page + (uint32_t)(pos & (c.page - 1));
       };
       const int k_off = lane / kKA * A.box + rank * Y::kKeys, v_off = lane / kVA * A.box;
       auto k_row = [&](int blk) { return lane < k_boxes ? place(blk, k_off) : none; };
@@ -380,30 +424,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (take() && lane < k_boxes)
           ptx::tma_load_3d(smem + Y::kSmemRing + ring.st * Y::kStage + lane % kKA * (Y::kKeys * 128) +
                                lane / kKA * A.box * 128,
-                           &maps.k, lane % kKA * 64, h, (int)at, &full[ring.st]);
+                           &maps.k, lane % kKA * 64, s.h, (int)at, &full[ring.st]);
         ring.step();
       };
       auto load_v = [&](uint32_t at) {
         if (take() && lane < v_boxes)
           ptx::tma_load_3d(smem + Y::kSmemRing + ring.st * Y::kStage + lane % kVA * (kBlk * 128) +
                                lane / kVA * A.box * 128,
-                           &maps.v, rank * Y::kCols + lane % kVA * 64, h, (int)at, &full[ring.st]);
+                           &maps.v, rank * Y::kCols + lane % kVA * 64, s.h, (int)at, &full[ring.st]);
         ring.step();
       };
-      uint32_t k_at = k_row(p.blk0), v_at = v_row(p.blk0);
+      uint32_t k_at = k_row(s.blk0), v_at = v_row(s.blk0);
 #pragma unroll 1
       for (int i = 0; i < nb; ++i) {
         // K of block i; V of block i goes before K of block i + 1 where one CTA has both
         // subtiles, behind it in a pair, as the products take them
-        const int ahead = p.blk0 + (i + 1 < nb ? i + 1 : i);
+        const int ahead = s.blk0 + (i + 1 < nb ? i + 1 : i);
         const uint32_t k_next = k_row(ahead), v_next = v_row(ahead);
         if (!PAIR || i == 0) load_k(k_at);
         if (PAIR && i + 1 < nb) load_k(k_next);
         load_v(v_at);
         k_at = k_next, v_at = v_next;
       }
-      if (p.last) more = false;
-      else step();
     }
     outside = __any_sync(0xffffffffu, outside);
     if (lane == 0 && outside) misc[2] = 1;
@@ -512,18 +554,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      auto values = [&](int e, int buf, int stage, uint32_t later) {
+      // O of subtile e from the weights in `buf`: steps of 16 keys from `i0` on
+      auto values = [&](int e, int buf, int stage, int i0, int i1, uint32_t later) {
         const uint64_t vd = vdesc + (uint64_t)(stage * (Y::kStage >> 4));
         if (one) {
 #pragma unroll
-          for (int i = 0; i < kBlk / 16; ++i) {
+          for (int i = i0; i < i1; ++i) {
             const uint32_t pa = tmem + buf * kBlk + 8 * i, d = tmem + Y::kColO + e * DH;
             const uint64_t vb = vd + (uint64_t)(i * (2048 >> 4));
             const uint32_t acc = i > 0 ? 1u : later;
             if constexpr (PAIR) ptx::mma_16_ts_pair(d, pa, vb, idesc_o, acc);
             else ptx::mma_bf16_ts(d, pa, vb, idesc_o, acc);
           }
-          commit(&o_bar[PAIR ? buf : e]);
+          if (i1 == kBlk / 16) commit(&o_bar[PAIR ? buf : e]);
         }
         __syncwarp();
       };
@@ -555,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             clear(s, s.blk0 + i, ring.st);
             if (!wait_all(&p_bar[qs[0] & 1], (qs[0] >> 1) & 1)) break;
             ptx::tc_fence_after();
-            values(0, qs[0] & 1, ring.st, i > 0);
+            values(0, qs[0] & 1, ring.st, 0, 8, i > 0);
             done(&empty[ring.st]);
             ring.step();
             ++qs[0];
@@ -568,7 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < live; ++e) {
               if (!wait_all(&p_bar[e], qs[e] & 1)) break;
               ptx::tc_fence_after();
-              values(e, e, ring.st, i > 0);
+              values(e, e, ring.st, 0, 4, i > 0);
+              if (!wait_all(&p2_bar[e], qs[e] & 1)) break;
+              ptx::tc_fence_after();
+              values(e, e, ring.st, 4, 8, 1u);
               if (e == live - 1) done(&empty[ring.st]);
               if (next) {
                 if (e == 0 && !arrived(ahead)) break;
@@ -619,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!PAIR && sub >= s.subs) continue;
       const int left = s.n - s.tok0 - sub * A.tp;  // tokens from the subtile's first on
       const int rows = (left < A.tp ? left : A.tp) * A.G;
-      const int tok = s.tok0 + sub * A.tp + r / A.G, head = s.h * A.G + r % A.G;
+      const int tok = s.tok0 + sub * A.tp + r / A.G;
       const bool real = r < rows, busy = quad * 32 < rows;
       // what the row sees: positions below `lim`, and of a tree the nodes in `path`
       int lim = real ? s.ctx + tok + 1 : 0x40000000;
@@ -642,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         if (!busy) {  // no rows: keep step with the others
           tell(&p_bar[ch]);
+          if constexpr (!PAIR) tell(&p2_bar[ch]);
           continue;
         }
         const uint32_t sc = tq + ch * kBlk;
@@ -665,13 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mb;
         {
-          float mx[8];
+          float mx[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = sv[e];
+          for (int e = 0; e < 4; ++e) mx[e] = max3(sv[3 * e], sv[3 * e + 1], sv[3 * e + 2]);
 #pragma unroll
-          for (int e = 8; e < Y::kMine; ++e) mx[e & 7] = fmaxf(mx[e & 7], sv[e]);
-          mb = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                     fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          for (int e = 12; e + 1 < Y::kMine; e += 2)
+            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], sv[e], sv[e + 1]);
+          mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         }
         if constexpr (PAIR) {
           // (two buffers: the other half may not have read the last block's yet)
@@ -691,39 +738,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_run = mb;
         }
         const float ref = m_run == -INFINITY ? 0.f : fmaf(m_run, sl2, -kLift<F16>);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e0 = 0; e0 < Y::kMine; e0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = ptx::ex2(fmaf(sv[e0 + 2 * e], sl2, -ref));
-            const float p1 = ptx::ex2(fmaf(sv[e0 + 2 * e + 1], sl2, -ref));
-            sum[e & 3] += p0 + p1;
-            pk[e] = pack2<F16>(p0, p1);
-          }
-          ptx::tmem_st16(sc + (PAIR ? hf * 32 : 0) + e0 / 2, pk);
-        }
-        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // rows whose reference moved rescale O, once the previous product is done
         if (__any_sync(0xffffffffu, need)) {
           if constexpr (PAIR) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
           else wait(&o_bar[hf], (q - 1) & 1);
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
-            float ov[32];
-            uint32_t w[32];
-            ptx::tmem_ld32(to + e0, ov);
+          for (int e0 = 0; e0 < Y::kOut; e0 += 16) {
+            float ov[16];
+            uint32_t w[16];
+            ptx::tmem_ld16(to + e0, ov);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(ov[e] * alpha);
-            ptx::tmem_st32(to + e0, w);
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(ov[e] * alpha);
+            ptx::tmem_st16(to + e0, w);
+          }
+        }
+        const uint64_t scale2 = both(sl2, sl2), ref2 = both(-ref, -ref);
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e0 = 0; e0 < Y::kMine; e0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = apart2(fma2(both(sv[e0 + 2 * e], sv[e0 + 2 * e + 1]), scale2, ref2));
+            const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
+            sum[e & 3] = add2(sum[e & 3], both(p0, p1));
+            pk[e] = pack2<F16>(p0, p1);
+          }
+          ptx::tmem_st16(sc + (PAIR ? hf * 32 : 0) + e0 / 2, pk);
+          if (!PAIR && e0 == 32) {  // half of the weights: their product may begin
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            tell(&p_bar[ch]);
           }
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        tell(&p_bar[ch]);
+        tell(PAIR ? &p_bar[ch] : &p2_bar[ch]);
+        const float2 s2 = apart2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l_run += s2.x + s2.y;
       }
 
       // ---- the segment's result: whole, or a partial ----
@@ -739,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float m2 = m_run == -INFINITY ? -INFINITY : fmaf(m_run, sl2, -kLift<F16>);
       const bool valid = !any_of(bar_id, Y::kGroup, bad);
-      // The row's place among the outputs, and what its O is multiplied with.  (A NaN
-      // among a row's scores makes its sum one, and the row with it.)
+      // A row's place among the outputs, and its lse.  (A NaN among a row's scores makes
+      // its sum one, and the row with it.)
       auto place = [&](int rw) {
         const int token = s.tok0 + sub * A.tp + rw / A.G;
         return ((size_t)s.l * c.M + s.row0 + token) * c.Hq + s.h * A.G + rw % A.G;
@@ -748,36 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto finish = [&](int rw, float m, float sum) {
         if (A.lse) A.lse[place(rw)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       };
-      if (s.pieces == 1) {
-        if (busy && valid) {
-          const float w = l_sum == 0.f ? 0.f : 1.f / l_sum;
-          if (real && (!PAIR || hf == 0)) finish(r, m2, l_sum);
-          uint4 *out = reinterpret_cast<uint4 *>(
-              A.o + (((size_t)s.l * c.M + s.row0 + tok) * c.Hq + head) * DH + (PAIR ? hf * Y::kOut : 0));
-#pragma unroll 1
-          for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
-            float ov[32];
-            ptx::tmem_ld32(to + e0, ov);
-            ptx::tmem_wait_ld();
-            if (!real) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t u[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f) {
-                const float a = ov[8 * e + 2 * f], b = ov[8 * e + 2 * f + 1];
-                u[f] = l_sum == 0.f ? 0u : pack2<F16>(a * w, b * w);
-              }
-              out[e0 / 8 + e] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-          }
-        }
-      } else if (rows > 0) {
-        // Piece e > 0 lies at its range's first place, the first piece at its second.
-        auto partial = [&](int e) {
-          const int at = 2 * (s.owner + e) + (e == 0 ? 1 : 0);
-          return A.part + (size_t)(2 * at + sub) * part_floats(DH);
-        };
+      // Piece e > 0 lies at its range's first place, the first piece at its second.
+      auto partial = [&](int e) {
+        const int at = 2 * (s.owner + e) + (e == 0 ? 1 : 0);
+        return A.part + (size_t)(2 * at + sub) * part_floats(DH);
+      };
+      constexpr int kCol0 = PAIR ? Y::kOut : 0;  // this thread's first column: hf times this
+      bool join = false;
+      if (s.pieces > 1 && rows > 0) {
         float *mine = partial(s.mine);
         if (busy && valid) {
 #pragma unroll 1
@@ -786,8 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_ld32(to + e0, ov);
             ptx::tmem_wait_ld();
             if (!real) continue;
-            float4 *at = reinterpret_cast<float4 *>(mine + 2 * kRows) +
-                         (size_t)((PAIR ? hf * Y::kOut : 0) + e0) / 4 * kRows + r;
+            float4 *at = reinterpret_cast<float4 *>(mine + 2 * kRows) + (hf * kCol0 + e0) / 4 * kRows + r;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               at[e * kRows] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
@@ -804,40 +835,123 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
         }
         ptx::named_sync(bar_id, Y::kGroup);
-        if (misc[4 + sub] && valid) {
-          // each row's largest reference and sum, then four columns of a row per thread
-          float *top_of = red + (PAIR ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
-          if (gt < rows) {
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-            for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + gt));
-            if (top == -INFINITY) top = 0.f;
-#pragma unroll 4
-            for (int e = 0; e < s.pieces; ++e) {
-              const float *f = partial(e) + gt;
-              sum = fmaf(ptx::ex2(__ldcg(f) - top), __ldcg(f + kRows), sum);
-            }
-            top_of[gt] = top, inv_of[gt] = sum == 0.f ? 0.f : 1.f / sum;
-            finish(gt, top, sum);
-          }
-          ptx::named_sync(bar_id, Y::kGroup);
-#pragma unroll 1
-          for (int idx = gt; idx < rows * (DH / 4); idx += Y::kGroup) {
-            const int rw = idx % rows, c4 = idx / rows;
-            const float top = top_of[rw], inv = inv_of[rw];
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        join = misc[4 + sub] != 0;
+      }
+      if (join && valid && rows <= kFewRows) {
+        // each row's largest reference and sum, then four columns of a row per thread
+        float *top_of = red + (PAIR ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
+        if (gt < rows) {
+          float top = -INFINITY, sum = 0.f;
 #pragma unroll 8
-            for (int e = 0; e < s.pieces; ++e) {
-              const float *from = partial(e);
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) +
-                                      (size_t)c4 * kRows + rw);
-              const float w = ptx::ex2(__ldcg(from + rw) - top);
-              f.x = fmaf(w, y.x, f.x), f.y = fmaf(w, y.y, f.y);
-              f.z = fmaf(w, y.z, f.z), f.w = fmaf(w, y.w, f.w);
-            }
-            const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
-            reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = inv == 0.f ? make_uint2(0u, 0u) : u;
+          for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + gt));
+          if (top == -INFINITY) top = 0.f;
+#pragma unroll 8
+          for (int e = 0; e < s.pieces; ++e) {
+            const float *f = partial(e) + gt;
+            sum = fmaf(ptx::ex2(__ldcg(f) - top), __ldcg(f + kRows), sum);
           }
+          top_of[gt] = top, inv_of[gt] = sum == 0.f ? 0.f : 1.f / sum;
+          finish(gt, top, sum);
+        }
+        ptx::named_sync(bar_id, Y::kGroup);
+#pragma unroll 1
+        for (int idx = gt; idx < rows * (DH / 4); idx += Y::kGroup) {
+          const int rw = idx % rows, c4 = idx / rows;
+          const float top = top_of[rw], inv = inv_of[rw];
+          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int e = 0; e < s.pieces; ++e) {
+            const float *from = partial(e);
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) +
+                                    (size_t)c4 * kRows + rw);
+            const float w = ptx::ex2(__ldcg(from + rw) - top);
+            f.x = fmaf(w, y.x, f.x), f.y = fmaf(w, y.y, f.y);
+            f.z = fmaf(w, y.z, f.z), f.w = fmaf(w, y.w, f.w);
+          }
+          const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
+          reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = inv == 0.f ? make_uint2(0u, 0u) : u;
+        }
+      } else if (busy && valid && (s.pieces == 1 || join)) {
+        // a row per thread (or half of one); this CTA's piece is still in tensor memory,
+        // the others' are added in the pieces' order, whichever CTA joins them
+        float top = m2, sum = l_sum;
+        if (join) {
+          top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+          for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + r));
+          if (top == -INFINITY) top = 0.f;
+#pragma unroll 1
+          for (int e = 0; e < s.pieces; ++e)
+            sum = fmaf(ptx::ex2(__ldcg(partial(e) + r) - top), __ldcg(partial(e) + kRows + r), sum);
+        }
+        const float w = sum == 0.f ? 0.f : 1.f / sum;
+        if (real && (!PAIR || hf == 0)) finish(r, top, sum);
+        const float w_own = join ? ptx::ex2(m2 - top) * w : w;
+        // where the four rows of this lane's group of lanes go
+        uint64_t rows_at[4];
+        {
+          const uint64_t at = real ? reinterpret_cast<uint64_t>(A.o + place(r) * DH + hf * kCol0) : 0ull;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rows_at[e] = __shfl_sync(0xffffffffu, at, (lane & ~3) + e);
+        }
+#pragma unroll 1
+        for (int e0 = 0; e0 < Y::kOut; e0 += 32) {
+          float v[32];
+          ptx::tmem_ld32(to + e0, v);
+          ptx::tmem_wait_ld();
+          if (join) {
+            float own[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) own[e] = v[e], v[e] = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < s.pieces; ++e) {
+              if (e == s.mine) {
+#pragma unroll
+                for (int f = 0; f < 32; ++f) v[f] = fmaf(w_own, own[f], v[f]);
+              } else if (real) {
+                const float *from = partial(e);
+                const float w_e = ptx::ex2(__ldcg(from + r) - top) * w;
+                const float4 *at = reinterpret_cast<const float4 *>(from + 2 * kRows) +
+                                   (hf * kCol0 + e0) / 4 * kRows + r;
+                float4 y[8];
+#pragma unroll
+                for (int f = 0; f < 8; ++f) y[f] = __ldcg(at + f * kRows);
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                  v[4 * f] = fmaf(w_e, y[f].x, v[4 * f]), v[4 * f + 1] = fmaf(w_e, y[f].y, v[4 * f + 1]);
+                  v[4 * f + 2] = fmaf(w_e, y[f].z, v[4 * f + 2]), v[4 * f + 3] = fmaf(w_e, y[f].w, v[4 * f + 3]);
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= w;
+          }
+          uint32_t pc[4][4];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pc[e >> 2][e & 3] = sum == 0.f ? 0u : pack2<F16>(v[2 * e], v[2 * e + 1]);
+          // four lanes exchange 16-byte pieces, so that a store of the warp writes 64
+          // bytes of eight rows instead of 16 of thirty-two
+#pragma unroll
+          for (int d = 1; d <= 2; d *= 2) {
+            const bool up = lane & d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (e & d) continue;
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? pc[e][f] : pc[e + d][f], d);
+                if (up) pc[e][f] = got;
+                else pc[e + d][f] = got;
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (rows_at[e])
+              reinterpret_cast<uint4 *>(rows_at[e])[e0 / 8 + (lane & 3)] =
+                  make_uint4(pc[e][0], pc[e][1], pc[e][2], pc[e][3]);
         }
       }
       ptx::tc_fence_before();

@@ -17,7 +17,7 @@
 namespace lbx {
 namespace paged {
 
-constexpr int kBlk = 128;   // keys per block
+constexpr int kBlk = 128;   // keys per block (its logarithm, 7, stands in entries_upto)
 constexpr int kRows = 128;  // rows per subtile
 constexpr int kLead = 2, kLeast = 2;
 constexpr int kMinRange = 4;  // entries of the list per CTA, at least
@@ -57,29 +57,20 @@ __host__ __device__ inline i64 entries_upto(const Shape &s, int ctx, int n, int 
   i64 sum = (i64)k * kLead;
   if (k >= all && all > 0) sum += blocks_of(s, ctx, n, all - 1);
   if (m <= 0) return sum;
-  const i64 c = (i64)ctx + s.W + kBlk - 1, whole = m / s.period * s.period;
-  const int g = kBlk / s.period;
-  const i64 x = whole * c + whole * (whole - 1) / 2 * s.W;
-  const i64 rest = whole * (c % g) + whole / s.period * ((i64)g * s.period * (s.period - 1) / 2);
-  sum += (x - rest) / kBlk;
-  for (i64 i = whole; i < m; ++i) sum += (c + i * s.W) / kBlk;
+  const uint32_t c = (uint32_t)ctx + s.W + kBlk - 1;  // (positions end at 2^30)
+  const int whole = m & -s.period, g = kBlk / s.period;
+  const i64 x = (i64)whole * c + (i64)whole * (whole - 1) / 2 * s.W;
+  const i64 rest = (i64)whole * (c & (g - 1)) + (i64)whole * (g * (s.period - 1)) / 2;
+  sum += (x - rest) >> 7;
+#ifdef __CUDA_ARCH__
+#pragma unroll 4
+#endif
+  for (int i = whole; i < m; ++i) sum += (c + (uint32_t)i * s.W) >> 7;
   return sum;
 }
 
 __host__ __device__ inline i64 entries_of(const Shape &s, int ctx, int n) {
   return n > 0 ? entries_upto(s, ctx, n, tiles_of(s, n)) : 0;
-}
-
-// The tile of a request that entry y of its own lies in; `before`: the entries before it.
-__host__ __device__ inline int tile_at(const Shape &s, int ctx, int n, i64 y, i64 &before) {
-  int a = 0, z = tiles_of(s, n) - 1;
-  while (a < z) {
-    const int h = (a + z + 1) >> 1;
-    if (entries_upto(s, ctx, n, h) <= y) a = h;
-    else z = h - 1;
-  }
-  before = entries_upto(s, ctx, n, a);
-  return a;
 }
 
 // How the list is cut: n ranges of `total` entries.
@@ -97,30 +88,29 @@ __host__ __device__ inline Cut cut_of(i64 total, int ctas) {
   return {total, n < 1 ? 1 : n < ctas ? (int)n : ctas};
 }
 
-// A tile's share of range `me`: its blocks, and the tile's pieces.  X: the tile's first
-// entry, nb: its blocks.
+// A tile's share of range `me`, from `from` = cut.at(me) to `to` = cut.at(me + 1): its
+// blocks, and the tile's pieces.  X: the tile's first entry, nb: its blocks.
 struct Piece {
   int blk0, blk1;
   int pieces, mine, owner;  // owner: the range of the first piece
   bool last;                // the range ends in this tile
 };
-__host__ __device__ inline bool piece_of(const Cut &c, int me, i64 X, int nb, Piece &p) {
-  const i64 lo = X + kLead + kLeast, hi = X + kLead + nb - kLeast;
-  int a = 1, z = 0;  // the boundaries inside the tile
-  if (lo <= hi) {
-    a = c.first(lo), z = c.last(hi);
+__host__ __device__ inline bool piece_of(const Cut &c, int me, i64 from, i64 to, i64 X, int nb,
+                                         Piece &p) {
+  const i64 lo = X + kLead + kLeast, hi = X + kLead + nb - kLeast;  // boundaries inside: lo..hi
+  // the range ends before the tile, or goes to the tile's edge
+  if (me + 1 < c.n && to < lo && to < X + kLead + nb) return false;
+  const bool begins = me > 0 && from >= lo && from <= hi;
+  p.last = me + 1 < c.n && to >= lo && to <= hi;
+  p.blk0 = begins ? (int)(from - X - kLead) : 0;
+  p.blk1 = p.last ? (int)(to - X - kLead) : nb;
+  p.pieces = 1, p.mine = 0, p.owner = me;
+  if (begins || p.last) {
+    int a = c.first(lo), z = c.last(hi);
     if (a < 1) a = 1;
     if (z > c.n - 1) z = c.n - 1;
+    p.pieces = z - a + 2, p.owner = a - 1, p.mine = me - p.owner;
   }
-  const bool any = a <= z;
-  // the range ends before the tile, or goes to the tile's edge
-  if (me + 1 < c.n && c.at(me + 1) < lo && c.at(me + 1) < X + kLead + nb) return false;
-  p.pieces = any ? z - a + 2 : 1;
-  p.owner = any ? a - 1 : me;
-  p.mine = any && me >= a ? me - a + 1 : 0;
-  p.blk0 = any && me >= a ? (int)(c.at(me) - X - kLead) : 0;
-  p.last = any && me + 1 >= a && me + 1 <= z;
-  p.blk1 = p.last ? (int)(c.at(me + 1) - X - kLead) : nb;
   return true;
 }
 
