@@ -44,8 +44,13 @@ namespace paged {
 
 using cache::Ring;
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;  // three warpgroups
+// Registers per thread: at launch 168 (65536 for 384 threads); softmax takes what the other
+// warps give: 256 * 208 + 128 * 80 <= 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 constexpr int kMaxCtas = cache::kMaxCtas;
+// Keys of a block whose weights are handed on while the others are still made.
+constexpr int kEarly = 64;
 // Most rows whose pieces are joined by columns instead of by rows.
 constexpr int kFewRows = 32;
 
@@ -194,7 +199,7 @@ __device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i
   g.cut = cut_of(total * c.L * c.Hkv, ctas);
   if (total == 0 || me >= g.cut.n) return 0;
   g.from = g.cut.at(me);
-  g.lh = (int)(g.from / total);
+  g.lh = (int)quot(g.from, total);
   i64 y = g.from - g.lh * total;
   const int owner = __syncthreads_count(upto <= y);  // the thread that has the request
   if (tid == owner) {
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing for this range (of a pair: for both)
     if (work < 0 && tid == 0 && A.status) *A.status = LBX_ETREE;
   } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- the walk, and copies of K and V ----
     const Cut cut = g.cut;
     int lh = g.lh, b = g.b, t = g.t, s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
@@ -457,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         (void)ptx::mbar_wait(&full[i % Y::kStages], (uint32_t)((i / Y::kStages) & 1));
     }
   } else if (warp == 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- queries, by tensor copies (tokens past the last row read as zeros) ----
     Seg s;
     uint32_t k = 0;
@@ -482,7 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) misc[1] = 1;
     // no copy is left behind
     if (lane == 0 && k > 0) (void)ptx::mbar_wait(here, (k - 1) & 1);
+  } else if (warp == 11) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- products: the warp waits as one, one lane issues ----
     Ring<Y::kStages> ring;
     uint32_t qs[2] = {0, 0};  // blocks so far, of each subtile (of a pair: in [0])
@@ -611,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < live; ++e) {
               if (!wait_all(&p_bar[e], qs[e] & 1)) break;
               ptx::tc_fence_after();
-              values(e, e, ring.st, 0, 4, i > 0);
+              values(e, e, ring.st, 0, kEarly / 16, i > 0);
               if (!wait_all(&p2_bar[e], qs[e] & 1)) break;
               ptx::tc_fence_after();
-              values(e, e, ring.st, 4, 8, 1u);
+              values(e, e, ring.st, kEarly / 16, 8, 1u);
               if (e == live - 1) done(&empty[ring.st]);
               if (next) {
                 if (e == 0 && !arrived(ahead)) break;
@@ -639,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ----
     const int quad = warp & 3, hf = warp >> 2;  // hf: the subtile, or a pair's half of the row
     const int sub = PAIR ? rank : hf;           // subtile of the tile
@@ -767,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e] = pack2<F16>(p0, p1);
           }
           ptx::tmem_st16(sc + (PAIR ? hf * 32 : 0) + e0 / 2, pk);
-          if (!PAIR && e0 == 32) {  // half of the weights: their product may begin
+          if (!PAIR && e0 == 32 * (kEarly / 32 - 1)) {  // most of the weights: their product may begin
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             tell(&p_bar[ch]);

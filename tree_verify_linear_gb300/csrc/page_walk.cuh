@@ -24,6 +24,13 @@ constexpr int kMinRange = 4;  // entries of the list per CTA, at least
 
 typedef long long i64;
 
+// a / b of numbers that are not negative; in 32 bits where they fit (a 64-bit division
+// takes hundreds of cycles).
+__host__ __device__ inline i64 quot(i64 a, i64 b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct Shape {
   int W;       // tokens per tile
   int period;  // tiles after which (position mod kBlk) repeats; a power of two
@@ -44,7 +51,7 @@ __host__ __device__ inline int tiles_of(const Shape &s, int n) { return (n + s.W
 // Blocks of tile t of a request of ctx cached and n new tokens.
 __host__ __device__ inline int blocks_of(const Shape &s, int ctx, int n, int t) {
   const i64 end = s.tree || (i64)(t + 1) * s.W >= n ? (i64)ctx + n : (i64)ctx + (i64)(t + 1) * s.W;
-  return (int)((end + kBlk - 1) / kBlk);
+  return (int)((end + kBlk - 1) >> 7);
 }
 
 // Entries of the list of a request's first k tiles, none of them its last (unless k is
@@ -77,14 +84,14 @@ __host__ __device__ inline i64 entries_of(const Shape &s, int ctx, int n) {
 struct Cut {
   i64 total;
   int n;
-  __host__ __device__ i64 at(int c) const { return (i64)c * total / n; }
+  __host__ __device__ i64 at(int c) const { return quot((i64)c * total, n); }
   // the first boundary at or past x, and the last one at or before it
-  __host__ __device__ int first(i64 x) const { return (int)((x * n + total - 1) / total); }
-  __host__ __device__ int last(i64 x) const { return (int)(((x + 1) * n + total - 1) / total) - 1; }
+  __host__ __device__ int first(i64 x) const { return (int)quot(x * n + total - 1, total); }
+  __host__ __device__ int last(i64 x) const { return (int)quot((x + 1) * n + total - 1, total) - 1; }
 };
 
 __host__ __device__ inline Cut cut_of(i64 total, int ctas) {
-  const i64 n = total / kMinRange;
+  const i64 n = quot(total, kMinRange);
   return {total, n < 1 ? 1 : n < ctas ? (int)n : ctas};
 }
 
