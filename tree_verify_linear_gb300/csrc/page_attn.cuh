@@ -154,29 +154,17 @@ __device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   i64 *warps = scratch + 4;
   const int per = c.Bq <= kThreads ? 1 : (c.Bq + kThreads - 1) / kThreads;
-  const i64 room = (i64)c.max_pages * c.page;
   int bad = 0;
   i64 sum = 0;
   if (A.parent) {  // the trees, a row per thread
     const int rows = A.start[c.Bq];
-#pragma unroll 1
-    for (int r = tid; r < rows && r < c.M; r += kThreads) {
-      const int p = A.parent[r];
-      int a = 0, z = c.Bq - 1;
-      while (a < z) {
-        const int h = (a + z + 1) >> 1;
-        if (A.start[h] <= r) a = h;
-        else z = h - 1;
-      }
-      const int i = r - A.start[a];
-      if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
-    }
+#pragma unroll 2
+    for (int r = tid; r < rows && r < c.M; r += kThreads) bad |= tree_bad(c, A.start, A.parent, r);
   }
 #pragma unroll 1
   for (int b = tid * per; b < (tid + 1) * per && b < c.Bq; ++b) {
     const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
-    if ((b == 0 && s != 0) || s < 0 || e < s || e > c.M || ctx < 0 || (i64)ctx + e - s > room ||
-        (A.parent && e - s > LBX_ATTN_MAX_NODES)) {
+    if (request_bad(c, b, s, e, ctx, A.parent != nullptr)) {
       bad = 1;
       break;
     }

@@ -26,7 +26,16 @@ __global__ void __launch_bounds__(kThreads) page_commit_kernel(const CommitArgs 
   const lbx_page_cfg &c = A.c;
   __shared__ int place[LBX_ATTN_MAX_NODES], from[LBX_ATTN_MAX_NODES], len;
   const int tid = threadIdx.x;
-  if (batch_bad(c, A.start, A.ctx_len, A.parent, A.accepted)) {
+  int bad = 0;
+  const int rows = A.start[c.Bq];
+#pragma unroll 4
+  for (int r = tid; r < rows && r < c.M; r += kThreads) bad |= tree_bad(c, A.start, A.parent, r);
+  for (int b = tid; b < c.Bq; b += kThreads) {
+    const int s = A.start[b], e = A.start[b + 1];
+    bad |= request_bad(c, b, s, e, A.ctx_len[b], true);
+    if (e > s) bad |= A.accepted[b] < 0 || A.accepted[b] >= e - s;
+  }
+  if (__syncthreads_or(bad)) {
     if (tid == 0 && A.status) *A.status = LBX_ETREE;
     return;
   }

@@ -54,34 +54,26 @@ inline bool all_apart(std::initializer_list<Span> outs, std::initializer_list<Sp
   return true;
 }
 
-// 1 in every thread of the block if the batch's rows, lengths, trees (may be NULL) or
-// accepted nodes (may be NULL) break the rules; the same verdict in every
-// block, so that a bad batch writes nothing at all.
-__device__ __forceinline__ int batch_bad(const lbx_page_cfg &c, const int32_t *start,
-                                         const int32_t *ctx_len, const int32_t *parent,
-                                         const int32_t *accepted) {
-  int bad = 0;
-  const long long room = (long long)c.max_pages * c.page;
-  for (int b = threadIdx.x; b < c.Bq; b += blockDim.x) {
-    const int s = start[b], e = start[b + 1], ctx = ctx_len[b];
-    if ((b == 0 && s != 0) || s < 0 || e < s || e > c.M || ctx < 0 ||
-        (long long)ctx + e - s > room) {
-      bad = 1;
-      continue;
-    }
-    if (accepted && e > s && (accepted[b] < 0 || accepted[b] >= e - s)) bad = 1;
-    if (parent) {
-      if (e - s > LBX_ATTN_MAX_NODES) {
-        bad = 1;
-        continue;
-      }
-      for (int i = 0; i < e - s; ++i) {
-        const int p = parent[s + i];
-        if (i == 0 ? p != -1 : (p < 0 || p >= i)) bad = 1;
-      }
-    }
+// Whether row r of the trees breaks their rules; start has been found to rise from 0 to
+// at most M, or the verdict does not matter.
+__device__ __forceinline__ int tree_bad(const lbx_page_cfg &c, const int32_t *start,
+                                        const int32_t *parent, int r) {
+  int a = 0, z = c.Bq - 1;  // the last request that starts at r or before
+  while (a < z) {
+    const int h = (a + z + 1) >> 1;
+    if (start[h] <= r) a = h;
+    else z = h - 1;
   }
-  return __syncthreads_or(bad);
+  const int p = parent[r], i = r - start[a];
+  return i == 0 ? p != -1 : (p < 0 || p >= i);
+}
+
+// Whether request b's rows and length break the rules.
+__device__ __forceinline__ int request_bad(const lbx_page_cfg &c, int b, int s, int e, int ctx,
+                                           bool tree) {
+  return (b == 0 && s != 0) || s < 0 || e < s || e > c.M || ctx < 0 ||
+         (long long)ctx + e - s > (long long)c.max_pages * c.page ||
+         (tree && e - s > LBX_ATTN_MAX_NODES);
 }
 
 }  // namespace paged
