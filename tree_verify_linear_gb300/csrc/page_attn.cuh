@@ -156,11 +156,7 @@ __device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i
   const int per = c.Bq <= kThreads ? 1 : (c.Bq + kThreads - 1) / kThreads;
   int bad = 0;
   i64 sum = 0;
-  if (A.parent) {  // the trees, a row per thread
-    const int rows = A.start[c.Bq];
-#pragma unroll 2
-    for (int r = tid; r < rows && r < c.M; r += kThreads) bad |= tree_bad(c, A.start, A.parent, r);
-  }
+  if (A.parent) bad = trees_bad(c, A.start, A.parent, warp, kThreads / 32);
 #pragma unroll 1
   for (int b = tid * per; b < (tid + 1) * per && b < c.Bq; ++b) {
     const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
@@ -222,27 +218,6 @@ __device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i
   return 1;
 }
 
-// Two fp32 at a time.
-__device__ __forceinline__ uint64_t both(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 apart2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // The largest of three (a NaN is passed over).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

@@ -26,10 +26,7 @@ __global__ void __launch_bounds__(kThreads) page_commit_kernel(const CommitArgs 
   const lbx_page_cfg &c = A.c;
   __shared__ int place[LBX_ATTN_MAX_NODES], from[LBX_ATTN_MAX_NODES], len;
   const int tid = threadIdx.x;
-  int bad = 0;
-  const int rows = A.start[c.Bq];
-#pragma unroll 4
-  for (int r = tid; r < rows && r < c.M; r += kThreads) bad |= tree_bad(c, A.start, A.parent, r);
+  int bad = trees_bad(c, A.start, A.parent, tid >> 5, kThreads / 32);
   for (int b = tid; b < c.Bq; b += kThreads) {
     const int s = A.start[b], e = A.start[b + 1];
     bad |= request_bad(c, b, s, e, A.ctx_len[b], true);
@@ -47,17 +44,40 @@ __global__ void __launch_bounds__(kThreads) page_commit_kernel(const CommitArgs 
     return;
   }
   if (tid < 32) {
-    uint64_t m = cache::warp_path(A.parent + s, n, A.accepted[b], tid);
+    // The path's nodes as bits, by doubling: after step k a lane has its two nodes' nearest
+    // 2^k ancestors and the one behind them.
+    const int acc = A.accepted[b];
+    int up[2] = {tid < n ? A.parent[s + tid] : -1, tid + 32 < n ? A.parent[s + tid + 32] : -1};
+    uint64_t anc[2] = {1ull << tid, 1ull << (tid + 32)};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      uint64_t add[2];
+      int to[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], up[e] & 31);
+        const uint64_t a1 = __shfl_sync(0xffffffffu, anc[1], up[e] & 31);
+        const int u0 = __shfl_sync(0xffffffffu, up[0], up[e] & 31);
+        const int u1 = __shfl_sync(0xffffffffu, up[1], up[e] & 31);
+        add[e] = up[e] < 0 ? 0ull : up[e] < 32 ? a0 : a1;
+        to[e] = up[e] < 0 ? -1 : up[e] < 32 ? u0 : u1;
+      }
+      anc[0] |= add[0], anc[1] |= add[1], up[0] = to[0], up[1] = to[1];
+    }
+    const uint64_t m0 = __shfl_sync(0xffffffffu, anc[0], acc & 31);
+    const uint64_t m1 = __shfl_sync(0xffffffffu, anc[1], acc & 31);
+    const uint64_t m = acc < 32 ? m0 : m1;
     const int count = __popcll(m);
     int outside = 0;
-    for (int i = 0; m; ++i, m &= m - 1) {
-      if ((i & 31) != tid) continue;
-      const int node = __ffsll((long long)m) - 1;
-      auto slot = [&](int p) {
-        const int id = A.table[(size_t)b * c.max_pages + (p >> A.shift)];
-        if (id < 0 || id >= c.n_pages) outside = 1;
-        return outside ? 0 : id * c.page + (p & (c.page - 1));
-      };
+    auto slot = [&](int p) {
+      const int id = A.table[(size_t)b * c.max_pages + (p >> A.shift)];
+      if (id < 0 || id >= c.n_pages) outside = 1;
+      return outside ? 0 : id * c.page + (p & (c.page - 1));
+    };
+#pragma unroll
+    for (int node = tid; node < LBX_ATTN_MAX_NODES; node += 32) {
+      if (!(m >> node & 1)) continue;
+      const int i = __popcll(m & ((1ull << node) - 1));
       place[i] = slot(ctx + i), from[i] = slot(ctx + node);
     }
     outside = __any_sync(0xffffffffu, outside);

@@ -54,18 +54,23 @@ inline bool all_apart(std::initializer_list<Span> outs, std::initializer_list<Sp
   return true;
 }
 
-// Whether row r of the trees breaks their rules; start has been found to rise from 0 to
-// at most M, or the verdict does not matter.
-__device__ __forceinline__ int tree_bad(const lbx_page_cfg &c, const int32_t *start,
-                                        const int32_t *parent, int r) {
-  int a = 0, z = c.Bq - 1;  // the last request that starts at r or before
-  while (a < z) {
-    const int h = (a + z + 1) >> 1;
-    if (start[h] <= r) a = h;
-    else z = h - 1;
+// Whether a tree breaks the rules, for warp w of n: requests by warps, nodes by lanes.
+// (start has been found to rise from 0 to at most M, or the verdict does not matter.)
+__device__ __forceinline__ int trees_bad(const lbx_page_cfg &c, const int32_t *start,
+                                         const int32_t *parent, int w, int n) {
+  int bad = 0;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int b = w; b < c.Bq; b += n) {
+    const int s = start[b], e = start[b + 1];
+#pragma unroll
+    for (int i = lane; i < LBX_ATTN_MAX_NODES; i += 32) {
+      if (s < 0 || i >= e - s || e > c.M) continue;
+      const int p = parent[s + i];
+      bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
+    }
   }
-  const int p = parent[r], i = r - start[a];
-  return i == 0 ? p != -1 : (p < 0 || p >= i);
+  return bad;
 }
 
 // Whether request b's rows and length break the rules.
@@ -74,6 +79,33 @@ __device__ __forceinline__ int request_bad(const lbx_page_cfg &c, int b, int s, 
   return (b == 0 && s != 0) || s < 0 || e < s || e > c.M || ctx < 0 ||
          (long long)ctx + e - s > (long long)c.max_pages * c.page ||
          (tree && e - s > LBX_ATTN_MAX_NODES);
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 apart2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 }  // namespace paged

@@ -11,6 +11,12 @@
 // Then the heads, a lane for two 16-byte pieces of one: with pairs in halves those that
 // turn with each other (where rot is a multiple of 16; else they meet in shared
 // memory), so that all arithmetic but the sum of squares stays in the lane.
+//
+// What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of
+// few warps.  8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in
+// halves: 56 us, 4.7 TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent
+// pairs, three axes: 76 us, 5.2 TB/s.  (A lane per 16 bytes and all pairs through
+// shared memory: 92 and 107 us; four CTAs per SM: 81 and 105 us, registers spilled.)
 #include "cache_walk.cuh"
 #include "page_common.cuh"
 
@@ -20,12 +26,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRows = 8;  // rows of a CTA
+constexpr int kMaxRows = 16;  // rows of a CTA
 
 struct RopeArgs {
   lbx_page_cfg c;
   lbx_rope_cfg r;
-  int half, rows, share, parts, passes;  // rows per CTA, warps per row, CTAs per row, passes of heads
+  int half, rows, parts, passes;  // rows per CTA, CTAs that share a row, passes of heads
   const uint4 *qkv;
   const float *qw, *kw, *freq;
   const int32_t *pos, *slot;
@@ -45,29 +51,31 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
          (uint64_t)__double2ll_rn(rest * 18446744073709551616.0);
 }
 
+// Eight values of a 16-byte piece, two at a time.
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &u, uint64_t *x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (F16) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+      x[i] = both(f.x, f.y);
     } else {
-      x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      x[i] = both(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
 }
 template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const uint64_t *x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const float2 f = apart2(x[i]);
     if constexpr (F16) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      const __half2 h = __floats2half2_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t *>(&h);
     } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
   }
@@ -75,7 +83,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 template <int DH, bool F16, int PAIRS>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs A) {
   constexpr int kLanes = DH / 16, kHeads = 32 / kLanes, kPieces = DH / 8;
   __shared__ float2 turn[kMaxRows][DH / 2];
   __shared__ float stage[PAIRS == kAnywhere ? kWarps : 1][512];
@@ -87,34 +95,36 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A) {
   const int m0 = group * A.rows, rows = c.M - m0 < A.rows ? c.M - m0 : A.rows;
   const int heads = c.Hq + 2 * c.Hkv;
   const uint4 *qkv = A.qkv + (size_t)l * c.M * heads * kPieces;
-  // the lane's two pieces of a head, and whether they turn
+  // the lane's two pieces of a head (neighbouring lanes' lie side by side), and whether
+  // they turn
   const int e = lane % kLanes, turning = A.half / 8;
   const bool turns = PAIRS != kInLane || e < turning;
-  const int p0 = PAIRS != kInLane ? 2 * e : e < turning ? e : 2 * e;
-  const int p1 = PAIRS != kInLane ? 2 * e + 1 : e < turning ? e + turning : 2 * e + 1;
+  const int p0 = PAIRS == kInLane && e >= turning ? turning + e : e;
+  const int p1 = PAIRS == kInLane && e < turning ? turning + e : kLanes + e;
 
-  // The warp's rows r0, r0 + by, .. and passes u0, u0 + step, .. of each.
-  const int r0 = warp / A.share, by = kWarps / A.share;
-  const int u0 = part * A.share + warp % A.share, step = A.parts * A.share;
-  auto load = [&](int r, int u, uint4 (&to)[2]) {
-    const int h = u * kHeads + lane / kLanes;
-    to[0] = to[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= rows || u >= A.passes || h >= heads) return;
-    const uint4 *from = qkv + ((size_t)(m0 + r) * heads + h) * kPieces;
-    to[0] = __ldcs(from + p0), to[1] = __ldcs(from + p1);
+  // The warp's share of the CTA's (row, pass) units, in order: a .. z - 1.
+  const int all = rows * A.passes, warps = A.parts * kWarps, gw = part * kWarps + warp;
+  const int a = (int)((long long)all * gw / warps), z = (int)((long long)all * (gw + 1) / warps);
+  // This lane's head in pass u is head0 + u * kHeads.
+  const int head0 = lane / kLanes;
+  uint4 next[2];  // the next unit
+  int left = z - a, lr = a / A.passes, lu = a % A.passes;  // the one to load
+  const uint4 *in = qkv + (size_t)(m0 + lr) * heads * kPieces + head0 * kPieces;
+  auto ahead = [&](uint4 (&to)[2]) {
+    if (--left < 0) return;
+    const int off = lu * (kHeads * kPieces);
+    if (head0 + lu * kHeads < heads) to[0] = __ldcs(in + off + p0), to[1] = __ldcs(in + off + p1);
+    if (++lu == A.passes) lu = 0, in += heads * kPieces;
   };
-  uint4 next[2];
-  load(r0, u0, next);
-  float qw[16];  // the lane's weights of queries
-  auto weights = [&](const float *w, float (&to)[16]) {
+  ahead(next);
+  auto weights = [&](const float *w, uint64_t (&to)[8]) {
     const float4 *from = reinterpret_cast<const float4 *>(w + (size_t)l * DH);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 f = __ldg(from + (i < 2 ? 2 * p0 : 2 * p1 - 2) + i);
-      to[4 * i] = f.x, to[4 * i + 1] = f.y, to[4 * i + 2] = f.z, to[4 * i + 3] = f.w;
+      to[2 * i] = both(f.x, f.y), to[2 * i + 1] = both(f.z, f.w);
     }
   };
-  if (A.qw) weights(A.qw, qw);
 
   if (tid < rows) {
     int s = A.slot[m0 + tid];
@@ -143,90 +153,112 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs A) {
   }
   __syncthreads();
 
+  // A row's cosines and sines: of pairs in the lane in twos, of adjacent ones (cos, cos)
+  // and (-sin, sin) per pair.
+  uint64_t cos2[PAIRS == kAdjacent ? 8 : 4], sin2[PAIRS == kAdjacent ? 8 : 4];
+  int slot = -1, r = a / A.passes, u = a % A.passes - 1;
+  bool fresh = true;  // the unit begins a row, or the share
+  uint4 *q_row = nullptr;
+  size_t kv_row = 0;
 #pragma unroll 1
-  for (int r = r0; r < rows; r += by) {
-    const int slot = slots[r], m = m0 + r;
-    float2 cs[8];
-    if (PAIRS != kAnywhere && turns) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        cs[i] = 8 * e + i < A.half ? turn[r][8 * e + i] : make_float2(1.f, 0.f);
-    }
-#pragma unroll 1
-    for (int u = u0; u < A.passes; u += step) {
-      const uint4 raw[2] = {next[0], next[1]};
-      if (u + step < A.passes) load(r, u + step, next);
-      else load(r + by, u0, next);
-      if (slot < 0) continue;  // the whole warp
-      const int h = u * kHeads + lane / kLanes;
-      const bool is_q = h < c.Hq, is_v = h >= c.Hq + c.Hkv;
-      uint4 out[2] = {raw[0], raw[1]};
-      if (__any_sync(0xffffffffu, !is_v)) {
-        float x[16], ss = 0.f;
-        unpack8<F16>(raw[0], *reinterpret_cast<float(*)[8]>(x));
-        unpack8<F16>(raw[1], *reinterpret_cast<float(*)[8]>(x + 8));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int d = 1; d < kLanes; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        const float inv = rsqrtf(fmaf(ss, 1.f / DH, A.r.eps));
-        if (is_q ? A.qw != nullptr : A.kw != nullptr && !is_v) {
-          if (is_q) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= inv * qw[i];
-          } else {
-            float w[16];
-            weights(A.kw, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= inv * w[i];
-          }
-        }
+  for (int unit = a; unit < z; ++unit) {
+    if (++u == A.passes) u = 0, ++r, fresh = true;
+    if (fresh) {
+      fresh = false;
+      slot = slots[r];
+      q_row = A.q + ((size_t)l * c.M + m0 + r) * c.Hq * kPieces;
+      kv_row = ((size_t)l * c.n_pages * c.page + (slot < 0 ? 0 : slot)) * c.Hkv * kPieces;
+      if (turns) {
+        auto of = [&](int i) { return i < A.half ? turn[r][i] : make_float2(1.f, 0.f); };
         if constexpr (PAIRS == kInLane) {
-          if (turns) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = x[i], b = x[8 + i];
-              x[i] = a * cs[i].x - b * cs[i].y, x[8 + i] = b * cs[i].x + a * cs[i].y;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = of(8 * e + 2 * i), g = of(8 * e + 2 * i + 1);
+            cos2[i] = both(f.x, g.x), sin2[i] = both(f.y, g.y);
           }
         } else if constexpr (PAIRS == kAdjacent) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * cs[i].x - b * cs[i].y, x[2 * i + 1] = b * cs[i].x + a * cs[i].y;
+            const float2 f = of(i < 4 ? 4 * p0 + i : 4 * p1 + i - 4);
+            cos2[i] = both(f.x, f.x), sin2[i] = both(-f.y, f.y);
           }
-        } else {
-          float *mine = stage[warp] + lane / kLanes * DH;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4 *>(mine + 16 * e)[i] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = 16 * e + i;
-            if (j >= 2 * A.half) break;
-            const bool second = j >= A.half;
-            const float2 t = turn[r][second ? j - A.half : j];
-            const float other = mine[second ? j - A.half : j + A.half];
-            x[i] = fmaf(x[i], t.x, second ? other * t.y : -other * t.y);
-          }
-          __syncwarp();
-        }
-        if (!is_v) {
-          out[0] = pack8<F16>(*reinterpret_cast<float(*)[8]>(x));
-          out[1] = pack8<F16>(*reinterpret_cast<float(*)[8]>(x + 8));
         }
       }
-      if (h >= heads) continue;
-      uint4 *to;
-      if (is_q)
-        to = A.q + (((size_t)l * c.M + m) * c.Hq + h) * kPieces;
-      else
-        to = (is_v ? A.v : A.k) + (((size_t)l * c.n_pages * c.page + slot) * c.Hkv +
-                                   (is_v ? h - c.Hq - c.Hkv : h - c.Hq)) * kPieces;
-      to[p0] = out[0], to[p1] = out[1];
     }
+    const uint4 raw[2] = {next[0], next[1]};
+    ahead(next);
+    if (slot < 0) continue;  // the whole warp
+    const int h = u * kHeads + head0;
+    const bool is_q = h < c.Hq, is_v = h >= c.Hq + c.Hkv;
+    uint4 out[2] = {raw[0], raw[1]};
+    if (__any_sync(0xffffffffu, !is_v)) {
+      uint64_t x[8], s2 = 0;
+      unpack8<F16>(raw[0], x);
+      unpack8<F16>(raw[1], x + 4);
+      const bool norm = is_q ? A.qw != nullptr : A.kw != nullptr && !is_v;
+      if (__any_sync(0xffffffffu, norm)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s2 = fma2(x[i], x[i], s2);
+        const float2 f = apart2(s2);
+        float ss = f.x + f.y;
+#pragma unroll
+        for (int d = 1; d < kLanes; d *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        const float inv = rsqrtf(fmaf(ss, 1.f / DH, A.r.eps));
+        const uint64_t inv2 = both(inv, inv);
+        if (norm) {
+          uint64_t w[8];
+          weights(is_q ? A.qw : A.kw, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(inv2, w[i]));
+        }
+      }
+      if constexpr (PAIRS == kInLane) {
+        if (turns) {
+          const uint64_t minus = both(-1.f, -1.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t p = x[i], q = x[4 + i];
+            x[i] = fma2(mul2(q, minus), sin2[i], mul2(p, cos2[i]));
+            x[4 + i] = fma2(p, sin2[i], mul2(q, cos2[i]));
+          }
+        }
+      } else if constexpr (PAIRS == kAdjacent) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = apart2(x[i]);
+          x[i] = fma2(both(f.y, f.x), sin2[i], mul2(x[i], cos2[i]));
+        }
+      } else {
+        float *mine = stage[warp] + head0 * DH;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = apart2(x[2 * i]), g = apart2(x[2 * i + 1]);
+          reinterpret_cast<float4 *>(mine)[(i < 2 ? 2 * p0 : 2 * p1 - 2) + i] =
+              make_float4(f.x, f.y, g.x, g.y);
+        }
+        __syncwarp();
+        auto turned = [&](int j, float y) {  // dimension j
+          if (j >= 2 * A.half) return y;
+          const bool second = j >= A.half;
+          const float2 t = turn[r][second ? j - A.half : j];
+          const float other = mine[second ? j - A.half : j + A.half];
+          return fmaf(y, t.x, second ? other * t.y : -other * t.y);
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = i < 4 ? 8 * p0 + 2 * i : 8 * p1 + 2 * i - 8;
+          const float2 f = apart2(x[i]);
+          x[i] = both(turned(j, f.x), turned(j + 1, f.y));
+        }
+        __syncwarp();
+      }
+      if (!is_v) out[0] = pack8<F16>(x), out[1] = pack8<F16>(x + 4);
+    }
+    if (h >= heads) continue;
+    uint4 *to = is_q   ? q_row + h * kPieces
+                : is_v ? A.v + kv_row + (h - c.Hq - c.Hkv) * kPieces
+                       : A.k + kv_row + (h - c.Hq) * kPieces;
+    to[p0] = out[0], to[p1] = out[1];
   }
 }
 
@@ -272,17 +304,22 @@ extern "C" int lbx_qk_norm_rope(const lbx_page_cfg *c, const lbx_rope_cfg *rope,
       (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
   const int heads = c->Hq + 2 * c->Hkv, at_once = 512 / c->dh;
-  RopeArgs A = {*c, *rope, rope->rot / 2, 1, kWarps, 1, (heads + at_once - 1) / at_once,
+  RopeArgs A = {*c, *rope, rope->rot / 2, 1, 1, (heads + at_once - 1) / at_once,
                 reinterpret_cast<const uint4 *>(qkv), q_weight, k_weight, inv_freq, pos, slot,
                 reinterpret_cast<uint4 *>(q_out), reinterpret_cast<uint4 *>(k_pages),
                 reinterpret_cast<uint4 *>(v_pages), d_status};
   const int nsm = lbx::cache::grid_limit();
   if (nsm < 1) return LBX_ECUDA;
-  // Few rows: a CTA per row and eight warps' heads, so that the call is one trip to
-  // memory.  Many: several rows share a CTA's fractions of a turn, a warp per row in the end.
-  const long long lm = (long long)c->L * c->M;
-  while (A.rows < kMaxRows && lm / (2 * A.rows) >= 4LL * nsm) A.rows *= 2, A.share /= 2;
-  if (A.rows == 1 && lm < 4LL * nsm) A.parts = (A.passes + kWarps - 1) / kWarps;
+  // Few rows: CTAs of eight warps' heads each, so that the call is one trip to memory.
+  // Many: as many rows per CTA as fill whole rounds of the three CTAs that an SM holds.
+  const long long lm = (long long)c->L * c->M, slots = 3LL * nsm;
+  if (lm >= slots) {
+    const long long rounds = (lm + slots * kMaxRows - 1) / (slots * kMaxRows);
+    A.rows = (int)((lm + slots * rounds - 1) / (slots * rounds));
+  } else {
+    const int most = (A.passes + kWarps - 1) / kWarps;
+    while (A.parts < most && lm * (A.parts + 1) <= slots) ++A.parts;
+  }
   const long long grid = (long long)c->L * ((c->M + A.rows - 1) / A.rows) * A.parts;
   if (grid > 0x7fffffffLL) return LBX_EINVAL;
   const unsigned n = (unsigned)grid;
