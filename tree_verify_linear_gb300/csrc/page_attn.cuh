@@ -144,78 +144,87 @@ struct Begin {
   int lh, b, t;
 };
 
-// Finds range `me` of the list for one of `ctas` CTAs (or pairs): sums over the requests,
-// consecutive ones per thread, then the request and the tile by counting. 1: there is
-// work for this range, 0: there is none, -1: the batch breaks the rules (in every
-// thread alike, and in every block).  `scratch`: shared memory.
-__device__ __forceinline__ int find_begin(const PageArgs &A, int me, int ctas, i64 *scratch,
-                                          Begin &g) {
+// Requests of a warp's share of the sums, a multiple of the lanes.
+__device__ __forceinline__ int share_of(int Bq) {
+  return (Bq + kThreads - 1) / kThreads * 32;
+}
+
+// Checks the batch and adds up the list's entries of the warp's share of the requests; the
+// same verdict in every thread and every block (after a barrier of the block).
+__device__ __forceinline__ int check_batch(const PageArgs &A, i64 *warps) {
   const lbx_page_cfg &c = A.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  i64 *warps = scratch + 4;
-  const int per = c.Bq <= kThreads ? 1 : (c.Bq + kThreads - 1) / kThreads;
-  int bad = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = share_of(c.Bq);
+  int bad = A.parent ? trees_bad(c, A.start, A.parent, warp, kThreads / 32) : 0;
   i64 sum = 0;
-  if (A.parent) bad = trees_bad(c, A.start, A.parent, warp, kThreads / 32);
 #pragma unroll 1
-  for (int b = tid * per; b < (tid + 1) * per && b < c.Bq; ++b) {
+  for (int b = warp * share + lane; b < (warp + 1) * share && b < c.Bq; b += 32) {
     const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
-    if (request_bad(c, b, s, e, ctx, A.parent != nullptr)) {
-      bad = 1;
-      break;
-    }
-    sum += entries_of(A.shape, ctx, e - s);
+    if (request_bad(c, b, s, e, ctx, A.parent != nullptr)) bad = 1;
+    else sum += entries_of(A.shape, ctx, e - s);
   }
-  i64 upto = sum;
+  if (warp * share < c.Bq) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  }
+  if (lane == 0) warps[warp] = sum;
+  return __syncthreads_or(bad);
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ i64 scan32(i64 v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const i64 o = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += o;
+    const i64 o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
   }
-  if (lane == 31) warps[warp] = upto;
-  if (__syncthreads_or(bad)) return -1;
-  i64 total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) upto += warps[w];
-    total += warps[w];
-  }
+  return v;
+}
+
+// Finds range `me` of the list for one of `ctas` CTAs (or pairs), by one warp: the warp
+// whose share it begins in, the request, the tile. False if there is nothing for it.
+__device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, const i64 *warps,
+                                           Begin &g) {
+  const lbx_page_cfg &c = A.c;
+  const int lane = threadIdx.x & 31, share = share_of(c.Bq);
+  i64 upto = scan32(lane < kThreads / 32 ? warps[lane] : 0);
+  const i64 total = __shfl_sync(0xffffffffu, upto, 31);
   g.cut = cut_of(total * c.L * c.Hkv, ctas);
-  if (total == 0 || me >= g.cut.n) return 0;
+  if (total == 0 || me >= g.cut.n) return false;
   g.from = g.cut.at(me);
   g.lh = (int)quot(g.from, total);
   i64 y = g.from - g.lh * total;
-  const int owner = __syncthreads_count(upto <= y);  // the thread that has the request
-  if (tid == owner) {
-    y -= upto - sum;
-    int b = tid * per;
-    if (per > 1)
-      for (;; ++b) {
-        const i64 e = entries_of(A.shape, A.ctx_len[b], A.start[b + 1] - A.start[b]);
-        if (y < e) break;
-        y -= e;
-      }
-    scratch[0] = y, scratch[1] = b;
+  const int w = __popc(__ballot_sync(0xffffffffu, upto <= y));
+  if (w > 0) y -= __shfl_sync(0xffffffffu, upto, w - 1);
+  int n = 0, ctx = 0;
+#pragma unroll 1
+  for (int b0 = w * share;; b0 += 32) {
+    const int b = b0 + lane;
+    ctx = b < c.Bq ? A.ctx_len[b] : 0, n = b < c.Bq ? A.start[b + 1] - A.start[b] : 0;
+    upto = scan32(entries_of(A.shape, ctx, n));
+    const int k = __popc(__ballot_sync(0xffffffffu, upto <= y));
+    if (k < 32) {
+      if (k > 0) y -= __shfl_sync(0xffffffffu, upto, k - 1);
+      g.b = b0 + k;
+      ctx = __shfl_sync(0xffffffffu, ctx, k), n = __shfl_sync(0xffffffffu, n, k);
+      break;
+    }
+    y -= __shfl_sync(0xffffffffu, upto, 31);
   }
-  __syncthreads();
-  y = scratch[0], g.b = (int)scratch[1];
-  const int ctx = A.ctx_len[g.b], n = A.start[g.b + 1] - A.start[g.b];
   g.t = 0;
   i64 before = 0;
 #pragma unroll 1
   for (int size = tiles_of(A.shape, n); size > 1;) {  // the last tile that begins at y or before
-    const int step = (size + kThreads - 1) / kThreads;
-    const bool in = (i64)tid * step < size;
-    const i64 e = in ? entries_upto(A.shape, ctx, n, g.t + tid * step) : 0;
-    const int k = __syncthreads_count(in && e <= y) - 1;
-    if (tid == k) scratch[2] = e;
-    __syncthreads();
-    before = scratch[2];
+    const int step = (size + 31) / 32;
+    const bool in = (i64)lane * step < size;
+    const i64 e = in ? entries_upto(A.shape, ctx, n, g.t + lane * step) : 0;
+    const int k = __popc(__ballot_sync(0xffffffffu, in && e <= y)) - 1;
+    before = __shfl_sync(0xffffffffu, e, k);
     g.t += k * step;
     size = size - k * step < step ? size - k * step : step;
   }
   g.X = g.from - (y - before);
-  return 1;
+  return true;
 }
 
 // The largest of three (a NaN is passed over).
@@ -267,10 +276,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::tc_fence_before();
   }
-  Begin g;
-  const int work = find_begin(A, me, ctas, reinterpret_cast<i64 *>(red), g);
-  __syncthreads();
-  if constexpr (PAIR) ptx::cluster_sync();  // the other CTA's barriers are set up
+  if (tid == 32) {
+    ptx::prefetch_map(&maps.q);
+    ptx::prefetch_map(&maps.k);
+    ptx::prefetch_map(&maps.v);
+  }
+  const bool wrong = check_batch(A, reinterpret_cast<i64 *>(red)) != 0;
+  if constexpr (PAIR) ptx::cluster_arrive();  // this CTA's barriers are set up
   ptx::tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
 
@@ -294,18 +306,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ok && s.have != 0;
   };
 
-  if (work <= 0) {
-    // nothing for this range (of a pair: for both)
-    if (work < 0 && tid == 0 && A.status) *A.status = LBX_ETREE;
+  // (the warps that reach the other CTA wait until its barriers are set up; the walking
+  // one does not, and waits at its end)
+  if constexpr (PAIR) {
+    if (wrong || warp != 9) ptx::cluster_wait();
+  }
+  if (wrong) {
+    if (tid == 0 && A.status) *A.status = LBX_ETREE;
   } else if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- the walk, and copies of K and V ----
+    Begin g;
+    bool more = find_begin(A, me, ctas, reinterpret_cast<const i64 *>(red), g);
     const Cut cut = g.cut;
-    int lh = g.lh, b = g.b, t = g.t, s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
+    int lh = g.lh, b = g.b, t = g.t, s0 = 0, n = 0, ctx = 0;
+    if (more) s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
     i64 X = g.X;
     const i64 to = cut.at(me + 1);
     const int n_lh = c.L * c.Hkv;
-    bool more = true;
     auto step = [&]() {  // to the next tile of the list
       X += kLead + blocks_of(A.shape, ctx, n, t);
       ++t;
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
       }
     };
-    {
+    if (more) {
       const i64 y = g.from - X;
       if (y >= kLead + kLeast && y > kLead + blocks_of(A.shape, ctx, n, t) - kLeast) step();
     }
@@ -416,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         k_at = k_next, v_at = v_next;
       }
     }
+    if constexpr (PAIR) ptx::cluster_wait();
     outside = __any_sync(0xffffffffu, outside);
     if (lane == 0 && outside) misc[2] = 1;
     if (bad) misc[1] = 1;

@@ -20,7 +20,7 @@ namespace paged {
 constexpr int kBlk = 128;   // keys per block (its logarithm, 7, stands in entries_upto)
 constexpr int kRows = 128;  // rows per subtile
 constexpr int kLead = 2, kLeast = 2;
-constexpr int kMinRange = 4;  // entries of the list per CTA, at least
+constexpr int kMinRange = 3;  // entries of the list per CTA, at least
 
 typedef long long i64;
 
