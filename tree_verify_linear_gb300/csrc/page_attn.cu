@@ -6,7 +6,13 @@ namespace lbx {
 namespace paged {
 namespace {
 
-constexpr size_t kCounterBytes = (2 * kMaxCtas * 4 + 255) & ~255;
+constexpr size_t kCounterBytes = (kFewUnits * kMaxCtas * 4 + 255) & ~255;
+static_assert(kFewUnits >= 2, "counters of two subtiles per CTA, or of the lists of few rows");
+// the units' partials of few rows lie where those of tiles do
+template <int DH>
+constexpr bool kFewFits =
+    (size_t)kFewUnits * kMaxCtas * kFewPart<DH> <= (DH == 256 ? 2 : 4) * kMaxCtas * part_floats(DH);
+static_assert(kFewFits<64> && kFewFits<128> && kFewFits<256>, "partials");
 
 bool encode_pool(CUtensorMap *map, const void *base, const lbx_page_cfg *c, int box) {
   const uint64_t row = (uint64_t)c->Hkv * c->dh * 2;
@@ -52,7 +58,7 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   A.shape = shape_of(A.G, parent != nullptr);
   A.scale_log2 = c->scale * 1.4426950408889634f;
   A.start = start, A.ctx_len = ctx_len, A.table = block_table, A.parent = parent;
-  A.o = o, A.lse = lse, A.status = d_status;
+  A.q = q, A.k = k_pages, A.v = v_pages, A.o = o, A.lse = lse, A.status = d_status;
   A.counters = static_cast<unsigned int *>(workspace);
   A.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kCounterBytes);
 

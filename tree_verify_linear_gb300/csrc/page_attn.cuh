@@ -37,6 +37,7 @@
 
 #include "cache_ptx.cuh"
 #include "cache_walk.cuh"
+#include "page_few.cuh"
 #include "page_walk.cuh"
 
 namespace lbx {
@@ -44,7 +45,6 @@ namespace paged {
 
 using cache::Ring;
 
-constexpr int kThreads = 384;  // three warpgroups
 // Registers per thread: at launch 168 (65536 for 384 threads); softmax takes what the other
 // warps give: 256 * 208 + 128 * 80 <= 384 * 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -60,18 +60,6 @@ __host__ __device__ constexpr size_t part_floats(int dh) { return 2 * kRows + (s
 struct PageMaps {
   CUtensorMap q;     // (dh, Hq, M, L), boxes of 64 columns of whole tokens' heads
   CUtensorMap k, v;  // (dh, Hkv, positions of all layers' pools), boxes of 64 columns
-};
-
-struct PageArgs {
-  lbx_page_cfg c;
-  int G, tp, box, shift;  // heads per group, tokens per subtile, positions per box
-  Shape shape;
-  float scale_log2;
-  const int32_t *start, *ctx_len, *table, *parent;
-  uint16_t *o;
-  float *lse, *part;
-  unsigned int *counters;  // per CTA and subtile: pieces of the tile that begins its cut there
-  int32_t *status;
 };
 
 // A CTA's share of a tile, as the walking warp publishes it.
@@ -112,17 +100,6 @@ struct Lay {
 template <bool F16>
 constexpr float kLift = F16 ? 7.f : 0.f;
 
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-}
-
 // Whether p holds in any of the threads that share a named barrier.
 __device__ __forceinline__ bool any_of(uint32_t id, uint32_t nthreads, bool p) {
   uint32_t r;
@@ -149,29 +126,43 @@ __device__ __forceinline__ int share_of(int Bq) {
   return (Bq + kThreads - 1) / kThreads * 32;
 }
 
-// Checks the batch and adds up the list's entries of the warp's share of the requests; the
-// same verdict in every thread and every block (after a barrier of the block).
-__device__ __forceinline__ int check_batch(const PageArgs &A, i64 *warps) {
+// Checks the batch and adds up the list's entries of the warp's share of the requests, and
+// the units of few rows (`units`: of all requests); the same verdict in every thread
+// and every block (after a barrier of the block).
+__device__ __forceinline__ int check_batch(const PageArgs &A, i64 *warps, int &units) {
   const lbx_page_cfg &c = A.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = share_of(c.Bq);
+  int *few = reinterpret_cast<int *>(warps + kThreads / 32);
   int bad = A.parent ? trees_bad(c, A.start, A.parent, warp, kThreads / 32) : 0;
   i64 sum = 0;
+  int own = 0;
 #pragma unroll 1
   for (int b = warp * share + lane; b < (warp + 1) * share && b < c.Bq; b += 32) {
     const int s = A.start[b], e = A.start[b + 1], ctx = A.ctx_len[b];
-    if (request_bad(c, b, s, e, ctx, A.parent != nullptr)) bad = 1;
-    else sum += entries_of(A.shape, ctx, e - s);
+    if (request_bad(c, b, s, e, ctx, A.parent != nullptr)) {
+      bad = 1;
+    } else {
+      sum += entries_of(A.shape, ctx, e - s);
+      own = min(own + min(few_units(A, ctx, e - s), 1 << 20), 1 << 20);
+    }
   }
   if (warp * share < c.Bq) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    for (int d = 16; d; d >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      own = min(own + __shfl_xor_sync(0xffffffffu, own, d), 1 << 20);
+    }
   }
-  if (lane == 0) warps[warp] = sum;
-  return __syncthreads_or(bad);
+  if (lane == 0) warps[warp] = sum, few[warp] = own;
+  const int verdict = __syncthreads_or(bad);
+  units = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) units = min(units + few[w], 1 << 20);
+  return verdict;
 }
 
 // Inclusive sums over the lanes.
-__device__ __forceinline__ i64 scan32(i64 v) {
+__device__ __forceinline__ i64 scan32_wide(i64 v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -187,7 +178,7 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
                                            Begin &g) {
   const lbx_page_cfg &c = A.c;
   const int lane = threadIdx.x & 31, share = share_of(c.Bq);
-  i64 upto = scan32(lane < kThreads / 32 ? warps[lane] : 0);
+  i64 upto = scan32_wide(lane < kThreads / 32 ? warps[lane] : 0);
   const i64 total = __shfl_sync(0xffffffffu, upto, 31);
   g.cut = cut_of(total * c.L * c.Hkv, ctas);
   if (total == 0 || me >= g.cut.n) return false;
@@ -201,7 +192,7 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
   for (int b0 = w * share;; b0 += 32) {
     const int b = b0 + lane;
     ctx = b < c.Bq ? A.ctx_len[b] : 0, n = b < c.Bq ? A.start[b + 1] - A.start[b] : 0;
-    upto = scan32(entries_of(A.shape, ctx, n));
+    upto = scan32_wide(entries_of(A.shape, ctx, n));
     const int k = __popc(__ballot_sync(0xffffffffu, upto <= y));
     if (k < 32) {
       if (k > 0) y -= __shfl_sync(0xffffffffu, upto, k - 1);
@@ -256,6 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int me = blockIdx.x / Y::kCtas, ctas = gridDim.x / Y::kCtas;
+  int units = 0;
+  if (check_batch(A, reinterpret_cast<i64 *>(red), units)) {
+    if (tid == 0 && A.status) *A.status = LBX_ETREE;
+    return;
+  }
+  if ((i64)units * c.L * c.Hkv <= (i64)kFewUnits * gridDim.x) {  // every CTA alike
+    if (!few_rows<DH, F16>(A, units, smem) && A.status) *A.status = LBX_EINVAL;
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < Y::kNBars; ++i)
       ptx::mbar_init(full + i, full + i >= p_bar && full + i < p_bar + 4
@@ -265,6 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    : 1);
     ptx::fence_mbar_init();
     misc[1] = misc[2] = 0;
+  }
+  if (tid == 32) {
+    ptx::prefetch_map(&maps.q);
+    ptx::prefetch_map(&maps.k);
+    ptx::prefetch_map(&maps.v);
   }
   if (warp == 8) {
     uint32_t *base = reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc);
@@ -276,12 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::tc_fence_before();
   }
-  if (tid == 32) {
-    ptx::prefetch_map(&maps.q);
-    ptx::prefetch_map(&maps.k);
-    ptx::prefetch_map(&maps.v);
-  }
-  const bool wrong = check_batch(A, reinterpret_cast<i64 *>(red)) != 0;
+  __syncthreads();
   if constexpr (PAIR) ptx::cluster_arrive();  // this CTA's barriers are set up
   ptx::tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
@@ -309,11 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the warps that reach the other CTA wait until its barriers are set up; the walking
   // one does not, and waits at its end)
   if constexpr (PAIR) {
-    if (wrong || warp != 9) ptx::cluster_wait();
+    if (warp != 9) ptx::cluster_wait();
   }
-  if (wrong) {
-    if (tid == 0 && A.status) *A.status = LBX_ETREE;
-  } else if (warp == 9) {
+  if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- the walk, and copies of K and V ----
     Begin g;
@@ -820,12 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::named_sync(bar_id, Y::kGroup);
         if (gt == 0) {
-          __threadfence();  // the group's partial, before its arrival
           unsigned int *count = A.counters + 2 * s.owner + sub;
-          const bool last = atomicAdd(count, 1u) == (unsigned)s.pieces - 1;
+          const bool last = arrive_count(count) == (unsigned)s.pieces - 1;
           if (last) *count = 0u;  // for the next call
           misc[4 + sub] = last;
-          __threadfence();
         }
         ptx::named_sync(bar_id, Y::kGroup);
         join = misc[4 + sub] != 0;
@@ -835,14 +831,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *top_of = red + (PAIR ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
         if (gt < rows) {
           float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-          for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + gt));
+          auto each = [&](auto f) {  // m and l of the pieces, eight at a time
+#pragma unroll 1
+            for (int e0 = 0; e0 < s.pieces; e0 += 8) {
+              float m[8], l[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float *from = partial(e0 + e < s.pieces ? e0 + e : e0) + gt;
+                m[e] = __ldcg(from), l[e] = __ldcg(from + kRows);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e0 + e < s.pieces) f(m[e], l[e]);
+            }
+          };
+          each([&](float m, float) { top = fmaxf(top, m); });
           if (top == -INFINITY) top = 0.f;
-#pragma unroll 8
-          for (int e = 0; e < s.pieces; ++e) {
-            const float *f = partial(e) + gt;
-            sum = fmaf(ptx::ex2(__ldcg(f) - top), __ldcg(f + kRows), sum);
-          }
+          each([&](float m, float l) { sum = fmaf(ptx::ex2(m - top), l, sum); });
           top_of[gt] = top, inv_of[gt] = sum == 0.f ? 0.f : 1.f / sum;
           finish(gt, top, sum);
         }
@@ -852,14 +857,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rw = idx % rows, c4 = idx / rows;
           const float top = top_of[rw], inv = inv_of[rw];
           float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int e = 0; e < s.pieces; ++e) {
-            const float *from = partial(e);
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) +
-                                    (size_t)c4 * kRows + rw);
-            const float w = ptx::ex2(__ldcg(from + rw) - top);
-            f.x = fmaf(w, y.x, f.x), f.y = fmaf(w, y.y, f.y);
-            f.z = fmaf(w, y.z, f.z), f.w = fmaf(w, y.w, f.w);
+#pragma unroll 1
+          for (int e0 = 0; e0 < s.pieces; e0 += 8) {  // eight loads in flight
+            float4 y[8];
+            float m[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float *from = partial(e0 + e < s.pieces ? e0 + e : e0);
+              y[e] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) + (size_t)c4 * kRows + rw);
+              m[e] = __ldcg(from + rw);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float w = e0 + e < s.pieces ? ptx::ex2(m[e] - top) : 0.f;
+              f.x = fmaf(w, y[e].x, f.x), f.y = fmaf(w, y[e].y, f.y);
+              f.z = fmaf(w, y[e].z, f.z), f.w = fmaf(w, y[e].w, f.w);
+            }
           }
           const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
           reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = inv == 0.f ? make_uint2(0u, 0u) : u;
