@@ -172,10 +172,23 @@ __device__ __forceinline__ i64 scan32_wide(i64 v) {
   return v;
 }
 
+// Rows and lengths of 32 requests from b0 on, one per lane: a warp that walks the list reads
+// them once (a load takes thousands of cycles while other CTAs' copies are in flight).
+struct Window {
+  int b0, row0, n, ctx;
+  __device__ __forceinline__ void load(const PageArgs &A, int from) {
+    const int b = from + (threadIdx.x & 31);
+    b0 = from;
+    row0 = b < A.c.Bq ? A.start[b] : 0;
+    n = b < A.c.Bq ? A.start[b + 1] - row0 : 0;
+    ctx = b < A.c.Bq ? A.ctx_len[b] : 0;
+  }
+};
+
 // Finds range `me` of the list for one of `ctas` CTAs (or pairs), by one warp: the warp
 // whose share it begins in, the request, the tile. False if there is nothing for it.
 __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, const i64 *warps,
-                                           Begin &g) {
+                                           Window &win, Begin &g) {
   const lbx_page_cfg &c = A.c;
   const int lane = threadIdx.x & 31, share = share_of(c.Bq);
   i64 upto = scan32_wide(lane < kThreads / 32 ? warps[lane] : 0);
@@ -187,21 +200,20 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
   i64 y = g.from - g.lh * total;
   const int w = __popc(__ballot_sync(0xffffffffu, upto <= y));
   if (w > 0) y -= __shfl_sync(0xffffffffu, upto, w - 1);
-  int n = 0, ctx = 0;
 #pragma unroll 1
   for (int b0 = w * share;; b0 += 32) {
-    const int b = b0 + lane;
-    ctx = b < c.Bq ? A.ctx_len[b] : 0, n = b < c.Bq ? A.start[b + 1] - A.start[b] : 0;
-    upto = scan32_wide(entries_of(A.shape, ctx, n));
+    if (b0 != win.b0) win.load(A, b0);
+    upto = scan32_wide(entries_of(A.shape, win.ctx, win.n));
     const int k = __popc(__ballot_sync(0xffffffffu, upto <= y));
     if (k < 32) {
       if (k > 0) y -= __shfl_sync(0xffffffffu, upto, k - 1);
       g.b = b0 + k;
-      ctx = __shfl_sync(0xffffffffu, ctx, k), n = __shfl_sync(0xffffffffu, n, k);
       break;
     }
     y -= __shfl_sync(0xffffffffu, upto, 31);
   }
+  const int ctx = __shfl_sync(0xffffffffu, win.ctx, g.b - win.b0);
+  const int n = __shfl_sync(0xffffffffu, win.n, g.b - win.b0);
   g.t = 0;
   i64 before = 0;
 #pragma unroll 1
@@ -248,6 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int me = blockIdx.x / Y::kCtas, ctas = gridDim.x / Y::kCtas;
   int units = 0;
+  Window win = {};
+  if (warp == 9) win.load(A, 0);
   if (check_batch(A, reinterpret_cast<i64 *>(red), units)) {
     if (tid == 0 && A.status) *A.status = LBX_ETREE;
     return;
@@ -315,10 +329,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---- the walk, and copies of K and V ----
     Begin g;
-    bool more = find_begin(A, me, ctas, reinterpret_cast<const i64 *>(red), g);
+    bool more = find_begin(A, me, ctas, reinterpret_cast<const i64 *>(red), win, g);
     const Cut cut = g.cut;
     int lh = g.lh, b = g.b, t = g.t, s0 = 0, n = 0, ctx = 0;
-    if (more) s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
+    auto request = [&]() {
+      if (b < win.b0 || b >= win.b0 + 32) win.load(A, b & ~31);
+      s0 = __shfl_sync(0xffffffffu, win.row0, b & 31);
+      n = __shfl_sync(0xffffffffu, win.n, b & 31);
+      ctx = __shfl_sync(0xffffffffu, win.ctx, b & 31);
+    };
+    if (more) request();
     i64 X = g.X;
     const i64 to = cut.at(me + 1);
     const int n_lh = c.L * c.Hkv;
@@ -332,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           b = 0;
           if (++lh == n_lh) return;
         }
-        s0 = A.start[b], n = A.start[b + 1] - s0, ctx = A.ctx_len[b];
+        request();
       }
     };
     if (more) {
