@@ -6,6 +6,7 @@ namespace lbx {
 namespace paged {
 namespace {
 
+constexpr long long kWideRows = 768;
 constexpr size_t kCounterBytes = (kFewUnits * kMaxCtas * 4 + 255) & ~255;
 static_assert(kFewUnits >= 2, "counters of two subtiles per CTA, or of the lists of few rows");
 // the units' partials of few rows lie where those of tiles do
@@ -30,7 +31,7 @@ bool encode_pool(CUtensorMap *map, const void *base, const lbx_page_cfg *c, int 
 extern "C" size_t lbx_paged_workspace_size(const lbx_page_cfg *c) {
   using namespace lbx::paged;
   if (!cfg_ok(c) || c->Hq / c->Hkv > LBX_PAGED_MAX_GROUP) return 0;
-  // per CTA a tile's first piece and another one, two subtiles each (of a pair one per CTA)
+  // per CTA a tile's first piece and another one, of each of its subtiles
   const size_t parts = c->dh == 256 ? 2 * kMaxCtas : 4 * kMaxCtas;
   return kCounterBytes + parts * part_floats(c->dh) * 4;
 }
@@ -55,7 +56,16 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   A.c = *c;
   A.G = c->Hq / c->Hkv, A.tp = kRows / A.G, A.box = c->page < 64 ? c->page : 64;
   while (1 << A.shift < c->page) ++A.shift;
-  A.shape = shape_of(A.G, parent != nullptr);
+  // Head dimension 128: a pair of CTAs shares products of 256 rows of both of its subtiles,
+  // which halves what shared memory has to deliver (prompts of 501 to 6001 tokens, 32/8
+  // heads: 520 us against 556 us on single CTAs); requests of few rows leave the second
+  // subtile empty and are better off with more and smaller tiles (16 requests of one token
+  // over 8001 to 16384 keys: 487 us against 845 us).  The lengths are on the device: M and
+  // Bq decide, by the rows of a request on average.  16 requests over 3000 keys, 32/8 heads,
+  // pairs against single CTAs: 192 tokens (768 rows) 154 against 135 us, 256 tokens 169
+  // against 177 us, 512 tokens 329 against 358 us.
+  const bool wide = c->dh == 128 && (long long)c->M * A.G > kWideRows * (long long)c->Bq;
+  A.shape = shape_of(A.G, wide ? 4 : 2, parent != nullptr);
   A.scale_log2 = c->scale * 1.4426950408889634f;
   A.start = start, A.ctx_len = ctx_len, A.table = block_table, A.parent = parent;
   A.q = q, A.k = k_pages, A.v = v_pages, A.o = o, A.lse = lse, A.status = d_status;
@@ -74,8 +84,9 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   if (nsm < 2) return LBX_ECUDA;
   const int grid = nsm / 2 * 2;
   const bool f16 = c->dtype == LBX_F16;
-  const cudaError_t e = c->dh == 64    ? launch_page_attn<64>(f16, maps, A, grid, stream)
-                        : c->dh == 128 ? launch_page_attn<128>(f16, maps, A, grid, stream)
-                                       : launch_page_attn<256>(f16, maps, A, grid, stream);
+  const cudaError_t e = c->dh == 64    ? launch_page_attn<64, false>(f16, maps, A, grid, stream)
+                        : c->dh == 256 ? launch_page_attn<256, false>(f16, maps, A, grid, stream)
+                        : wide         ? launch_page_attn<128, true>(f16, maps, A, grid, stream)
+                                       : launch_page_attn<128, false>(f16, maps, A, grid, stream);
   return e == cudaSuccess ? LBX_OK : LBX_ECUDA;
 }

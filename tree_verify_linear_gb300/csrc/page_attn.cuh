@@ -71,14 +71,17 @@ struct Seg {
   int pieces, mine, owner;
 };
 
-template <int DH>
+template <int DH, bool WIDE>
 struct Lay {
-  static constexpr bool kPair = DH == 256;
-  static constexpr int kCtas = kPair ? 2 : 1, kSubs = kPair ? 1 : 2;
+  // a pair of CTAs per tile; one subtile per CTA, with two buffers of S and two threads per
+  // row, or two subtiles
+  static constexpr bool kOne = DH == 256, kPair = kOne || WIDE;
+  static_assert(!WIDE || DH == 128, "half of V's columns fills a swizzled row of 64");
+  static constexpr int kCtas = kPair ? 2 : 1, kSubs = kOne ? 1 : 2;
   static constexpr int kKeys = kBlk / kCtas, kCols = DH / kCtas;  // of a block, per CTA
-  static constexpr int kMine = kPair ? 64 : 128;                  // keys per softmax thread
-  static constexpr int kGroup = kPair ? 256 : 128;                // threads of a subtile
-  static constexpr int kOut = kPair ? DH / 2 : DH;                // O's columns per thread
+  static constexpr int kMine = kOne ? 64 : 128;                   // keys per softmax thread
+  static constexpr int kGroup = kOne ? 256 : 128;                 // threads of a subtile
+  static constexpr int kOut = kOne ? DH / 2 : DH;                 // O's columns per thread
   static constexpr int kStage = kKeys * DH * 2;
   static_assert(kStage == kBlk * kCols * 2, "K and V take the same place");
   static constexpr int kQSub = kRows * DH * 2, kQBytes = kSubs * kQSub;
@@ -237,11 +240,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-template <int DH, bool F16>
+template <int DH, bool F16, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     page_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ PageArgs A) {
-  using Y = Lay<DH>;
-  constexpr bool PAIR = Y::kPair;
+  using Y = Lay<DH, WIDE>;
+  constexpr bool PAIR = Y::kPair, ONE = Y::kOne;
   extern __shared__ __align__(1024) unsigned char page_smem[];
   unsigned char *smem = page_smem;
   const lbx_page_cfg &c = A.c;
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.have = nb > 0 && piece_of(cut, me, g.from, to, X, nb, p);
       if (!s.have) return;
       s.l = lh / c.Hkv, s.h = lh - s.l * c.Hkv, s.b = b, s.row0 = s0, s.n = n, s.ctx = ctx;
-      s.tok0 = t * A.shape.W, s.subs = n - s.tok0 > A.tp ? 2 : 1;
+      s.tok0 = t * A.shape.W, s.subs = n - s.tok0 > Y::kCtas * A.tp ? 2 : 1;
       s.blk0 = p.blk0, s.nb = p.blk1 - p.blk0;
       s.pieces = p.pieces, s.mine = p.mine, s.owner = p.owner;
       if (p.last) more = false;
@@ -442,12 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t k_at = k_row(s.blk0), v_at = v_row(s.blk0);
 #pragma unroll 1
       for (int i = 0; i < nb; ++i) {
-        // K of block i; V of block i goes before K of block i + 1 where one CTA has both
-        // subtiles, behind it in a pair, as the products take them
+        // K of block i; V of block i goes before K of block i + 1 where a CTA has two
+        // subtiles, else behind it, as the products take them
         const int ahead = s.blk0 + (i + 1 < nb ? i + 1 : i);
         const uint32_t k_next = k_row(ahead), v_next = v_row(ahead);
-        if (!PAIR || i == 0) load_k(k_at);
-        if (PAIR && i + 1 < nb) load_k(k_next);
+        if (!ONE || i == 0) load_k(k_at);
+        if (ONE && i + 1 < nb) load_k(k_next);
         load_v(v_at);
         k_at = k_next, v_at = v_next;
       }
@@ -472,14 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; next_seg(k, s); ++k) {
       if (k > 0) wait(q_free, (k - 1) & 1);  // the last segment's score products are done
       if (lane == 0 && !bad) {
-        const int live = PAIR ? 1 : s.subs;
+        const int live = ONE ? 1 : s.subs;
         ptx::mbar_arrive_expect_tx(here, (uint32_t)(live * A.tp * A.G * DH * 2));
 #pragma unroll 1
         for (int e = 0; e < live; ++e)
 #pragma unroll 1
           for (int a = 0; a < DH / 64; ++a)
             ptx::tma_load_4d(smem + e * Y::kQSub + a * kRows * 128, &maps.q, a * 64, s.h * A.G,
-                             s.row0 + s.tok0 + (PAIR ? rank : e) * A.tp, s.l, here);
+                             s.row0 + s.tok0 + (e * Y::kCtas + rank) * A.tp, s.l, here);
         if constexpr (PAIR) {
           if (wait(qh_bar, k & 1)) ptx::mbar_arrive_at(q_bar, 0);
         }
@@ -532,10 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; next_seg(k, s); ++k) {
 #pragma unroll 1
         for (int i = 0; i < 2 * s.nb; ++i, ring.step()) {
-          // K 0, K 1, V 0, K 2, V 1, .., V nb - 1
-          const bool is_v = i == 2 * s.nb - 1 || (i > 0 && i % 2 == 0);
+          // K 0, K 1, V 0, K 2, V 1, .., V nb - 1, or K 0, V 0, K 1, ..
+          const bool is_v = ONE ? i == 2 * s.nb - 1 || (i > 0 && i % 2 == 0) : i % 2 == 1;
           if (!wait_all(&full[ring.st], ring.ph)) break;
-          if (is_v) clear(s, s.blk0 + (i == 2 * s.nb - 1 ? s.nb - 1 : i / 2 - 1), ring.st);
+          if (is_v) clear(s, s.blk0 + (!ONE ? i / 2 : i == 2 * s.nb - 1 ? s.nb - 1 : i / 2 - 1), ring.st);
           if (lane == 0) ptx::mbar_arrive_at(&peer[ring.st], 0);
         }
       }
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (PAIR) ptx::mma_16_ts_pair(d, pa, vb, idesc_o, acc);
             else ptx::mma_bf16_ts(d, pa, vb, idesc_o, acc);
           }
-          if (i1 == kBlk / 16) commit(&o_bar[PAIR ? buf : e]);
+          if (i1 == kBlk / 16) commit(&o_bar[ONE ? buf : e]);
         }
         __syncwarp();
       };
@@ -587,16 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (; !bad && next_seg(k, s); ++k) {
         if (!wait_all(q_bar, k & 1) || !arrived(ring)) break;
-        const int live = PAIR ? 1 : s.subs;
+        const int live = ONE ? 1 : s.subs;
 #pragma unroll 1
-        for (int e = 0; e < live; ++e) scores(e, PAIR ? qs[0] & 1 : e, ring.st);
+        for (int e = 0; e < live; ++e) scores(e, ONE ? qs[0] & 1 : e, ring.st);
         done(&empty[ring.st]);
         if (s.nb == 1) done(q_free);
         ring.step();
 #pragma unroll 1
         for (int i = 0; i < s.nb; ++i) {
           const bool next = i + 1 < s.nb;
-          if constexpr (PAIR) {
+          if constexpr (ONE) {
             if (next) {
               if (!arrived(ring)) break;
               scores(0, (qs[0] + 1) & 1, ring.st);
@@ -652,11 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ----
     const int quad = warp & 3, hf = warp >> 2;  // hf: the subtile, or a pair's half of the row
-    const int sub = PAIR ? rank : hf;           // subtile of the tile
-    const int gt = PAIR ? tid : tid & 127;      // thread of the subtile's group
-    const uint32_t bar_id = PAIR ? 5 : 5 + hf;
+    const int sub = ONE ? rank : hf * Y::kCtas + rank;  // subtile of the tile
+    const int gt = ONE ? tid : tid & 127;      // thread of the subtile's group
+    const uint32_t bar_id = ONE ? 5 : 5 + hf;
     const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t to = tq + Y::kColO + (PAIR ? hf * Y::kOut : hf * DH);  // this thread's O
+    const uint32_t to = tq + Y::kColO + (ONE ? hf * Y::kOut : hf * DH);  // this thread's O
+    constexpr int kTileSubs = Y::kSubs * Y::kCtas;
     const int r = quad * 32 + lane;             // row of the subtile
     const float sl2 = A.scale_log2;
     auto tell = [&](uint64_t *bar) {
@@ -673,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (all of a group's threads go on, or none)
       const bool over = !next_seg(k, s);
       if (any_of(bar_id, Y::kGroup, over)) break;
-      if (!PAIR && sub >= s.subs) continue;
+      if (!ONE && hf >= s.subs) continue;
       const int left = s.n - s.tok0 - sub * A.tp;  // tokens from the subtile's first on
       const int rows = (left < A.tp ? left : A.tp) * A.G;
       const int tok = s.tok0 + sub * A.tp + r / A.G;
@@ -693,22 +697,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll 1
       for (int i = 0; i < s.nb; ++i, ++q) {
-        const int ch = PAIR ? (int)(q & 1) : hf;
-        const uint32_t ph = PAIR ? (q >> 1) & 1 : q & 1;
+        const int ch = ONE ? (int)(q & 1) : hf;
+        const uint32_t ph = ONE ? (q >> 1) & 1 : q & 1;
         wait(&s_bar[ch], ph);
         ptx::tc_fence_after();
         if (!busy) {  // no rows: keep step with the others
           tell(&p_bar[ch]);
-          if constexpr (!PAIR) tell(&p2_bar[ch]);
+          if constexpr (!ONE) tell(&p2_bar[ch]);
           continue;
         }
         const uint32_t sc = tq + ch * kBlk;
         float sv[Y::kMine];
 #pragma unroll
         for (int e = 0; e < Y::kMine; e += 32)
-          ptx::tmem_ld32(sc + (PAIR ? hf * 64 : 0) + e, *reinterpret_cast<float(*)[32]>(sv + e));
+          ptx::tmem_ld32(sc + (ONE ? hf * 64 : 0) + e, *reinterpret_cast<float(*)[32]>(sv + e));
         ptx::tmem_wait_ld();
-        const int k0 = (s.blk0 + i) * kBlk + (PAIR ? hf * 64 : 0);
+        const int k0 = (s.blk0 + i) * kBlk + (ONE ? hf * 64 : 0);
         if (!__all_sync(0xffffffffu, lim - k0 >= Y::kMine)) {
 #pragma unroll
           for (int w = 0; w < Y::kMine / 64; ++w) {
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], sv[e], sv[e + 1]);
           mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         }
-        if constexpr (PAIR) {
+        if constexpr (ONE) {
           // (two buffers: the other half may not have read the last block's yet)
           float *max_of = red + (q & 1) * 2 * kRows;
           max_of[hf * kRows + r] = mb;
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = m_run == -INFINITY ? 0.f : fmaf(m_run, sl2, -kLift<F16>);
         // rows whose reference moved rescale O, once the previous product is done
         if (__any_sync(0xffffffffu, need)) {
-          if constexpr (PAIR) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
+          if constexpr (ONE) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
           else wait(&o_bar[hf], (q - 1) & 1);
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -777,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[e & 3] = add2(sum[e & 3], both(p0, p1));
             pk[e] = pack2<F16>(p0, p1);
           }
-          ptx::tmem_st16(sc + (PAIR ? hf * 32 : 0) + e0 / 2, pk);
-          if (!PAIR && e0 == 32 * (kEarly / 32 - 1)) {  // most of the weights: their product may begin
+          ptx::tmem_st16(sc + (ONE ? hf * 32 : 0) + e0 / 2, pk);
+          if (!ONE && e0 == 32 * (kEarly / 32 - 1)) {  // most of the weights: their product may begin
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             tell(&p_bar[ch]);
@@ -786,17 +790,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        tell(PAIR ? &p_bar[ch] : &p2_bar[ch]);
+        tell(ONE ? &p_bar[ch] : &p2_bar[ch]);
         const float2 s2 = apart2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         l_run += s2.x + s2.y;
       }
 
       // ---- the segment's result: whole, or a partial ----
-      if constexpr (PAIR) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
+      if constexpr (ONE) wait(&o_bar[(q - 1) & 1], ((q - 1) >> 1) & 1);
       else wait(&o_bar[hf], (q - 1) & 1);
       ptx::tc_fence_after();
       float l_sum = l_run;
-      if constexpr (PAIR) {
+      if constexpr (ONE) {
         ptx::named_sync(1 + quad, 64);  // the last maxima are read
         red[hf * kRows + r] = l_run;
         ptx::named_sync(1 + quad, 64);
@@ -816,9 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Piece e > 0 lies at its range's first place, the first piece at its second.
       auto partial = [&](int e) {
         const int at = 2 * (s.owner + e) + (e == 0 ? 1 : 0);
-        return A.part + (size_t)(2 * at + sub) * part_floats(DH);
+        return A.part + (size_t)(kTileSubs * at + sub) * part_floats(DH);
       };
-      constexpr int kCol0 = PAIR ? Y::kOut : 0;  // this thread's first column: hf times this
+      constexpr int kCol0 = ONE ? Y::kOut : 0;  // this thread's first column: hf times this
       bool join = false;
       if (s.pieces > 1 && rows > 0) {
         float *mine = partial(s.mine);
@@ -834,11 +838,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 8; ++e)
               at[e * kRows] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
           }
-          if (real && (!PAIR || hf == 0)) mine[r] = m2, mine[kRows + r] = l_sum;
+          if (real && (!ONE || hf == 0)) mine[r] = m2, mine[kRows + r] = l_sum;
         }
         ptx::named_sync(bar_id, Y::kGroup);
         if (gt == 0) {
-          unsigned int *count = A.counters + 2 * s.owner + sub;
+          unsigned int *count = A.counters + kTileSubs * s.owner + sub;
           const bool last = arrive_count(count) == (unsigned)s.pieces - 1;
           if (last) *count = 0u;  // for the next call
           misc[4 + sub] = last;
@@ -848,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (join && valid && rows <= kFewRows) {
         // each row's largest reference and sum, then four columns of a row per thread
-        float *top_of = red + (PAIR ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
+        float *top_of = red + (ONE ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
         if (gt < rows) {
           float top = -INFINITY, sum = 0.f;
           auto each = [&](auto f) {  // m and l of the pieces, eight at a time
@@ -911,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = fmaf(ptx::ex2(__ldcg(partial(e) + r) - top), __ldcg(partial(e) + kRows + r), sum);
         }
         const float w = sum == 0.f ? 0.f : 1.f / sum;
-        if (real && (!PAIR || hf == 0)) finish(r, top, sum);
+        if (real && (!ONE || hf == 0)) finish(r, top, sum);
         const float w_own = join ? ptx::ex2(m2 - top) * w : w;
         // where the four rows of this lane's group of lanes go
         uint64_t rows_at[4];
@@ -1001,14 +1005,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Launches of one head dimension (instances in page_attn_*.cu).
-template <int DH>
+template <int DH, bool WIDE>
 cudaError_t launch_page_attn(bool f16, const PageMaps &maps, const PageArgs &A, int grid,
                              cudaStream_t stream);
-template <int DH, bool F16>
+template <int DH, bool F16, bool WIDE>
 cudaError_t launch_page_attn_of(const PageMaps &maps, const PageArgs &A, int grid,
                                 cudaStream_t stream) {
-  auto kernel = page_attn_kernel<DH, F16>;
-  constexpr int bytes = Lay<DH>::kSmemTotal;
+  auto kernel = page_attn_kernel<DH, F16, WIDE>;
+  constexpr int bytes = Lay<DH, WIDE>::kSmemTotal;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1016,7 +1020,7 @@ cudaError_t launch_page_attn_of(const PageMaps &maps, const PageArgs &A, int gri
   cfg.dynamicSmemBytes = bytes, cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = Lay<DH>::kCtas, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = Lay<DH, WIDE>::kCtas, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps, A);
 }

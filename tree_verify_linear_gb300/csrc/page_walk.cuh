@@ -2,7 +2,7 @@
 // query rows, blocks of keys, one list of the blocks of all tiles cut into equal
 // ranges, one per CTA (or pair).
 //
-// A tile is two subtiles of whole tokens, as many as fit 128 rows of G heads each.
+// A tile is two or four subtiles of whole tokens, as many as fit 128 rows of G heads each.
 // Its keys are the positions up to its last token's (all of a tree's), in blocks of
 // 128; a chunk's tiles are as much longer as they stand later.  The list runs over
 // (layer, KV head), request, tile, block; every tile begins with kLead blocks that
@@ -37,9 +37,9 @@ struct Shape {
   int tree;
 };
 
-__host__ __device__ inline Shape shape_of(int G, bool tree) {
+__host__ __device__ inline Shape shape_of(int G, int subtiles, bool tree) {
   Shape s;
-  s.W = 2 * (kRows / G);
+  s.W = subtiles * (kRows / G);
   const int low = s.W & -s.W;  // gcd with kBlk, a power of two
   s.period = low >= kBlk ? 1 : kBlk / low;
   s.tree = tree;
