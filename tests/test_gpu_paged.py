@@ -573,3 +573,157 @@ def serve(steps=3, graph=False):
 
 def test_a_server_of_prompts_and_trees():
     serve(steps=6)
+
+
+def test_the_example_serves():
+    """Pages add up, paths are accepted, and the last round's attention is the definition's."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import paged_cache
+    s, out = paged_cache.main(["--rounds", "4", "--chunk", "70"])
+    ctx, held = s.ctx.tolist(), s.held.tolist()
+    assert int(s.n_free) + sum(held) == paged_cache.N_PAGES
+    assert all(c >= p + 4 for c, p in zip(ctx, paged_cache.PROMPTS)) and sum(ctx) > sum(paged_cache.PROMPTS) + 12
+    inp = {k: out[k].cpu() for k in ("start", "ctx_len", "block_table", "parent", "q", "k_pages", "v_pages")}
+    ref, ref_lse, tol, lse_tol = R.attention(inp)
+    live = int(inp["start"][-1])
+    assert (np.abs(out["o"].cpu().double().numpy() - ref)[:, :live] <= tol[:, :live]).all()
+    assert (np.abs(out["lse"].cpu().double().numpy() - ref_lse)[:, :live] <= lse_tol[:, :live]).all()
+
+
+@pytest.mark.parametrize("kind", ["decode", "chunk", "tree"])
+def test_a_step_in_a_graph(kind):
+    """All four calls captured once and replayed with other lengths, tokens and trees in the
+    same arrays: each replay is what the calls give then."""
+    B, page, Hq, Hkv, dh, L, M, width, n_pages = 3, 16, 8, 2, 128, 2, 150, 40, 130
+    cfg = lbx.make_page_cfg(L, B, M, Hq, Hkv, dh, page, n_pages, width)
+    rc, g = lbx.make_rope_cfg([24]), torch.Generator().manual_seed(4)
+    a = {k: i32(np.zeros(n)) for k, n in (("ctx_len", B), ("new_len", B), ("held", B), ("n_free", 1),
+                                          ("held_out", B), ("n_free_out", 1), ("start", B + 1), ("slot", M),
+                                          ("pos", M), ("accepted", B), ("ctx_out", B), ("parent", M))}
+    a["block_table"], a["free_list"] = i32(np.zeros((B, width))), i32(np.arange(n_pages))
+    a["inv_freq"] = (1e4 ** (-torch.arange(24).double() / 24)).float().cuda()
+    a["qkv"] = torch.zeros(L, M, Hq + 2 * Hkv, dh, dtype=torch.bfloat16, device="cuda")
+    for k, shape in (("k_pages", (L, n_pages, page, Hkv, dh)), ("v_pages", (L, n_pages, page, Hkv, dh)),
+                     ("q", (L, M, Hq, dh)), ("o", (L, M, Hq, dh))):
+        a[k] = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    a["lse"], status, ws = torch.zeros(L, M, Hq, device="cuda"), status_word(), lbx.new_paged_workspace(cfg)
+
+    def calls():
+        lbx.lbx_page_tables(cfg, a["ctx_len"], a["new_len"], a["held"], a["n_free"], a["block_table"],
+                            a["free_list"], a["held_out"], a["n_free_out"], a["start"], a["slot"], a["pos"],
+                            d_status=status)
+        lbx.lbx_qk_norm_rope(cfg, rc, a["qkv"], a["inv_freq"], a["pos"].view(1, M), a["slot"], a["q"],
+                             a["k_pages"], a["v_pages"], d_status=status)
+        lbx.lbx_paged_attention(cfg, a["start"], a["ctx_len"], a["block_table"], a["q"], a["k_pages"],
+                                a["v_pages"], a["o"], ws, parent=a["parent"] if kind == "tree" else None,
+                                lse=a["lse"], d_status=status)
+        if kind == "tree":
+            lbx.lbx_page_commit(cfg, a["start"], a["ctx_len"], a["block_table"], a["parent"], a["accepted"],
+                                a["k_pages"], a["v_pages"], a["ctx_out"], d_status=status)
+
+    def fill(seed):
+        rng = np.random.default_rng(seed)
+        ctx = rng.integers(0, 400, B)
+        new = np.ones(B, int) if kind == "decode" else rng.integers(1, 40 if kind == "tree" else 50, B)
+        a["ctx_len"].copy_(i32(ctx)), a["new_len"].copy_(i32(new)), a["held"].zero_()
+        a["n_free"].fill_(n_pages), a["free_list"].copy_(i32(rng.permutation(n_pages)))
+        a["qkv"].copy_((torch.randn(a["qkv"].shape, generator=g) * 2).to(torch.bfloat16))
+        for k in ("k_pages", "v_pages"):
+            a[k].copy_(torch.randn(a[k].shape, generator=g).to(torch.bfloat16))
+        trees = [p for n in new for p in R.tree(rng, int(n))]
+        a["parent"][:len(trees)] = i32(trees)
+        a["accepted"].copy_(i32(new - 1))
+
+    side = torch.cuda.Stream()
+    fill(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    outs = ("held_out", "n_free_out", "start", "slot", "pos", "block_table", "free_list", "q", "k_pages",
+            "v_pages", "o", "lse", "ctx_out")
+    for seed in (1, 2, 3):
+        fill(seed)
+        start = {k: v.clone() for k, v in a.items()}
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: a[k].clone() for k in outs}
+        for k, v in start.items():
+            a[k].copy_(v)
+        calls()
+        torch.cuda.synchronize()
+        for k in outs:
+            assert torch.equal(got[k].view(torch.uint8) if got[k].is_floating_point() else got[k],
+                               a[k].view(torch.uint8) if got[k].is_floating_point() else a[k]), (seed, k)
+    assert int(status.item()) == 0
+
+
+def test_calls_side_by_side_and_on_one_workspace():
+    """Calls of all head dimensions and lengths take turns on one workspace, and run on two
+    streams with a workspace each: the bits are those of calls by themselves."""
+    cases = [R.make_attention([900, 30], [1, 1], 8, 2, 64, 16, seed=1),
+             R.make_attention([3000, 700, 5], [40, 300, 1], 8, 2, 128, 32, seed=2),
+             R.make_attention([2500], [22], 12, 2, 256, 64, kind="random", seed=3),
+             R.make_attention([0], [1500], 8, 1, 128, 64, dtype="f16", seed=4),
+             R.make_attention([5000, 1], [1, 1], 8, 2, 256, 16, seed=5)]
+    alone = [run_attention(c) for c in cases]
+    cfgs = [page_cfg(c) for c in cases]
+    size = max(lbx.lbx_paged_workspace_size(c) for c in cfgs)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    dev = [{k: None if v is None else v.cuda() for k, v in c.items()} for c in cases]
+    outs = [[(torch.zeros_like(d["q"]), torch.zeros(d["q"].shape[:-1], device="cuda")) for d in dev]
+            for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s in range(2):
+            for i in range(len(cases)) if s == 0 else reversed(range(len(cases))):
+                d, (o, lse) = dev[i], outs[s][i]
+                lbx.lbx_paged_attention(cfgs[i], d["start"], d["ctx_len"], d["block_table"], d["q"],
+                                        d["k_pages"], d["v_pages"], o, spaces[s], parent=d["parent"], lse=lse,
+                                        stream=streams[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for (o, lse), (ref_o, ref_lse, _) in zip(outs[s], alone):
+            assert torch.equal(o.cpu(), ref_o)
+            assert torch.equal(lse.cpu(), ref_lse)
+
+
+@pytest.mark.parametrize("dh,dtype", [(64, "bf16"), (128, "f16"), (256, "bf16")])
+def test_single_tokens_with_scores_of_minus_infinity_and_nan(dh, dtype):
+    """As above for the few rows of a decode step, over one unit of keys and over many."""
+    inp = R.make_attention([20, 1000, 300, 900], [1, 1, 1, 1], 4, 2, dh, 16, dtype=dtype, seed=6)
+    clean, clean_lse, _ = run_attention(inp)
+    q, k = inp["q"], inp["k_pages"]
+    q[:, [0, 3]] = q[:, [0, 3]].abs() + 0.5
+    for b, n in ((0, 21), (3, 901)):
+        for p in range(n):
+            k[:, inp["block_table"][b, p // 16], p % 16] = -torch.inf
+    q[0, 1, 2, 5] = torch.nan
+    o, lse, status = run_attention(inp)
+    assert status == 0
+    assert (o[:, [0, 3]] == 0).all() and (lse[:, [0, 3]] == -torch.inf).all()
+    assert o[0, 1, 2].isnan().all() and lse[0, 1, 2].isnan()
+    assert torch.equal(o[:, 2], clean[:, 2]) and torch.equal(lse[:, 2], clean_lse[:, 2])
+    assert torch.equal(o[0, 1, [0, 1, 3]], clean[0, 1, [0, 1, 3]])
+
+
+FEW = {
+    "unit_edges": dict(ctx=[126, 127, 128, 255, 256], new=[1] * 5, Hq=4, Hkv=2, dh=128, page=16),
+    "rows_8": dict(ctx=[500, 3], new=[2, 1], Hq=8, Hkv=2, dh=64, page=32, dtype="f16"),
+    "chunk_of_8": dict(ctx=[300, 0], new=[8, 5], Hq=3, Hkv=3, dh=256, page=64),
+    "tree_of_8": dict(ctx=[300, 0, 127], new=[8, 1, 6], Hq=3, Hkv=3, dh=128, page=16, kind="random"),
+    "tree_over_a_unit": dict(ctx=[125], new=[7], Hq=1, Hkv=1, dh=64, page=256, kind="star", dtype="f16"),
+    "many_units": dict(ctx=[9000], new=[1], Hq=6, Hkv=1, dh=256, page=64),
+    "rows_9_beside_1": dict(ctx=[40, 700], new=[9, 1], Hq=2, Hkv=2, dh=128, page=16),
+}
+
+
+@pytest.mark.parametrize("name", sorted(FEW))
+def test_few_rows(name):
+    check_attention(R.make_attention(**FEW[name], seed=900 + len(name)), calls=2)

@@ -5,6 +5,10 @@
 // the path moves to place i; its index m_i is at least i, and m_j > m_i >= i for
 // every later node, so that no move overwrites what a later one reads: each thread
 // takes its column of the path's rows in order, eight loads in flight.
+//
+// What bounds it: copies of scattered rows.  64 requests, paths of 40 nodes, 16 layers,
+// 8 heads of dimension 128: 59 us, 5.5 TB/s read and written (copies reach 6.79 TB/s); five
+// paths of 6 nodes, 16 layers, 4 heads of 256: 3.5 us in a captured graph, the trips to memory.
 #include "page_common.cuh"
 
 namespace lbx {

@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const TableArgs A
 
   int outside = 0;
 #pragma unroll 1
-  for (int r = blockIdx.x * kThreads + tid; r < A.M; r += gridDim.x * kThreads) {
+  for (uint32_t i = blockIdx.x * kThreads + tid; i < (uint32_t)A.M; i += gridDim.x * kThreads) {
+    const int r = (int)i;
     int slot = -1, p = -1;
     if (r < rows) {
       const int b = find(first, r);
