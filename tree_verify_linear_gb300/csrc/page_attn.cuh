@@ -175,19 +175,6 @@ __device__ __forceinline__ i64 scan32_wide(i64 v) {
   return v;
 }
 
-// Rows and lengths of 32 requests from b0 on, one per lane: a warp that walks the list reads
-// them once (a load takes thousands of cycles while other CTAs' copies are in flight).
-struct Window {
-  int b0, row0, n, ctx;
-  __device__ __forceinline__ void load(const PageArgs &A, int from) {
-    const int b = from + (threadIdx.x & 31);
-    b0 = from;
-    row0 = b < A.c.Bq ? A.start[b] : 0;
-    n = b < A.c.Bq ? A.start[b + 1] - row0 : 0;
-    ctx = b < A.c.Bq ? A.ctx_len[b] : 0;
-  }
-};
-
 // Finds range `me` of the list for one of `ctas` CTAs (or pairs), by one warp: the warp
 // whose share it begins in, the request, the tile. False if there is nothing for it.
 __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, const i64 *warps,
@@ -263,14 +250,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int me = blockIdx.x / Y::kCtas, ctas = gridDim.x / Y::kCtas;
   int units = 0;
-  Window win = {};
-  if (warp == 9) win.load(A, 0);
+  Window win;
+  win.load(A, 0);
   if (check_batch(A, reinterpret_cast<i64 *>(red), units)) {
     if (tid == 0 && A.status) *A.status = LBX_ETREE;
     return;
   }
   if ((i64)units * c.L * c.Hkv <= (i64)kFewUnits * gridDim.x) {  // every CTA alike
-    if (!few_rows<DH, F16>(A, units, smem) && A.status) *A.status = LBX_EINVAL;
+    if (!few_rows<DH, F16>(A, units, win, smem) && A.status) *A.status = LBX_EINVAL;
     return;
   }
   if (tid == 0) {

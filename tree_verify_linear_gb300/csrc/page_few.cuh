@@ -65,6 +65,19 @@ __device__ __forceinline__ int few_units(const PageArgs &A, int ctx, int n) {
   return n > 0 ? (ctx + n + kFewKeys - 1) / kFewKeys : 0;
 }
 
+// Rows and lengths of 32 requests from b0 on, one per lane: a warp that walks the list reads
+// them once (a load takes thousands of cycles while other CTAs' copies are in flight).
+struct Window {
+  int b0, row0, n, ctx;
+  __device__ __forceinline__ void load(const PageArgs &A, int from) {
+    const int b = from + (threadIdx.x & 31);
+    b0 = from;
+    row0 = b < A.c.Bq ? A.start[b] : 0;
+    n = b < A.c.Bq ? A.start[b + 1] - row0 : 0;
+    ctx = b < A.c.Bq ? A.ctx_len[b] : 0;
+  }
+};
+
 __device__ __forceinline__ int scan32(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -98,13 +111,15 @@ constexpr int kFewPart = kFewMost * DH + 2 * kFewMost;
 // All units of this CTA; `units`: of one (layer, KV head).  False where a page lies
 // outside the pool.
 template <int DH, bool F16>
-__device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned char *smem) {
+__device__ __forceinline__ bool few_rows(const PageArgs &A, int units, Window win,
+                                         unsigned char *smem) {
   constexpr int kWarps = kFewWarps;
   constexpr float kUp = F16 ? 7.f : 0.f;  // f16 weights are taken 2^7 times as large
   const lbx_page_cfg &c = A.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
+  constexpr int kPitch = DH + 4;                      // of a row, so that fewer share a bank
   float *sums = reinterpret_cast<float *>(smem);      // [warp][row][DH]
-  float *m_of = sums + kWarps * kFewMost * DH, *l_of = m_of + kWarps * kFewMost;  // [warp][row]
+  float *m_of = sums + kWarps * kFewMost * kPitch, *l_of = m_of + kWarps * kFewMost;  // [warp][row]
   int *flag = reinterpret_cast<int *>(l_of + kWarps * kFewMost);
   const float sl2 = A.scale_log2;
   bool inside = true;
@@ -112,21 +127,22 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned 
   for (int u = blockIdx.x; u < units * c.L * c.Hkv; u += gridDim.x) {
     const int lh = u / units, l = lh / c.Hkv, h = lh - l * c.Hkv;
     int chunk = u - lh * units, b = 0, n = 0, ctx = 0;
+    int row0 = 0;
 #pragma unroll 1
     for (int b0 = 0;; b0 += 32) {
-      b = b0 + lane;
-      ctx = b < c.Bq ? A.ctx_len[b] : 0, n = b < c.Bq ? A.start[b + 1] - A.start[b] : 0;
-      const int mine = few_units(A, ctx, n), upto = scan32(mine);
+      if (b0 != win.b0) win.load(A, b0);
+      const int mine = few_units(A, win.ctx, win.n), upto = scan32(mine);
       const int k = __popc(__ballot_sync(0xffffffffu, upto <= chunk));
       if (k < 32) {
         chunk -= __shfl_sync(0xffffffffu, upto - mine, k);
         b = b0 + k;
-        ctx = __shfl_sync(0xffffffffu, ctx, k), n = __shfl_sync(0xffffffffu, n, k);
+        row0 = __shfl_sync(0xffffffffu, win.row0, k);
+        ctx = __shfl_sync(0xffffffffu, win.ctx, k), n = __shfl_sync(0xffffffffu, win.n, k);
         break;
       }
       chunk -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    const int row0 = A.start[b], rows = n * A.G, kv_len = ctx + n, pieces = few_units(A, ctx, n);
+    const int rows = n * A.G, kv_len = ctx + n, pieces = few_units(A, ctx, n);
     auto place = [&](int r) {
       return ((size_t)l * c.M + row0 + r / A.G) * c.Hq + h * A.G + r % A.G;
     };
@@ -164,8 +180,11 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned 
           v[e] = id >= 0 && first + key < kv_len ? v0[key * by_key + d0 / 8 + g] : zero;
         }
       };
-      uint4 v[4];
-      load_v(0, v);
+      // (the first half ahead of the scores, the rest as soon as K's registers are free)
+      constexpr int kWide = DH / 64, kAhead = kWide < 2 ? 1 : 2;
+      uint4 v[kWide][4];
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) load_v(64 * d, v[d]);
       // what the lane's row sees
       const int tok = g / A.G;
       int lim = id < 0 || g >= rows ? 0 : ctx + tok + 1;
@@ -183,6 +202,8 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned 
           mma_8rows<F16>(x[t], q[s].x, q[s].y, kx[t][s].x, kx[t][s].y);
           mma_8rows<F16>(x[t], q[s].z, q[s].w, kx[t][s].z, kx[t][s].w);
         }
+#pragma unroll
+      for (int d = kAhead; d < kWide; ++d) load_v(64 * d, v[d]);
       float m = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -206,28 +227,26 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned 
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       if (j == 0) m_of[warp * kFewMost + g] = ref, l_of[warp * kFewMost + g] = sum;
-      float *to = sums + (warp * kFewMost + g) * DH + 16 * j;
-#pragma unroll 1
-      for (int d0 = 0; d0 < DH; d0 += 64) {
-        uint4 next[4];
-        if (d0 + 64 < DH) load_v(d0 + 64, next);
+      float *to = sums + (warp * kFewMost + g) * kPitch + 16 * j;
+#pragma unroll
+      for (int d = 0; d < kWide; ++d) {
         // product t: dimension 8 n + t of the 64 is column n
         float y[16];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          auto word = [&](int e) { return t < 2 ? v[e].x : t < 4 ? v[e].y : t < 6 ? v[e].z : v[e].w; };
+          auto word = [&](int e) {
+            return t < 2 ? v[d][e].x : t < 4 ? v[d][e].y : t < 6 ? v[d][e].z : v[d][e].w;
+          };
           const uint32_t half = t & 1 ? 0x7632u : 0x5410u;
-          float d[4] = {};
-          mma_8rows<F16>(d, p[0], p[1], __byte_perm(word(0), word(1), half),
+          float f[4] = {};
+          mma_8rows<F16>(f, p[0], p[1], __byte_perm(word(0), word(1), half),
                          __byte_perm(word(2), word(3), half));
-          y[t] = d[0], y[8 + t] = d[1];
+          y[t] = f[0], y[8 + t] = f[1];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          reinterpret_cast<float4 *>(to + d0)[e] =
+          reinterpret_cast<float4 *>(to + 64 * d)[e] =
               make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = next[e];
       }
     }
     __syncthreads();
@@ -258,7 +277,7 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, unsigned 
         const float l_w = l_of[w * kFewMost + r];
         if (l_w == 0.f) continue;
         const float by = ptx::ex2(m_of[w * kFewMost + r] - base);
-        const float4 y = reinterpret_cast<const float4 *>(sums + (w * kFewMost + r) * DH)[c4];
+        const float4 y = reinterpret_cast<const float4 *>(sums + (w * kFewMost + r) * kPitch)[c4];
         l_sum = fmaf(by, l_w, l_sum);
         f.x = fmaf(by, y.x, f.x), f.y = fmaf(by, y.y, f.y);
         f.z = fmaf(by, y.z, f.z), f.w = fmaf(by, y.w, f.w);
