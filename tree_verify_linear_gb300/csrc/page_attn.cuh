@@ -181,14 +181,17 @@ __device__ __forceinline__ bool find_begin(const PageArgs &A, int me, int ctas, 
                                            Window &win, Begin &g) {
   const lbx_page_cfg &c = A.c;
   const int lane = threadIdx.x & 31, share = share_of(c.Bq);
-  i64 upto = scan32_wide(lane < kThreads / 32 ? warps[lane] : 0);
-  const i64 total = __shfl_sync(0xffffffffu, upto, 31);
+  i64 upto = 0, total = warps[0];
+  if (c.Bq > share) {  // more than the first warp's share
+    upto = scan32_wide(lane < kThreads / 32 ? warps[lane] : 0);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  }
   g.cut = cut_of(total * c.L * c.Hkv, ctas);
   if (total == 0 || me >= g.cut.n) return false;
   g.from = g.cut.at(me);
   g.lh = (int)quot(g.from, total);
   i64 y = g.from - g.lh * total;
-  const int w = __popc(__ballot_sync(0xffffffffu, upto <= y));
+  const int w = c.Bq > share ? __popc(__ballot_sync(0xffffffffu, upto <= y)) : 0;
   if (w > 0) y -= __shfl_sync(0xffffffffu, upto, w - 1);
 #pragma unroll 1
   for (int b0 = w * share;; b0 += 32) {
@@ -838,55 +841,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         join = misc[4 + sub] != 0;
       }
       if (join && valid && rows <= kFewRows) {
-        // each row's largest reference and sum, then four columns of a row per thread
-        float *top_of = red + (ONE ? 2 * kRows : hf * 2 * kRows), *inv_of = top_of + kRows;
-        if (gt < rows) {
-          float top = -INFINITY, sum = 0.f;
-          auto each = [&](auto f) {  // m and l of the pieces, eight at a time
-#pragma unroll 1
-            for (int e0 = 0; e0 < s.pieces; e0 += 8) {
-              float m[8], l[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float *from = partial(e0 + e < s.pieces ? e0 + e : e0) + gt;
-                m[e] = __ldcg(from), l[e] = __ldcg(from + kRows);
-              }
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (e0 + e < s.pieces) f(m[e], l[e]);
-            }
-          };
-          each([&](float m, float) { top = fmaxf(top, m); });
-          if (top == -INFINITY) top = 0.f;
-          each([&](float m, float l) { sum = fmaf(ptx::ex2(m - top), l, sum); });
-          top_of[gt] = top, inv_of[gt] = sum == 0.f ? 0.f : 1.f / sum;
-          finish(gt, top, sum);
-        }
-        ptx::named_sync(bar_id, Y::kGroup);
+        // four columns of a row per thread, eight pieces' loads in flight, the reference
+        // moving as it does over blocks of keys
 #pragma unroll 1
         for (int idx = gt; idx < rows * (DH / 4); idx += Y::kGroup) {
           const int rw = idx % rows, c4 = idx / rows;
-          const float top = top_of[rw], inv = inv_of[rw];
+          float top = -INFINITY, sum = 0.f;
           float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int e0 = 0; e0 < s.pieces; e0 += 8) {  // eight loads in flight
+          for (int e0 = 0; e0 < s.pieces; e0 += 8) {
             float4 y[8];
-            float m[8];
+            float m[8], l[8], most = top;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float *from = partial(e0 + e < s.pieces ? e0 + e : e0);
+              const bool in = e0 + e < s.pieces;
+              const float *from = partial(in ? e0 + e : e0);
+              m[e] = __ldcg(from + rw), l[e] = __ldcg(from + kRows + rw);
               y[e] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * kRows) + (size_t)c4 * kRows + rw);
-              m[e] = __ldcg(from + rw);
+              if (!in) m[e] = -INFINITY;
             }
 #pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, m[e]);
+            const float base = most == -INFINITY ? 0.f : most;
+            const float old = ptx::ex2(top - base);
+            f.x *= old, f.y *= old, f.z *= old, f.w *= old, sum *= old;
+            top = most;
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float w = e0 + e < s.pieces ? ptx::ex2(m[e] - top) : 0.f;
+              const float w = ptx::ex2(m[e] - base);
+              sum = fmaf(w, l[e], sum);
               f.x = fmaf(w, y[e].x, f.x), f.y = fmaf(w, y[e].y, f.y);
               f.z = fmaf(w, y[e].z, f.z), f.w = fmaf(w, y[e].w, f.w);
             }
           }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
-          reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = inv == 0.f ? make_uint2(0u, 0u) : u;
+          reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = sum == 0.f ? make_uint2(0u, 0u) : u;
+          if (c4 == 0) finish(rw, top, sum);
         }
       } else if (busy && valid && (s.pieces == 1 || join)) {
         // a row per thread (or half of one); this CTA's piece is still in tensor memory,
@@ -895,11 +886,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (join) {
           top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-          for (int e = 0; e < s.pieces; ++e) top = fmaxf(top, __ldcg(partial(e) + r));
+          for (int e0 = 0; e0 < s.pieces; e0 += 4) {
+            float m[4], l[4], most = top;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool in = e0 + e < s.pieces;
+              const float *from = partial(in ? e0 + e : e0) + r;
+              m[e] = __ldcg(from), l[e] = __ldcg(from + kRows);
+              if (!in) m[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, m[e]);
+            const float base = most == -INFINITY ? 0.f : most;
+            sum *= ptx::ex2(top - base);
+            top = most;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = fmaf(ptx::ex2(m[e] - base), l[e], sum);
+          }
           if (top == -INFINITY) top = 0.f;
-#pragma unroll 1
-          for (int e = 0; e < s.pieces; ++e)
-            sum = fmaf(ptx::ex2(__ldcg(partial(e) + r) - top), __ldcg(partial(e) + kRows + r), sum);
         }
         const float w = sum == 0.f ? 0.f : 1.f / sum;
         if (real && (!ONE || hf == 0)) finish(r, top, sum);

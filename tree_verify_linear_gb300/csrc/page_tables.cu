@@ -17,7 +17,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMost = LBX_PAGE_MAX_REQUESTS;
 constexpr int kPer = kMost / kThreads;  // requests per thread, at most
-constexpr int kRowsPerCta = 2048;       // rows of a CTA's share
+constexpr int kRowsPerCta = 512;        // rows of a CTA's share
 
 struct TableArgs {
   int Bq, M, page, shift, n_pages, max_pages;

@@ -455,20 +455,18 @@ def make_rope_cfg(sections, eps=1e-6, pairing=LBX_ROPE_HALVES) -> lbx_rope_cfg:
 def lbx_page_tables(cfg, ctx_len, new_len, held, n_free, block_table, free_list, held_out, n_free_out,
                     start, slot, pos, d_status=None, stream=None):
     """Block tables and slot maps of a step from the requests' lengths."""
-    i32, per = torch.int32, (cfg.Bq,)
-    _check("lbx_page_tables", load().lbx_page_tables(
+    i32, one, Bq, rows = torch.int32, (1,), cfg.Bq, (cfg.M,)
+    per = (Bq,)
+    rc = load().lbx_page_tables(
         ctypes.byref(cfg), _at(ctx_len, per, i32, "ctx_len"), _at(new_len, per, i32, "new_len"),
-        _at(held, per, i32, "held"), _at(n_free, (1,), i32, "n_free"),
-        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
+        _at(held, per, i32, "held"), _at(n_free, one, i32, "n_free"),
+        _at(block_table, (Bq, cfg.max_pages), i32, "block_table"),
         _at(free_list, (cfg.n_pages,), i32, "free_list"), _at(held_out, per, i32, "held_out"),
-        _at(n_free_out, (1,), i32, "n_free_out"), _at(start, (cfg.Bq + 1,), i32, "start"),
-        _at(slot, (cfg.M,), i32, "slot"), _at(pos, (cfg.M,), i32, "pos"),
-        _i32(d_status, "d_status"), _stream_of(slot, stream)))
-
-
-def _pages(cfg, k_pages, v_pages, el):
-    shape = (cfg.L, cfg.n_pages, cfg.page, cfg.Hkv, cfg.dh)
-    return _at(k_pages, shape, el, "k_pages"), _at(v_pages, shape, el, "v_pages")
+        _at(n_free_out, one, i32, "n_free_out"), _at(start, (Bq + 1,), i32, "start"),
+        _at(slot, rows, i32, "slot"), _at(pos, rows, i32, "pos"),
+        None if d_status is None else _i32(d_status, "d_status"), _stream_of(slot, stream))
+    if rc:
+        _check("lbx_page_tables", rc)
 
 
 def lbx_qk_norm_rope(cfg, rope, qkv, inv_freq, pos, slot, q_out, k_pages, v_pages, q_weight=None,
@@ -476,15 +474,19 @@ def lbx_qk_norm_rope(cfg, rope, qkv, inv_freq, pos, slot, q_out, k_pages, v_page
     """Norms of queries and keys per head and their rotation; keys and values
     go to their pages."""
     el, i32, f32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, torch.float32
-    weights = [None if w is None else _at(w, (cfg.L, cfg.dh), f32, name)
-               for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
-    _check("lbx_qk_norm_rope", load().lbx_qk_norm_rope(
-        ctypes.byref(cfg), ctypes.byref(rope),
-        _at(qkv, (cfg.L, cfg.M, cfg.Hq + 2 * cfg.Hkv, cfg.dh), el, "qkv"), *weights,
+    L, M, Hq, Hkv, dh = cfg.L, cfg.M, cfg.Hq, cfg.Hkv, cfg.dh
+    pool, w = (L, cfg.n_pages, cfg.page, Hkv, dh), (L, dh)
+    rc = load().lbx_qk_norm_rope(
+        ctypes.byref(cfg), ctypes.byref(rope), _at(qkv, (L, M, Hq + 2 * Hkv, dh), el, "qkv"),
+        None if q_weight is None else _at(q_weight, w, f32, "q_weight"),
+        None if k_weight is None else _at(k_weight, w, f32, "k_weight"),
         None if inv_freq is None else _at(inv_freq, (rope.rot // 2,), f32, "inv_freq"),
-        _at(pos, (rope.axes, cfg.M), i32, "pos"), _at(slot, (cfg.M,), i32, "slot"),
-        _at(q_out, (cfg.L, cfg.M, cfg.Hq, cfg.dh), el, "q_out"), *_pages(cfg, k_pages, v_pages, el),
-        _i32(d_status, "d_status"), _stream_of(qkv, stream)))
+        _at(pos, (rope.axes, M), i32, "pos"), _at(slot, (M,), i32, "slot"),
+        _at(q_out, (L, M, Hq, dh), el, "q_out"), _at(k_pages, pool, el, "k_pages"),
+        _at(v_pages, pool, el, "v_pages"), None if d_status is None else _i32(d_status, "d_status"),
+        _stream_of(qkv, stream))
+    if rc:
+        _check("lbx_qk_norm_rope", rc)
 
 
 def lbx_paged_workspace_size(cfg: lbx_page_cfg) -> int:
@@ -502,25 +504,32 @@ def new_paged_workspace(cfg: lbx_page_cfg, device="cuda") -> torch.Tensor:
 def lbx_paged_attention(cfg, start, ctx_len, block_table, q, k_pages, v_pages, o, workspace,
                         parent=None, lse=None, d_status=None, stream=None):
     """Attention of each request's new tokens (a chunk, a tree, one token) over its pages."""
-    el, i32, qs = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, (cfg.L, cfg.M, cfg.Hq, cfg.dh)
-    _check("lbx_paged_attention", load().lbx_paged_attention(
-        ctypes.byref(cfg), _at(start, (cfg.Bq + 1,), i32, "start"),
-        _at(ctx_len, (cfg.Bq,), i32, "ctx_len"),
-        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
-        None if parent is None else _at(parent, (cfg.M,), i32, "parent"), _at(q, qs, el, "q"),
-        *_pages(cfg, k_pages, v_pages, el), _at(o, qs, el, "o"),
-        None if lse is None else _at(lse, qs[:3], torch.float32, "lse"),
-        _ptr(workspace, None, "workspace"), workspace.nbytes, _i32(d_status, "d_status"),
-        _stream_of(q, stream)))
+    el, i32 = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32
+    L, Bq, M, Hq, dh = cfg.L, cfg.Bq, cfg.M, cfg.Hq, cfg.dh
+    qs, pool = (L, M, Hq, dh), (L, cfg.n_pages, cfg.page, cfg.Hkv, dh)
+    rc = load().lbx_paged_attention(
+        ctypes.byref(cfg), _at(start, (Bq + 1,), i32, "start"), _at(ctx_len, (Bq,), i32, "ctx_len"),
+        _at(block_table, (Bq, cfg.max_pages), i32, "block_table"),
+        None if parent is None else _at(parent, (M,), i32, "parent"), _at(q, qs, el, "q"),
+        _at(k_pages, pool, el, "k_pages"), _at(v_pages, pool, el, "v_pages"), _at(o, qs, el, "o"),
+        None if lse is None else _at(lse, (L, M, Hq), torch.float32, "lse"),
+        _ptr(workspace, None, "workspace"), workspace.nbytes,
+        None if d_status is None else _i32(d_status, "d_status"), _stream_of(q, stream))
+    if rc:
+        _check("lbx_paged_attention", rc)
 
 
 def lbx_page_commit(cfg, start, ctx_len, block_table, parent, accepted, k_pages, v_pages, ctx_out,
                     d_status=None, stream=None):
     """Move the accepted path's keys and values to the positions behind the context."""
-    el, i32, per = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, (cfg.Bq,)
-    _check("lbx_page_commit", load().lbx_page_commit(
-        ctypes.byref(cfg), _at(start, (cfg.Bq + 1,), i32, "start"), _at(ctx_len, per, i32, "ctx_len"),
-        _at(block_table, (cfg.Bq, cfg.max_pages), i32, "block_table"),
+    el, i32, Bq = _ELEM.get(cfg.dtype, torch.bfloat16), torch.int32, cfg.Bq
+    per, pool = (Bq,), (cfg.L, cfg.n_pages, cfg.page, cfg.Hkv, cfg.dh)
+    rc = load().lbx_page_commit(
+        ctypes.byref(cfg), _at(start, (Bq + 1,), i32, "start"), _at(ctx_len, per, i32, "ctx_len"),
+        _at(block_table, (Bq, cfg.max_pages), i32, "block_table"),
         _at(parent, (cfg.M,), i32, "parent"), _at(accepted, per, i32, "accepted"),
-        *_pages(cfg, k_pages, v_pages, el), _at(ctx_out, per, i32, "ctx_out"),
-        _i32(d_status, "d_status"), _stream_of(k_pages, stream)))
+        _at(k_pages, pool, el, "k_pages"), _at(v_pages, pool, el, "v_pages"),
+        _at(ctx_out, per, i32, "ctx_out"), None if d_status is None else _i32(d_status, "d_status"),
+        _stream_of(k_pages, stream))
+    if rc:
+        _check("lbx_page_commit", rc)
