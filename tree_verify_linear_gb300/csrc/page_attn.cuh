@@ -1,25 +1,27 @@
 // page_attn.cuh -- attention of each request's new tokens over its pages on the
 // tensor cores (sm_103a): the kernel behind lbx_paged_attention.
 //
-// Rows are (token, head of the group) pairs of one KV head, 128 to a subtile, two
-// subtiles to a tile.  Per block of 128 keys and subtile
+// Rows are (token, head of the group) pairs of one KV head, 128 to a subtile.  Per block
+// of 128 keys and subtile
 //   S = Q K^T          tensor cores, operands in shared memory
 //   softmax            online, base 2, statistics in fp32
 //   O += P V           tensor cores, P from tensor memory, in V's type
 // The running reference of a row moves only when a block's maximum exceeds it by more
 // than 2^8, so that O is rescaled rarely; the result is the same softmax taken from
 // another reference.  P is rounded to the 16-bit type once (2^-8 of a weight in bf16,
-// 2^-11 in f16), which adds about as much error as the rounding of o; f16 weights are
-// taken 2^7 times as large, so that what falls below its range is 2^-32 of the
-// reference.
+// 2^-11 in f16), which adds about as much error as the rounding of o (a second product
+// for what bf16 leaves would cost half the rate again); f16 weights are taken 2^7 times
+// as large, so that what falls below its range is 2^-32 of the reference.
 //
-// Head dimensions 64 and 128: a CTA holds both subtiles of a tile, each with its own
-// softmax warps (a row per thread), so that the tensor cores work on one while the
-// other's softmax runs, and K and V are read once for 256 rows.  Head dimension 256: O
-// takes half of tensor memory, so that a CTA holds one subtile, with two buffers of
-// S; a pair of CTAs shares products of 256 rows, each with half of the keys and half of
-// V's columns in its shared memory; two threads share a row, 64 keys each.  P lies over
-// its S.  The products of a CTA run in the order they are issued.
+// Head dimensions 64 and 128: a CTA holds two subtiles, each with its own four softmax
+// warps (a row per thread), so that the tensor cores work on one while the other's softmax
+// runs; half of a block's weights are handed on while the others are made.  Head dimension
+// 256: O takes half of tensor memory, so that a CTA holds one subtile, with two buffers of
+// S and two threads per row, 64 keys each.  Pairs of CTAs (256, and 128 where WIDE) share
+// products of 256 rows, each with half of the keys and half of V's columns in its shared
+// memory: its operand reads and the copies halve.  P lies over its S.  The products of a CTA
+// run in the order they are issued, so that the next block's scores follow the product that
+// reads the weights they overwrite without a wait in between.
 //
 // K and V come by tensor copies of whole page rows (boxes of at most 64 positions of
 // one head), a lane per box; a box past the request's last position is aimed outside the
@@ -28,11 +30,20 @@
 //
 // The work is cut as page_walk.cuh says.  A tile cut into pieces leaves partials (m,
 // l, O) in the workspace; the CTA that finishes a tile's last piece joins them in
-// the pieces' order.
+// the pieces' order.  Few rows over few keys are page_few.cuh's.
 //
 // Warps 0-7 softmax, 8 issues the products, 9 walks the list and copies K and V, 10
-// brings the queries.  Every wait is bounded; a thread whose wait gives up waits no
-// more, the call reports LBX_ETIMEOUT, and the CTA leaves after its copies have landed.
+// brings the queries, 11 only gives its registers.  Every wait is bounded; a thread whose wait
+// gives up waits no more, the call reports LBX_ETIMEOUT, and the CTA leaves after its copies
+// have landed.
+//
+// What bounds it, measured on one GB300 (copies reach 6.79 TB/s, cuBLAS 1898 TFLOP/s in
+// bf16).  A chunk of 2048 tokens over 6144 keys, 24/4 heads of 256: 220 us, 1640 TFLOP/s, the
+// tensor pipe.  Prompts of 501 to 6001 tokens, 32/8 heads of 128: 520 us, 1330 TFLOP/s, the chain
+// from scores to weights (2700 cycles per block, 2048 of products).  16 requests of one token over
+// 8001 to 16384 keys, 4 layers, 32/8 heads of 128 in f16: 485 us, 6.59 TB/s.  Trees of 22, five
+// requests of 2049 to 4096 keys, 16 layers, 24/4 heads of 256: 200 us, 5.3 TB/s and what beginning
+// and ending a tile takes (7 us).
 #pragma once
 
 #include "cache_ptx.cuh"

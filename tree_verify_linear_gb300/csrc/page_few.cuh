@@ -9,8 +9,12 @@
 // own softmax are an operand of its product with V as they come out of the first.  The
 // warps meet in shared memory; lists of more than one unit are joined by the CTA that
 // finishes last, in the units' order.  Written for the number of instructions: each is
-// fetched once and runs once (on CUDA cores, 12 times as many, a call of 2001 keys at 24/4
-// heads of 256 took 18.5 us; the tensor-memory kernel 22.5 us).
+// fetched once and runs once (on CUDA cores, with several times as many, a call of one token
+// over 2001 keys at 24/4 heads of 256 took 18.5 us; here 14.3; in tensor memory 22.5 us).
+//
+// What bounds it: that call takes 23000 cycles, 2000 for the check of the batch, 2300 to find the
+// unit, 5000 for the loads and the scores, 3000 for V, 2200 for the warps' sums, 1500 for the
+// arrival and 6000 for the join.
 #pragma once
 
 #include "cache_ptx.cuh"
@@ -22,7 +26,8 @@ namespace paged {
 constexpr int kThreads = 384;  // three warpgroups
 constexpr int kFewWarps = 8, kFewKeys = 16 * kFewWarps;  // keys of a unit
 constexpr int kFewMost = 8;                                // most rows of a list
-// Units per CTA, at most.
+// Units per CTA, at most: beyond, the tensor-memory kernel's copies are faster (one token over 16000
+// keys, 24/4 heads of 64, 128 and 256, 3.3 units per CTA: 29, 38 and 68 us here, 22, 27 and 27 us there).
 constexpr int kFewUnits = 2;
 
 struct PageArgs {
