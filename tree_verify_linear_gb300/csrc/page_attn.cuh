@@ -96,7 +96,7 @@ struct Lay {
   static constexpr int kStage = kKeys * DH * 2;
   static_assert(kStage == kBlk * kCols * 2, "K and V take the same place");
   static constexpr int kQSub = kRows * DH * 2, kQBytes = kSubs * kQSub;
-  static constexpr int kStages = (227 * 1024 - 3072 - kQBytes) / kStage;
+  static constexpr int kStages = (224 * 1024 - kQBytes) / kStage;  // 3 KB for the rest
   static_assert(kStages >= 4, "the next block's K beside this one's V");
   static constexpr int kSmemRing = kQBytes;
   static constexpr int kSmemRed = kSmemRing + kStages * kStage;  // float [4][128]
