@@ -78,6 +78,7 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   const uint64_t strides[3] = {(uint64_t)c->dh * 2, row, row * (uint64_t)c->M};
   const uint32_t box[4] = {64, (uint32_t)A.G, (uint32_t)A.tp, 1};
   if (!lbx::cache::encode_16bit(&maps.q, q, 4, dims, strides, box) ||
+      !lbx::cache::encode_16bit(&maps.o, o, 4, dims, strides, box) ||
       !encode_pool(&maps.k, k_pages, c, A.box) || !encode_pool(&maps.v, v_pages, c, A.box))
     return LBX_ECUDA;
   const int nsm = lbx::cache::grid_limit();

@@ -69,7 +69,7 @@ constexpr int kFewRows = 32;
 __host__ __device__ constexpr size_t part_floats(int dh) { return 2 * kRows + (size_t)kRows * dh; }
 
 struct PageMaps {
-  CUtensorMap q;     // (dh, Hq, M, L), boxes of 64 columns of whole tokens' heads
+  CUtensorMap q, o;  // (dh, Hq, M, L), boxes of 64 columns of whole tokens' heads
   CUtensorMap k, v;  // (dh, Hkv, positions of all layers' pools), boxes of 64 columns
 };
 
@@ -96,9 +96,12 @@ struct Lay {
   static constexpr int kStage = kKeys * DH * 2;
   static_assert(kStage == kBlk * kCols * 2, "K and V take the same place");
   static constexpr int kQSub = kRows * DH * 2, kQBytes = kSubs * kQSub;
-  static constexpr int kStages = (224 * 1024 - kQBytes) / kStage;  // 3 KB for the rest
+  // where whole subtiles' results wait for their copy out (where the ring can spare it)
+  static constexpr bool kStaged = DH == 64 || WIDE;
+  static constexpr int kOutBytes = kStaged ? kQBytes : 0;
+  static constexpr int kStages = (224 * 1024 - kQBytes - kOutBytes) / kStage;  // 3 KB for the rest
   static_assert(kStages >= 4, "the next block's K beside this one's V");
-  static constexpr int kSmemRing = kQBytes;
+  static constexpr int kSmemOut = kQBytes, kSmemRing = kSmemOut + kOutBytes;
   static constexpr int kSmemRed = kSmemRing + kStages * kStage;  // float [4][128]
   static constexpr int kSmemSegs = kSmemRed + 4 * kRows * 4;     // Seg [4]
   static constexpr int kSmemMisc = kSmemSegs + 4 * (int)sizeof(Seg);  // int [16]
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_map(&maps.q);
     ptx::prefetch_map(&maps.k);
     ptx::prefetch_map(&maps.v);
+    if (Y::kStaged) ptx::prefetch_map(&maps.o);
   }
   if (warp == 8) {
     uint32_t *base = reinterpret_cast<uint32_t *>(smem + Y::kSmemMisc);
@@ -808,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_sum = red[r] + red[kRows + r];
       }
       const float m2 = m_run == -INFINITY ? -INFINITY : fmaf(m_run, sl2, -kLift<F16>);
+      if (Y::kStaged && gt == 0) ptx::bulk_wait_read_all();  // the last copy out has left its place
       const bool valid = !any_of(bar_id, Y::kGroup, bad);
       // A row's place among the outputs, and its lse.  (A NaN among a row's scores makes
       // its sum one, and the row with it.)
@@ -889,6 +894,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint2 u = make_uint2(pack2<F16>(f.x * inv, f.y * inv), pack2<F16>(f.z * inv, f.w * inv));
           reinterpret_cast<uint2 *>(A.o + place(rw) * DH)[c4] = sum == 0.f ? make_uint2(0u, 0u) : u;
           if (c4 == 0) finish(rw, top, sum);
+        }
+      } else if (Y::kStaged && s.pieces == 1 && valid && rows == A.tp * A.G) {
+        // a whole subtile: through shared memory, as the tensor copy reads it (rows of 128
+        // bytes, 16-byte pieces swizzled), which runs beside the next tile
+        unsigned char *out = smem + Y::kSmemOut + hf * Y::kQSub;
+        if (busy) {
+          const float w = l_sum == 0.f ? 0.f : 1.f / l_sum;
+          if (real) finish(r, m2, l_sum);
+#pragma unroll 1
+          for (int e0 = 0; e0 < DH; e0 += 32) {
+            float v[32];
+            ptx::tmem_ld32(to + e0, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                u[f] = l_sum == 0.f ? 0u : pack2<F16>(v[8 * e + 2 * f] * w, v[8 * e + 2 * f + 1] * w);
+              const int piece = (e0 / 8 + e) & 7;
+              *reinterpret_cast<uint4 *>(out + (e0 / 64) * (kRows * 128) + r * 128 +
+                                         ((piece ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+          ptx::fence_proxy_async();
+        }
+        ptx::named_sync(bar_id, Y::kGroup);
+        if (gt == 0) {
+#pragma unroll 1
+          for (int a = 0; a < DH / 64; ++a)
+            ptx::tma_store_4d(&maps.o, a * 64, s.h * A.G, s.row0 + s.tok0 + sub * A.tp, s.l,
+                              out + a * kRows * 128);
+          ptx::bulk_commit();
         }
       } else if (busy && valid && (s.pieces == 1 || join)) {
         // a row per thread (or half of one); this CTA's piece is still in tensor memory,
@@ -990,6 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::named_sync(bar_id, Y::kGroup);  // red is free again
     }
     if (bad) misc[1] = 1;
+    if (Y::kStaged && gt == 0) ptx::bulk_wait_all();
   }
 
   ptx::tc_fence_before();
