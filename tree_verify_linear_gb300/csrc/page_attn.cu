@@ -58,7 +58,7 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   while (1 << A.shift < c->page) ++A.shift;
   // Head dimension 128: a pair of CTAs shares products of 256 rows of both of its subtiles,
   // which halves what shared memory has to deliver (prompts of 501 to 6001 tokens, 32/8
-  // heads: 520 us against 556 us on single CTAs); requests of few rows leave the second
+  // heads: 508 us against 556 us on single CTAs); requests of few rows leave the second
   // subtile empty and are better off with more and smaller tiles (16 requests of one token
   // over 8001 to 16384 keys: 487 us against 845 us).  The lengths are on the device: M and
   // Bq decide, by the rows of a request on average.  16 requests over 3000 keys, 32/8 heads,

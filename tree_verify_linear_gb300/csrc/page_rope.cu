@@ -15,7 +15,9 @@
 // What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of
 // few warps.  8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in
 // halves: 56 us, 4.7 TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent
-// pairs, three axes: 76 us, 5.2 TB/s.  (A lane per 16 bytes and all pairs through
+// pairs, three axes: 76 us, 5.2 TB/s.  Halves whose partners meet in shared memory (2 layers of
+// 13728 rows, 20/4 heads of 128 in f16): 107 us with 90 dimensions turned, 83 us with 128, whose
+// partners share a lane.  (A lane per 16 bytes and all pairs through
 // shared memory: 92 and 107 us; four CTAs per SM: 81 and 105 us, registers spilled.)
 #include "cache_walk.cuh"
 #include "page_common.cuh"
@@ -83,10 +85,13 @@ __device__ __forceinline__ uint4 pack8(const uint64_t *x) {
 }
 
 template <int DH, bool F16, int PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_kernel(const RopeArgs A) {
   constexpr int kLanes = DH / 16, kHeads = 32 / kLanes, kPieces = DH / 8;
   __shared__ float2 turn[kMaxRows][DH / 2];
-  __shared__ float stage[PAIRS == kAnywhere ? kWarps : 1][512];
+  // A head's dimension j lies at j + j / 8 of its kPitch: neighbouring lanes' pieces and heads
+  // are nine banks apart.  Behind them a zero.
+  constexpr int kPitch = 18 * kLanes + (32 - 9 * kLanes % 32) % 32;
+  __shared__ float stage[PAIRS == kAnywhere ? kWarps : 1][kHeads * kPitch + 1];
   __shared__ int slots[kMaxRows];
   const lbx_page_cfg &c = A.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -153,9 +158,24 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs A) {
   }
   __syncthreads();
 
-  // A row's cosines and sines: of pairs in the lane in twos, of adjacent ones (cos, cos)
-  // and (-sin, sin) per pair.
-  uint64_t cos2[PAIRS == kAdjacent ? 8 : 4], sin2[PAIRS == kAdjacent ? 8 : 4];
+  // A row's cosines and sines: of pairs in the lane in twos, else per dimension, the sines
+  // with the sign that the other one of the pair takes.
+  uint64_t cos2[PAIRS == kInLane ? 4 : 8], sin2[PAIRS == kInLane ? 4 : 8];
+  // where the other one of the pair lies, of each dimension: 8 p + i turns with 8 p + i + half or
+  // 8 p + i - half, those past the last pair with the zero
+  int other[PAIRS == kAnywhere ? 16 : 1];
+  const bool second_turns = 2 * A.half > 8 * kLanes;  // any of the lanes' second pieces
+  if constexpr (PAIRS == kAnywhere) {
+    if (lane == 0) stage[warp][kHeads * kPitch] = 0.f;
+    const int full = A.half >> 3, over = A.half & 7;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int p = k < 8 ? p0 : p1, i = k & 7, j = 8 * p + i;
+      const int up = 9 * (p + full) + over + i + (i + over >= 8 ? 1 : 0);
+      const int down = 9 * (p - full) - over + i - (i < over ? 1 : 0);
+      other[k] = j < 2 * A.half ? head0 * kPitch + (j < A.half ? up : down) : kHeads * kPitch;
+    }
+  }
   int slot = -1, r = a / A.passes, u = a % A.passes - 1;
   bool fresh = true;  // the unit begins a row, or the share
   uint4 *q_row = nullptr;
@@ -181,6 +201,18 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs A) {
           for (int i = 0; i < 8; ++i) {
             const float2 f = of(i < 4 ? 4 * p0 + i : 4 * p1 + i - 4);
             cos2[i] = both(f.x, f.x), sin2[i] = both(-f.y, f.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = (i < 4 ? 8 * p0 + 2 * i : 8 * p1 + 2 * i - 8) + k;
+              f[k] = j < A.half ? turn[r][j] : j < 2 * A.half ? turn[r][j - A.half] : make_float2(1.f, 0.f);
+              if (j < A.half) f[k].y = -f[k].y;
+            }
+            cos2[i] = both(f[0].x, f[1].x), sin2[i] = both(f[0].y, f[1].y);
           }
         }
       }
@@ -229,26 +261,20 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs A) {
           x[i] = fma2(both(f.y, f.x), sin2[i], mul2(x[i], cos2[i]));
         }
       } else {
-        float *mine = stage[warp] + head0 * DH;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = apart2(x[2 * i]), g = apart2(x[2 * i + 1]);
-          reinterpret_cast<float4 *>(mine)[(i < 2 ? 2 * p0 : 2 * p1 - 2) + i] =
-              make_float4(f.x, f.y, g.x, g.y);
-        }
-        __syncwarp();
-        auto turned = [&](int j, float y) {  // dimension j
-          if (j >= 2 * A.half) return y;
-          const bool second = j >= A.half;
-          const float2 t = turn[r][second ? j - A.half : j];
-          const float other = mine[second ? j - A.half : j + A.half];
-          return fmaf(y, t.x, second ? other * t.y : -other * t.y);
-        };
+        float *mine = stage[warp] + head0 * kPitch;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int j = i < 4 ? 8 * p0 + 2 * i : 8 * p1 + 2 * i - 8;
+          if (i >= 4 && !second_turns) break;
           const float2 f = apart2(x[i]);
-          x[i] = both(turned(j, f.x), turned(j + 1, f.y));
+          float *to = mine + (i < 4 ? 9 * p0 + 2 * i : 9 * p1 + 2 * i - 8);
+          to[0] = f.x, to[1] = f.y;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= 4 && !second_turns) break;
+          x[i] = fma2(both(stage[warp][other[2 * i]], stage[warp][other[2 * i + 1]]), sin2[i],
+                      mul2(x[i], cos2[i]));
         }
         __syncwarp();
       }
