@@ -333,6 +333,13 @@ BUSY = {
     "chunk_long_256_f16": dict(ctx=[100], new=[1800], Hq=8, Hkv=2, dh=256, page=128, dtype="f16"),
     "chunk_long_64": dict(ctx=[4000, 0], new=[1000, 2100], Hq=6, Hkv=2, dh=64, page=64),
     "layers": dict(ctx=[800, 333, 0], new=[1, 300, 77], Hq=8, Hkv=4, dh=128, page=64, L=5),
+    "requests_700": dict(ctx=[(13 * b) % 170 for b in range(700)], new=[(b * 7) % 4 for b in range(700)],
+                         Hq=12, Hkv=2, dh=64, page=16),
+    "requests_500_of_256": dict(ctx=[(29 * b) % 300 for b in range(500)],
+                                new=[40 if b % 50 == 3 else b % 2 for b in range(500)], Hq=4, Hkv=2, dh=256,
+                                page=32, pad=9),
+    "trees_of_400": dict(ctx=[(31 * b) % 200 for b in range(400)], new=[(b * 11) % 23 for b in range(400)],
+                         Hq=4, Hkv=1, dh=128, page=16, kind="random"),
     "wide_batch": dict(ctx=[(37 * b) % 900 for b in range(150)], new=[1] * 150, Hq=8, Hkv=2, dh=128, page=16),
 }
 
@@ -720,6 +727,10 @@ FEW = {
     "tree_of_8": dict(ctx=[300, 0, 127], new=[8, 1, 6], Hq=3, Hkv=3, dh=128, page=16, kind="random"),
     "tree_over_a_unit": dict(ctx=[125], new=[7], Hq=1, Hkv=1, dh=64, page=256, kind="star", dtype="f16"),
     "many_units": dict(ctx=[9000], new=[1], Hq=6, Hkv=1, dh=256, page=64),
+    "requests_100": dict(ctx=[(7 * b) % 120 for b in range(100)], new=[b % 2 for b in range(100)], Hq=4, Hkv=1,
+                         dh=128, page=16),
+    "requests_60_layers": dict(ctx=[(7 * b) % 90 for b in range(60)], new=[1] * 60, Hq=8, Hkv=2, dh=64, page=32,
+                               L=2, pad=3),
     "rows_9_beside_1": dict(ctx=[40, 700], new=[9, 1], Hq=2, Hkv=2, dh=128, page=16),
 }
 
