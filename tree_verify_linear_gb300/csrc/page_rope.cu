@@ -13,12 +13,14 @@
 // memory), so that all arithmetic but the sum of squares stays in the lane.
 //
 // What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of
-// few warps.  8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in
-// halves: 56 us, 4.7 TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent
-// pairs, three axes: 76 us, 5.2 TB/s.  Halves whose partners meet in shared memory (2 layers of
-// 13728 rows, 20/4 heads of 128 in f16): 107 us with 90 dimensions turned, 83 us with 128, whose
-// partners share a lane.  (A lane per 16 bytes and all pairs through
-// shared memory: 92 and 107 us; four CTAs per SM: 81 and 105 us, registers spilled.)
+// few warps.  8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in halves: 52 us, 5.1 TB/s; 16006
+// rows of 32/8 heads of 128 in f16, all turned, adjacent pairs, three axes: 69 us, 5.7 TB/s.
+// Halves whose partners meet in shared memory (2 layers of 13728 rows, 20/4 heads of 128 in
+// f16): 93 us with 90 dimensions turned, 77 us with 128, whose partners share a lane.  (A lane
+// per 16 bytes and all pairs through shared memory: 92 and 107 us for the first two; pieces
+// loaded one unit ahead into registers: 56, 76, 107 and 83 us; four CTAs per SM, registers
+// spilled, slower; two CTAs with the queries' weights in registers: 53, 72 and 85 us where
+// partners share a lane, but 5 us faster where they meet in shared memory, so there alone.)
 #include "cache_walk.cuh"
 #include "page_common.cuh"
 
@@ -40,6 +42,14 @@ struct RopeArgs {
   uint4 *q, *k, *v;
   int32_t *status;
 };
+
+// 16 bytes into shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint4 *to, const uint4 *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
 
 // Where the partners of a pair are: in a lane's two pieces, next to each other in one, or
 // anywhere in the head.
@@ -112,16 +122,25 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_ker
   const int a = (int)((long long)all * gw / warps), z = (int)((long long)all * (gw + 1) / warps);
   // This lane's head in pass u is head0 + u * kHeads.
   const int head0 = lane / kLanes;
-  uint4 next[2];  // the next unit
-  int left = z - a, lr = a / A.passes, lu = a % A.passes;  // the one to load
-  const uint4 *in = qkv + (size_t)(m0 + lr) * heads * kPieces + head0 * kPieces;
-  auto ahead = [&](uint4 (&to)[2]) {
-    if (--left < 0) return;
-    const int off = lu * (kHeads * kPieces);
-    if (head0 + lu * kHeads < heads) to[0] = __ldcs(in + off + p0), to[1] = __ldcs(in + off + p1);
-    if (++lu == A.passes) lu = 0, in += heads * kPieces;
+  // The units' pieces come ahead through shared memory, which costs no registers: each lane
+  // reads what it copied itself.  (Of dimension 256 with its stage there is room for one.)
+  constexpr int kAheadUnits = PAIRS != kAnywhere ? 3 : DH == 256 ? 1 : 2;
+  __shared__ uint4 ring[kWarps][kAheadUnits][2][32];
+  int left = z - a, lu = a % A.passes, at_slot = 0;  // the one to load
+  const uint4 *in = qkv + (size_t)(m0 + a / A.passes) * heads * kPieces + head0 * kPieces;
+  auto ahead = [&](int to) {
+    if (--left >= 0) {
+      const int off = lu * (kHeads * kPieces);
+      if (head0 + lu * kHeads < heads) {
+        copy16(&ring[warp][to][0][lane], in + off + p0);
+        copy16(&ring[warp][to][1][lane], in + off + p1);
+      }
+      if (++lu == A.passes) lu = 0, in += heads * kPieces;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  ahead(next);
+#pragma unroll
+  for (int k = 0; k < kAheadUnits; ++k) ahead(k);
   auto weights = [&](const float *w, uint64_t (&to)[8]) {
     const float4 *from = reinterpret_cast<const float4 *>(w + (size_t)l * DH);
 #pragma unroll
@@ -176,6 +195,9 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_ker
       other[k] = j < 2 * A.half ? head0 * kPitch + (j < A.half ? up : down) : kHeads * kPitch;
     }
   }
+  constexpr bool kKeep = PAIRS == kAnywhere;  // the queries' weights, in registers
+  uint64_t wq[8];
+  if (kKeep && A.qw) weights(A.qw, wq);
   int slot = -1, r = a / A.passes, u = a % A.passes - 1;
   bool fresh = true;  // the unit begins a row, or the share
   uint4 *q_row = nullptr;
@@ -217,8 +239,10 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_ker
         }
       }
     }
-    const uint4 raw[2] = {next[0], next[1]};
-    ahead(next);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAheadUnits - 1) : "memory");
+    const uint4 raw[2] = {ring[warp][at_slot][0][lane], ring[warp][at_slot][1][lane]};
+    ahead(at_slot);
+    if (++at_slot == kAheadUnits) at_slot = 0;
     if (slot < 0) continue;  // the whole warp
     const int h = u * kHeads + head0;
     const bool is_q = h < c.Hq, is_v = h >= c.Hq + c.Hkv;
@@ -238,10 +262,17 @@ __global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_ker
         const float inv = rsqrtf(fmaf(ss, 1.f / DH, A.r.eps));
         const uint64_t inv2 = both(inv, inv);
         if (norm) {
-          uint64_t w[8];
-          weights(is_q ? A.qw : A.kw, w);
+          auto scale = [&](const uint64_t (&w)[8]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(inv2, w[i]));
+            for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], mul2(inv2, w[i]));
+          };
+          if (kKeep && is_q) {
+            scale(wq);
+          } else {
+            uint64_t w[8];
+            weights(is_q ? A.qw : A.kw, w);
+            scale(w);
+          }
         }
       }
       if constexpr (PAIRS == kInLane) {
