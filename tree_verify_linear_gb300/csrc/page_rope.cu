@@ -12,15 +12,15 @@
 // turn with each other (where rot is a multiple of 16; else they meet in shared
 // memory), so that all arithmetic but the sum of squares stays in the lane.
 //
-// What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of
-// few warps.  8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in halves: 52 us, 5.1 TB/s; 16006
-// rows of 32/8 heads of 128 in f16, all turned, adjacent pairs, three axes: 69 us, 5.7 TB/s.
-// Halves whose partners meet in shared memory (2 layers of 13728 rows, 20/4 heads of 128 in
-// f16): 93 us with 90 dimensions turned, 77 us with 128, whose partners share a lane.  (A lane
-// per 16 bytes and all pairs through shared memory: 92 and 107 us for the first two; pieces
-// loaded one unit ahead into registers: 56, 76, 107 and 83 us; four CTAs per SM, registers
-// spilled, slower; two CTAs with the queries' weights in registers: 53, 72 and 85 us where
-// partners share a lane, but 5 us faster where they meet in shared memory, so there alone.)
+// What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of few warps.
+// 8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in halves: 52 us, 5.1
+// TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent pairs, three axes: 69 us, 5.7
+// TB/s. Halves whose partners meet in shared memory (2 layers of 13728 rows, 20/4 heads of 128 in
+// f16): 93 us with 90 dimensions turned, 77 us with 128, whose partners share a lane.  (A lane per
+// 16 bytes and all pairs through shared memory: 92 and 107 us for the first two; pieces loaded one
+// unit ahead into registers: 56, 76, 107 and 83 us; four CTAs per SM, registers spilled, slower;
+// two CTAs with the queries' weights in registers: 53, 72 and 85 us where partners share a lane,
+// but 5 us faster where they meet in shared memory, so there alone.)
 #include "cache_walk.cuh"
 #include "page_common.cuh"
 
@@ -54,6 +54,7 @@ __device__ __forceinline__ void copy16(uint4 *to, const uint4 *from) {
 // Where the partners of a pair are: in a lane's two pieces, next to each other in one, or
 // anywhere in the head.
 enum { kInLane, kAdjacent, kAnywhere };
+constexpr int ctas_per_sm(int pairs) { return pairs == kAnywhere ? 2 : 3; }
 
 // f / (2 pi) modulo 1, in units of 2^-64.
 __device__ __forceinline__ uint64_t turns_of(float f) {
@@ -95,7 +96,8 @@ __device__ __forceinline__ uint4 pack8(const uint64_t *x) {
 }
 
 template <int DH, bool F16, int PAIRS>
-__global__ void __launch_bounds__(kThreads, PAIRS == kAnywhere ? 2 : 3) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
+    rope_kernel(const RopeArgs A) {
   constexpr int kLanes = DH / 16, kHeads = 32 / kLanes, kPieces = DH / 8;
   __shared__ float2 turn[kMaxRows][DH / 2];
   // A head's dimension j lies at j + j / 8 of its kPitch: neighbouring lanes' pieces and heads
@@ -332,14 +334,18 @@ bool rope_ok(const lbx_page_cfg *c, const lbx_rope_cfg *r) {
   return sum == r->rot / 2;
 }
 
+int pairs_of(const RopeArgs &A) {
+  if (A.r.pairing == LBX_ROPE_ADJACENT) return kAdjacent;
+  return A.half % 8 == 0 ? kInLane : kAnywhere;
+}
+
 template <int DH, bool F16>
 void launch(const RopeArgs &A, unsigned grid, cudaStream_t stream) {
-  if (A.r.pairing == LBX_ROPE_ADJACENT)
-    rope_kernel<DH, F16, kAdjacent><<<grid, kThreads, 0, stream>>>(A);
-  else if (A.half % 8 == 0)
-    rope_kernel<DH, F16, kInLane><<<grid, kThreads, 0, stream>>>(A);
-  else
-    rope_kernel<DH, F16, kAnywhere><<<grid, kThreads, 0, stream>>>(A);
+  switch (pairs_of(A)) {
+    case kAdjacent: rope_kernel<DH, F16, kAdjacent><<<grid, kThreads, 0, stream>>>(A); break;
+    case kInLane: rope_kernel<DH, F16, kInLane><<<grid, kThreads, 0, stream>>>(A); break;
+    default: rope_kernel<DH, F16, kAnywhere><<<grid, kThreads, 0, stream>>>(A);
+  }
 }
 
 }  // namespace
@@ -368,8 +374,8 @@ extern "C" int lbx_qk_norm_rope(const lbx_page_cfg *c, const lbx_rope_cfg *rope,
   const int nsm = lbx::cache::grid_limit();
   if (nsm < 1) return LBX_ECUDA;
   // Few rows: CTAs of eight warps' heads each, so that the call is one trip to memory.
-  // Many: as many rows per CTA as fill whole rounds of the three CTAs that an SM holds.
-  const long long lm = (long long)c->L * c->M, slots = 3LL * nsm;
+  // Many: as many rows per CTA as fill whole rounds of the CTAs that the SMs hold.
+  const long long lm = (long long)c->L * c->M, slots = (long long)ctas_per_sm(pairs_of(A)) * nsm;
   if (lm >= slots) {
     const long long rounds = (lm + slots * kMaxRows - 1) / (slots * kMaxRows);
     A.rows = (int)((lm + slots * rounds - 1) / (slots * rounds));
