@@ -3,26 +3,27 @@
 //
 // A CTA takes a few rows of one layer.  First the angles: pair i of a row turns by
 // pos * inv_freq[i], of which only the fraction of a turn matters.  inv_freq / (2 pi)
-// is taken once per pair and CTA as a 64-bit fixed-point fraction of a turn (two
-// doubles hold 1 / (2 pi)), times pos in integers modulo 2^64: no position is so far
-// that an angle loses digits, as it does in a product of two floats (2^-24 of a
-// million radians).  Cosines and sines lie in shared memory for all heads of the row,
-// and from there in a lane's registers for as long as its warp stays with the row.
-// Then the heads, a lane for two 16-byte pieces of one: with pairs in halves those that
-// turn with each other (where rot is a multiple of 16; else they meet in shared
+// is taken once per pair and CTA as a 64-bit fixed-point fraction of a turn, in integers
+// (two doubles for 1 / (2 pi) took 1 us more at 5000 rows: an SM does few of them a cycle), times
+// pos modulo 2^64: no position is so far that an angle loses digits, as it does in a
+// product of two floats (2^-24 of a million radians).  Cosines and sines lie in shared memory
+// for all heads of the row, and from there in a lane's registers for as long as its warp stays
+// with the row.  Then the heads, a lane for two 16-byte pieces of one: with pairs in halves
+// those that turn with each other (where rot is a multiple of 16; else they meet in shared
 // memory), so that all arithmetic but the sum of squares stays in the lane.
 //
 // What bounds it, measured on one GB300 (copies reach 6.79 TB/s): the instructions of few warps.
-// 8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in halves: 52 us, 5.1
-// TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent pairs, three axes: 69 us, 5.7
+// 8052 rows of 24/4 heads of dimension 256 in bf16, 64 dimensions turned in halves: 51 us, 5.1
+// TB/s; 16006 rows of 32/8 heads of 128 in f16, all turned, adjacent pairs, three axes: 68 us, 5.8
 // TB/s. Halves whose partners meet in shared memory (2 layers of 13728 rows, 20/4 heads of 128 in
-// f16): 93 us with 90 dimensions turned, 77 us with 128, whose partners share a lane.  (A lane per
+// f16): 91 us with 90 dimensions turned, 77 us with 128, whose partners share a lane.  (A lane per
 // 16 bytes and all pairs through shared memory: 92 and 107 us for the first two; pieces loaded one
 // unit ahead into registers: 56, 76, 107 and 83 us; four CTAs per SM, registers spilled, slower;
 // two CTAs with the queries' weights in registers: 53, 72 and 85 us where partners share a lane,
 // but 5 us faster where they meet in shared memory, so there alone.)
 #include "cache_walk.cuh"
 #include "page_common.cuh"
+#include "page_turn.cuh"
 
 namespace lbx {
 namespace paged {
@@ -55,14 +56,6 @@ __device__ __forceinline__ void copy16(uint4 *to, const uint4 *from) {
 // anywhere in the head.
 enum { kInLane, kAdjacent, kAnywhere };
 constexpr int ctas_per_sm(int pairs) { return pairs == kAnywhere ? 2 : 3; }
-
-// f / (2 pi) modulo 1, in units of 2^-64.
-__device__ __forceinline__ uint64_t turns_of(float f) {
-  const double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-  const double x = f, p = x * kHi, rest = fma(x, kLo, fma(x, kHi, -p));
-  return __double2ull_rz((p - floor(p)) * 18446744073709551616.0) +
-         (uint64_t)__double2ll_rn(rest * 18446744073709551616.0);
-}
 
 // Eight values of a 16-byte piece, two at a time.
 template <bool F16>
@@ -99,7 +92,7 @@ template <int DH, bool F16, int PAIRS>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
     rope_kernel(const RopeArgs A) {
   constexpr int kLanes = DH / 16, kHeads = 32 / kLanes, kPieces = DH / 8;
-  __shared__ float2 turn[kMaxRows][DH / 2];
+  __shared__ __align__(128) float2 turn[kMaxRows][DH / 2];
   // A head's dimension j lies at j + j / 8 of its kPitch: neighbouring lanes' pieces and heads
   // are nine banks apart.  Behind them a zero.
   constexpr int kPitch = 18 * kLanes + (32 - 9 * kLanes % 32) % 32;
@@ -126,8 +119,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
   const int head0 = lane / kLanes;
   // The units' pieces come ahead through shared memory, which costs no registers: each lane
   // reads what it copied itself.  (Of dimension 256 with its stage there is room for one.)
+  // On lines of 128 bytes: 16 bytes off them the first measured case takes 55 us.
   constexpr int kAheadUnits = PAIRS != kAnywhere ? 3 : DH == 256 ? 1 : 2;
-  __shared__ uint4 ring[kWarps][kAheadUnits][2][32];
+  __shared__ __align__(128) uint4 ring[kWarps][kAheadUnits][2][32];
   int left = z - a, lu = a % A.passes, at_slot = 0;  // the one to load
   const uint4 *in = qkv + (size_t)(m0 + a / A.passes) * heads * kPieces + head0 * kPieces;
   auto ahead = [&](int to) {
@@ -166,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
     if (i < A.half) {
       int axis = 0, end = A.r.section[0];
       while (i >= end) end += A.r.section[++axis];
-      const uint64_t by_pos = turns_of(A.freq[i]);
+      const uint64_t by_pos = turns_of(__float_as_uint(A.freq[i]));
 #pragma unroll 1
       for (int r = tid / wide; r < rows; r += kThreads / wide) {
         const int64_t p = A.pos[(size_t)axis * c.M + m0 + r];
