@@ -415,6 +415,23 @@ def test_bad_batches_write_no_outputs(name):
     assert status == lbx.LBX_ETREE and (o == 55.0).all() and (lse == 55.0).all()
 
 
+WILD = [(2 ** 31 - 1, -2 ** 31), (1_800_000_000, -1_800_000_000), (2 ** 30, -2 ** 31), (-2 ** 31, 2 ** 31 - 1),
+        (2 ** 31 - 1, 2 ** 31 - 1), (-1, -2 ** 31)]
+
+
+@pytest.mark.parametrize("first,second", WILD)
+def test_starts_whose_differences_wrap_are_refused(first, second):
+    def change(inp):
+        inp["start"][1], inp["start"][2] = first, second
+    o, lse, status = bad_attention(change)
+    assert status == lbx.LBX_ETREE and (o == 55.0).all() and (lse == 55.0).all()
+    inp = commit_case([15, 31], [22, 22], [3, 20], 16)
+    change(inp)
+    k, v, out, status = run_commit(inp)
+    assert status == lbx.LBX_ETREE and out == [-3, -3]
+    assert same_bits(k, inp["k_pages"]) and same_bits(v, inp["v_pages"])
+
+
 def test_a_tree_of_65_nodes_is_refused():
     inp = R.make_attention([4], [65], 1, 1, 64, 16, kind="chain", seed=9)
     o, lse, status = run_attention(inp)

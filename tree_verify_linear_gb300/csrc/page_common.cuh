@@ -55,7 +55,7 @@ inline bool all_apart(std::initializer_list<Span> outs, std::initializer_list<Sp
 }
 
 // Whether a tree breaks the rules, for warp w of n: requests by warps, nodes by lanes.
-// (start has been found to rise from 0 to at most M, or the verdict does not matter.)
+// Requests whose rows request_bad refuses are passed over, whatever start holds.
 __device__ __forceinline__ int trees_bad(const lbx_page_cfg &c, const int32_t *start,
                                          const int32_t *parent, int w, int n) {
   int bad = 0;
@@ -65,7 +65,7 @@ __device__ __forceinline__ int trees_bad(const lbx_page_cfg &c, const int32_t *s
     const int s = start[b], e = start[b + 1];
 #pragma unroll
     for (int i = lane; i < LBX_ATTN_MAX_NODES; i += 32) {
-      if (s < 0 || i >= e - s || e > c.M) continue;
+      if (s < 0 || e < s || e > c.M || i >= e - s) continue;
       const int p = parent[s + i];
       bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
     }
