@@ -498,7 +498,7 @@ int lbx_cache_evict(const lbx_attn_cfg *cfg, int budget, int n_recent, const int
 typedef struct lbx_page_cfg {
   int L, Bq;      /* layers, requests (Bq <= LBX_PAGE_MAX_REQUESTS)             */
   int M;          /* rows of new tokens, padding included (>= 1)                */
-  int Hq, Hkv;    /* query / KV heads, Hq % Hkv == 0                            */
+  int Hq, Hkv;    /* query / KV heads, Hq % Hkv == 0, Hq * dh < 2^29            */
   int dh;         /* head dimension: 64, 128 or 256                             */
   int page;       /* positions per page: 16, 32, 64, 128 or 256                 */
   int n_pages;    /* pages of each layer's pool; L * n_pages * page < 2^31      */
@@ -565,7 +565,8 @@ typedef struct lbx_rope_cfg {
  *     slots are written, nothing else is touched
  * Sums and products are fp32, results rounded once.  A slot at or past
  * n_pages * page is reported as LBX_EINVAL through d_status and its row skipped.  Two
- * rows must not name one slot.  q_out must not overlap the other arrays.
+ * rows must not name one slot.  The outputs must not overlap the other arrays
+ * (q_out and qkv: LBX_EINVAL).
  */
 int lbx_qk_norm_rope(const lbx_page_cfg *cfg, const lbx_rope_cfg *rope, const uint16_t *qkv,
                      const float *q_weight, const float *k_weight, const float *inv_freq,
@@ -598,7 +599,8 @@ size_t lbx_paged_workspace_size(const lbx_page_cfg *cfg);
  * anything, NaN included; a key that one query of a request sees and another
  * does not has to have a finite value.  A query all of whose scores are -inf gets o = 0
  * and lse = -inf; one with a NaN among its scores gets NaN for both.
- * Hq / Hkv <= LBX_PAGED_MAX_GROUP.  Returns as lbx_window_attention.  Through
+ * Hq / Hkv <= LBX_PAGED_MAX_GROUP.  o, lse and the workspace must not overlap each other
+ * or the inputs (each other or q: LBX_EINVAL).  Returns as lbx_window_attention.  Through
  * d_status, with nothing written: LBX_ETREE if start does not rise from 0 to at
  * most M, a length is negative or beyond the table, or a tree breaks its rules.  A
  * page outside the pool is not read: LBX_EINVAL through d_status, and the outputs of

@@ -108,6 +108,30 @@ def test_commit_refuses_lengths_over_its_inputs(lib, on, size):
         assert call(lib, "commit", cfg(), args) == lbx.LBX_EINVAL, at
 
 
+@pytest.mark.parametrize("op", ["tables", "rope", "attention", "commit"])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_rows_of_a_gigabyte_are_refused(lib, op, dh):
+    assert call(lib, op, cfg(L=1, M=1, Hq=2 ** 29 // dh, Hkv=2 ** 22 // dh, dh=dh)) == lbx.LBX_EINVAL
+
+
+# 2 layers of 32 rows: q has 8 heads of 64, qkv 12; lse a word per head
+@pytest.mark.parametrize("at", [0, 2 * 32 * 12 * 128 - 16, 16 - 2 * 32 * 8 * 128])
+def test_rotation_refuses_queries_over_its_input(lib, at):
+    args = apart(9)
+    args[6] = args[0] + at
+    assert call(lib, "rope", cfg(), args) == lbx.LBX_EINVAL
+
+
+# q is 4, o 7, lse 8, the workspace 9
+@pytest.mark.parametrize("out,on,size,own", [(7, 4, 65536, 65536), (8, 4, 65536, 2048), (8, 7, 65536, 2048),
+                                             (9, 4, 65536, 4096), (9, 7, 65536, 4096), (9, 8, 2048, 4096)])
+def test_attention_refuses_outputs_over_queries_and_each_other(lib, out, on, size, own):
+    for at in (0, size - 16, 16 - own):
+        args = apart(10)
+        args[out] = args[on] + at
+        assert call(lib, "attention", cfg(), args) == lbx.LBX_EINVAL, at
+
+
 BAD_ROPE = [dict(rot=-2), dict(rot=3), dict(rot=66), dict(axes=0), dict(axes=5), dict(pairing=2),
             dict(pairing=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(rot=18)]
 

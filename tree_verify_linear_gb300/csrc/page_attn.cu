@@ -52,6 +52,10 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   if ((parent && !aligned_to(parent, 4)) || (lse && !aligned_to(lse, 4)) ||
       !aligned_to(workspace, 16) || (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
+  // tiles of one request read q while others write o
+  const size_t rows = (size_t)c->L * c->M * c->Hq, values = rows * c->dh * 2;
+  if (!all_apart({{o, values}, {lse, lse ? rows * 4 : 0}, {workspace, need}}, {{q, values}}))
+    return LBX_EINVAL;
   PageArgs A = {};
   A.c = *c;
   A.G = c->Hq / c->Hkv, A.tp = kRows / A.G, A.box = c->page < 64 ? c->page : 64;

@@ -33,7 +33,8 @@ inline bool cfg_ok(const lbx_page_cfg *c) {
   if (lm > most || lm * c->Hq > most) return false;
   if ((long long)c->n_pages * c->page > most / c->L) return false;
   if ((long long)c->max_pages * c->page > (1LL << 30)) return false;
-  return (long long)c->Hkv * c->dh * 2 < (1LL << 30) && (long long)c->L * c->Hkv < (1LL << 30);
+  // and values of a row
+  return (long long)c->Hq * c->dh < (1LL << 29) && (long long)c->L * c->Hkv < (1LL << 30);
 }
 
 struct Span {

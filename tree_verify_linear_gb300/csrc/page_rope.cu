@@ -361,6 +361,8 @@ extern "C" int lbx_qk_norm_rope(const lbx_page_cfg *c, const lbx_rope_cfg *rope,
       (d_status && !aligned_to(d_status, 4)))
     return LBX_EINVAL;
   const int heads = c->Hq + 2 * c->Hkv, at_once = 512 / c->dh;
+  const size_t head = (size_t)c->L * c->M * c->dh * 2;
+  if (!apart({q_out, head * c->Hq}, {qkv, head * heads})) return LBX_EINVAL;
   RopeArgs A = {*c, *rope, rope->rot / 2, 1, 1, (heads + at_once - 1) / at_once,
                 reinterpret_cast<const uint4 *>(qkv), q_weight, k_weight, inv_freq, pos, slot,
                 reinterpret_cast<uint4 *>(q_out), reinterpret_cast<uint4 *>(k_pages),
