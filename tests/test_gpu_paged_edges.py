@@ -1,0 +1,65 @@
+"""GPU parity of the paged cache's operators at the edges of their paths: lists of as
+many pieces as one call joins, values that are not finite, angles far below one.  The
+bounds are page_ref's unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import page_ref as R
+from test_gpu_paged import built, check_attention, page_cfg, run_attention, status_word  # noqa: F401
+from tree_verify_linear_gb300 import lbx
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- few rows over the longest list that their path takes -------------------------
+
+def longest(pieces_off=9, dh=64, **kw):
+    """One request of one layer and KV head with two units of 128 keys per CTA, less
+    `pieces_off`: the most pieces that few rows join."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    units = 2 * (sms // 2 * 2) - pieces_off
+    return units, R.make_attention([128 * units - 5], [1], 4, 1, dh, 16, seed=21, **kw)
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("off", [0, 9])
+def test_one_token_over_the_longest_list_of_few_rows(dh, off):
+    check_attention(longest(off, dh)[1], device="cuda", calls=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_pieces_of_minus_infinity_among_the_most(dtype):
+    """Units of keys whose scores are all -inf, at both ends of the list: the row is that of a
+    request without them."""
+    units, inp = longest(dtype=dtype)
+    inp["q"] = inp["q"].abs() + 0.5
+    dead = list(range(0, 3)) + list(range(units // 2, units - 1))
+    pages = [8 * u + j for u in dead for j in range(8)]
+    alive = [p for p in range(8 * units) if p not in set(pages)]
+    table = inp["block_table"]
+    inp["k_pages"][:, table[0, pages].long()] = -torch.inf
+    o, lse, status = run_attention(inp, calls=2)
+    assert status == 0
+    ref, ref_lse, tol, lse_tol = R.attention(
+        dict(inp, block_table=table[:, alive], ctx_len=inp["ctx_len"] - 128 * len(dead)), device="cuda")
+    assert (np.abs(o.double().numpy() - ref) <= tol).all()
+    assert (np.abs(lse.double().numpy() - ref_lse) <= lse_tol).all()
+
+
+def test_pages_outside_the_pool_among_the_most_pieces():
+    """They are reported, and the workspace serves the next call."""
+    units, inp = longest()
+    cfg, d = page_cfg(inp), {k: None if v is None else v.cuda() for k, v in inp.items()}
+    ws, status, o = lbx.new_paged_workspace(cfg), status_word(), torch.zeros_like(d["q"])
+    bad = d["block_table"].clone()
+    bad[0, 8 * (units // 2):8 * (units - 1)] = -1
+    torch.cuda.synchronize()
+    for table in (bad, d["block_table"]):
+        lbx.lbx_paged_attention(cfg, d["start"], d["ctx_len"], table, d["q"], d["k_pages"], d["v_pages"], o, ws,
+                                d_status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == (lbx.LBX_EINVAL if table is bad else 0)
+        status.zero_()
+    ref, _, tol, _ = R.attention(inp, device="cuda")
+    assert (np.abs(o.cpu().double().numpy() - ref) <= tol).all()

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "cache_ptx.cuh"
+#include "cache_walk.cuh"
 #include "page_walk.cuh"
 
 namespace lbx {
@@ -125,7 +126,11 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, Window wi
   constexpr int kPitch = DH + 4;                      // of a row, so that fewer share a bank
   float *sums = reinterpret_cast<float *>(smem);      // [warp][row][DH]
   float *m_of = sums + kWarps * kFewMost * kPitch, *l_of = m_of + kWarps * kFewMost;  // [warp][row]
-  int *flag = reinterpret_cast<int *>(l_of + kWarps * kFewMost);
+  // last of the list's pieces; behind all that the join keeps (m and l of every piece, the rows'
+  // sums), which it begins to write while warps still read the flag
+  constexpr int kMet = kWarps * kFewMost * (kPitch + 2);
+  constexpr int kJoined = (2 * kFewUnits * cache::kMaxCtas + 1) * kFewMost;
+  int *flag = reinterpret_cast<int *>(sums + (kMet > kJoined ? kMet : kJoined));
   const float sl2 = A.scale_log2;
   bool inside = true;
 #pragma unroll 1
