@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import page_ref as R
-from test_gpu_paged import built, check_attention, page_cfg, run_attention, status_word  # noqa: F401
+from test_gpu_paged import (built, check_attention, page_cfg, rope_inputs, run_attention,  # noqa: F401
+                            run_rope, status_word)
 from tree_verify_linear_gb300 import lbx
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +64,34 @@ def test_pages_outside_the_pool_among_the_most_pieces():
         status.zero_()
     ref, _, tol, _ = R.attention(inp, device="cuda")
     assert (np.abs(o.cpu().double().numpy() - ref) <= tol).all()
+
+
+# ---- dimensions that do not turn ---------------------------------------------------
+
+ODD = [torch.inf, -torch.inf, torch.nan, -0.0]
+
+
+@pytest.mark.parametrize("pairing,dh,half", [("adjacent", 64, 3), ("adjacent", 128, 37), ("adjacent", 256, 64),
+                                             ("halves", 64, 3), ("halves", 128, 45), ("halves", 256, 5),
+                                             ("halves", 128, 16), ("halves", 64, 0), ("adjacent", 64, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_dimensions_that_do_not_turn_stay(pairing, dh, half, dtype):
+    """Without a norm the dimensions past the last pair are the input's, whatever stands beside
+    them; and what turns does not see them."""
+    inp = rope_inputs(M=24, Hq=4, Hkv=2, dh=dh, sections=[half], dtype=dtype, norm=False, seed=5)
+    clean = run_rope(inp, 4, [half], pairing)
+    rng = np.random.default_rng(6)
+    x = inp["qkv"]
+    for i in range(2 * half, dh):
+        at = torch.from_numpy(rng.random(x.shape[:3]) < 0.3)
+        x[..., i][at] = ODD[i % 4]
+    q, k, _, status = run_rope(inp, 4, [half], pairing)
+    assert status == 0
+    slot = inp["slot"].long()
+    for got, was, came in ((q, clean[0], x[:, :, :4]),
+                           (k.flatten(1, 2)[:, slot], clean[1].flatten(1, 2)[:, slot], x[:, :, 4:6])):
+        assert torch.equal(got[..., :2 * half], was[..., :2 * half])
+        rest, want = got[..., 2 * half:], came[..., 2 * half:]
+        number = ~want.isnan()
+        assert torch.equal(rest.isnan(), ~number)
+        assert torch.equal(rest[number].view(torch.int16), want[number].view(torch.int16))

@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
   constexpr int kLanes = DH / 16, kHeads = 32 / kLanes, kPieces = DH / 8;
   __shared__ __align__(128) float2 turn[kMaxRows][DH / 2];
   // A head's dimension j lies at j + j / 8 of its kPitch: neighbouring lanes' pieces and heads
-  // are nine banks apart.  Behind them a zero.
+  // are nine banks apart.  Behind them a zero (-0: a dimension that does not turn takes it times
+  // a sine of 0, which leaves the sign of a zero).
   constexpr int kPitch = 18 * kLanes + (32 - 9 * kLanes % 32) % 32;
   __shared__ float stage[PAIRS == kAnywhere ? kWarps : 1][kHeads * kPitch + 1];
   __shared__ int slots[kMaxRows];
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
   int other[PAIRS == kAnywhere ? 16 : 1];
   const bool second_turns = 2 * A.half > 8 * kLanes;  // any of the lanes' second pieces
   if constexpr (PAIRS == kAnywhere) {
-    if (lane == 0) stage[warp][kHeads * kPitch] = 0.f;
+    if (lane == 0) stage[warp][kHeads * kPitch] = -0.f;
     const int full = A.half >> 3, over = A.half & 7;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -190,6 +191,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
       const int down = 9 * (p - full) - over + i - (i < over ? 1 : 0);
       other[k] = j < 2 * A.half ? head0 * kPitch + (j < A.half ? up : down) : kHeads * kPitch;
     }
+  }
+  // which of the lane's pairs turn: the others' values stay, whatever their neighbours are
+  uint32_t turned = 0;
+  if constexpr (PAIRS == kAdjacent) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turned |= (uint32_t)((i < 4 ? 4 * p0 + i : 4 * p1 + i - 4) < A.half) << i;
   }
   constexpr bool kKeep = PAIRS == kAnywhere;  // the queries' weights, in registers
   uint64_t wq[8];
@@ -285,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 f = apart2(x[i]);
-          x[i] = fma2(both(f.y, f.x), sin2[i], mul2(x[i], cos2[i]));
+          const uint64_t y = fma2(both(f.y, f.x), sin2[i], mul2(x[i], cos2[i]));
+          x[i] = turned >> i & 1 ? y : x[i];
         }
       } else {
         float *mine = stage[warp] + head0 * kPitch;
