@@ -557,8 +557,8 @@ typedef struct lbx_rope_cfg {
  *   qkv [L][M][Hq + 2 Hkv][dh] of cfg->dtype: each row's query, key and value heads
  *   q_weight, k_weight [L][dh] fp32 (NULL: no norm)
  *   inv_freq [rot/2] fp32 (may be NULL when rot == 0; finite): any scaling of
- *     positions is in them.  t is taken modulo a turn exactly, then rounded to 2^-26 of
- *     a turn (to fp32 where it is small), at every position
+ *     positions is in them.  Modulo a turn t is off by less than |pos| 2^-64 of a turn,
+ *     then rounded to fp32: by 2^-24 of itself, 2^-26 of a turn at most
  *   pos [axes][M] int32, any values; slot [M] int32: a row's place in every layer's
  *     pool; a negative one marks a row that is skipped (padding)
  *   q_out [L][M][Hq][dh] out; k_pages, v_pages [L][n_pages][page][Hkv][dh]: the rows'

@@ -95,3 +95,33 @@ def test_dimensions_that_do_not_turn_stay(pairing, dh, half, dtype):
         number = ~want.isnan()
         assert torch.equal(rest.isnan(), ~number)
         assert torch.equal(rest[number].view(torch.int16), want[number].view(torch.int16))
+
+
+# ---- small angles ------------------------------------------------------------------
+
+@pytest.mark.parametrize("pairing", ["halves", "adjacent"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("half", [32, 29])
+def test_angles_far_below_one_keep_their_digits(pairing, dtype, half):
+    """One value of a pair is 0, so that the other one's sine stands alone: it is off by 16 2^-24
+    of itself (the frequency's fraction of a turn to 2^-24, its product, the conversion, pi, the
+    sine, the product) and the rounding of the result, in f16 half a step of 2^-24 at most."""
+    M, dh = 16, 64
+    inp = rope_inputs(M=M, Hq=2, Hkv=1, dh=dh, sections=[half], dtype=dtype, norm=False)
+    inp["inv_freq"] = (10.0 ** (-3 - 6 * torch.arange(half).double() / (half - 1))).float()
+    inp["pos"][0] = torch.tensor([1, -1, 2, -2, 3, -3, 5, -5, 7, -7, 100, -100, 1001, -1001, 4000, -4000],
+                                 dtype=torch.int32)
+    first = torch.arange(half) if pairing == "halves" else 2 * torch.arange(half)
+    second = first + (half if pairing == "halves" else 1)
+    for zero, one, sign in ((first, second, -1.0), (second, first, 1.0)):
+        x = inp["qkv"]
+        x[..., one], x[..., zero] = 1.5, 0.0
+        q, k, _, status = run_rope(inp, 2, [half], pairing)
+        assert status == 0
+        t = inp["pos"][0].double()[:, None] * inp["inv_freq"].double()
+        ref = sign * 1.5 * torch.sin(t)
+        u = R.U[R.DTYPE[dtype]]
+        tol = (u + 17 * 2.0 ** -24) * ref.abs() + (2.0 ** -25 if dtype == "f16" else 0.0)
+        for got in (q[0], k.flatten(1, 2)[0, inp["slot"].long()]):
+            off = (got[..., zero].double() - ref[:, None]).abs() / tol[:, None]
+            assert off.max() <= 1, float(off.max())

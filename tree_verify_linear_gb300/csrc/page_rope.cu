@@ -6,7 +6,7 @@
 // is taken once per pair and CTA as a 64-bit fixed-point fraction of a turn, in integers
 // (two doubles for 1 / (2 pi) took 1 us more at 5000 rows: an SM does few of them a cycle), times
 // pos modulo 2^64: no position is so far that an angle loses digits, as it does in a
-// product of two floats (2^-24 of a million radians).  Cosines and sines lie in shared memory
+// product of two floats (2^-24 of a million radians), and no angle so small.  Cosines and sines lie in shared memory
 // for all heads of the row, and from there in a lane's registers for as long as its warp stays
 // with the row.  Then the heads, a lane for two 16-byte pieces of one: with pairs in halves
 // those that turn with each other (where rot is a multiple of 16; else they meet in shared
@@ -164,10 +164,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAIRS))
       const uint64_t by_pos = turns_of(__float_as_uint(A.freq[i]));
 #pragma unroll 1
       for (int r = tid / wide; r < rows; r += kThreads / wide) {
-        const int64_t p = A.pos[(size_t)axis * c.M + m0 + r];
-        const int32_t part_of_turn = (int32_t)(((uint64_t)p * by_pos) >> 32);
         float2 cs;
-        sincospif((float)part_of_turn * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31
+        sincospif(half_turns(A.pos[(size_t)axis * c.M + m0 + r], by_pos), &cs.y, &cs.x);
         turn[r][i] = cs;
       }
     }

@@ -1,4 +1,5 @@
-// page_turn.cuh -- a frequency as a fraction of a turn, for lbx_qk_norm_rope.
+// page_turn.cuh -- a frequency as a fraction of a turn, and a position's angle, for
+// lbx_qk_norm_rope.
 #pragma once
 
 #include <cstdint>
@@ -30,6 +31,13 @@ __host__ __device__ inline uint64_t turns_of(uint32_t f) {
     turns = (by ? lo >> by | hi << (64 - by) : lo) + (below >> (under & 63) & 1);
   }
   return f >> 31 ? 0 - turns : turns;
+}
+
+// pos times a frequency (by_pos, of turns_of) as halves of a turn, -1 .. 1: the product modulo a
+// turn is exact, and all 64 bits of it go into one conversion, so that an angle has fp32's 24
+// digits however small it is.
+__host__ __device__ inline float half_turns(int32_t pos, uint64_t by_pos) {
+  return (float)(int64_t)((uint64_t)(int64_t)pos * by_pos) * 1.0842021724855044e-19f;  // 2^-63
 }
 
 }  // namespace paged
