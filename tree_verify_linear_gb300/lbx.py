@@ -332,12 +332,10 @@ def _refuse(t, shape, dtype, name):
 def _at(t, shape, dtype, name):
     """The address of a contiguous CUDA tensor of this shape and type (the calls
     below check a dozen of them, which for a small call costs as much as the
-    kernel: one line for the ordinary case; only tensors have torch's types)."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
+    kernel: one line for the ordinary case)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        return t.data_ptr()
     return _refuse(t, shape, dtype, name)
 
 
