@@ -594,10 +594,13 @@ size_t lbx_paged_workspace_size(const lbx_page_cfg *cfg);
  *   or NULL; q [L][M][Hq][dh], k_pages, v_pages [L][n_pages][page][Hkv][dh] of
  *   cfg->dtype; o [L][M][Hq][dh] out of cfg->dtype, lse [L][M][Hq] fp32 out (may be
  *   NULL).
- * Sums and softmax statistics are fp32; the weights meet V in its type, rounded once.
+ * Sums and softmax statistics are fp32; the weights meet V in its type, rounded once (at
+ * most 8 rows, tokens times Hq / Hkv, of every request over few keys: in two parts, which
+ * are good to 2^-16 of a weight, 2^-22 in f16).
  * What a request's pages hold past its last token, and other pages, may be
  * anything, NaN included; a key that one query of a request sees and another
- * does not has to have a finite value.  A query all of whose scores are -inf gets o = 0
+ * does not has to have a finite value; one that is not finite leaves that dimension of o
+ * without a meaning (infinite or NaN).  A query all of whose scores are -inf gets o = 0
  * and lse = -inf; one with a NaN among its scores gets NaN for both.
  * Hq / Hkv <= LBX_PAGED_MAX_GROUP.  o, lse and the workspace must not overlap each other
  * or the inputs (each other or q: LBX_EINVAL).  Returns as lbx_window_attention.  Through

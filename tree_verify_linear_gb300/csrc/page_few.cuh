@@ -6,7 +6,9 @@
 // products are 8 (of 16) rows by 16 keys: warp-wide products (mma.sync) whose operands
 // come straight from memory, a lane for 16 bytes of a row, with the dimensions in an order of
 // their own (of K and Q the same, so that sums do not see it).  The weights of the warp's
-// own softmax are an operand of its product with V as they come out of the first.  The
+// own softmax are an operand of its product with V as they come out of the first: rounded to V's
+// type in the upper eight rows, what that loses in the lower eight, so that they are good to
+// 2^-16 (f16 2^-22) at no further product.  The
 // warps meet in shared memory; lists of more than one unit are joined by the CTA that
 // finishes last, in the units' order.  Written for the number of instructions: each is
 // fetched once and runs once (on CUDA cores, with several times as many, a call of one token
@@ -57,6 +59,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+  else return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+// What a and b lose in pack2, rounded in its turn.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t packed) {
+  const float2 f = unpack2<F16>(packed);
+  return pack2<F16>(a - f.x, b - f.y);
+}
+
 // One arrival that others of the GPU see after what this block has written before its last
 // barrier; what they wrote before theirs is seen after it.
 __device__ __forceinline__ unsigned arrive_count(unsigned int *count) {
@@ -94,20 +108,21 @@ __device__ __forceinline__ int scan32(int v) {
   return v;
 }
 
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8) of 16-bit values; rows 8-15 of A are zeros.
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8) of 16-bit values; a0 and a2 are the lane's of A's
+// rows 0-7, a1 and a3 of rows 8-15.
 template <bool F16>
-__device__ __forceinline__ void mma_8rows(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
-                                          uint32_t b1) {
+__device__ __forceinline__ void mma_16rows(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Floats of a unit's partial: a row's sums over V, then m (base 2) and l of the rows.
@@ -209,8 +224,8 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, Window wi
       for (int s = 0; s < DH / 32; ++s)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          mma_8rows<F16>(x[t], q[s].x, q[s].y, kx[t][s].x, kx[t][s].y);
-          mma_8rows<F16>(x[t], q[s].z, q[s].w, kx[t][s].z, kx[t][s].w);
+          mma_16rows<F16>(x[t], q[s].x, 0u, q[s].y, 0u, kx[t][s].x, kx[t][s].y);
+          mma_16rows<F16>(x[t], q[s].z, 0u, q[s].w, 0u, kx[t][s].z, kx[t][s].w);
         }
 #pragma unroll
       for (int d = kAhead; d < kWide; ++d) load_v(64 * d, v[d]);
@@ -227,12 +242,12 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, Window wi
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const float ref = m == -INFINITY ? 0.f : m - kUp;
-      uint32_t p[2];
+      uint32_t p[2], rest[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float p0 = ptx::ex2(x[t][0] - ref), p1 = ptx::ex2(x[t][1] - ref);
         sum += p0 + p1;
-        p[t] = pack2<F16>(p0, p1);
+        p[t] = pack2<F16>(p0, p1), rest[t] = pack2_rest<F16>(p0, p1, p[t]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -249,9 +264,9 @@ __device__ __forceinline__ bool few_rows(const PageArgs &A, int units, Window wi
           };
           const uint32_t half = t & 1 ? 0x7632u : 0x5410u;
           float f[4] = {};
-          mma_8rows<F16>(f, p[0], p[1], __byte_perm(word(0), word(1), half),
-                         __byte_perm(word(2), word(3), half));
-          y[t] = f[0], y[8 + t] = f[1];
+          mma_16rows<F16>(f, p[0], rest[0], p[1], rest[1], __byte_perm(word(0), word(1), half),
+                          __byte_perm(word(2), word(3), half));
+          y[t] = f[0] + f[2], y[8 + t] = f[1] + f[3];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
