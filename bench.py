@@ -104,7 +104,8 @@ OTHER_OPS = ("accept_walk.cu", "ddtree_build.cu", "tree_attn.cu", "cache_common.
              "cache_attn_256.cu", "cache_ptx.cuh", "cache_walk.cuh", "cache_mass.cu", "cache_evict.cu",
              "page_common.cuh", "page_walk.cuh", "page_turn.cuh", "page_tables.cu", "page_rope.cu", "page_commit.cu",
              "page_attn.cu", "page_attn.cuh", "page_few.cuh", "page_attn_64.cu", "page_attn_128.cu",
-             "page_attn_128_wide.cu", "page_attn_256.cu")
+             "page_attn_128_wide.cu", "page_attn_256.cu", "page_attn_64_split.cu", "page_attn_128_split.cu",
+             "page_attn_128_wide_split.cu", "page_attn_256_split.cu")
 
 
 def kernel_source_hash(op: str = "verify") -> str:

@@ -495,6 +495,12 @@ int lbx_cache_evict(const lbx_attn_cfg *cfg, int budget, int n_recent, const int
 #define LBX_PAGE_MAX_REQUESTS 2048
 #define LBX_PAGED_MAX_GROUP 128 /* lbx_paged_attention: Hq / Hkv */
 
+/* How lbx_paged_attention's softmax weights meet V, whose type has 16 bits.  SPLIT is as
+ * accurate as lbx_window_attention in bf16 and takes a tenth (one layer of draft trees or
+ * single tokens) to two fifths longer (prompts; many layers at head dimension 256). */
+#define LBX_WEIGHTS_ROUNDED 0 /* rounded once: 2^-8 of a weight in bf16, 2^-11 in f16 */
+#define LBX_WEIGHTS_SPLIT 1   /* in two parts: 2^-16 and 2^-22                        */
+
 typedef struct lbx_page_cfg {
   int L, Bq;      /* layers, requests (Bq <= LBX_PAGE_MAX_REQUESTS)             */
   int M;          /* rows of new tokens, padding included (>= 1)                */
@@ -505,6 +511,7 @@ typedef struct lbx_page_cfg {
   int max_pages;  /* columns of the block table; max_pages * page <= 2^30       */
   int dtype;      /* LBX_BF16 or LBX_F16                                        */
   float scale;    /* scale of q . k (> 0, finite)                               */
+  int weights;    /* LBX_WEIGHTS_*: how softmax weights meet V                  */
 } lbx_page_cfg;
 
 /*
@@ -594,9 +601,9 @@ size_t lbx_paged_workspace_size(const lbx_page_cfg *cfg);
  *   or NULL; q [L][M][Hq][dh], k_pages, v_pages [L][n_pages][page][Hkv][dh] of
  *   cfg->dtype; o [L][M][Hq][dh] out of cfg->dtype, lse [L][M][Hq] fp32 out (may be
  *   NULL).
- * Sums and softmax statistics are fp32; the weights meet V in its type, rounded once (at
- * most 8 rows, tokens times Hq / Hkv, of every request over few keys: in two parts, which
- * are good to 2^-16 of a weight, 2^-22 in f16).
+ * Sums and softmax statistics are fp32; the weights meet V in its type, as cfg->weights says
+ * (at most 8 rows, tokens times Hq / Hkv, of every request over few keys: always in two parts,
+ * which cost nothing there).
  * What a request's pages hold past its last token, and other pages, may be
  * anything, NaN included; a key that one query of a request sees and another
  * does not has to have a finite value; one that is not finite leaves that dimension of o

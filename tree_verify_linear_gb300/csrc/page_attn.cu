@@ -89,9 +89,11 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   if (nsm < 2) return LBX_ECUDA;
   const int grid = nsm / 2 * 2;
   const bool f16 = c->dtype == LBX_F16;
-  const cudaError_t e = c->dh == 64    ? launch_page_attn<64, false>(f16, maps, A, grid, stream)
-                        : c->dh == 256 ? launch_page_attn<256, false>(f16, maps, A, grid, stream)
-                        : wide         ? launch_page_attn<128, true>(f16, maps, A, grid, stream)
-                                       : launch_page_attn<128, false>(f16, maps, A, grid, stream);
-  return e == cudaSuccess ? LBX_OK : LBX_ECUDA;
+  const bool split = c->weights == LBX_WEIGHTS_SPLIT;
+  const auto launch = c->dh == 64    ? split ? launch_page_attn<64, false, true> : launch_page_attn<64, false, false>
+                      : c->dh == 256 ? split ? launch_page_attn<256, false, true> : launch_page_attn<256, false, false>
+                      : wide         ? split ? launch_page_attn<128, true, true> : launch_page_attn<128, true, false>
+                      : split        ? launch_page_attn<128, false, true>
+                                     : launch_page_attn<128, false, false>;
+  return launch(f16, maps, A, grid, stream) == cudaSuccess ? LBX_OK : LBX_ECUDA;
 }

@@ -9,9 +9,15 @@
 // The running reference of a row moves only when a block's maximum exceeds it by more
 // than 2^8, so that O is rescaled rarely; the result is the same softmax taken from
 // another reference.  P is rounded to the 16-bit type once (2^-8 of a weight in bf16,
-// 2^-11 in f16), which adds about as much error as the rounding of o (a second product
-// for what bf16 leaves would cost half the rate again); f16 weights are taken 2^7 times
-// as large, so that what falls below its range is 2^-32 of the reference.
+// 2^-11 in f16), which adds about as much error as the rounding of o, or (SPLIT, the
+// caller's choice) takes two parts, P rounded and what that loses, each with a product of its
+// own: good to 2^-16 and 2^-22.  The second product is half of the tensor cores' work again,
+// more than copies hide at head dimension 256: there single tokens over long caches (4 layers, 16
+// requests of 8001 to 16384 keys, bf16) take 627 us instead of 481, trees of 22 on 16 layers 258
+// instead of 200, five of them on one layer 45.5 instead of 42.7, the chunk below 309 instead of
+// 221; at 128 the tokens below 561 instead of 487, the prompts 672 instead of 515.  f16
+// weights are taken 2^7 times as large, so that what falls below its range is 2^-32 of
+// the reference.
 //
 // Head dimensions 64 and 128: a CTA holds two subtiles, each with its own four softmax
 // warps (a row per thread), so that the tensor cores work on one while the other's softmax
@@ -244,7 +250,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-template <int DH, bool F16, bool WIDE>
+template <int DH, bool F16, bool WIDE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     page_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ PageArgs A) {
   using Y = Lay<DH, WIDE>;
@@ -577,13 +583,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = vdesc + (uint64_t)(stage * (Y::kStage >> 4));
         if (one) {
 #pragma unroll
-          for (int i = i0; i < i1; ++i) {
-            const uint32_t pa = tmem + buf * kBlk + 8 * i, d = tmem + Y::kColO + e * DH;
-            const uint64_t vb = vd + (uint64_t)(i * (2048 >> 4));
-            const uint32_t acc = i > 0 ? 1u : later;
-            if constexpr (PAIR) ptx::mma_16_ts_pair(d, pa, vb, idesc_o, acc);
-            else ptx::mma_bf16_ts(d, pa, vb, idesc_o, acc);
-          }
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+            for (int i = i0; i < i1; ++i) {
+              const uint32_t pa = tmem + buf * kBlk + part * (kBlk / 2) + 8 * i;
+              const uint32_t d = tmem + Y::kColO + e * DH;
+              const uint64_t vb = vd + (uint64_t)(i * (2048 >> 4));
+              const uint32_t acc = i > 0 || part > 0 ? 1u : later;
+              if constexpr (PAIR) ptx::mma_16_ts_pair(d, pa, vb, idesc_o, acc);
+              else ptx::mma_bf16_ts(d, pa, vb, idesc_o, acc);
+            }
           if (i1 == kBlk / 16) commit(&o_bar[ONE ? buf : e]);
         }
         __syncwarp();
@@ -785,8 +794,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
             sum[e & 3] = add2(sum[e & 3], both(p0, p1));
             pk[e] = pack2<F16>(p0, p1);
+            if constexpr (SPLIT) sv[e0 + 2 * e] = p0, sv[e0 + 2 * e + 1] = p1;
           }
           ptx::tmem_st16(sc + (ONE ? hf * 32 : 0) + e0 / 2, pk);
+          if constexpr (SPLIT) {  // the second part, over the rest of S
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              pk[e] = pack2_rest<F16>(sv[e0 + 2 * e], sv[e0 + 2 * e + 1], pk[e]);
+            ptx::tmem_st16(sc + kBlk / 2 + (ONE ? hf * 32 : 0) + e0 / 2, pk);
+          }
           if (!ONE && e0 == 32 * (kEarly / 32 - 1)) {  // most of the weights: their product may begin
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -1046,13 +1062,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Launches of one head dimension (instances in page_attn_*.cu).
-template <int DH, bool WIDE>
+template <int DH, bool WIDE, bool SPLIT>
 cudaError_t launch_page_attn(bool f16, const PageMaps &maps, const PageArgs &A, int grid,
                              cudaStream_t stream);
-template <int DH, bool F16, bool WIDE>
+template <int DH, bool F16, bool WIDE, bool SPLIT>
 cudaError_t launch_page_attn_of(const PageMaps &maps, const PageArgs &A, int grid,
                                 cudaStream_t stream) {
-  auto kernel = page_attn_kernel<DH, F16, WIDE>;
+  auto kernel = page_attn_kernel<DH, F16, WIDE, SPLIT>;
   constexpr int bytes = Lay<DH, WIDE>::kSmemTotal;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;

@@ -27,6 +27,7 @@ inline bool cfg_ok(const lbx_page_cfg *c) {
     return false;
   if (c->n_pages < 1 || c->max_pages < 1) return false;
   if (c->dtype != LBX_BF16 && c->dtype != LBX_F16) return false;
+  if (c->weights != LBX_WEIGHTS_ROUNDED && c->weights != LBX_WEIGHTS_SPLIT) return false;
   if (!(c->scale > 0.f) || !isfinite(c->scale)) return false;
   // rows, heads of rows, slots of all layers and positions have 32-bit numbers
   const long long lm = (long long)c->L * c->M, most = 0x7fffffffLL;

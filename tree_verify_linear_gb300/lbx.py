@@ -40,6 +40,7 @@ LBX_BF16, LBX_F16 = 0, 1
 LBX_EVICT_MAX_T = 1 << 20
 LBX_PAGE_MAX_REQUESTS, LBX_PAGED_MAX_GROUP = 2048, 128
 LBX_ROPE_HALVES, LBX_ROPE_ADJACENT, LBX_ROPE_MAX_AXES = 0, 1, 4
+LBX_WEIGHTS_ROUNDED, LBX_WEIGHTS_SPLIT = 0, 1
 
 
 class LbxError(RuntimeError):
@@ -66,7 +67,7 @@ class lbx_page_cfg(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int), ("Bq", ctypes.c_int), ("M", ctypes.c_int),
                 ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("dh", ctypes.c_int),
                 ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
-                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("weights", ctypes.c_int)]
 
 
 class lbx_rope_cfg(ctypes.Structure):
@@ -435,10 +436,12 @@ def lbx_cache_evict(cfg, budget, n_recent, ctx_len, seen, parent, accepted, k_tr
 
 
 def make_page_cfg(L, Bq, M, Hq, Hkv, dh, page, n_pages, max_pages, dtype=LBX_BF16,
-                  scale=None) -> lbx_page_cfg:
-    """Config of the paged cache's operators; scale defaults to 1/sqrt(dh)."""
+                  scale=None, weights=LBX_WEIGHTS_ROUNDED) -> lbx_page_cfg:
+    """Config of the paged cache's operators; scale defaults to 1/sqrt(dh), weights says how
+    the attention's softmax weights meet V (LBX_WEIGHTS_SPLIT: in two 16-bit parts)."""
     return lbx_page_cfg(L=L, Bq=Bq, M=M, Hq=Hq, Hkv=Hkv, dh=dh, page=page, n_pages=n_pages,
-                        max_pages=max_pages, dtype=dtype, scale=dh ** -0.5 if scale is None else scale)
+                        max_pages=max_pages, dtype=dtype, scale=dh ** -0.5 if scale is None else scale,
+                        weights=weights)
 
 
 def make_rope_cfg(sections, eps=1e-6, pairing=LBX_ROPE_HALVES) -> lbx_rope_cfg:
