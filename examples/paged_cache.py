@@ -7,7 +7,10 @@ and values into their pages (lbx_qk_norm_rope), and attends over the pages
 (lbx_paged_attention).  Prompts come in chunks of tokens; after them every
 request verifies a draft tree per round: the draft's top-K scores become a tree
 (lbx_ddtree_build), the target's choices walk it (lbx_accept_walk), and the
-accepted path stays in the cache (lbx_page_commit).  Projections, logits and draft
+accepted path stays in the cache (lbx_page_commit).  The tree's arrays have N nodes per
+request, unused ones at the end; the paged calls take rows without gaps, so that nodes are
+packed on the way (a draft of few candidates gives a smaller tree, and a request may
+have a smaller budget, 1 for none).  Projections, logits and draft
 scores are synthetic; everything stays on the device.
 
     python examples/paged_cache.py [--rounds 10] [--chunk 96]
@@ -25,6 +28,7 @@ L, BQ, N, HQ, HKV, DH = 2, 3, 22, 24, 4, 256  # layers, requests, nodes, heads, 
 PAGE, N_PAGES, WIDTH, ROT = 64, 48, 16, 64
 VOCAB, DEPTH, TOPK = 1000, 8, 4
 PROMPTS = (300, 77, 150)
+MOST = (N, N, N)  # nodes that each request's tree may have
 
 
 class Server:
@@ -57,7 +61,8 @@ class Server:
                             self.n_free2, start, slot, pos[0], d_status=self.status)
         self.held, self.held2, self.n_free, self.n_free2 = self.held2, self.held, self.n_free2, self.n_free
         if depth is not None:  # a tree's nodes stand at their depth behind the context
-            pos = (self.ctx[:, None] + depth).view(1, rows)
+            pos = self.pack(self.ctx[:, None] + depth, new).view(1, rows)
+            parent = self.pack(parent, new)
         qkv = torch.randn(L, rows, HQ + 2 * HKV, DH, generator=self.gen, device="cuda", dtype=torch.bfloat16)
         q = torch.zeros(L, rows, HQ, DH, dtype=torch.bfloat16, device="cuda")
         lbx.lbx_qk_norm_rope(cfg, self.rope, qkv, self.inv_freq, pos, slot, q, self.k_pages, self.v_pages,
@@ -66,6 +71,12 @@ class Server:
         lbx.lbx_paged_attention(cfg, start, self.ctx, self.table, q, self.k_pages, self.v_pages, o, self.ws,
                                 parent=parent, lse=lse, d_status=self.status)
         return {"cfg": cfg, "start": start, "q": q, "o": o, "lse": lse, "parent": parent}
+
+    def pack(self, x, n_nodes):
+        """Nodes [BQ][N] as rows: request after request, without the unused ones (-1 behind)."""
+        node, end = torch.arange(N, device="cuda"), n_nodes.cumsum(0)
+        row = torch.where(node < n_nodes[:, None], (end - n_nodes)[:, None] + node, BQ * N)
+        return torch.full((BQ * N + 1,), -1, **self.i32).scatter_(0, row.flatten(), x.flatten())[:-1]
 
     def prompts(self, chunk):
         left = torch.tensor(PROMPTS, **self.i32)
@@ -81,12 +92,17 @@ class Server:
         parent, token, depth = (torch.empty(BQ, N, **self.i32) for _ in range(3))
         n_nodes = torch.empty(BQ, **self.i32)
         lbx.lbx_ddtree_build(p.log(), tok, root, N, parent, token, n_nodes, depth_out=depth)
-        out = self.step(n_nodes, BQ * N, parent=parent.view(-1), depth=depth)
+        # the first nodes of a tree are one; the walk takes N nodes: unused ones hang on the root
+        # with a token that never matches
+        n_nodes = torch.minimum(n_nodes, torch.tensor(MOST, **self.i32))
+        nodes = torch.arange(N, device="cuda").expand(BQ, N)
+        used = nodes < n_nodes[:, None]
+        parent, token = torch.where(used, parent, 0), torch.where(used, token, -1)
+        out = self.step(n_nodes, BQ * N, parent=parent, depth=depth)
         # the target's choices: at most nodes the draft token of a child, so that paths are accepted
         logits = torch.randn(BQ, N, VOCAB, generator=self.gen, device="cuda")
-        nodes = torch.arange(N, device="cuda").expand(BQ, N)
         child = torch.zeros(BQ, N + 1, dtype=torch.long, device="cuda")
-        child.scatter_reduce_(1, torch.where(parent >= 0, parent, N).long(), nodes, "amax")
+        child.scatter_reduce_(1, torch.where(used & (parent >= 0), parent, N).long(), nodes, "amax")
         agree = 20.0 * (torch.rand(BQ, N, 1, generator=self.gen, device="cuda") < 0.8)
         logits.scatter_add_(2, token.long().gather(1, child[:, :N])[..., None], agree)
         accepted, nxt = torch.empty(BQ, **self.i32), torch.empty(BQ, **self.i32)
