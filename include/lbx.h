@@ -521,7 +521,9 @@ typedef struct lbx_page_cfg {
  * the pages it holds beyond that go onto the free stack (request after request,
  * in order of position), then missing ones come off the stack's top (the same
  * order).  So an ended request (both lengths 0) gives its pages back, and one
- * whose draft was rejected those that only the draft had needed.
+ * whose draft was rejected those that only the draft had needed.  A page belongs to one
+ * request: nothing counts references, and a page that two requests hold would go onto the
+ * stack twice (lbx_prefix_attention reads a shared prompt from an array of its own).
  *   ctx_len, new_len, held [Bq], n_free [1] int32: in
  *   block_table [Bq][max_pages], free_list [n_pages] int32: in/out; entries past
  *     held_out, and places of the stack at or past its top, keep what they held
@@ -609,6 +611,10 @@ size_t lbx_paged_workspace_size(const lbx_page_cfg *cfg);
  * does not has to have a finite value; one that is not finite leaves that dimension of o
  * without a meaning (infinite or NaN).  A query all of whose scores are -inf gets o = 0
  * and lse = -inf; one with a NaN among its scores gets NaN for both.
+ * M, padding included, and Bq decide how the work is laid out at head dimension 128: past 768
+ * rows (tokens times Hq / Hkv) per request for long chunks, where single tokens over long caches
+ * take 1.7 times as long.  A step of single tokens that is captured in a graph should have an
+ * M of its own, not that of prompts.
  * Hq / Hkv <= LBX_PAGED_MAX_GROUP.  o, lse and the workspace must not overlap each other
  * or the inputs (each other or q: LBX_EINVAL).  Returns as lbx_window_attention.  Through
  * d_status, with nothing written: LBX_ETREE if start does not rise from 0 to at

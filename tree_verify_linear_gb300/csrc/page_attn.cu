@@ -65,7 +65,8 @@ extern "C" int lbx_paged_attention(const lbx_page_cfg *c, const int32_t *start,
   // heads: 508 us against 556 us on single CTAs); requests of few rows leave the second
   // subtile empty and are better off with more and smaller tiles (16 requests of one token
   // over 8001 to 16384 keys: 487 us against 845 us).  The lengths are on the device: M and
-  // Bq decide, by the rows of a request on average.  16 requests over 3000 keys, 32/8 heads,
+  // Bq decide, by the rows of a request on average, padding included (it is what the header tells
+  // callers: these single tokens padded to 4096 rows take 841 us).  16 requests over 3000 keys, 32/8 heads,
   // pairs against single CTAs: 192 tokens (768 rows) 154 against 135 us, 256 tokens 169
   // against 177 us, 512 tokens 329 against 358 us.
   const bool wide = c->dh == 128 && (long long)c->M * A.G > kWideRows * (long long)c->Bq;
