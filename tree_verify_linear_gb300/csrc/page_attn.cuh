@@ -44,8 +44,8 @@
 // have landed.
 //
 // What bounds it, measured on one GB300 (copies reach 6.79 TB/s, cuBLAS 1898 TFLOP/s in
-// bf16).  A chunk of 2048 tokens over 6144 keys, 24/4 heads of 256: 220 us, 1640 TFLOP/s, the
-// tensor pipe.  Prompts of 501 to 6001 tokens, 32/8 heads of 128: 508 us, 1365 TFLOP/s, the chain
+// bf16).  A chunk of 2048 tokens over 6144 keys, 24/4 heads of 256: 221 us, 1630 TFLOP/s, the
+// tensor pipe.  Prompts of 501 to 6001 tokens, 32/8 heads of 128: 512 us, 1355 TFLOP/s, the chain
 // from scores to weights (2900 cycles per block, 2060 of products).  16 requests of one token over
 // 8001 to 16384 keys, 4 layers, 32/8 heads of 128 in f16: 485 us, 6.59 TB/s.  Trees of 22, five
 // requests of 2049 to 4096 keys, 16 layers, 24/4 heads of 256: 200 us, 5.3 TB/s and what beginning
