@@ -496,8 +496,9 @@ int lbx_cache_evict(const lbx_attn_cfg *cfg, int budget, int n_recent, const int
 #define LBX_PAGED_MAX_GROUP 128 /* lbx_paged_attention: Hq / Hkv */
 
 /* How lbx_paged_attention's softmax weights meet V, whose type has 16 bits.  SPLIT is as
- * accurate as lbx_window_attention in bf16 and takes a tenth (one layer of draft trees or
- * single tokens) to two fifths longer (prompts; many layers at head dimension 256). */
+ * accurate as lbx_window_attention in bf16 and takes longer: a tenth to a fifth for one layer
+ * of draft trees or single tokens, up to two fifths for prompts and for many layers at
+ * head dimension 256. */
 #define LBX_WEIGHTS_ROUNDED 0 /* rounded once: 2^-8 of a weight in bf16, 2^-11 in f16 */
 #define LBX_WEIGHTS_SPLIT 1   /* in two parts: 2^-16 and 2^-22                        */
 
